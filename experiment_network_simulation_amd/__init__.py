@@ -3,7 +3,8 @@
 Thousands of independent experiments -- collective-communication traffic over
 switched topologies -- simulated tick by tick in one HIP megakernel behind the
 C ABI of include/msim.h.  `inputs` builds seeded synthetic batches; `sim.Sim`
-is the thin binding over libmsim.so.
+is the thin binding over libmsim.so; `moe` routes tokens to experts on the GPU
+and counts the all-to-all traffic they cause.
 """
 
 from . import inputs  # noqa: F401

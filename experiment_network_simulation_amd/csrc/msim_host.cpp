@@ -25,6 +25,7 @@
 #include <vector>
 
 #include "msim.h"
+#include "msim_error.h"
 #include "msim_layout.h"
 
 static_assert(CC_DCTCP == MSIM_CC_DCTCP && CC_DCQCN == MSIM_CC_DCQCN && CC_HPCC == MSIM_CC_HPCC, "congestion-control codes");
@@ -1643,3 +1644,13 @@ extern "C" const char *msim_last_error(const msim_ctx *ctx)
 }
 
 extern "C" void msim_destroy(msim_ctx *ctx) { delete ctx; }
+
+void msim_set_error(const char *what) noexcept
+{
+    try { g_create_error = what; } catch (...) { g_create_error.clear(); }
+}
+
+void msim_set_error2(const char *what, const char *why) noexcept
+{
+    try { g_create_error = std::string(what) + ": " + why; } catch (...) { g_create_error.clear(); }
+}

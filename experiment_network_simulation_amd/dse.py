@@ -1,7 +1,8 @@
 """Design-space exploration over the batched simulator.
 
-Two drivers from the pages, each scoring its candidates by simulation, all
-candidates of one step in one batch (single program, many experiments):
+Three drivers, each scoring its candidates by simulation, all candidates of one
+step in one batch (single program, many experiments), the first two from the
+pages:
 
   tune()        AutoCCL section 4.3: subspace-oriented tuning (Algorithm 1) with a
                 coordinate descent over the resource parameters in each subspace
@@ -12,6 +13,10 @@ candidates of one step in one batch (single program, many experiments):
                 load-balance-only, DFS-with-pruning and randomised greedy
                 schedulers, turned into task graphs of pipelined broadcasts and
                 scored in one batch.
+  route_designs()  expert-parallel router designs (top-k, groups, balance bias,
+                assignment dropout, expert placement) on one set of gate logits:
+                the GPU routes the tokens and counts the traffic, the all-to-all
+                dispatches of all designs are scored in one batch.
 
 Readings (the same as the plain reference of the test-suite):
   - A subspace is the algorithm: ring or tree for an all-reduce, ring otherwise.
@@ -422,4 +427,74 @@ def reshard(instances: Sequence[Tuple[I.Topology, Sequence[I.UnitComm]]], K: int
         t = ticks[k:k + len(scheds)]
         k += len(scheds)
         out.append(ReshardResult(names, scheds, t, int(np.argmin(t))))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Expert-parallel router designs
+# ---------------------------------------------------------------------------
+
+
+@dataclass
+class RouteDesign:
+    """A router and a placement to score.  place[e]: the host of expert e.
+    balance_steps rounds move the balance bias of each expert by balance_rate
+    against its load, as a training run does between its steps.  drop, per_row:
+    the share of assignments (of whole tokens) left out."""
+    top_k: int
+    place: Sequence[int]
+    score: str = "sigmoid"
+    groups: int = 1
+    top_groups: int = 1
+    group_top: int = 1
+    balance_steps: int = 0
+    balance_rate: float = 0.002
+    drop: float = 0.0
+    per_row: bool = False
+    token_bytes: int = 14336
+
+
+@dataclass
+class RouteScore:
+    ticks: int                           # completion tick of the dispatch all-to-all; 0: nothing travels
+    packets: int                         # packets of the dispatch
+    busiest: float                       # load of the busiest expert over the mean load
+    bias: np.ndarray                     # the balance bias it ended with
+    work: I.Workload                     # the simulated flows
+
+
+def route_designs(logits, token_off: Sequence[int], home: Sequence[int], designs: Sequence[RouteDesign],
+                  topo: I.Topology, evaluate, queue_pkts: int = 16, ecmp_seed: int = 0,
+                  seed: int = 0) -> List[RouteScore]:
+    """Scores every design on the tokens whose gate logits ([tokens, experts], a
+    GPU tensor) are given; the tokens of segment s, token_off[s] ..
+    token_off[s + 1] - 1, lie on host home[s].  evaluate(probes) -> ticks."""
+    import torch
+    from . import moe
+    dev = logits.device
+    hosts = int(topo.hosts().size)
+    off = torch.as_tensor(np.asarray(token_off, np.int64)).to(dev)
+    at = torch.as_tensor(np.asarray(home, np.int32)).to(dev)
+    routed = []
+    for d in designs:
+        how = dict(score=d.score, groups=d.groups, top_groups=d.top_groups, group_top=d.group_top)
+        bias = torch.zeros(logits.shape[1], device=dev) if d.balance_steps else None
+        r = moe.route(logits, d.top_k, bias=bias, **how)
+        for _ in range(d.balance_steps):
+            load = r.load.to(torch.float32)
+            bias.add_(torch.sign(load.mean() - load), alpha=d.balance_rate)
+            r = moe.route(logits, d.top_k, bias=bias, **how)
+        place = torch.as_tensor(np.asarray(d.place, np.int32)).to(dev)
+        pkts = moe.traffic(r.ids, off, at, place, hosts, token_bytes=d.token_bytes, pkt_bytes=I.PKT_BYTES,
+                           drop=d.drop, seed=seed, per_row=d.per_row)
+        routed.append((r.load, bias, pkts))
+    works = [I.traffic_flows(pkts.cpu().numpy(), home) for _, _, pkts in routed]
+    some = [k for k, w in enumerate(works) if w.xsrc.size]
+    ticks = np.zeros(len(works), np.int64)
+    ticks[some] = evaluate([Probe(topo, works[k], queue_pkts, ecmp_seed) for k in some])
+    out = []
+    for (load, bias, _), w, t in zip(routed, works, ticks):
+        n = load.cpu().numpy().astype(np.float64)
+        out.append(RouteScore(int(t), int(w.xpkts.sum(dtype=np.int64)), float(n.max() / n.mean()) if n.any() else 0.0,
+                              np.zeros(logits.shape[1], np.float32) if bias is None else bias.cpu().numpy(), w))
     return out

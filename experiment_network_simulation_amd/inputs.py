@@ -95,6 +95,17 @@ class SplitMix64:
         return a
 
 
+def splitmix_draws(seed: int, n: int, offset: int = 0) -> np.ndarray:
+    """Outputs offset .. offset + n - 1 of SplitMix64(seed) as u64: the generator
+    reads at any position, its state being seed + (position + 1) * gamma."""
+    with np.errstate(over="ignore"):
+        z = np.arange(n, dtype=np.uint64) + np.uint64((offset + 1) & _M64)
+        z = z * np.uint64(0x9E3779B97F4A7C15) + np.uint64(seed & _M64)
+        z = (z ^ (z >> np.uint64(30))) * np.uint64(0xBF58476D1CE4E5B9)
+        z = (z ^ (z >> np.uint64(27))) * np.uint64(0x94D049BB133111EB)
+        return z ^ (z >> np.uint64(31))
+
+
 def exp_rng(base: int, e: int) -> SplitMix64:
     """Per-experiment stream: seeded with one SplitMix64 output of base ^ e."""
     return SplitMix64(SplitMix64(base ^ e).next())
@@ -304,6 +315,35 @@ def xflows(pairs: Sequence[tuple]) -> Workload:
         w.xsrc, w.xdst, w.xpkts = (arr[:, 0].astype(np.uint32), arr[:, 1].astype(np.uint32),
                                    arr[:, 2].astype(np.uint32))
     return w
+
+
+def traffic_flows(packets: np.ndarray, home: Optional[Sequence[int]] = None) -> Workload:
+    """The explicit flows of an all-to-all: packets[s, h] from the host of
+    segment s (home[s]; default: host s) to host h, as moe.traffic() counts
+    them; zero-packet pairs carry no flow.  Segments of one host add up.  Flows
+    are listed by source, then destination id."""
+    pk = np.asarray(packets, np.int64)
+    n = pk.shape[1]
+    src = np.arange(pk.shape[0]) if home is None else np.asarray(home, np.int64)
+    if src.shape != (pk.shape[0],) or (src < 0).any() or (src >= n).any():
+        raise ValueError("home must name one of the hosts for every segment")
+    total = np.zeros((n, n), np.int64)
+    np.add.at(total, src, pk)
+    np.fill_diagonal(total, 0)
+    a, b = np.nonzero(total)
+    w = Workload()
+    w.xsrc, w.xdst, w.xpkts = a.astype(np.uint32), b.astype(np.uint32), total[a, b].astype(np.uint32)
+    return w
+
+
+def gate_logits(seed: int, rows: int, experts: int, spread: float = 1.5, popularity: float = 0.5) -> np.ndarray:
+    """Synthetic gate logits, float32 [rows, experts]: normal with deviation
+    `spread` around a popularity of each expert (normal with deviation
+    `popularity`), which skews the load as untrained gates do."""
+    n = rows * experts + experts
+    u = splitmix_draws(seed, 2 * n).astype(np.float64) / 2.0 ** 64
+    z = np.sqrt(-2.0 * np.log(1.0 - u[:n])) * np.cos(2.0 * np.pi * u[n:])      # Box and Muller, 1958
+    return (spread * z[experts:].reshape(rows, experts) + popularity * z[:experts]).astype(np.float32)
 
 
 # ---------------------------------------------------------------------------

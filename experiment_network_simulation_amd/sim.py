@@ -30,7 +30,8 @@ KERNEL_NAMES = ["msim_megakernel", "msim_megakernel_c8h_r1", "msim_megakernel_c8
 EXPORTED = ["msim_create", "msim_workspace_size", "msim_bind", "msim_run", "msim_run_noalloc", "msim_reset",
             "msim_results",
             "msim_flow_count", "msim_flow_ticks", "msim_task_count", "msim_task_ticks", "msim_get_info",
-            "msim_last_error", "msim_destroy", "msim_lds_probe"]
+            "msim_last_error", "msim_destroy", "msim_lds_probe",
+            "msim_route", "msim_route_backward", "msim_dropout", "msim_traffic"]
 
 _P8, _P32, _P64 = C.POINTER(C.c_uint8), C.POINTER(C.c_uint32), C.POINTER(C.c_uint64)
 
@@ -61,6 +62,20 @@ class _Options(C.Structure):
     _fields_ = [("version", C.c_uint32), ("n_record", C.c_uint32), ("record_exp", _P32),
                 ("host_threads", C.c_uint32), ("force_global", C.c_uint32), ("block_threads", C.c_uint32),
                 ("no_ring_path", C.c_uint32), ("reserved", C.c_uint32 * 7)]
+
+
+class RouteSpec(C.Structure):
+    _fields_ = [("version", C.c_uint32), ("dtype", C.c_uint32), ("score", C.c_uint32),
+                ("experts", C.c_uint32), ("top_k", C.c_uint32),
+                ("groups", C.c_uint32), ("top_groups", C.c_uint32), ("group_top", C.c_uint32),
+                ("renorm", C.c_uint32), ("scale", C.c_float), ("rows", C.c_uint64), ("row_stride", C.c_uint64)]
+
+
+class TrafficSpec(C.Structure):
+    _fields_ = [("version", C.c_uint32), ("experts", C.c_uint32), ("top_k", C.c_uint32), ("hosts", C.c_uint32),
+                ("rows", C.c_uint64), ("n_seg", C.c_uint64), ("token_bytes", C.c_uint32), ("pkt_bytes", C.c_uint32),
+                ("drop", C.c_double), ("seed", C.c_uint64), ("offset", C.c_uint64),
+                ("per_row", C.c_uint32), ("reserved", C.c_uint32)]
 
 
 class _Info(C.Structure):
@@ -101,6 +116,11 @@ def load_library():
     lib.msim_destroy.argtypes = [vp]
     lib.msim_destroy.restype = None
     lib.msim_lds_probe.argtypes = [vp, C.c_uint64, C.c_uint32, C.c_uint32, vp]
+    lib.msim_route.argtypes = [C.POINTER(RouteSpec), vp, vp, vp, vp, vp, vp]
+    lib.msim_route_backward.argtypes = [C.POINTER(RouteSpec), vp, vp, vp, vp, C.c_uint64, vp]
+    lib.msim_dropout.argtypes = [C.c_uint32, vp, vp, C.c_uint64, C.c_uint64, C.c_uint64, C.c_uint64, C.c_double,
+                                 C.c_uint64, C.c_uint64, C.c_uint32, vp]
+    lib.msim_traffic.argtypes = [C.POINTER(TrafficSpec), vp, vp, vp, vp, vp, vp]
     for name in EXPORTED:
         if name not in ("msim_last_error", "msim_destroy"):
             getattr(lib, name).restype = C.c_int

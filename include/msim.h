@@ -395,7 +395,8 @@ typedef struct msim_info {
 int msim_get_info(const msim_ctx *ctx, msim_info *info);
 
 /* Message of the last error on this context (or, for ctx == NULL, of the last
- * failed msim_create on the calling thread). */
+ * failed call without a context on the calling thread: msim_create,
+ * msim_route, msim_route_backward, msim_dropout, msim_traffic). */
 const char *msim_last_error(const msim_ctx *ctx);
 
 /* Frees host-side state; the workspace stays the caller's. */
@@ -412,6 +413,124 @@ void msim_destroy(msim_ctx *ctx);
  * MSIM_E_ARG for a NULL dev_out, too small an out_bytes, blocks == 0 or
  * > 2^20, or iters == 0; MSIM_E_HIP if the launch fails. */
 int msim_lds_probe(void *dev_out, uint64_t out_bytes, uint32_t blocks, uint32_t iters, void *hip_stream);
+
+/*
+ * Expert-parallel routing: from gate logits to the explicit flows of an
+ * all-to-all experiment (sparse, variable-volume rank-to-rank traffic, the
+ * expert-parallel + data-parallel discussion of the Perplexity MoE page).  The
+ * calls below work on device memory of the caller, enqueue on hip_stream and
+ * return at once; they allocate nothing, keep nothing between calls and may be
+ * captured into a graph.  The device that holds the arrays must be current.
+ * Calls on different streams may overlap when their outputs do not.  On error
+ * nothing is launched, the return code says why (MSIM_E_ARG, MSIM_E_LIMIT,
+ * MSIM_E_HIP) and msim_last_error(NULL) gives the message on the same thread.
+ */
+
+/* element types of logits, gradients and dropout's tensors */
+#define MSIM_F32 0
+#define MSIM_F16 1
+#define MSIM_BF16 2
+
+/* scores of the router */
+#define MSIM_SCORE_SOFTMAX 0     /* over all experts of the row */
+#define MSIM_SCORE_SIGMOID 1     /* each expert by itself */
+
+#define MSIM_MAX_EXPERTS 1024
+#define MSIM_MAX_EXPERT_GROUPS 64
+#define MSIM_MAX_TOP_K 32
+#define MSIM_MAX_TRAFFIC_HOSTS 16384
+
+/*
+ * A router.  Logits: rows x experts of type dtype, experts contiguous, row r at
+ * element r * row_stride.  With score s (softmax or sigmoid of the logits) and
+ * an optional balance bias b (one per expert):
+ *  - a logit of -inf, or a bias of -inf or NaN, takes an expert out for the row;
+ *    a row with a NaN logit (softmax: or one of +inf) is void: ids -1, weights
+ *    NaN, counted nowhere;
+ *  - the key of an expert is s + b, without bias the logit itself (the same
+ *    order).  Keys are compared as the real numbers the inputs define, to the
+ *    precision of 64-bit arithmetic, not as rounded scores; ties go to the
+ *    lower index;
+ *  - groups > 1: the experts in groups of experts / groups consecutive ones; a
+ *    group is worth the sum of its group_top (1 or 2) largest values of s + b
+ *    among its experts still in (group_top 1 without bias: its largest logit);
+ *    only the top_groups best groups with an expert still in stay;
+ *  - the top_k largest keys are chosen, in descending order; slots that find no
+ *    expert get id -1 and weight 0;
+ *  - weight = scale * s, with renorm scale * s / (sum of the chosen s).
+ * Limits: experts <= MSIM_MAX_EXPERTS, groups <= MSIM_MAX_EXPERT_GROUPS and a
+ * divisor of experts, top_k <= MSIM_MAX_TOP_K and <= top_groups * experts /
+ * groups.
+ */
+typedef struct msim_route_spec {
+    uint32_t version;            /* MSIM_ABI_VERSION */
+    uint32_t dtype;              /* MSIM_F32, MSIM_F16 or MSIM_BF16 */
+    uint32_t score;              /* MSIM_SCORE_* */
+    uint32_t experts, top_k;
+    uint32_t groups, top_groups, group_top;   /* 1, 1, 1: no groups */
+    uint32_t renorm;             /* 0 or 1 */
+    float scale;                 /* finite */
+    uint64_t rows, row_stride;   /* row_stride >= experts, in elements */
+} msim_route_spec;
+
+/*
+ * Routes every row: ids and weights are rows x top_k (contiguous), load (may be
+ * NULL) has one count per expert, the rows that chose it.  bias: experts
+ * floats, or NULL.  Every output element is written.
+ */
+int msim_route(const msim_route_spec *spec, const void *logits, const float *bias, int32_t *ids,
+               float *weights, int32_t *load, void *hip_stream);
+
+/*
+ * The gradient of msim_route's weights with respect to the logits, the choice
+ * held fixed.  ids as msim_route wrote them (entries outside 0 .. experts - 1
+ * are no choice; an expert named twice adds up), grad: rows x top_k.  Writes
+ * every element of grad_logits (type dtype, row r at r * grad_stride).  Scores
+ * are recomputed from the logits.  A row that chose nothing has gradient 0.
+ * spec's groups, top_groups and group_top are not used.
+ */
+int msim_route_backward(const msim_route_spec *spec, const void *logits, const int32_t *ids,
+                        const float *grad, void *grad_logits, uint64_t grad_stride, void *hip_stream);
+
+/*
+ * Dropout with a mask that is drawn again wherever it is needed and never
+ * stored: y = x / (1 - p) where kept, 0 where dropped (also where x is not
+ * finite).  Element i = row * cols + column (per_row: i = row) takes one half,
+ * the low one for even i, of output number offset + floor(i / 2) of the
+ * SplitMix64 stream of `seed` (the generator of the simulator's inputs, read at
+ * any position); it is dropped if that half is below round(p * 2^32).  p in
+ * [0, 1].  x_stride, y_stride: elements between rows.  y may be x (same
+ * stride).  The backward pass is the same call on the gradient.
+ */
+int msim_dropout(uint32_t dtype, const void *x, void *y, uint64_t rows, uint64_t cols, uint64_t x_stride,
+                 uint64_t y_stride, double p, uint64_t seed, uint64_t offset, uint32_t per_row,
+                 void *hip_stream);
+
+/*
+ * The all-to-all that routed tokens cause.  Tokens token_off[s] ..
+ * token_off[s+1]-1 (device array of n_seg + 1, ascending, within 0 .. rows)
+ * lie on host home[s] (a value outside 0 .. hosts - 1: on none of them); token
+ * t chose the experts ids[t * top_k ..], expert e lives on host place[e].
+ * Entries of ids outside 0 .. experts - 1 and of place outside 0 .. hosts - 1
+ * go nowhere.  With drop > 0, assignment (t, j) is dropped where msim_dropout
+ * with p = drop, this seed and offset drops element t * top_k + j (per_row:
+ * row t).  packets[s * hosts + h] = ceil(token_bytes / pkt_bytes * the tokens
+ * of s with an assignment left on host h), each token once per host, and 0 for
+ * h = home[s]; 0x7FFFFFFF where it would be more.  Rows behind token_off[n_seg]
+ * are not read.  Every element of packets is written.
+ */
+typedef struct msim_traffic_spec {
+    uint32_t version;            /* MSIM_ABI_VERSION */
+    uint32_t experts, top_k, hosts;
+    uint64_t rows, n_seg;
+    uint32_t token_bytes, pkt_bytes;   /* >= 1 */
+    double drop;
+    uint64_t seed, offset;
+    uint32_t per_row, reserved;
+} msim_traffic_spec;
+
+int msim_traffic(const msim_traffic_spec *spec, const int32_t *ids, const int64_t *token_off,
+                 const int32_t *home, const int32_t *place, int32_t *packets, void *hip_stream);
 
 #ifdef __cplusplus
 }
