@@ -75,7 +75,103 @@ struct RouteP {
     uint64_t rows, stride;
     uint32_t E, K, G, TG, gtop, renorm, sigmoid;
     float scale;
+    uint32_t lanes, glanes, part, vec;     /* msim_route_lists: lanes a row and a group, experts a lane, 16-byte loads */
 };
+
+/* Exchange with another lane of the same 16 (M = 1, 2: lane ^ M; 7, 15: the
+ * mirror of 8 and of 16), of the same 32 (16) or of the wavefront (32). */
+template <int M> __device__ __forceinline__ uint32_t other(uint32_t v)
+{
+    if constexpr (M == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);
+    else if constexpr (M == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);
+    else if constexpr (M == 7) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);
+    else if constexpr (M == 15) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);
+    else if constexpr (M == 16) return __builtin_amdgcn_ds_swizzle(v, 0x401F);
+    else return __shfl_xor(v, 32);
+}
+template <int M> __device__ __forceinline__ float other(float v)
+{
+    return __builtin_bit_cast(float, other<M>(__builtin_bit_cast(uint32_t, v)));
+}
+template <int M> __device__ __forceinline__ double other(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)other<M>((uint32_t)(u >> 32)) << 32 | other<M>((uint32_t)u));
+}
+
+/* Folds v over blocks of n lanes (a power of two); every lane has the result. */
+template <typename T, typename F> __device__ __forceinline__ T fold(T v, uint32_t n, F f)
+{
+    if (n > 1) v = f(v, other<1>(v));
+    if (n > 2) v = f(v, other<2>(v));
+    if (n > 4) v = f(v, other<7>(v));
+    if (n > 8) v = f(v, other<15>(v));
+    if (n > 16) v = f(v, other<16>(v));
+    if (n > 32) v = f(v, other<32>(v));
+    return v;
+}
+struct Max { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
+struct Min { __device__ float operator()(float a, float b) const { return fminf(a, b); } };
+struct Sum { __device__ float operator()(float a, float b) const { return a + b; } };
+
+/* A key and its expert in one 64-bit number that v_max_f64 orders: the high
+ * word is the key as a float, which orders as the high word of a double does
+ * (only a float's NaN would be one there), the low word the expert, so coded
+ * that of equal keys the lower expert is the larger.  One instruction compares
+ * both.  Written out, because fmax would quiet its operands first. */
+__device__ __forceinline__ double max64(double a, double b)
+{
+    double d;
+    asm("v_max_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
+}
+__device__ __forceinline__ double min64(double a, double b)
+{
+    double d;
+    asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
+}
+struct Max64 { __device__ double operator()(double a, double b) const { return max64(a, b); } };
+
+__device__ __forceinline__ double pack(float key, uint32_t e)
+{
+    const int32_t hi = __builtin_bit_cast(int32_t, key);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)hi << 32 | ((uint32_t)(hi >> 31) ^ ~e));
+}
+__device__ __forceinline__ float key_of(double v)
+{
+    return __builtin_bit_cast(float, (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 32));
+}
+__device__ __forceinline__ uint32_t expert_of(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return ~((uint32_t)u ^ (uint32_t)((int32_t)(u >> 32) >> 31));
+}
+
+__device__ __forceinline__ void order(double &a, double &b)
+{
+    const double x = max64(a, b);
+    b = min64(a, b);
+    a = x;
+}
+/* eight numbers in descending order, 19 comparisons */
+__device__ __forceinline__ void sort8(double *a)
+{
+    order(a[0], a[2]); order(a[1], a[3]); order(a[4], a[6]); order(a[5], a[7]);
+    order(a[0], a[4]); order(a[1], a[5]); order(a[2], a[6]); order(a[3], a[7]);
+    order(a[0], a[1]); order(a[2], a[3]); order(a[4], a[5]); order(a[6], a[7]);
+    order(a[2], a[4]); order(a[3], a[5]);
+    order(a[1], a[4]); order(a[3], a[6]);
+    order(a[1], a[2]); order(a[3], a[4]); order(a[5], a[6]);
+}
+/* a and b in descending order: a becomes the eight largest of both, in order */
+__device__ __forceinline__ void keep8(double *a, const double *b)
+{
+    for (int i = 0; i < 8; i++) a[i] = max64(a[i], b[7 - i]);      /* a bitonic sequence */
+    for (int d = 4; d; d >>= 1)
+        for (int i = 0; i < 8; i++)
+            if (!(i & d)) order(a[i], a[i + d]);
+}
 
 template <typename T> __device__ __forceinline__ T wave_max(T v)
 {
@@ -88,6 +184,30 @@ template <typename T> __device__ __forceinline__ T wave_sum(T v)
     return v;
 }
 
+/* The weight of the slot this lane has (got: it has one), logit xs, over the
+ * row's n lanes.  s = e^min(x,0) / (1 + e^-|x|) for a sigmoid, e^(x - top) inv
+ * for a softmax; renormalised, the exponentials are taken relative to the
+ * largest chosen one, so that no sum vanishes. */
+__device__ __forceinline__ float weight_of(const RouteP &p, float xs, bool got, uint32_t n, float top, float inv)
+{
+    float q;
+    if (p.sigmoid) {
+        const float lo = fminf(xs, 0.0f);
+        const float c = p.renorm ? fold(got ? lo : -INFINITY, n, Max()) : 0.0f;
+        q = expf(lo - c) / (1.0f + expf(-fabsf(xs)));
+    } else if (p.renorm) {
+        q = expf(xs - fold(got ? xs : -INFINITY, n, Max()));
+    } else {
+        q = expf(xs - top) * inv;
+    }
+    if (!got) q = 0.0f;
+    if (p.renorm) {
+        const float sum = fold(q, n, Sum());
+        if (got) q /= sum;
+    }
+    return p.scale * q;
+}
+
 __device__ __forceinline__ double score64(double x, bool sigmoid, double top, double inv)
 {
     if (sigmoid) {
@@ -97,135 +217,295 @@ __device__ __forceinline__ double score64(double x, bool sigmoid, double top, do
     return exp(x - top) * inv;
 }
 
-/* One row by one wavefront, keys in 64 bits.  Lane l holds experts l, l + 64,
- * ...: loads are consecutive, and each of top_k rounds finds the best key left
- * by exchanges of (key, index) between lanes. */
-template <typename D, int VPL>
-__device__ void route_row(const RouteP &p, uint64_t row, int32_t *hist)
+/* One row by one wavefront, keys in 64 bits, held in key[] (LDS, experts
+ * doubles of this wavefront's own).  Lane l works on experts l, l + 64, ...:
+ * loads are consecutive, no lane reads another's keys, and each of top_k rounds
+ * finds the best key left by exchanges of (key, index) between lanes. */
+template <typename D> __device__ void route_row(const RouteP &p, uint64_t row, double *key, int32_t *hist)
 {
-    const int lane = threadIdx.x & 63;
+    const uint32_t lane = threadIdx.x & 63;
     const typename D::raw *x = (const typename D::raw *)p.x + row * p.stride;
-    float v[VPL];
-    double key[VPL];
     bool bad = false;
     float top = -INFINITY;
-    for (int i = 0; i < VPL; i++) {
-        const uint32_t e = i * WAVE + lane;
-        v[i] = e < p.E ? D::get(x[e]) : -INFINITY;
-        bad |= v[i] != v[i] || (!p.sigmoid && v[i] == INFINITY);
-        top = fmaxf(top, v[i]);
+    for (uint32_t e = lane; e < p.E; e += WAVE) {
+        const float v = D::get(x[e]);
+        bad |= v != v || (!p.sigmoid && v == INFINITY);
+        top = fmaxf(top, v);
     }
     const bool is_void = __any(bad);
-    top = wave_max(top);
+    top = fold(top, WAVE, Max());
     int32_t my_id = -1;
+    double inv = 1.0;
     if (!is_void && top > -INFINITY) {
-        double inv = 1.0;
-        if (!p.sigmoid) {
+        if (!p.sigmoid && (p.bias || p.gtop > 1 || !p.renorm)) {
             double sum = 0;
-            for (int i = 0; i < VPL; i++) sum += v[i] > -INFINITY ? exp((double)v[i] - top) : 0.0;
-            inv = 1.0 / wave_sum(sum);
-        }
-        for (int i = 0; i < VPL; i++) {
-            const uint32_t e = i * WAVE + lane;
-            key[i] = v[i];
-            if (p.bias && e < p.E && v[i] > -INFINITY) {
-                const double b = p.bias[e];
-                key[i] = b > -INFINITY ? score64(v[i], p.sigmoid, top, inv) + b : -INFINITY;
+            for (uint32_t e = lane; e < p.E; e += WAVE) {
+                const float v = D::get(x[e]);
+                if (v > -INFINITY) sum += exp((double)v - top);
             }
+            for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
+            inv = 1.0 / sum;
+        }
+        for (uint32_t e = lane; e < p.E; e += WAVE) {
+            const float v = D::get(x[e]);
+            double k = v;
+            if (p.bias && v > -INFINITY)
+                k = p.bias[e] > -INFINITY ? score64(v, p.sigmoid, top, inv) + p.bias[e] : -INFINITY;
+            key[e] = k;
         }
         if (p.G > 1) {
             /* lane g walks group g: its one or two best members */
             const uint32_t size = p.E / p.G;
-            double total = -INFINITY;
-            if (lane < (int)p.G) {
+            double worth = -INFINITY;
+            if (lane < p.G) {
                 double a = -INFINITY, c = -INFINITY;
-                for (uint32_t k = 0; k < size; k++) {
-                    const uint32_t e = lane * size + k;
-                    const float t = D::get(x[e]);
-                    double q = t;
-                    if (t > -INFINITY && (p.bias || p.gtop > 1)) {
-                        q = score64(t, p.sigmoid, top, inv);
-                        if (p.bias) q = p.bias[e] > -INFINITY ? q + p.bias[e] : -INFINITY;
+                for (uint32_t e = lane * size; e < (lane + 1) * size; e++) {
+                    const float v = D::get(x[e]);
+                    double k = v;
+                    if (v > -INFINITY && (p.bias || p.gtop > 1)) {
+                        k = score64(v, p.sigmoid, top, inv);
+                        if (p.bias) k = p.bias[e] > -INFINITY ? k + p.bias[e] : -INFINITY;
                     }
-                    if (q > a) { c = a; a = q; }
-                    else if (q > c) c = q;
+                    if (k > a) { c = a; a = k; }
+                    else if (k > c) c = k;
                 }
-                total = p.gtop > 1 && c > -INFINITY ? a + c : a;
+                worth = p.gtop > 1 && c > -INFINITY ? a + c : a;
             }
             uint32_t before = 0;           /* groups better than this lane's */
             for (uint32_t g = 0; g < p.G; g++) {
-                const double t = __shfl(total, (int)g);
-                before += t > total || (t == total && g < (uint32_t)lane);
+                const double w = __shfl(worth, (int)g);
+                before += w > worth || (w == worth && g < lane);
             }
-            const uint64_t stay = __ballot(lane < (int)p.G && before < p.TG);
-            for (int i = 0; i < VPL; i++) {
-                const uint32_t e = i * WAVE + lane;
-                if (e < p.E && !((stay >> (e / size)) & 1)) key[i] = -INFINITY;
-            }
+            const uint64_t stay = __ballot(lane < p.G && before < p.TG);
+            for (uint32_t e = lane; e < p.E; e += WAVE)
+                if (!((stay >> (e / size)) & 1)) key[e] = -INFINITY;
         }
         for (uint32_t r = 0; r < p.K; r++) {
             double best = -INFINITY;
             int at = -1;
-            for (int i = 0; i < VPL; i++)
-                if (key[i] > best) { best = key[i]; at = i * WAVE + lane; }
+            for (uint32_t e = lane; e < p.E; e += WAVE)
+                if (key[e] > best) { best = key[e]; at = e; }
             for (int m = 32; m; m >>= 1) {
                 const double ob = __shfl_xor(best, m);
                 const int oa = __shfl_xor(at, m);
                 if (oa >= 0 && (at < 0 || ob > best || (ob == best && oa < at))) { best = ob; at = oa; }
             }
             if (at < 0) break;
-            for (int i = 0; i < VPL; i++)
-                if (i * WAVE + lane == at) key[i] = -INFINITY;
-            if (lane == (int)r) my_id = at;
+            if ((at & 63) == (int)lane) key[at] = -INFINITY;
+            if (lane == r) my_id = at;
         }
     }
     /* weights: lane j has slot j */
     const float xs = my_id >= 0 ? D::get(x[my_id]) : -INFINITY;
-    float q;
-    if (p.sigmoid) {
-        /* s = e^min(x,0) / (1 + e^-|x|); renormalised, the first factor is
-         * taken relative to the largest chosen one, so that no sum vanishes */
-        const float lo = fminf(xs, 0.0f);
-        const float c = p.renorm ? wave_max(lo) : 0.0f;
-        q = my_id >= 0 ? expf(lo - c) / (1.0f + expf(-fabsf(xs))) : 0.0f;
-    } else {
-        const float c = p.renorm ? wave_max(xs) : top;
-        q = my_id >= 0 ? expf(xs - c) : 0.0f;
-        if (!p.renorm) {
-            float sum = 0;
-            for (int i = 0; i < VPL; i++) sum += v[i] > -INFINITY ? expf(v[i] - top) : 0.0f;
-            q /= wave_sum(sum);
-        }
-    }
-    if (p.renorm) {
-        const float sum = wave_sum(q);
-        q = my_id >= 0 ? q / sum : 0.0f;
-    }
-    if (my_id < 0) q = 0.0f;
-    if (lane < (int)p.K) {
+    const float q = weight_of(p, xs, my_id >= 0, WAVE, top, (float)inv);
+    if (lane < p.K) {
         p.ids[row * p.K + lane] = my_id;
-        p.w[row * p.K + lane] = is_void ? NAN : p.scale * q;
+        p.w[row * p.K + lane] = is_void ? NAN : q;
         if (p.load && my_id >= 0) atomicAdd(&hist[my_id], 1);
     }
 }
 
-template <typename D, int VPL> __global__ void __launch_bounds__(256) msim_route_rows(RouteP p)
+/* the workgroup's counts join the others' */
+__device__ __forceinline__ void add_load(const RouteP &p, const int32_t *hist)
+{
+    if (!p.load) return;
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
+        if (gridDim.x == 1) p.load[e] = hist[e];
+        else if (hist[e]) atomicAdd(&p.load[e], hist[e]);
+    }
+}
+
+/* any top_k, experts and groups: a wavefront a row */
+template <typename D> __global__ void __launch_bounds__(256) msim_route_rows(RouteP p)
 {
     __shared__ int32_t hist[MSIM_MAX_EXPERTS];
-    if (p.load) {
+    extern __shared__ double keys[];
+    if (p.load)
         for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
-        __syncthreads();
-    }
+    __syncthreads();
     const uint64_t step = (uint64_t)gridDim.x * (blockDim.x / WAVE);
     for (uint64_t row = (uint64_t)blockIdx.x * (blockDim.x / WAVE) + threadIdx.x / WAVE; row < p.rows; row += step)
-        route_row<D, VPL>(p, row, hist);
-    if (p.load) {
-        __syncthreads();
-        for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
-            if (gridDim.x == 1) p.load[e] = hist[e];
-            else if (hist[e]) atomicAdd(&p.load[e], hist[e]);
+        route_row<D>(p, row, keys + threadIdx.x / WAVE * p.E, hist);
+    add_load(p, hist);
+}
+
+/* Eight or fewer choices a row, several rows a wavefront.
+ *
+ * A row has `lanes` lanes (8 .. 64), each with up to VPL consecutive experts;
+ * with groups a group has its own lanes, so that its best members meet in few
+ * or no exchanges.  A lane sorts its experts' keys eight at a time and keeps its
+ * eight largest in order; top_k rounds then take the largest head of the row's
+ * lists.  Per value that is a score and about eight comparisons, no exchange.
+ *
+ * Without bias keys are the logits and the choice is exact.  With bias (and for
+ * sums of two scores) the keys here are 32-bit approximations with a known
+ * error, and a row whose choice depends on a difference within twice that error
+ * is routed again in 64 bits by route_row.  Errors: a sigmoid is off by less
+ * than 2^-22 (v_exp_f32 and v_rcp_f32 are off by 2^-23 relative, the argument
+ * x log2 e by 1.5 2^-24 |x| and |x| s (1 - s) < 0.23); a softmax score by less
+ * than 2^-24 (0.6 + 48 s) (a sum of 32 terms a lane, six exchanges); the sum
+ * with the bias by 2^-24 |key| more. */
+template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
+{
+    constexpr int PER16 = 16 / sizeof(typename D::raw);
+    typedef typename D::raw vec __attribute__((ext_vector_type(PER16)));
+    __shared__ int32_t hist[MSIM_MAX_EXPERTS];
+    __shared__ float lds_bias[BIAS ? 64 * (VPL + 4) : 1];
+    extern __shared__ double keys[];       /* of route_row */
+    const uint32_t lane = threadIdx.x & 63, l = lane & (p.lanes - 1), sub = l & (p.glanes - 1);
+    const uint32_t g = l / p.glanes, size = p.E / p.G;
+    const uint32_t first = g * size + sub * p.part;           /* this lane's experts */
+    const uint32_t past = g < p.G ? min(first + p.part, (g + 1) * size) : first;
+    const uint32_t n = past > first ? past - first : 0;
+    if (p.load)
+        for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
+    if (BIAS && threadIdx.x < p.lanes)
+        for (uint32_t i = 0; i < VPL; i++) {
+            const float b = i < n ? p.bias[first + i] : -INFINITY;
+            lds_bias[l * (VPL + 4) + i] = b == b ? b : -INFINITY;
+        }
+    __syncthreads();
+    const uint32_t rpw = WAVE / p.lanes;                      /* rows a wavefront */
+    const uint64_t step = (uint64_t)gridDim.x * (blockDim.x / WAVE) * rpw;
+    const uint64_t row0 = ((uint64_t)blockIdx.x * (blockDim.x / WAVE) + threadIdx.x / WAVE) * rpw;
+    const bool sigmoid = p.sigmoid;
+    for (uint64_t rows = row0; rows < p.rows; rows += step) {
+        const uint64_t row = min(rows + lane / p.lanes, p.rows - 1);
+        const bool mine = rows + lane / p.lanes < p.rows;
+        const typename D::raw *x = (const typename D::raw *)p.x + row * p.stride;
+        float v[VPL];
+        if (p.vec) {
+            for (int c = 0; c < VPL / PER16; c++) {
+                vec t = {};
+                if (n) t = *(const vec *)(x + first + c * PER16);
+                for (int i = 0; i < PER16; i++) v[c * PER16 + i] = n ? D::get(t[i]) : -INFINITY;
+            }
+        } else {
+            for (int i = 0; i < VPL; i++) v[i] = (uint32_t)i < n ? D::get(x[first + i]) : -INFINITY;
+        }
+        /* is anything not finite?  0 * x is NaN then */
+        float odd = 0.0f;
+        for (int i = 0; i < VPL; i++) odd = __builtin_fmaf(v[i], 0.0f, odd);
+        bool is_void = false;
+        if (__any(odd != odd)) {
+            bool bad = false;
+            for (int i = 0; i < VPL; i++) bad |= v[i] != v[i] || (!sigmoid && v[i] == INFINITY);
+            is_void = fold(bad ? 1.0f : 0.0f, p.lanes, Max()) > 0.0f;
+        }
+        float top = 0.0f, inv = 1.0f;
+        if (!sigmoid && (BIAS || p.G > 1 || !p.renorm)) {
+            top = v[0];
+            for (int i = 1; i < VPL; i++) top = fmaxf(top, v[i]);
+            top = fold(top, p.lanes, Max());
+            if (!(top > -INFINITY && top < INFINITY)) top = 0.0f;     /* nothing in, or void */
+        }
+        double a[8];
+        if (BIAS || (!sigmoid && !p.renorm)) {
+            float s[VPL];
+            if (!sigmoid) {
+                float sum = 0.0f;
+                for (int i = 0; i < VPL; i++) {
+                    s[i] = __builtin_amdgcn_exp2f((v[i] - top) * 1.44269504f);
+                    sum += s[i];
+                }
+                inv = 1.0f / fold(sum, p.lanes, Sum());
+            }
+            if (BIAS) {
+                for (int c = 0; c < VPL; c += 4) {
+                    const f32x4 b = *(const f32x4 *)&lds_bias[l * (VPL + 4) + c];
+                    for (int i = 0; i < 4; i++) {
+                        const float t = v[c + i];
+                        const float q = sigmoid
+                            ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t * -1.44269504f)) : s[c + i] * inv;
+                        v[c + i] = t > -INFINITY ? q + b[i] : -INFINITY;
+                    }
+                }
+            }
+        }
+        for (int c = 0; c < VPL; c += 8) {
+            double b[8];
+            /* + 0: the two zeros are equal; a NaN (of a void row) is ordered as it falls */
+            for (int i = 0; i < 8; i++) (c ? b : a)[i] = pack(v[c + i] + 0.0f, first + c + i);
+            sort8(c ? b : a);
+            if (c) keep8(a, b);
+        }
+        const float slack = sigmoid ? 0x1p-20f : 0x1p-22f + 0x1p-17f * inv;
+        bool near = false;
+        if (p.G > 1) {
+            float t1 = key_of(a[0]), t2 = key_of(a[1]);
+            for (uint32_t m = 1; m < p.glanes; m <<= 1) {
+                const float o1 = __shfl_xor(t1, (int)m), o2 = __shfl_xor(t2, (int)m);
+                t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
+                t1 = fmaxf(t1, o1);
+            }
+            if (!BIAS && p.gtop > 1) {
+                if (sigmoid) {
+                    t1 = t1 > -INFINITY ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t1 * -1.44269504f)) : t1;
+                    t2 = t2 > -INFINITY ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t2 * -1.44269504f)) : t2;
+                } else {
+                    t1 = t1 > -INFINITY ? __builtin_amdgcn_exp2f((t1 - top) * 1.44269504f) : t1;
+                    t2 = t2 > -INFINITY ? __builtin_amdgcn_exp2f((t2 - top) * 1.44269504f) : t2;
+                }
+            }
+            const float worth = p.gtop > 1 && t2 > -INFINITY ? t1 + t2 : t1;
+            uint32_t before = 0;
+            for (uint32_t o = p.glanes; o < p.lanes; o += p.glanes) {
+                const float w = __shfl_xor(worth, (int)o);
+                before += w > worth || (w == worth && (l ^ o) < l);
+            }
+            const bool stay = before < p.TG;
+            if (BIAS || p.gtop > 1) {
+                const float in = fold(stay ? worth : INFINITY, p.lanes, Min());
+                const float out = fold(stay ? -INFINITY : worth, p.lanes, Max());
+                near = out > -INFINITY && !(in - out > 2.0f * slack + 0x1p-20f * fabsf(in));
+            }
+            if (!stay)
+                for (int i = 0; i < 8; i++) a[i] = pack(-INFINITY, 0);
+        }
+        double slot = pack(-INFINITY, 0), last = slot;
+        for (uint32_t r = 0; r <= (BIAS ? p.K : p.K - 1); r++) {
+            const double m = fold(a[0], p.lanes, Max64());
+            if (l == r) slot = m;
+            if (BIAS) last = m;
+            const bool won = __builtin_bit_cast(uint64_t, m) == __builtin_bit_cast(uint64_t, a[0]);
+            for (int i = 0; i < 7; i++) a[i] = won ? a[i + 1] : a[i];
+            a[7] = won ? pack(-INFINITY, 0) : a[7];
+        }
+        const bool got = l < p.K && key_of(slot) > -INFINITY && !is_void;
+        const int32_t id = got ? (int32_t)expert_of(slot) : -1;
+        const float xs = got ? (BIAS ? D::get(x[id]) : key_of(slot)) : -INFINITY;
+        if (BIAS) {
+            const float k0 = key_of(slot);
+            float k1 = __shfl_down(k0, 1);
+            if (l == p.K - 1) k1 = key_of(last);
+            bool close = got && !(k0 - k1 > slack + 0x1p-22f * fabsf(k0));
+            if (__any(close)) {
+                /* the same logit and the same bias: the same key, in order already */
+                const float b = got ? p.bias[id] : 0.0f;
+                const float xn = __shfl_down(xs, 1), bn = __shfl_down(b, 1);
+                if (l < p.K - 1 && xs == xn && b == bn) close = false;
+            }
+            near |= close;
+        }
+        bool again = false;
+        if (BIAS || p.gtop > 1) again = fold(near ? 1.0f : 0.0f, p.lanes, Max()) > 0.0f && !is_void;
+        const float q = weight_of(p, xs, got, p.lanes, top, inv);
+        if (mine && !again && l < p.K) {
+            p.ids[row * p.K + l] = id;
+            p.w[row * p.K + l] = is_void ? NAN : q;
+            if (p.load && got) atomicAdd(&hist[id], 1);
+        }
+        if (BIAS || p.gtop > 1) {
+            uint64_t todo = __ballot(mine && again && l == 0);
+            while (todo) {
+                const int at = __builtin_ctzll(todo);
+                todo &= todo - 1;
+                route_row<D>(p, rows + at / p.lanes, keys + threadIdx.x / WAVE * p.E, hist);
+            }
         }
     }
+    add_load(p, hist);
 }
 
 __global__ void msim_fill_words(int32_t *out, uint32_t n)
@@ -421,16 +701,47 @@ const char *check_route(const msim_route_spec *s, bool backward, int *code)
     return nullptr;
 }
 
-template <typename D> void launch_route(const RouteP &p, hipStream_t st)
+uint32_t pow2(uint32_t v)
 {
+    uint32_t p = 1;
+    while (p < v) p *= 2;
+    return p;
+}
+
+template <typename D, int VPL> void launch_lists(const RouteP &p, hipStream_t st)
+{
+    const uint32_t rows = 4 * WAVE / p.lanes;
+    const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + rows - 1) / rows, 1024);
+    if (p.load && grid != 1) msim_fill_words<<<(p.E + 255) / 256, 256, 0, st>>>(p.load, p.E);
+    if (!grid) return;
+    const size_t keys = p.bias || p.gtop > 1 ? 4 * p.E * sizeof(double) : 0;
+    if (p.bias) msim_route_lists<D, VPL, true><<<grid, 256, keys, st>>>(p);
+    else msim_route_lists<D, VPL, false><<<grid, 256, keys, st>>>(p);
+}
+
+template <typename D> void launch_route(RouteP p, hipStream_t st)
+{
+    /* lists of eight: lanes for every group, at most 32 experts a lane */
+    const uint32_t size = p.E / p.G, g2 = pow2(p.G);
+    uint32_t glanes = std::max(1u, 8 / g2);
+    while ((size + glanes - 1) / glanes > 32) glanes *= 2;
+    if (p.K <= 8 && g2 * glanes <= WAVE) {
+        const size_t sz = sizeof(typename D::raw);
+        p.glanes = glanes;
+        p.lanes = g2 * glanes;
+        p.part = (size + glanes - 1) / glanes;
+        const uint32_t vpl = std::max(8u, pow2(p.part));
+        p.vec = p.part == vpl && p.part * glanes == size && (size * sz) % 16 == 0 && (p.stride * sz) % 16 == 0 &&
+                (uintptr_t)p.x % 16 == 0;
+        if (vpl == 8) launch_lists<D, 8>(p, st);
+        else if (vpl == 16) launch_lists<D, 16>(p, st);
+        else launch_lists<D, 32>(p, st);
+        return;
+    }
     const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + 3) / 4, 2048);
     if (p.load && grid != 1) msim_fill_words<<<(p.E + 255) / 256, 256, 0, st>>>(p.load, p.E);
     if (!grid) return;
-    if (p.E <= 64) msim_route_rows<D, 1><<<grid, 256, 0, st>>>(p);
-    else if (p.E <= 128) msim_route_rows<D, 2><<<grid, 256, 0, st>>>(p);
-    else if (p.E <= 256) msim_route_rows<D, 4><<<grid, 256, 0, st>>>(p);
-    else if (p.E <= 512) msim_route_rows<D, 8><<<grid, 256, 0, st>>>(p);
-    else msim_route_rows<D, 16><<<grid, 256, 0, st>>>(p);
+    msim_route_rows<D><<<grid, 256, 4 * p.E * sizeof(double), st>>>(p);
 }
 
 } // namespace
@@ -442,8 +753,8 @@ extern "C" int msim_route(const msim_route_spec *s, const void *logits, const fl
     if (const char *why = check_route(s, false, &code)) return fail(code, why);
     if (s->rows && (!logits || !ids || !weights)) return fail(MSIM_E_ARG, "route: null logits, ids or weights");
     RouteP p = {logits, bias, ids, weights, load, s->rows, s->row_stride, s->experts, s->top_k, s->groups,
-                s->top_groups, s->group_top, s->renorm, s->score == MSIM_SCORE_SIGMOID, s->scale};
-    if (p.TG == p.G) p.G = p.TG = 1;       /* every group stays */
+                s->top_groups, s->group_top, s->renorm, s->score == MSIM_SCORE_SIGMOID, s->scale, 0, 0, 0, 0};
+    if (p.TG == p.G) p.G = p.TG = p.gtop = 1;       /* every group stays */
     hipStream_t st = (hipStream_t)hip_stream;
     if (s->dtype == MSIM_F32) launch_route<F32>(p, st);
     else if (s->dtype == MSIM_F16) launch_route<F16>(p, st);
