@@ -18,6 +18,7 @@ typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int WAVE = 64;
+constexpr uint32_t REDO = 32;          /* turns of a wavefront after which undecided rows are routed again */
 
 /* ------------------------------------------------------------------------ */
 /* element types                                                             */
@@ -208,26 +209,24 @@ __device__ __forceinline__ float weight_of(const RouteP &p, float xs, bool got, 
     return p.scale * q;
 }
 
-__device__ __forceinline__ double score64(double x, bool sigmoid, double top, double inv)
+/* what the wavefront's lanes wrote to LDS is there for its other lanes */
+__device__ __forceinline__ void wave_sync()
 {
-    if (sigmoid) {
-        const double e = exp(-fabs(x));
-        return (x >= 0 ? 1.0 : e) / (1.0 + e);
-    }
-    return exp(x - top) * inv;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 /* One row by one wavefront, keys in 64 bits, held in key[] (LDS, experts
  * doubles of this wavefront's own).  Lane l works on experts l, l + 64, ...:
- * loads are consecutive, no lane reads another's keys, and each of top_k rounds
- * finds the best key left by exchanges of (key, index) between lanes. */
+ * loads are consecutive, and each of top_k rounds finds the best key left by
+ * exchanges of (key, index) between lanes. */
 template <typename D> __device__ void route_row(const RouteP &p, uint64_t row, double *key, int32_t *hist)
 {
     const uint32_t lane = threadIdx.x & 63;
     const typename D::raw *x = (const typename D::raw *)p.x + row * p.stride;
     bool bad = false;
     float top = -INFINITY;
-    for (uint32_t e = lane; e < p.E; e += WAVE) {
+    _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE) {
         const float v = D::get(x[e]);
         bad |= v != v || (!p.sigmoid && v == INFINITY);
         top = fmaxf(top, v);
@@ -237,53 +236,58 @@ template <typename D> __device__ void route_row(const RouteP &p, uint64_t row, d
     int32_t my_id = -1;
     double inv = 1.0;
     if (!is_void && top > -INFINITY) {
-        if (!p.sigmoid && (p.bias || p.gtop > 1 || !p.renorm)) {
+        const bool scored = p.bias || p.gtop > 1;
+        if (scored || (!p.sigmoid && !p.renorm)) {
             double sum = 0;
-            for (uint32_t e = lane; e < p.E; e += WAVE) {
-                const float v = D::get(x[e]);
-                if (v > -INFINITY) sum += exp((double)v - top);
+            _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE) {
+                const double v = D::get(x[e]);
+                const double t = exp(p.sigmoid ? -fabs(v) : v - top);
+                sum += t;
+                key[e] = t;
             }
             for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
-            inv = 1.0 / sum;
+            inv = p.sigmoid ? 1.0 : 1.0 / sum;
         }
-        for (uint32_t e = lane; e < p.E; e += WAVE) {
+        _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE) {
             const float v = D::get(x[e]);
             double k = v;
-            if (p.bias && v > -INFINITY)
-                k = p.bias[e] > -INFINITY ? score64(v, p.sigmoid, top, inv) + p.bias[e] : -INFINITY;
+            if (scored && v > -INFINITY) {
+                const double t = key[e];
+                k = p.sigmoid ? (v >= 0 ? 1.0 : t) / (1.0 + t) : t * inv;
+                if (p.bias) k = p.bias[e] > -INFINITY ? k + p.bias[e] : -INFINITY;
+            }
             key[e] = k;
         }
         if (p.G > 1) {
-            /* lane g walks group g: its one or two best members */
+            /* lane g walks group g: its one or two best members, other lanes' keys among them */
+            wave_sync();
             const uint32_t size = p.E / p.G;
             double worth = -INFINITY;
             if (lane < p.G) {
                 double a = -INFINITY, c = -INFINITY;
-                for (uint32_t e = lane * size; e < (lane + 1) * size; e++) {
-                    const float v = D::get(x[e]);
-                    double k = v;
-                    if (v > -INFINITY && (p.bias || p.gtop > 1)) {
-                        k = score64(v, p.sigmoid, top, inv);
-                        if (p.bias) k = p.bias[e] > -INFINITY ? k + p.bias[e] : -INFINITY;
-                    }
+                _Pragma("unroll 1") for (uint32_t e = lane * size; e < (lane + 1) * size; e++) {
+                    const double k = key[e];
                     if (k > a) { c = a; a = k; }
                     else if (k > c) c = k;
                 }
                 worth = p.gtop > 1 && c > -INFINITY ? a + c : a;
             }
+            wave_sync();
             uint32_t before = 0;           /* groups better than this lane's */
-            for (uint32_t g = 0; g < p.G; g++) {
+            _Pragma("unroll 1") for (uint32_t g = 0; g < p.G; g++) {
                 const double w = __shfl(worth, (int)g);
                 before += w > worth || (w == worth && g < lane);
             }
             const uint64_t stay = __ballot(lane < p.G && before < p.TG);
-            for (uint32_t e = lane; e < p.E; e += WAVE)
+            _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE) {
                 if (!((stay >> (e / size)) & 1)) key[e] = -INFINITY;
+                else if (!p.bias) key[e] = D::get(x[e]);
+            }
         }
-        for (uint32_t r = 0; r < p.K; r++) {
+        _Pragma("unroll 1") for (uint32_t r = 0; r < p.K; r++) {
             double best = -INFINITY;
             int at = -1;
-            for (uint32_t e = lane; e < p.E; e += WAVE)
+            _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE)
                 if (key[e] > best) { best = key[e]; at = e; }
             for (int m = 32; m; m >>= 1) {
                 const double ob = __shfl_xor(best, m);
@@ -346,23 +350,24 @@ template <typename D> __global__ void __launch_bounds__(256) msim_route_rows(Rou
  * x log2 e by 1.5 2^-24 |x| and |x| s (1 - s) < 0.23); a softmax score by less
  * than 2^-24 (0.6 + 48 s) (a sum of 32 terms a lane, six exchanges); the sum
  * with the bias by 2^-24 |key| more. */
-template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
+template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256, VPL == 32 ? 5 : 6) msim_route_lists(RouteP p)
 {
     constexpr int PER16 = 16 / sizeof(typename D::raw);
     typedef typename D::raw vec __attribute__((ext_vector_type(PER16)));
     __shared__ int32_t hist[MSIM_MAX_EXPERTS];
     __shared__ float lds_bias[BIAS ? 64 * (VPL + 4) : 1];
+    __shared__ uint64_t lds_redo[4][REDO];
     extern __shared__ double keys[];       /* of route_row */
     const uint32_t lane = threadIdx.x & 63, l = lane & (p.lanes - 1), sub = l & (p.glanes - 1);
     const uint32_t g = l / p.glanes, size = p.E / p.G;
-    const uint32_t first = g * size + sub * p.part;           /* this lane's experts */
-    const uint32_t past = g < p.G ? min(first + p.part, (g + 1) * size) : first;
-    const uint32_t n = past > first ? past - first : 0;
+    const uint32_t first0 = g * size + sub * p.part;          /* this lane's experts */
+    const uint32_t past = g < p.G ? min(first0 + p.part, (g + 1) * size) : first0;
+    const uint32_t n0 = past > first0 ? past - first0 : 0;
     if (p.load)
         for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
     if (BIAS && threadIdx.x < p.lanes)
         for (uint32_t i = 0; i < VPL; i++) {
-            const float b = i < n ? p.bias[first + i] : -INFINITY;
+            const float b = i < n0 ? p.bias[first0 + i] : -INFINITY;
             lds_bias[l * (VPL + 4) + i] = b == b ? b : -INFINITY;
         }
     __syncthreads();
@@ -370,63 +375,64 @@ template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256)
     const uint64_t step = (uint64_t)gridDim.x * (blockDim.x / WAVE) * rpw;
     const uint64_t row0 = ((uint64_t)blockIdx.x * (blockDim.x / WAVE) + threadIdx.x / WAVE) * rpw;
     const bool sigmoid = p.sigmoid;
-    for (uint64_t rows = row0; rows < p.rows; rows += step) {
+    uint64_t *const redo = lds_redo[threadIdx.x / WAVE];
+    for (uint64_t base = row0; base < p.rows; base += REDO * step) {
+    uint32_t turns = 0;
+    bool some = false;
+    for (uint64_t rows = base; rows < p.rows && turns < REDO; rows += step, turns++) {
+        /* computed again each time: kept over the loop, what follows from them takes a register for every expert */
+        uint32_t first = first0, n = n0;
+        asm("" : "+v"(first), "+v"(n));
         const uint64_t row = min(rows + lane / p.lanes, p.rows - 1);
         const bool mine = rows + lane / p.lanes < p.rows;
         const typename D::raw *x = (const typename D::raw *)p.x + row * p.stride;
-        float v[VPL];
+        vec raw[VPL / PER16];
+        const typename D::raw none = D::put(-INFINITY);
         if (p.vec) {
             for (int c = 0; c < VPL / PER16; c++) {
-                vec t = {};
-                if (n) t = *(const vec *)(x + first + c * PER16);
-                for (int i = 0; i < PER16; i++) v[c * PER16 + i] = n ? D::get(t[i]) : -INFINITY;
+                raw[c] = none;
+                if (n) raw[c] = *(const vec *)(x + first + c * PER16);
             }
         } else {
-            for (int i = 0; i < VPL; i++) v[i] = (uint32_t)i < n ? D::get(x[first + i]) : -INFINITY;
+            for (int i = 0; i < VPL; i++) raw[i / PER16][i % PER16] = (uint32_t)i < n ? x[first + i] : none;
         }
+        auto v = [&](int i) { return D::get(raw[i / PER16][i % PER16]); };
         /* is anything not finite?  0 * x is NaN then */
         float odd = 0.0f;
-        for (int i = 0; i < VPL; i++) odd = __builtin_fmaf(v[i], 0.0f, odd);
+        for (int i = 0; i < VPL; i++) odd = __builtin_fmaf(v(i), 0.0f, odd);
         bool is_void = false;
         if (__any(odd != odd)) {
             bool bad = false;
-            for (int i = 0; i < VPL; i++) bad |= v[i] != v[i] || (!sigmoid && v[i] == INFINITY);
+            for (int i = 0; i < VPL; i++) bad |= v(i) != v(i) || (!sigmoid && v(i) == INFINITY);
             is_void = fold(bad ? 1.0f : 0.0f, p.lanes, Max()) > 0.0f;
         }
         float top = 0.0f, inv = 1.0f;
         if (!sigmoid && (BIAS || p.G > 1 || !p.renorm)) {
-            top = v[0];
-            for (int i = 1; i < VPL; i++) top = fmaxf(top, v[i]);
+            top = v(0);
+            for (int i = 1; i < VPL; i++) top = fmaxf(top, v(i));
             top = fold(top, p.lanes, Max());
             if (!(top > -INFINITY && top < INFINITY)) top = 0.0f;     /* nothing in, or void */
-        }
-        double a[8];
-        if (BIAS || (!sigmoid && !p.renorm)) {
-            float s[VPL];
-            if (!sigmoid) {
+            if (BIAS || !p.renorm) {
                 float sum = 0.0f;
-                for (int i = 0; i < VPL; i++) {
-                    s[i] = __builtin_amdgcn_exp2f((v[i] - top) * 1.44269504f);
-                    sum += s[i];
-                }
+                for (int i = 0; i < VPL; i++) sum += __builtin_amdgcn_exp2f((v(i) - top) * 1.44269504f);
                 inv = 1.0f / fold(sum, p.lanes, Sum());
             }
-            if (BIAS) {
-                for (int c = 0; c < VPL; c += 4) {
-                    const f32x4 b = *(const f32x4 *)&lds_bias[l * (VPL + 4) + c];
-                    for (int i = 0; i < 4; i++) {
-                        const float t = v[c + i];
-                        const float q = sigmoid
-                            ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t * -1.44269504f)) : s[c + i] * inv;
-                        v[c + i] = t > -INFINITY ? q + b[i] : -INFINITY;
-                    }
-                }
-            }
         }
+        double a[8];
         for (int c = 0; c < VPL; c += 8) {
             double b[8];
+            float k[8];
+            for (int i = 0; i < 8; i++) k[i] = v(c + i);
+            if (BIAS) {
+                const f32x4 *t = (const f32x4 *)&lds_bias[l * (VPL + 4) + c];
+                for (int i = 0; i < 8; i++) {
+                    const float q = sigmoid ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(k[i] * -1.44269504f))
+                                            : __builtin_amdgcn_exp2f((k[i] - top) * 1.44269504f) * inv;
+                    k[i] = k[i] > -INFINITY ? q + t[i / 4][i % 4] : -INFINITY;
+                }
+            }
             /* + 0: the two zeros are equal; a NaN (of a void row) is ordered as it falls */
-            for (int i = 0; i < 8; i++) (c ? b : a)[i] = pack(v[c + i] + 0.0f, first + c + i);
+            for (int i = 0; i < 8; i++) (c ? b : a)[i] = pack(k[i] + 0.0f, first + c + i);
             sort8(c ? b : a);
             if (c) keep8(a, b);
         }
@@ -497,13 +503,22 @@ template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256)
             if (p.load && got) atomicAdd(&hist[id], 1);
         }
         if (BIAS || p.gtop > 1) {
-            uint64_t todo = __ballot(mine && again && l == 0);
+            const uint64_t todo = __ballot(mine && again && l == 0);
+            some |= todo != 0;
+            if (lane == 0) redo[turns] = todo;
+        }
+    }
+    if (some) {
+        /* the rows that 32 bits do not decide, after the others: in their loop route_row's registers would be taken from it */
+        for (uint32_t k = 0; k < turns; k++) {
+            uint64_t todo = redo[k];
             while (todo) {
                 const int at = __builtin_ctzll(todo);
                 todo &= todo - 1;
-                route_row<D>(p, rows + at / p.lanes, keys + threadIdx.x / WAVE * p.E, hist);
+                route_row<D>(p, base + k * step + at / p.lanes, keys + threadIdx.x / WAVE * p.E, hist);
             }
         }
+    }
     }
     add_load(p, hist);
 }
