@@ -18,7 +18,8 @@ typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int WAVE = 64;
-constexpr uint32_t REDO = 32;          /* turns of a wavefront after which undecided rows are routed again */
+constexpr float LOG2E = 1.44269504f;
+constexpr int32_t UNDECIDED = INT32_MIN;   /* ids of a row that msim_route_lists leaves to the 64-bit path */
 
 /* ------------------------------------------------------------------------ */
 /* element types                                                             */
@@ -76,7 +77,8 @@ struct RouteP {
     uint64_t rows, stride;
     uint32_t E, K, G, TG, gtop, renorm, sigmoid;
     float scale;
-    uint32_t lanes, glanes, part, vec;     /* msim_route_lists: lanes a row and a group, experts a lane, 16-byte loads */
+    uint32_t size, lglanes, part, vec;     /* msim_route_lists: experts a group, log2 of its lanes, experts a lane,
+                                              16-byte loads */
 };
 
 /* Exchange with another lane of the same 16 (M = 1, 2: lane ^ M; 7, 15: the
@@ -100,15 +102,15 @@ template <int M> __device__ __forceinline__ double other(double v)
     return __builtin_bit_cast(double, (uint64_t)other<M>((uint32_t)(u >> 32)) << 32 | other<M>((uint32_t)u));
 }
 
-/* Folds v over blocks of n lanes (a power of two); every lane has the result. */
-template <typename T, typename F> __device__ __forceinline__ T fold(T v, uint32_t n, F f)
+/* Folds v over blocks of N lanes; every lane has the result. */
+template <int N, typename T, typename F> __device__ __forceinline__ T fold(T v, F f)
 {
-    if (n > 1) v = f(v, other<1>(v));
-    if (n > 2) v = f(v, other<2>(v));
-    if (n > 4) v = f(v, other<7>(v));
-    if (n > 8) v = f(v, other<15>(v));
-    if (n > 16) v = f(v, other<16>(v));
-    if (n > 32) v = f(v, other<32>(v));
+    v = f(v, other<1>(v));
+    v = f(v, other<2>(v));
+    v = f(v, other<7>(v));
+    if constexpr (N > 8) v = f(v, other<15>(v));
+    if constexpr (N > 16) v = f(v, other<16>(v));
+    if constexpr (N > 32) v = f(v, other<32>(v));
     return v;
 }
 struct Max { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
@@ -119,19 +121,9 @@ struct Sum { __device__ float operator()(float a, float b) const { return a + b;
  * word is the key as a float, which orders as the high word of a double does
  * (only a float's NaN would be one there), the low word the expert, so coded
  * that of equal keys the lower expert is the larger.  One instruction compares
- * both.  Written out, because fmax would quiet its operands first. */
-__device__ __forceinline__ double max64(double a, double b)
-{
-    double d;
-    asm("v_max_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
-    return d;
-}
-__device__ __forceinline__ double min64(double a, double b)
-{
-    double d;
-    asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
-    return d;
-}
+ * both. */
+__device__ __forceinline__ double max64(double a, double b) { return __builtin_fmax(a, b); }
+__device__ __forceinline__ double min64(double a, double b) { return __builtin_fmin(a, b); }
 struct Max64 { __device__ double operator()(double a, double b) const { return max64(a, b); } };
 
 __device__ __forceinline__ double pack(float key, uint32_t e)
@@ -186,24 +178,19 @@ template <typename T> __device__ __forceinline__ T wave_sum(T v)
 }
 
 /* The weight of the slot this lane has (got: it has one), logit xs, over the
- * row's n lanes.  s = e^min(x,0) / (1 + e^-|x|) for a sigmoid, e^(x - top) inv
+ * row's N lanes.  s = e^min(x,0) / (1 + e^-|x|) for a sigmoid, e^(x - top) inv
  * for a softmax; renormalised, the exponentials are taken relative to the
  * largest chosen one, so that no sum vanishes. */
-__device__ __forceinline__ float weight_of(const RouteP &p, float xs, bool got, uint32_t n, float top, float inv)
+template <int N> __device__ __forceinline__ float weight_of(const RouteP &p, float xs, bool got, float top, float inv)
 {
-    float q;
-    if (p.sigmoid) {
-        const float lo = fminf(xs, 0.0f);
-        const float c = p.renorm ? fold(got ? lo : -INFINITY, n, Max()) : 0.0f;
-        q = expf(lo - c) / (1.0f + expf(-fabsf(xs)));
-    } else if (p.renorm) {
-        q = expf(xs - fold(got ? xs : -INFINITY, n, Max()));
-    } else {
-        q = expf(xs - top) * inv;
-    }
+    const float t = p.sigmoid ? fminf(xs, 0.0f) : xs;
+    const float c = p.renorm ? fold<N>(got ? t : -INFINITY, Max()) : p.sigmoid ? 0.0f : top;
+    float q = expf(t - c);
+    if (p.sigmoid) q /= 1.0f + expf(-fabsf(xs));
+    else if (!p.renorm) q *= inv;
     if (!got) q = 0.0f;
     if (p.renorm) {
-        const float sum = fold(q, n, Sum());
+        const float sum = fold<N>(q, Sum());
         if (got) q /= sum;
     }
     return p.scale * q;
@@ -216,122 +203,163 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_wave_barrier();
 }
 
-/* One row by one wavefront, keys in 64 bits, held in key[] (LDS, experts
- * doubles of this wavefront's own).  Lane l works on experts l, l + 64, ...:
+/* One row by one wavefront, keys in 64 bits.  Lane l has experts l, l + 64, ...:
  * loads are consecutive, and each of top_k rounds finds the best key left by
- * exchanges of (key, index) between lanes. */
-template <typename D> __device__ void route_row(const RouteP &p, uint64_t row, double *key, int32_t *hist)
+ * exchanges between lanes.  lds: experts doubles of this wavefront's own, for
+ * the groups.  hist: counts of the chosen experts, or NULL. */
+template <typename D, int VPL> __device__ void route_row(const RouteP &p, uint64_t row, double *lds, int32_t *hist)
 {
     const uint32_t lane = threadIdx.x & 63;
     const typename D::raw *x = (const typename D::raw *)p.x + row * p.stride;
+    float v[VPL];
+    double key[VPL];
     bool bad = false;
     float top = -INFINITY;
-    _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE) {
-        const float v = D::get(x[e]);
-        bad |= v != v || (!p.sigmoid && v == INFINITY);
-        top = fmaxf(top, v);
+    for (int i = 0; i < VPL; i++) v[i] = i * WAVE + lane < p.E ? D::get(x[i * WAVE + lane]) : -INFINITY;
+    for (int i = 0; i < VPL; i++) {
+        bad |= v[i] != v[i] || (!p.sigmoid && v[i] == INFINITY);
+        top = fmaxf(top, v[i]);
     }
     const bool is_void = __any(bad);
-    top = fold(top, WAVE, Max());
+    top = fold<WAVE>(top, Max());
     int32_t my_id = -1;
     double inv = 1.0;
     if (!is_void && top > -INFINITY) {
         const bool scored = p.bias || p.gtop > 1;
         if (scored || (!p.sigmoid && !p.renorm)) {
             double sum = 0;
-            _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE) {
-                const double v = D::get(x[e]);
-                const double t = exp(p.sigmoid ? -fabs(v) : v - top);
-                sum += t;
-                key[e] = t;
+            for (int i = 0; i < VPL; i++) {
+                key[i] = exp(p.sigmoid ? -fabs((double)v[i]) : (double)v[i] - top);
+                sum += key[i];
             }
-            for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
-            inv = p.sigmoid ? 1.0 : 1.0 / sum;
+            if (!p.sigmoid) {
+                for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
+                inv = 1.0 / sum;
+            }
         }
-        _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE) {
-            const float v = D::get(x[e]);
-            double k = v;
-            if (scored && v > -INFINITY) {
-                const double t = key[e];
-                k = p.sigmoid ? (v >= 0 ? 1.0 : t) / (1.0 + t) : t * inv;
-                if (p.bias) k = p.bias[e] > -INFINITY ? k + p.bias[e] : -INFINITY;
+        for (int i = 0; i < VPL; i++) {
+            const uint32_t e = i * WAVE + lane;
+            double k = v[i];
+            if (scored) {
+                const float b = p.bias && e < p.E ? p.bias[e] : 0.0f;
+                k = p.sigmoid ? (v[i] >= 0 ? 1.0 : key[i]) / (1.0 + key[i]) : key[i] * inv;
+                k = v[i] > -INFINITY && b > -INFINITY ? k + b : -INFINITY;
             }
-            key[e] = k;
+            key[i] = k;
         }
         if (p.G > 1) {
             /* lane g walks group g: its one or two best members, other lanes' keys among them */
-            wave_sync();
             const uint32_t size = p.E / p.G;
+            for (int i = 0; i < VPL; i++)
+                if (i * WAVE + lane < p.E) lds[i * WAVE + lane] = key[i];
+            wave_sync();
             double worth = -INFINITY;
             if (lane < p.G) {
                 double a = -INFINITY, c = -INFINITY;
-                _Pragma("unroll 1") for (uint32_t e = lane * size; e < (lane + 1) * size; e++) {
-                    const double k = key[e];
-                    if (k > a) { c = a; a = k; }
-                    else if (k > c) c = k;
+                _Pragma("unroll 4") for (uint32_t e = lane * size; e < (lane + 1) * size; e++) {
+                    const double k = lds[e];
+                    c = fmax(c, fmin(a, k));
+                    a = fmax(a, k);
                 }
                 worth = p.gtop > 1 && c > -INFINITY ? a + c : a;
             }
             wave_sync();
             uint32_t before = 0;           /* groups better than this lane's */
-            _Pragma("unroll 1") for (uint32_t g = 0; g < p.G; g++) {
+            for (uint32_t g = 0; g < p.G; g++) {
                 const double w = __shfl(worth, (int)g);
                 before += w > worth || (w == worth && g < lane);
             }
             const uint64_t stay = __ballot(lane < p.G && before < p.TG);
-            _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE) {
-                if (!((stay >> (e / size)) & 1)) key[e] = -INFINITY;
-                else if (!p.bias) key[e] = D::get(x[e]);
+            for (int i = 0; i < VPL; i++) {
+                const uint32_t e = i * WAVE + lane;
+                const double k = p.bias ? key[i] : (double)v[i];
+                key[i] = e < p.E && (stay >> (e / size) & 1) ? k : -INFINITY;
             }
         }
         _Pragma("unroll 1") for (uint32_t r = 0; r < p.K; r++) {
             double best = -INFINITY;
-            int at = -1;
-            _Pragma("unroll 1") for (uint32_t e = lane; e < p.E; e += WAVE)
-                if (key[e] > best) { best = key[e]; at = e; }
-            for (int m = 32; m; m >>= 1) {
-                const double ob = __shfl_xor(best, m);
-                const int oa = __shfl_xor(at, m);
-                if (oa >= 0 && (at < 0 || ob > best || (ob == best && oa < at))) { best = ob; at = oa; }
+            int at = INT32_MAX;
+            for (int i = 0; i < VPL; i++)
+                if (key[i] > best) { best = key[i]; at = i * WAVE + lane; }
+            const double m = fold<WAVE>(best, Max64());
+            if (m == -INFINITY) break;
+            /* of equal keys the lowest index: hardly ever more than one lane has the best */
+            uint64_t has = __ballot(best == m);
+            int win = INT32_MAX;
+            while (has) {
+                win = min(win, __builtin_amdgcn_readlane(at, __builtin_ctzll(has)));
+                has &= has - 1;
             }
-            if (at < 0) break;
-            if ((at & 63) == (int)lane) key[at] = -INFINITY;
-            if (lane == r) my_id = at;
+            for (int i = 0; i < VPL; i++)
+                if (i * WAVE + (int)lane == win) key[i] = -INFINITY;
+            if (lane == r) my_id = win;
         }
     }
     /* weights: lane j has slot j */
     const float xs = my_id >= 0 ? D::get(x[my_id]) : -INFINITY;
-    const float q = weight_of(p, xs, my_id >= 0, WAVE, top, (float)inv);
+    const float q = weight_of<WAVE>(p, xs, my_id >= 0, top, (float)inv);
     if (lane < p.K) {
         p.ids[row * p.K + lane] = my_id;
         p.w[row * p.K + lane] = is_void ? NAN : q;
-        if (p.load && my_id >= 0) atomicAdd(&hist[my_id], 1);
+        if (hist && my_id >= 0) atomicAdd(&hist[my_id], 1);
     }
 }
 
-/* the workgroup's counts join the others' */
-__device__ __forceinline__ void add_load(const RouteP &p, const int32_t *hist)
+/* the kernel that chooses clears the counts for the one that counts */
+__device__ __forceinline__ void clear_load(const RouteP &p)
 {
-    if (!p.load) return;
-    __syncthreads();
-    for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
-        if (gridDim.x == 1) p.load[e] = hist[e];
-        else if (hist[e]) atomicAdd(&p.load[e], hist[e]);
-    }
+    if (p.load && blockIdx.x == 0)
+        for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) p.load[e] = 0;
 }
 
-/* any top_k, experts and groups: a wavefront a row */
-template <typename D> __global__ void __launch_bounds__(256) msim_route_rows(RouteP p)
+/* A wavefront a row: any top_k, experts and groups. */
+template <typename D, int VPL> __global__ void __launch_bounds__(256) msim_route_rows(RouteP p)
 {
-    __shared__ int32_t hist[MSIM_MAX_EXPERTS];
     extern __shared__ double keys[];
-    if (p.load)
-        for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
-    __syncthreads();
+    clear_load(p);
     const uint64_t step = (uint64_t)gridDim.x * (blockDim.x / WAVE);
     for (uint64_t row = (uint64_t)blockIdx.x * (blockDim.x / WAVE) + threadIdx.x / WAVE; row < p.rows; row += step)
-        route_row<D>(p, row, keys + threadIdx.x / WAVE * p.E, hist);
-    add_load(p, hist);
+        route_row<D, VPL>(p, row, keys + threadIdx.x / WAVE * p.E, nullptr);
+}
+
+/* The end of a routing: counts the ids, and routes the rows that
+ * msim_route_lists left undecided.  That path is not in the other kernel, whose
+ * rows it cost more, by its registers and by a wavefront that finishes late,
+ * than this launch; and counted here few workgroups add to the same few
+ * addresses, at about 13 ns each (1,024 workgroups that each added their own
+ * counts took 13 us longer).  Every workgroup has `part` rows. */
+template <typename D, int VPL> __global__ void __launch_bounds__(512) msim_route_finish(RouteP p, uint64_t part, uint32_t undecided)
+{
+    extern __shared__ double keys[];
+    __shared__ int32_t hist[MSIM_MAX_EXPERTS];
+    __shared__ uint32_t some;
+    const uint64_t lo = blockIdx.x * part, hi = min(lo + part, p.rows);
+    for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
+    if (threadIdx.x == 0) some = 0;
+    __syncthreads();
+    bool mine = false;
+    for (uint64_t i = lo * p.K + threadIdx.x; i < hi * p.K; i += blockDim.x) {
+        const int32_t id = p.ids[i];
+        mine |= id == UNDECIDED;
+        if (p.load && id >= 0) atomicAdd(&hist[id], 1);
+    }
+    if (mine) some = 1;
+    __syncthreads();
+    if (undecided && some) {
+        const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x / WAVE;
+        for (uint64_t rows = lo + wave * WAVE; rows < hi; rows += blockDim.x) {
+            uint64_t todo = __ballot(rows + lane < hi && p.ids[(rows + lane) * p.K] == UNDECIDED);
+            while (todo) {
+                const int at = __builtin_ctzll(todo);
+                todo &= todo - 1;
+                route_row<D, VPL>(p, rows + at, keys + wave * p.E, p.load ? hist : nullptr);
+            }
+        }
+        __syncthreads();
+    }
+    if (p.load)
+        for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x)
+            if (hist[e]) atomicAdd(&p.load[e], hist[e]);
 }
 
 /* Eight or fewer choices a row, several rows a wavefront.
@@ -345,46 +373,46 @@ template <typename D> __global__ void __launch_bounds__(256) msim_route_rows(Rou
  * Without bias keys are the logits and the choice is exact.  With bias (and for
  * sums of two scores) the keys here are 32-bit approximations with a known
  * error, and a row whose choice depends on a difference within twice that error
- * is routed again in 64 bits by route_row.  Errors: a sigmoid is off by less
+ * is left to msim_route_finish, which compares in 64 bits.  Errors: a sigmoid is off by less
  * than 2^-22 (v_exp_f32 and v_rcp_f32 are off by 2^-23 relative, the argument
  * x log2 e by 1.5 2^-24 |x| and |x| s (1 - s) < 0.23); a softmax score by less
  * than 2^-24 (0.6 + 48 s) (a sum of 32 terms a lane, six exchanges); the sum
  * with the bias by 2^-24 |key| more. */
-template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256, VPL == 32 ? 5 : 6) msim_route_lists(RouteP p)
+template <typename D, int VPL, int LANES, bool BIAS>
+__global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
 {
     constexpr int PER16 = 16 / sizeof(typename D::raw);
     typedef typename D::raw vec __attribute__((ext_vector_type(PER16)));
     __shared__ int32_t hist[MSIM_MAX_EXPERTS];
-    __shared__ float lds_bias[BIAS ? 64 * (VPL + 4) : 1];
-    __shared__ uint64_t lds_redo[4][REDO];
-    extern __shared__ double keys[];       /* of route_row */
-    const uint32_t lane = threadIdx.x & 63, l = lane & (p.lanes - 1), sub = l & (p.glanes - 1);
-    const uint32_t g = l / p.glanes, size = p.E / p.G;
+    __shared__ float lds_bias[BIAS ? LANES * (VPL + 4) : 1];
+    constexpr uint32_t ROWS = WAVE / LANES;                   /* rows a wavefront */
+    const uint32_t glanes = 1u << p.lglanes;
+    const uint32_t lane = threadIdx.x & 63, l = lane % LANES, sub = l & (glanes - 1);
+    const uint32_t g = l >> p.lglanes, size = p.size;
     const uint32_t first0 = g * size + sub * p.part;          /* this lane's experts */
     const uint32_t past = g < p.G ? min(first0 + p.part, (g + 1) * size) : first0;
     const uint32_t n0 = past > first0 ? past - first0 : 0;
-    if (p.load)
+    /* one workgroup that leaves no row undecided counts by itself */
+    const bool count = p.load && gridDim.x == 1 && !(BIAS || p.gtop > 1);
+    if (count)
         for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
-    if (BIAS && threadIdx.x < p.lanes)
+    else
+        clear_load(p);
+    if (BIAS && threadIdx.x < LANES)
         for (uint32_t i = 0; i < VPL; i++) {
             const float b = i < n0 ? p.bias[first0 + i] : -INFINITY;
             lds_bias[l * (VPL + 4) + i] = b == b ? b : -INFINITY;
         }
     __syncthreads();
-    const uint32_t rpw = WAVE / p.lanes;                      /* rows a wavefront */
-    const uint64_t step = (uint64_t)gridDim.x * (blockDim.x / WAVE) * rpw;
-    const uint64_t row0 = ((uint64_t)blockIdx.x * (blockDim.x / WAVE) + threadIdx.x / WAVE) * rpw;
+    const uint64_t step = (uint64_t)gridDim.x * (blockDim.x / WAVE) * ROWS;
+    const uint64_t row0 = ((uint64_t)blockIdx.x * (blockDim.x / WAVE) + threadIdx.x / WAVE) * ROWS;
     const bool sigmoid = p.sigmoid;
-    uint64_t *const redo = lds_redo[threadIdx.x / WAVE];
-    for (uint64_t base = row0; base < p.rows; base += REDO * step) {
-    uint32_t turns = 0;
-    bool some = false;
-    for (uint64_t rows = base; rows < p.rows && turns < REDO; rows += step, turns++) {
+    _Pragma("unroll 1") for (uint64_t rows = row0; rows < p.rows; rows += step) {
         /* computed again each time: kept over the loop, what follows from them takes a register for every expert */
         uint32_t first = first0, n = n0;
         asm("" : "+v"(first), "+v"(n));
-        const uint64_t row = min(rows + lane / p.lanes, p.rows - 1);
-        const bool mine = rows + lane / p.lanes < p.rows;
+        const uint64_t row = min(rows + lane / LANES, p.rows - 1);
+        const bool mine = rows + lane / LANES < p.rows;
         const typename D::raw *x = (const typename D::raw *)p.x + row * p.stride;
         vec raw[VPL / PER16];
         const typename D::raw none = D::put(-INFINITY);
@@ -400,22 +428,23 @@ template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256,
         /* is anything not finite?  0 * x is NaN then */
         float odd = 0.0f;
         for (int i = 0; i < VPL; i++) odd = __builtin_fmaf(v(i), 0.0f, odd);
+        const bool any_odd = __any(odd != odd);
         bool is_void = false;
-        if (__any(odd != odd)) {
+        if (any_odd) {
             bool bad = false;
             for (int i = 0; i < VPL; i++) bad |= v(i) != v(i) || (!sigmoid && v(i) == INFINITY);
-            is_void = fold(bad ? 1.0f : 0.0f, p.lanes, Max()) > 0.0f;
+            is_void = fold<LANES>(bad ? 1.0f : 0.0f, Max()) > 0.0f;
         }
         float top = 0.0f, inv = 1.0f;
         if (!sigmoid && (BIAS || p.G > 1 || !p.renorm)) {
             top = v(0);
             for (int i = 1; i < VPL; i++) top = fmaxf(top, v(i));
-            top = fold(top, p.lanes, Max());
+            top = fold<LANES>(top, Max());
             if (!(top > -INFINITY && top < INFINITY)) top = 0.0f;     /* nothing in, or void */
             if (BIAS || !p.renorm) {
                 float sum = 0.0f;
-                for (int i = 0; i < VPL; i++) sum += __builtin_amdgcn_exp2f((v(i) - top) * 1.44269504f);
-                inv = 1.0f / fold(sum, p.lanes, Sum());
+                for (int i = 0; i < VPL; i++) sum += __builtin_amdgcn_exp2f((v(i) - top) * LOG2E);
+                inv = 1.0f / fold<LANES>(sum, Sum());
             }
         }
         double a[8];
@@ -425,11 +454,13 @@ template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256,
             for (int i = 0; i < 8; i++) k[i] = v(c + i);
             if (BIAS) {
                 const f32x4 *t = (const f32x4 *)&lds_bias[l * (VPL + 4) + c];
-                for (int i = 0; i < 8; i++) {
-                    const float q = sigmoid ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(k[i] * -1.44269504f))
-                                            : __builtin_amdgcn_exp2f((k[i] - top) * 1.44269504f) * inv;
-                    k[i] = k[i] > -INFINITY ? q + t[i / 4][i % 4] : -INFINITY;
-                }
+                if (sigmoid)
+                    for (int i = 0; i < 8; i++) k[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(k[i] * -LOG2E));
+                else
+                    for (int i = 0; i < 8; i++) k[i] = __builtin_amdgcn_exp2f((k[i] - top) * LOG2E) * inv;
+                for (int i = 0; i < 8; i++) k[i] += t[i / 4][i % 4];
+                if (any_odd)
+                    for (int i = 0; i < 8; i++) k[i] = v(c + i) > -INFINITY ? k[i] : -INFINITY;
             }
             /* + 0: the two zeros are equal; a NaN (of a void row) is ordered as it falls */
             for (int i = 0; i < 8; i++) (c ? b : a)[i] = pack(k[i] + 0.0f, first + c + i);
@@ -440,38 +471,38 @@ template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256,
         bool near = false;
         if (p.G > 1) {
             float t1 = key_of(a[0]), t2 = key_of(a[1]);
-            for (uint32_t m = 1; m < p.glanes; m <<= 1) {
+            _Pragma("unroll 1") for (uint32_t m = 1; m < glanes; m <<= 1) {
                 const float o1 = __shfl_xor(t1, (int)m), o2 = __shfl_xor(t2, (int)m);
                 t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
                 t1 = fmaxf(t1, o1);
             }
             if (!BIAS && p.gtop > 1) {
                 if (sigmoid) {
-                    t1 = t1 > -INFINITY ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t1 * -1.44269504f)) : t1;
-                    t2 = t2 > -INFINITY ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t2 * -1.44269504f)) : t2;
+                    t1 = t1 > -INFINITY ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t1 * -LOG2E)) : t1;
+                    t2 = t2 > -INFINITY ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t2 * -LOG2E)) : t2;
                 } else {
-                    t1 = t1 > -INFINITY ? __builtin_amdgcn_exp2f((t1 - top) * 1.44269504f) : t1;
-                    t2 = t2 > -INFINITY ? __builtin_amdgcn_exp2f((t2 - top) * 1.44269504f) : t2;
+                    t1 = t1 > -INFINITY ? __builtin_amdgcn_exp2f((t1 - top) * LOG2E) : t1;
+                    t2 = t2 > -INFINITY ? __builtin_amdgcn_exp2f((t2 - top) * LOG2E) : t2;
                 }
             }
             const float worth = p.gtop > 1 && t2 > -INFINITY ? t1 + t2 : t1;
             uint32_t before = 0;
-            for (uint32_t o = p.glanes; o < p.lanes; o += p.glanes) {
+            _Pragma("unroll 1") for (uint32_t o = glanes; o < LANES; o += glanes) {
                 const float w = __shfl_xor(worth, (int)o);
                 before += w > worth || (w == worth && (l ^ o) < l);
             }
             const bool stay = before < p.TG;
             if (BIAS || p.gtop > 1) {
-                const float in = fold(stay ? worth : INFINITY, p.lanes, Min());
-                const float out = fold(stay ? -INFINITY : worth, p.lanes, Max());
+                const float in = fold<LANES>(stay ? worth : INFINITY, Min());
+                const float out = fold<LANES>(stay ? -INFINITY : worth, Max());
                 near = out > -INFINITY && !(in - out > 2.0f * slack + 0x1p-20f * fabsf(in));
             }
             if (!stay)
                 for (int i = 0; i < 8; i++) a[i] = pack(-INFINITY, 0);
         }
         double slot = pack(-INFINITY, 0), last = slot;
-        for (uint32_t r = 0; r <= (BIAS ? p.K : p.K - 1); r++) {
-            const double m = fold(a[0], p.lanes, Max64());
+        _Pragma("unroll 1") for (uint32_t r = 0; r <= (BIAS ? p.K : p.K - 1); r++) {
+            const double m = fold<LANES>(a[0], Max64());
             if (l == r) slot = m;
             if (BIAS) last = m;
             const bool won = __builtin_bit_cast(uint64_t, m) == __builtin_bit_cast(uint64_t, a[0]);
@@ -495,39 +526,21 @@ template <typename D, int VPL, bool BIAS> __global__ void __launch_bounds__(256,
             near |= close;
         }
         bool again = false;
-        if (BIAS || p.gtop > 1) again = fold(near ? 1.0f : 0.0f, p.lanes, Max()) > 0.0f && !is_void;
-        const float q = weight_of(p, xs, got, p.lanes, top, inv);
-        if (mine && !again && l < p.K) {
-            p.ids[row * p.K + l] = id;
+        if (BIAS || p.gtop > 1) again = fold<LANES>(near ? 1.0f : 0.0f, Max()) > 0.0f && !is_void;
+        const float q = weight_of<LANES>(p, xs, got, top, inv);
+        if (mine && l < p.K) {
+            p.ids[row * p.K + l] = again ? UNDECIDED : id;
             p.w[row * p.K + l] = is_void ? NAN : q;
-            if (p.load && got) atomicAdd(&hist[id], 1);
-        }
-        if (BIAS || p.gtop > 1) {
-            const uint64_t todo = __ballot(mine && again && l == 0);
-            some |= todo != 0;
-            if (lane == 0) redo[turns] = todo;
+            if (count && got) atomicAdd(&hist[id], 1);
         }
     }
-    if (some) {
-        /* the rows that 32 bits do not decide, after the others: in their loop route_row's registers would be taken from it */
-        for (uint32_t k = 0; k < turns; k++) {
-            uint64_t todo = redo[k];
-            while (todo) {
-                const int at = __builtin_ctzll(todo);
-                todo &= todo - 1;
-                route_row<D>(p, base + k * step + at / p.lanes, keys + threadIdx.x / WAVE * p.E, hist);
-            }
-        }
+    if (count) {
+        __syncthreads();
+        for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) p.load[e] = hist[e];
     }
-    }
-    add_load(p, hist);
 }
 
-__global__ void msim_fill_words(int32_t *out, uint32_t n)
-{
-    const uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < n) out[i] = 0;
-}
+__global__ void msim_route_nothing(RouteP p) { clear_load(p); }
 
 /* ------------------------------------------------------------------------ */
 /* the router's gradient                                                     */
@@ -723,40 +736,60 @@ uint32_t pow2(uint32_t v)
     return p;
 }
 
-template <typename D, int VPL> void launch_lists(const RouteP &p, hipStream_t st)
+template <typename D> void launch_finish(const RouteP &p, bool undecided, hipStream_t st)
 {
-    const uint32_t rows = 4 * WAVE / p.lanes;
+    if (!undecided && !p.load) return;
+    /* 64 rows a wavefront, while the workgroups are few enough to add to the same counts */
+    const uint64_t part = std::max<uint64_t>(512, (p.rows + 127) / 128);
+    const uint32_t grid = (uint32_t)((p.rows + part - 1) / part);
+    const uint32_t block = p.E <= 256 ? 512 : 256;            /* LDS: at most 32 KiB of keys */
+    const size_t lds = undecided && p.G > 1 ? block / WAVE * p.E * sizeof(double) : 0;
+    if (p.E <= 256) msim_route_finish<D, 4><<<grid, block, lds, st>>>(p, part, undecided);
+    else msim_route_finish<D, 16><<<grid, block, lds, st>>>(p, part, undecided);
+}
+
+template <typename D, int VPL, int LANES> void launch_lists(const RouteP &p, hipStream_t st)
+{
+    const uint32_t rows = 4 * WAVE / LANES;
     const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + rows - 1) / rows, 1024);
-    if (p.load && grid != 1) msim_fill_words<<<(p.E + 255) / 256, 256, 0, st>>>(p.load, p.E);
-    if (!grid) return;
-    const size_t keys = p.bias || p.gtop > 1 ? 4 * p.E * sizeof(double) : 0;
-    if (p.bias) msim_route_lists<D, VPL, true><<<grid, 256, keys, st>>>(p);
-    else msim_route_lists<D, VPL, false><<<grid, 256, keys, st>>>(p);
+    const bool undecided = p.bias || p.gtop > 1;
+    if (p.bias) msim_route_lists<D, VPL, LANES, true><<<grid, 256, 0, st>>>(p);
+    else msim_route_lists<D, VPL, LANES, false><<<grid, 256, 0, st>>>(p);
+    if (grid > 1 || undecided) launch_finish<D>(p, undecided, st);
 }
 
 template <typename D> void launch_route(RouteP p, hipStream_t st)
 {
+    if (p.rows == 0) {
+        if (p.load) msim_route_nothing<<<1, 256, 0, st>>>(p);
+        return;
+    }
     /* lists of eight: lanes for every group, at most 32 experts a lane */
     const uint32_t size = p.E / p.G, g2 = pow2(p.G);
     uint32_t glanes = std::max(1u, 8 / g2);
     while ((size + glanes - 1) / glanes > 32) glanes *= 2;
-    if (p.K <= 8 && g2 * glanes <= WAVE) {
+    const uint32_t lanes = g2 * glanes;
+    if (p.K <= 8 && lanes <= 32) {
         const size_t sz = sizeof(typename D::raw);
-        p.glanes = glanes;
-        p.lanes = g2 * glanes;
+        p.size = size;
+        p.lglanes = __builtin_ctz(glanes);
         p.part = (size + glanes - 1) / glanes;
-        const uint32_t vpl = std::max(8u, pow2(p.part));
+        const uint32_t vpl = std::max(lanes == 8 ? 8u : lanes == 16 ? 16u : 32u, pow2(p.part));
         p.vec = p.part == vpl && p.part * glanes == size && (size * sz) % 16 == 0 && (p.stride * sz) % 16 == 0 &&
                 (uintptr_t)p.x % 16 == 0;
-        if (vpl == 8) launch_lists<D, 8>(p, st);
-        else if (vpl == 16) launch_lists<D, 16>(p, st);
-        else launch_lists<D, 32>(p, st);
+        if (lanes == 32) launch_lists<D, 32, 32>(p, st);
+        else if (lanes == 16 && vpl == 32) launch_lists<D, 32, 16>(p, st);
+        else if (lanes == 16) launch_lists<D, 16, 16>(p, st);
+        else if (vpl == 32) launch_lists<D, 32, 8>(p, st);
+        else if (vpl == 16) launch_lists<D, 16, 8>(p, st);
+        else launch_lists<D, 8, 8>(p, st);
         return;
     }
     const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + 3) / 4, 2048);
-    if (p.load && grid != 1) msim_fill_words<<<(p.E + 255) / 256, 256, 0, st>>>(p.load, p.E);
-    if (!grid) return;
-    msim_route_rows<D><<<grid, 256, 4 * p.E * sizeof(double), st>>>(p);
+    const size_t lds = p.G > 1 ? 4 * p.E * sizeof(double) : 0;
+    if (p.E <= 256) msim_route_rows<D, 4><<<grid, 256, lds, st>>>(p);
+    else msim_route_rows<D, 16><<<grid, 256, lds, st>>>(p);
+    launch_finish<D>(p, false, st);
 }
 
 } // namespace
