@@ -131,6 +131,11 @@ __device__ __forceinline__ double pack(float key, uint32_t e)
     const int32_t hi = __builtin_bit_cast(int32_t, key);
     return __builtin_bit_cast(double, (uint64_t)(uint32_t)hi << 32 | ((uint32_t)(hi >> 31) ^ ~e));
 }
+/* where the order of equal keys is looked at again: the code of positive keys for all */
+__device__ __forceinline__ double pack_approx(float key, uint32_t e)
+{
+    return __builtin_bit_cast(double, (uint64_t)__builtin_bit_cast(uint32_t, key) << 32 | (uint32_t)~e);
+}
 __device__ __forceinline__ float key_of(double v)
 {
     return __builtin_bit_cast(float, (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 32));
@@ -338,10 +343,13 @@ template <typename D, int VPL> __global__ void __launch_bounds__(512) msim_route
     if (threadIdx.x == 0) some = 0;
     __syncthreads();
     bool mine = false;
-    for (uint64_t i = lo * p.K + threadIdx.x; i < hi * p.K; i += blockDim.x) {
-        const int32_t id = p.ids[i];
-        mine |= id == UNDECIDED;
-        if (p.load && id >= 0) atomicAdd(&hist[id], 1);
+    for (uint64_t i = lo * p.K + threadIdx.x; i < hi * p.K; i += 8 * blockDim.x) {
+        int32_t id[8];                     /* eight loads on their way at once */
+        for (int j = 0; j < 8; j++) id[j] = i + j * blockDim.x < hi * p.K ? p.ids[i + j * blockDim.x] : -1;
+        for (int j = 0; j < 8; j++) {
+            mine |= id[j] == UNDECIDED;
+            if (p.load && id[j] >= 0) atomicAdd(&hist[id[j]], 1);
+        }
     }
     if (mine) some = 1;
     __syncthreads();
@@ -462,8 +470,10 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
                 if (any_odd)
                     for (int i = 0; i < 8; i++) k[i] = v(c + i) > -INFINITY ? k[i] : -INFINITY;
             }
-            /* + 0: the two zeros are equal; a NaN (of a void row) is ordered as it falls */
-            for (int i = 0; i < 8; i++) (c ? b : a)[i] = pack(k[i] + 0.0f, first + c + i);
+            /* + 0: the two zeros are equal (a sum of a score and a bias is never -0); a NaN (of a void row) is
+             * ordered as it falls */
+            for (int i = 0; i < 8; i++)
+                (c ? b : a)[i] = BIAS ? pack_approx(k[i], first + c + i) : pack(k[i] + 0.0f, first + c + i);
             sort8(c ? b : a);
             if (c) keep8(a, b);
         }
@@ -501,7 +511,9 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
                 for (int i = 0; i < 8; i++) a[i] = pack(-INFINITY, 0);
         }
         double slot = pack(-INFINITY, 0), last = slot;
-        _Pragma("unroll 1") for (uint32_t r = 0; r <= (BIAS ? p.K : p.K - 1); r++) {
+        /* with bias one round more, for the difference to the first that is not chosen.  A loop: written out for
+         * each round, with lists that get shorter, it is a quarter slower (131,072 x 256 bf16) */
+        _Pragma("unroll 1") for (uint32_t r = 0; r < p.K + BIAS; r++) {
             const double m = fold<LANES>(a[0], Max64());
             if (l == r) slot = m;
             if (BIAS) last = m;
@@ -510,7 +522,7 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
             a[7] = won ? pack(-INFINITY, 0) : a[7];
         }
         const bool got = l < p.K && key_of(slot) > -INFINITY && !is_void;
-        const int32_t id = got ? (int32_t)expert_of(slot) : -1;
+        const int32_t id = got ? (int32_t)(BIAS ? ~(uint32_t)__builtin_bit_cast(uint64_t, slot) : expert_of(slot)) : -1;
         const float xs = got ? (BIAS ? D::get(x[id]) : key_of(slot)) : -INFINITY;
         if (BIAS) {
             const float k0 = key_of(slot);
@@ -518,10 +530,10 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
             if (l == p.K - 1) k1 = key_of(last);
             bool close = got && !(k0 - k1 > slack + 0x1p-22f * fabsf(k0));
             if (__any(close)) {
-                /* the same logit and the same bias: the same key, in order already */
+                /* the same logit and the same bias: the same key, in order already (of positive keys) */
                 const float b = got ? p.bias[id] : 0.0f;
                 const float xn = __shfl_down(xs, 1), bn = __shfl_down(b, 1);
-                if (l < p.K - 1 && xs == xn && b == bn) close = false;
+                if (l < p.K - 1 && xs == xn && b == bn && k0 >= 0.0f) close = false;
             }
             near |= close;
         }
@@ -622,6 +634,7 @@ struct DropP {
     uint32_t per_row;
 };
 
+/* any layout: an element a thread */
 template <typename D> __global__ void __launch_bounds__(256) msim_dropout_any(DropP p)
 {
     const uint64_t n = p.rows * p.cols, step = (uint64_t)gridDim.x * blockDim.x;
@@ -630,6 +643,51 @@ template <typename D> __global__ void __launch_bounds__(256) msim_dropout_any(Dr
         const float v = D::get(((const typename D::raw *)p.x)[r * p.xs + c]);
         const bool keep = draw32(p.base, p.per_row ? r : i) >= p.limit;
         ((typename D::raw *)p.y)[r * p.ys + c] = D::put(keep ? v * p.scale : 0.0f);
+    }
+}
+
+/* Elements that lie next to each other, PER of them (16 bytes) a thread and
+ * turn: bound by the memory, and nearly by the generator, a 64-bit mix for two
+ * elements, so a mix is used whole and its counter moves by an addition. */
+template <typename D> __global__ void __launch_bounds__(256) msim_dropout_flat(DropP p)
+{
+    constexpr int PER = 16 / sizeof(typename D::raw);
+    typedef typename D::raw vec __attribute__((ext_vector_type(PER)));
+    const uint64_t n = p.rows * p.cols, step = (uint64_t)gridDim.x * blockDim.x * PER;
+    const uint32_t limit = (uint32_t)p.limit;          /* p < 1 here */
+    for (uint64_t i = ((uint64_t)blockIdx.x * blockDim.x + threadIdx.x) * PER; i < n; i += step) {
+        const typename D::raw *x = (const typename D::raw *)p.x + i;
+        typename D::raw *y = (typename D::raw *)p.y + i;
+        uint64_t z = p.base + (i >> 1) * GAMMA;
+        bool keep[PER];
+        for (int j = 0; j < PER; j += 2, z += GAMMA) {
+            const uint64_t d = mix64(z);
+            keep[j] = (uint32_t)d >= limit;
+            keep[j + 1] = (uint32_t)(d >> 32) >= limit;
+        }
+        if (i + PER <= n) {
+            vec v = *(const vec *)x;
+            for (int j = 0; j < PER; j++) v[j] = D::put(keep[j] ? D::get(v[j]) * p.scale : 0.0f);
+            *(vec *)y = v;
+        } else {
+            for (int j = 0; j < PER; j++)
+                if (i + j < n) y[j] = D::put(keep[j] ? D::get(x[j]) * p.scale : 0.0f);
+        }
+    }
+}
+
+/* Rows that stay or go whole: one draw a row, a workgroup's 256 threads on it
+ * or, of short rows, on several at once. */
+template <typename D> __global__ void __launch_bounds__(256) msim_dropout_rows(DropP p, uint32_t lwide)
+{
+    const uint32_t wide = 1u << lwide;                 /* threads a row */
+    const uint64_t step = (uint64_t)gridDim.x * (blockDim.x >> lwide);
+    for (uint64_t r = (uint64_t)blockIdx.x * (blockDim.x >> lwide) + (threadIdx.x >> lwide); r < p.rows; r += step) {
+        const bool keep = draw32(p.base, r) >= p.limit;
+        const typename D::raw *x = (const typename D::raw *)p.x + r * p.xs;
+        typename D::raw *y = (typename D::raw *)p.y + r * p.ys;
+        for (uint64_t c = threadIdx.x & (wide - 1); c < p.cols; c += wide)
+            y[c] = keep ? D::put(D::get(x[c]) * p.scale) : D::put(0.0f);
     }
 }
 
@@ -739,8 +797,8 @@ uint32_t pow2(uint32_t v)
 template <typename D> void launch_finish(const RouteP &p, bool undecided, hipStream_t st)
 {
     if (!undecided && !p.load) return;
-    /* 64 rows a wavefront, while the workgroups are few enough to add to the same counts */
-    const uint64_t part = std::max<uint64_t>(512, (p.rows + 127) / 128);
+    /* at most 256 workgroups, which is few enough to add to the same counts */
+    const uint64_t part = std::max<uint64_t>(256, (p.rows + 255) / 256);
     const uint32_t grid = (uint32_t)((p.rows + part - 1) / part);
     const uint32_t block = p.E <= 256 ? 512 : 256;            /* LDS: at most 32 KiB of keys */
     const size_t lds = undecided && p.G > 1 ? block / WAVE * p.E * sizeof(double) : 0;
@@ -790,6 +848,21 @@ template <typename D> void launch_route(RouteP p, hipStream_t st)
     if (p.E <= 256) msim_route_rows<D, 4><<<grid, 256, lds, st>>>(p);
     else msim_route_rows<D, 16><<<grid, 256, lds, st>>>(p);
     launch_finish<D>(p, false, st);
+}
+
+template <typename D> void launch_dropout(const DropP &d, hipStream_t st)
+{
+    const uint64_t n = d.rows * d.cols, per = 16 / sizeof(typename D::raw);
+    if (d.per_row) {
+        const uint32_t lwide = d.cols >= 256 ? 8 : 31 - __builtin_clz(pow2((uint32_t)d.cols));
+        const uint64_t rows = 256 >> lwide;
+        msim_dropout_rows<D><<<(uint32_t)std::min<uint64_t>((d.rows + rows - 1) / rows, 1u << 16), 256, 0, st>>>(d, lwide);
+    } else if ((d.rows == 1 || (d.xs == d.cols && d.ys == d.cols)) && (uintptr_t)d.x % 16 == 0 &&
+               (uintptr_t)d.y % 16 == 0 && d.limit >> 32 == 0) {
+        msim_dropout_flat<D><<<(uint32_t)std::min<uint64_t>((n + 256 * per - 1) / (256 * per), 1u << 16), 256, 0, st>>>(d);
+    } else {
+        msim_dropout_any<D><<<(uint32_t)std::min<uint64_t>((n + 255) / 256, 1u << 16), 256, 0, st>>>(d);
+    }
 }
 
 } // namespace
@@ -845,10 +918,9 @@ extern "C" int msim_dropout(uint32_t dtype, const void *x, void *y, uint64_t row
         return fail(MSIM_E_LIMIT, "dropout: more than 2^44 elements");
     d.scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.0f;
     hipStream_t st = (hipStream_t)hip_stream;
-    const uint32_t grid = (uint32_t)std::min<uint64_t>((rows * cols + 255) / 256, 1u << 16);
-    if (dtype == MSIM_F32) msim_dropout_any<F32><<<grid, 256, 0, st>>>(d);
-    else if (dtype == MSIM_F16) msim_dropout_any<F16><<<grid, 256, 0, st>>>(d);
-    else msim_dropout_any<BF16><<<grid, 256, 0, st>>>(d);
+    if (dtype == MSIM_F32) launch_dropout<F32>(d, st);
+    else if (dtype == MSIM_F16) launch_dropout<F16>(d, st);
+    else launch_dropout<BF16>(d, st);
     return launched("dropout launch");
 }
 

@@ -44,33 +44,36 @@ class Routing(NamedTuple):
 def _need(t, name: str, dtype, device, shape=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device != device or t.device.type != "cuda":
+    if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device if device.type == 'cuda' else 'a GPU'}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _need_rows(t, name: str):
-    """A [rows, columns] tensor whose columns lie next to each other; its row stride."""
+    """Checks for a [rows, columns] tensor whose columns lie next to each other;
+    its device, rows, columns and row stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, not on a GPU")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    stride, inner = t.stride()
+    if cols > 1 and inner != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if t.shape[0] <= 1:
-        return max(t.shape[1], 1)
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)} for {t.shape[1]} columns)")
-    return t.stride(0)
+    if rows <= 1:
+        stride = max(cols, 1)
+    elif stride < cols:
+        raise ValueError(f"{name}: rows overlap (stride {stride} for {cols} columns)")
+    return t.device, rows, cols, stride
 
 
 def _range(value, name: str, lo: int, hi: int) -> int:
@@ -80,9 +83,24 @@ def _range(value, name: str, lo: int, hi: int) -> int:
     return v
 
 
-class _On:
-    """Makes the tensors' device and the call's stream current, so that results
-    are allocated there; `ptr` is the stream's handle."""
+class _Here:
+    """The tensors' device is current and the call goes to its current stream:
+    nothing to switch (what torch's context managers cost is a multiple of the
+    call)."""
+
+    def __init__(self, ptr):
+        self.ptr = ptr
+
+    def __enter__(self):
+        return self.ptr
+
+    def __exit__(self, *exc):
+        return False
+
+
+class _There:
+    """Makes the tensors' device and the given stream current, so that results
+    are allocated there."""
 
     def __init__(self, device, stream):
         if stream is None:
@@ -91,19 +109,26 @@ class _On:
             stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self.ptr = C.c_void_p(stream.cuda_stream)
+        self.ptr = stream.cuda_stream
         self._ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
         self._ctx.__enter__()
-        return self
+        return self.ptr
 
     def __exit__(self, *exc):
         return self._ctx.__exit__(*exc)
 
 
+def _on(device, stream):
+    """Context of a call: its value is the handle of the stream."""
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return _Here(torch._C._cuda_getCurrentRawStream(device.index))
+    return _There(device, stream)
+
+
 def _p(t: Optional[torch.Tensor]):
-    return C.c_void_p(t.data_ptr() if t is not None else None)
+    return None if t is None else t.data_ptr()
 
 
 def _call(rc: int):
@@ -128,26 +153,25 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Opt
     worth the sum of its group_top (1 or 2) largest keys.  renorm divides a
     row's weights by their sum; scale multiplies them.  A logit of -inf takes
     an expert out; ties go to the lower expert."""
-    stride = _need_rows(logits, "logits")
-    dev, (rows, experts) = logits.device, logits.shape
+    dev, rows, experts, stride = _need_rows(logits, "logits")
     k = _range(top_k, "top_k", 1, max(experts, 1))
     if bias is not None:
         _need(bias, "bias", torch.float32, dev, (experts,))
     spec = RouteSpec(ABI_VERSION, _DTYPES[logits.dtype], _score(score), experts, k,
                      _range(groups, "groups", 1, 1 << 20), _range(top_groups, "top_groups", 1, 1 << 20),
                      _range(group_top, "group_top", 1, 2), 1 if renorm else 0, float(scale), rows, stride)
-    with _On(dev, stream) as on:
+    with _on(dev, stream) as on:
         if out is None:
-            out = Routing(torch.empty(rows, k, dtype=torch.int32, device=dev),
-                          torch.empty(rows, k, dtype=torch.float32, device=dev),
-                          torch.empty(experts, dtype=torch.int32, device=dev))
+            out = Routing(logits.new_empty((rows, k), dtype=torch.int32),
+                          logits.new_empty((rows, k), dtype=torch.float32),
+                          logits.new_empty(experts, dtype=torch.int32))
         else:
             _need(out.ids, "out.ids", torch.int32, dev, (rows, k))
             _need(out.weights, "out.weights", torch.float32, dev, (rows, k))
             if out.load is not None:
                 _need(out.load, "out.load", torch.int32, dev, (experts,))
         _call(load_library().msim_route(C.byref(spec), _p(logits), _p(bias), _p(out.ids), _p(out.weights),
-                                        _p(out.load), on.ptr))
+                                        _p(out.load), on))
     return out
 
 
@@ -158,8 +182,7 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, grad: torch.Tensor, 
     (float32 [rows, top_k]) is that of the weights, ids are the forward pass's,
     score, renorm and scale the forward pass's arguments.  The choice itself,
     and so bias and groups, has no gradient."""
-    stride = _need_rows(logits, "logits")
-    dev, (rows, experts) = logits.device, logits.shape
+    dev, rows, experts, stride = _need_rows(logits, "logits")
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids must be a tensor of two dimensions")
     k = _range(ids.shape[1], "the number of ids in a row", 1, max(experts, 1))
@@ -167,17 +190,18 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, grad: torch.Tensor, 
     _need(grad, "grad", torch.float32, dev, (rows, k))
     spec = RouteSpec(ABI_VERSION, _DTYPES[logits.dtype], _score(score), experts, k, 1, 1, 1, 1 if renorm else 0,
                      float(scale), rows, stride)
-    with _On(dev, stream) as on:
+    with _on(dev, stream) as on:
         if out is None:
-            out = torch.empty(rows, experts, dtype=logits.dtype, device=dev)
-        out_stride = _out_rows(out, "out", logits)
+            out, out_stride = logits.new_empty((rows, experts)), experts
+        else:
+            out_stride = _out_rows(out, "out", logits)
         _call(load_library().msim_route_backward(C.byref(spec), _p(logits), _p(ids), _p(grad), _p(out), out_stride,
-                                                 on.ptr))
+                                                 on))
     return out
 
 
 def _out_rows(out, name: str, like) -> int:
-    stride = _need_rows(out, name)
+    stride = _need_rows(out, name)[3]
     if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
         raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)} on {like.device}")
     return stride
@@ -189,17 +213,17 @@ def dropout(x: torch.Tensor, p: float, seed: int, *, offset: int = 0, per_row: b
     probability p and the others divided by 1 - p.  The mask is a function of
     (seed, offset, element): it is never stored, and the same call on a
     gradient is the backward pass.  out may be x."""
-    xs = _need_rows(x, "x")
-    rows, cols = x.shape
+    dev, rows, cols, xs = _need_rows(x, "x")
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be in [0, 1], not {p!r}")
     seed, offset = _range(seed, "seed", 0, (1 << 64) - 1), _range(offset, "offset", 0, (1 << 64) - 1)
-    with _On(x.device, stream) as on:
+    with _on(dev, stream) as on:
         if out is None:
-            out = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
-        ys = _out_rows(out, "out", x)
+            out, ys = x.new_empty((rows, cols)), max(cols, 1)
+        else:
+            ys = _out_rows(out, "out", x)
         _call(load_library().msim_dropout(_DTYPES[x.dtype], _p(x), _p(out), rows, cols, xs, ys, float(p), seed,
-                                          offset, 1 if per_row else 0, on.ptr))
+                                          offset, 1 if per_row else 0, on))
     return out
 
 
@@ -244,9 +268,10 @@ def traffic(ids: torch.Tensor, token_off: torch.Tensor, home: torch.Tensor, plac
                        _range(pkt_bytes, "pkt_bytes", 1, (1 << 32) - 1), float(drop),
                        _range(seed, "seed", 0, (1 << 64) - 1), _range(offset, "offset", 0, (1 << 64) - 1),
                        1 if per_row else 0, 0)
-    with _On(dev, stream) as on:
+    with _on(dev, stream) as on:
         if out is None:
-            out = torch.empty(n_seg, h, dtype=torch.int32, device=dev)
-        _need(out, "out", torch.int32, dev, (n_seg, h))
-        _call(load_library().msim_traffic(C.byref(spec), _p(ids), _p(token_off), _p(home), _p(place), _p(out), on.ptr))
+            out = ids.new_empty((n_seg, h))
+        else:
+            _need(out, "out", torch.int32, dev, (n_seg, h))
+        _call(load_library().msim_traffic(C.byref(spec), _p(ids), _p(token_off), _p(home), _p(place), _p(out), on))
     return out
