@@ -16,6 +16,7 @@ namespace {
 
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int WAVE = 64;
 constexpr float LOG2E = 1.44269504f;
@@ -566,58 +567,124 @@ struct BackP {
     uint64_t rows, stride, dstride;
     uint32_t E, K, renorm, sigmoid;
     float scale;
+    uint32_t vec;                          /* rows of whole 16 bytes, aligned */
 };
 
-template <typename D> __global__ void __launch_bounds__(256) msim_route_back(BackP p)
+/* The slots of a row on LANES lanes (at least top_k), 64 / LANES rows a
+ * wavefront.  Only the chosen logits are read, unless all have a gradient; the
+ * gradient's rows, nearly all zeros, are put together in LDS, CHUNK experts at
+ * a time, and leave it in 16-byte stores: bound by those.  What was put there is
+ * taken out again afterwards, so the rest stays zero. */
+template <typename D, int LANES> __global__ void __launch_bounds__(256) msim_route_back(BackP p)
 {
-    const int lane = threadIdx.x & 63;
-    const uint64_t step = (uint64_t)gridDim.x * (blockDim.x / WAVE);
-    for (uint64_t row = (uint64_t)blockIdx.x * (blockDim.x / WAVE) + threadIdx.x / WAVE; row < p.rows; row += step) {
+    constexpr int PER = 16 / sizeof(typename D::raw), ROWS = WAVE / LANES;
+    constexpr uint32_t CHUNK = 256;
+    typedef typename D::raw vec __attribute__((ext_vector_type(PER)));
+    __shared__ float lds[4][ROWS][CHUNK + 4];
+    const uint32_t lane = threadIdx.x & 63, l = lane % LANES;
+    float (*const buf)[CHUNK + 4] = lds[threadIdx.x / WAVE];
+    for (uint32_t i = lane; i < ROWS * (CHUNK + 4); i += WAVE) (&buf[0][0])[i] = 0.0f;
+    wave_sync();
+    const bool every = !p.sigmoid && !p.renorm;        /* all experts have a gradient */
+    const uint64_t step = (uint64_t)gridDim.x * 4 * ROWS;
+    for (uint64_t rows = ((uint64_t)blockIdx.x * 4 + threadIdx.x / WAVE) * ROWS; rows < p.rows; rows += step) {
+        const uint64_t row = min(rows + lane / LANES, p.rows - 1);
+        const bool mine = rows + lane / LANES < p.rows;
         const typename D::raw *x = (const typename D::raw *)p.x + row * p.stride;
-        typename D::raw *dx = (typename D::raw *)p.dx + row * p.dstride;
-        /* lane j has slot j */
-        int32_t id = lane < (int)p.K ? p.ids[row * p.K + lane] : -1;
+        int32_t id = l < p.K ? p.ids[row * p.K + l] : -1;
+        float g = l < p.K ? p.g[row * p.K + l] : 0.0f;
         if ((uint32_t)id >= p.E) id = -1;
-        float xs = id >= 0 ? D::get(x[id]) : -INFINITY;
+        const float xs = id >= 0 ? D::get(x[id]) : -INFINITY;
         if (xs == -INFINITY) id = -1;      /* an expert out of the row has no score to change */
-        const float g = id >= 0 ? p.g[row * p.K + lane] : 0.0f;
-        const bool any = __any(id >= 0);
-        const bool every = !p.sigmoid && !p.renorm;    /* all experts have a gradient */
-        float top = -INFINITY, z = 1.0f, q, d;
+        const bool got = id >= 0;
+        if (!got) g = 0.0f;
+        float top = -INFINITY, inv = 1.0f;
         if (every) {
-            for (uint32_t e = lane; e < p.E; e += WAVE) top = fmaxf(top, D::get(x[e]));
-            top = wave_max(top);
-            float sum = 0;
-            for (uint32_t e = lane; e < p.E; e += WAVE) sum += expf(D::get(x[e]) - top);
-            z = wave_sum(sum);
-            q = id >= 0 ? expf(xs - top) / z : 0.0f;
-        } else if (p.sigmoid) {
-            const float lo = fminf(xs, 0.0f);
-            const float c = p.renorm ? wave_max(id >= 0 ? lo : -INFINITY) : 0.0f;
-            q = id >= 0 ? expf(lo - c) / (1.0f + expf(-fabsf(xs))) : 0.0f;
-        } else {
-            const float c = wave_max(xs);
-            q = id >= 0 ? expf(xs - c) : 0.0f;
-        }
-        if (p.renorm) {
-            const float sum = wave_sum(q);
-            q = id >= 0 ? q / sum : 0.0f;
-        }
-        const float mean = wave_sum(g * q);
-        d = q * (p.renorm || every ? g - mean : g);
-        if (every) d = q * g;
-        if (p.sigmoid) d *= xs > 0 ? expf(-xs) / (1.0f + expf(-xs)) : 1.0f / (1.0f + expf(xs));
-        d = id >= 0 ? d * p.scale : 0.0f;
-        /* an expert's gradient is the sum over the slots that name it, in slot order */
-        for (uint32_t e0 = 0; e0 < p.E; e0 += WAVE) {
-            const uint32_t e = e0 + lane;
-            float v = every && any && e < p.E ? -p.scale * mean * (expf(D::get(x[e]) - top) / z) : 0.0f;
-            for (uint32_t j = 0; j < p.K; j++) {
-                const int oi = __shfl(id, (int)j);
-                const float od = __shfl(d, (int)j);
-                if (oi == (int)e) v += od;
+            if (p.vec) {
+                for (uint32_t e = l * PER; e < p.E; e += LANES * PER) {
+                    const vec t = *(const vec *)(x + e);
+                    for (int i = 0; i < PER; i++) top = fmaxf(top, D::get(t[i]));
+                }
+            } else {
+                for (uint32_t e = l; e < p.E; e += LANES) top = fmaxf(top, D::get(x[e]));
             }
-            if (e < p.E) dx[e] = D::put(v);
+            top = fold<LANES>(top, Max());
+            float sum = 0.0f;
+            if (p.vec) {
+                for (uint32_t e = l * PER; e < p.E; e += LANES * PER) {
+                    const vec t = *(const vec *)(x + e);
+                    for (int i = 0; i < PER; i++) sum += __builtin_amdgcn_exp2f((D::get(t[i]) - top) * LOG2E);
+                }
+            } else {
+                for (uint32_t e = l; e < p.E; e += LANES) sum += __builtin_amdgcn_exp2f((D::get(x[e]) - top) * LOG2E);
+            }
+            inv = 1.0f / fold<LANES>(sum, Sum());
+        }
+        /* the scores, renormalised or not, as msim_route has them */
+        const float t = p.sigmoid ? fminf(xs, 0.0f) : xs;
+        const float c = p.renorm ? fold<LANES>(got ? t : -INFINITY, Max()) : p.sigmoid ? 0.0f : top;
+        float q = expf(t - c);
+        if (p.sigmoid) q /= 1.0f + expf(-fabsf(xs));
+        else if (!p.renorm) q *= inv;
+        if (!got) q = 0.0f;
+        if (p.renorm) {
+            const float sum = fold<LANES>(q, Sum());
+            if (got) q /= sum;
+        }
+        const float mean = fold<LANES>(g * q, Sum());
+        float d = q * (p.renorm ? g - mean : g);
+        if (p.sigmoid) d *= xs > 0.0f ? expf(-xs) / (1.0f + expf(-xs)) : 1.0f / (1.0f + expf(xs));
+        d = got ? d * p.scale : 0.0f;
+        const float base = -p.scale * mean;            /* times a score: what every expert gets */
+        const bool some = fold<LANES>(got ? 1.0f : 0.0f, Max()) > 0.0f;
+        /* an expert named twice: its first slot has the sum, in slot order */
+        float total = 0.0f;
+        bool first = got;
+        for (uint32_t j = 0; j < p.K; j++) {
+            const int at = (int)(lane - l + j);
+            const int32_t oi = __shfl(id, at);
+            const float od = __shfl(d, at);
+            if (oi == id) {
+                total += od;
+                if (j < l) first = false;
+            }
+        }
+        typename D::raw *dx = (typename D::raw *)p.dx + row * p.dstride;
+        for (uint32_t e0 = 0; e0 < p.E; e0 += CHUNK) {
+            const bool in = first && (uint32_t)id - e0 < CHUNK;
+            if (in) buf[lane / LANES][id - e0] = total;
+            wave_sync();
+            const uint32_t end = min(CHUNK, p.E - e0);
+            if (p.vec) {
+                for (uint32_t e = l * PER; e < end; e += LANES * PER) {
+                    float v[PER];
+                    for (int i = 0; i < PER; i += 4) *(f32x4 *)&v[i] = *(const f32x4 *)&buf[lane / LANES][e + i];
+                    if (every && some) {
+                        const vec t = *(const vec *)(x + e0 + e);
+                        for (int i = 0; i < PER; i++)
+                            v[i] += base * (__builtin_amdgcn_exp2f((D::get(t[i]) - top) * LOG2E) * inv);
+                    }
+                    vec o;
+                    for (int i = 0; i < PER; i++) o[i] = D::put(v[i]);
+                    if (mine) *(vec *)(dx + e0 + e) = o;
+                }
+            } else {
+                /* rows of any alignment, one after the other */
+                for (uint32_t r = 0; r < ROWS && rows + r < p.rows; r++) {
+                    const float rb = __shfl(base, (int)(r * LANES)), rt = __shfl(top, (int)(r * LANES));
+                    const float ri = __shfl(inv, (int)(r * LANES));
+                    const bool rs = every && __shfl(some, (int)(r * LANES));
+                    const typename D::raw *rx = (const typename D::raw *)p.x + (rows + r) * p.stride + e0;
+                    typename D::raw *ro = (typename D::raw *)p.dx + (rows + r) * p.dstride + e0;
+                    for (uint32_t e = lane; e < end; e += WAVE) {
+                        float v = buf[r][e];
+                        if (rs) v += rb * (__builtin_amdgcn_exp2f((D::get(rx[e]) - rt) * LOG2E) * ri);
+                        ro[e] = D::put(v);
+                    }
+                }
+            }
+            wave_sync();
+            if (in) buf[lane / LANES][id - e0] = 0.0f;
         }
     }
 }
@@ -633,18 +700,6 @@ struct DropP {
     float scale;
     uint32_t per_row;
 };
-
-/* any layout: an element a thread */
-template <typename D> __global__ void __launch_bounds__(256) msim_dropout_any(DropP p)
-{
-    const uint64_t n = p.rows * p.cols, step = (uint64_t)gridDim.x * blockDim.x;
-    for (uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
-        const uint64_t r = i / p.cols, c = i - r * p.cols;
-        const float v = D::get(((const typename D::raw *)p.x)[r * p.xs + c]);
-        const bool keep = draw32(p.base, p.per_row ? r : i) >= p.limit;
-        ((typename D::raw *)p.y)[r * p.ys + c] = D::put(keep ? v * p.scale : 0.0f);
-    }
-}
 
 /* Elements that lie next to each other, PER of them (16 bytes) a thread and
  * turn: bound by the memory, and nearly by the generator, a 64-bit mix for two
@@ -676,18 +731,27 @@ template <typename D> __global__ void __launch_bounds__(256) msim_dropout_flat(D
     }
 }
 
-/* Rows that stay or go whole: one draw a row, a workgroup's 256 threads on it
- * or, of short rows, on several at once. */
-template <typename D> __global__ void __launch_bounds__(256) msim_dropout_rows(DropP p, uint32_t lwide)
+/* Rows with a stride, or that stay or go whole: 2^lwide threads a row, two
+ * elements of one mix a thread and turn. */
+template <typename D, bool WHOLE> __global__ void __launch_bounds__(256) msim_dropout_rows(DropP p, uint32_t lwide)
 {
-    const uint32_t wide = 1u << lwide;                 /* threads a row */
+    const uint32_t wide = 1u << lwide, me = threadIdx.x & (wide - 1);
     const uint64_t step = (uint64_t)gridDim.x * (blockDim.x >> lwide);
     for (uint64_t r = (uint64_t)blockIdx.x * (blockDim.x >> lwide) + (threadIdx.x >> lwide); r < p.rows; r += step) {
-        const bool keep = draw32(p.base, r) >= p.limit;
         const typename D::raw *x = (const typename D::raw *)p.x + r * p.xs;
         typename D::raw *y = (typename D::raw *)p.y + r * p.ys;
-        for (uint64_t c = threadIdx.x & (wide - 1); c < p.cols; c += wide)
-            y[c] = keep ? D::put(D::get(x[c]) * p.scale) : D::put(0.0f);
+        if (WHOLE) {
+            const bool keep = draw32(p.base, r) >= p.limit;
+            for (uint64_t c = me; c < p.cols; c += wide) y[c] = D::put(keep ? D::get(x[c]) * p.scale : 0.0f);
+        } else {
+            /* element i of the tensor is column i - i0; pairs begin at even i */
+            const uint64_t i0 = r * p.cols, i1 = i0 + p.cols;
+            for (uint64_t i = (i0 & ~1ull) + 2 * me; i < i1; i += 2 * wide) {
+                const uint64_t d = mix64(p.base + (i >> 1) * GAMMA);
+                if (i >= i0) y[i - i0] = D::put((uint32_t)d >= p.limit ? D::get(x[i - i0]) * p.scale : 0.0f);
+                if (i + 1 < i1) y[i + 1 - i0] = D::put((d >> 32) >= p.limit ? D::get(x[i + 1 - i0]) * p.scale : 0.0f);
+            }
+        }
     }
 }
 
@@ -702,36 +766,71 @@ struct TrafficP {
     int32_t *out;
     uint64_t rows, n_seg, base, limit;
     uint32_t E, K, H, token_bytes, pkt_bytes, per_row;
+    uint32_t vec, small, recip;            /* ids by 16 bytes; bytes below 2^31; floor((2^32 - 1) / pkt_bytes) */
 };
 
-/* One workgroup a segment: a count per host in LDS, each token by one thread. */
-__global__ void __launch_bounds__(256) msim_traffic_segments(TrafficP p)
+/* A workgroup a segment: a count per host in LDS, a token a thread, its hosts
+ * in registers where each is compared with those before it.  Bound by latency:
+ * offsets, ids, hosts and counts follow from one another, so a segment has no
+ * more threads than tokens and as many segments as fit run side by side. */
+template <int KMAX> __global__ void __launch_bounds__(1024) msim_traffic_segments(TrafficP p)
 {
     extern __shared__ uint32_t count[];
     for (uint64_t s = blockIdx.x; s < p.n_seg; s += gridDim.x) {
-        for (uint32_t h = threadIdx.x; h < p.H; h += blockDim.x) count[h] = 0;
-        __syncthreads();
         const uint64_t lo = min((uint64_t)max(p.off[s], (int64_t)0), p.rows);
         const uint64_t hi = min((uint64_t)max(p.off[s + 1], (int64_t)0), p.rows);
+        const uint32_t home = p.home[s];
+        for (uint32_t h = threadIdx.x; h < p.H; h += blockDim.x) count[h] = 0;
+        __syncthreads();
         for (uint64_t t = lo + threadIdx.x; t < hi; t += blockDim.x) {
-            int32_t seen[MSIM_MAX_TOP_K];
-            for (uint32_t j = 0; j < p.K; j++) {
-                const int32_t id = p.ids[t * p.K + j];
-                int32_t h = (uint32_t)id < p.E ? p.place[id] : -1;
-                if (p.limit && draw32(p.base, p.per_row ? t : t * p.K + j) < p.limit) h = -1;
-                if ((uint32_t)h >= p.H) h = -1;
-                bool again = false;
-                for (uint32_t i = 0; i < j; i++) again |= seen[i] == h;
-                seen[j] = h;
-                if (h >= 0 && !again) atomicAdd(&count[h], 1u);
+            int32_t h[KMAX];
+            if (KMAX >= 4 && p.vec) {
+                for (int j = 0; j < KMAX; j += 4) {
+                    i32x4 id = {-1, -1, -1, -1};
+                    if (j < (int)p.K) id = *(const i32x4 *)(p.ids + t * p.K + j);
+                    for (int i = 0; i < 4 && j + i < KMAX; i++) h[j + i] = id[i];
+                }
+            } else {
+                for (int j = 0; j < KMAX; j++) h[j] = j < (int)p.K ? p.ids[t * p.K + j] : -1;
+            }
+            for (int j = 0; j < KMAX; j++) h[j] = (uint32_t)h[j] < p.E ? p.place[h[j]] : -1;
+            if (p.limit) {
+                if (p.per_row) {
+                    if (draw32(p.base, t) < p.limit)
+                        for (int j = 0; j < KMAX; j++) h[j] = -1;
+                } else if (p.K % 2 == 0) {
+                    uint64_t z = p.base + (t * p.K >> 1) * GAMMA;
+                    for (int j = 0; j < KMAX; j += 2, z += GAMMA) {
+                        const uint64_t d = mix64(z);
+                        if ((uint32_t)d < p.limit) h[j] = -1;
+                        if (j + 1 < KMAX && (d >> 32) < p.limit) h[j + 1] = -1;
+                    }
+                } else {
+                    for (int j = 0; j < KMAX; j++)
+                        if (draw32(p.base, t * p.K + j) < p.limit) h[j] = -1;
+                }
+            }
+            for (int j = 0; j < KMAX; j++) {
+                bool go = (uint32_t)h[j] < p.H;
+                for (int i = 0; i < j; i++) go &= h[i] != h[j];
+                if (go) atomicAdd(&count[h[j]], 1u);
             }
         }
         __syncthreads();
-        const int32_t home = p.home[s];
         for (uint32_t h = threadIdx.x; h < p.H; h += blockDim.x) {
-            const uint64_t b = (uint64_t)count[h] * p.token_bytes;
-            const uint64_t k = b / p.pkt_bytes + (b % p.pkt_bytes != 0);
-            p.out[s * p.H + h] = (int32_t)h == home ? 0 : (int32_t)min(k, (uint64_t)0x7FFFFFFF);
+            uint32_t k = 0;
+            if (h != home && p.small) {
+                /* b < 2^31: the quotient by the reciprocal is right or one short */
+                const uint32_t b = count[h] * p.token_bytes;
+                k = __umulhi(b, p.recip);
+                uint32_t rest = b - k * p.pkt_bytes;
+                if (rest >= p.pkt_bytes) { k++; rest -= p.pkt_bytes; }
+                k += rest != 0;
+            } else if (h != home) {
+                const uint64_t b = (uint64_t)count[h] * p.token_bytes;
+                k = (uint32_t)min(b / p.pkt_bytes + (b % p.pkt_bytes != 0), (uint64_t)0x7FFFFFFF);
+            }
+            p.out[s * p.H + h] = (int32_t)k;
         }
         __syncthreads();
     }
@@ -850,19 +949,29 @@ template <typename D> void launch_route(RouteP p, hipStream_t st)
     launch_finish<D>(p, false, st);
 }
 
+template <typename D> void launch_back(const BackP &p, hipStream_t st)
+{
+    const uint64_t rows = 4 * WAVE / (p.K <= 8 ? 8 : p.K <= 16 ? 16 : 32);
+    const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + rows - 1) / rows, 4096);
+    if (p.K <= 8) msim_route_back<D, 8><<<grid, 256, 0, st>>>(p);
+    else if (p.K <= 16) msim_route_back<D, 16><<<grid, 256, 0, st>>>(p);
+    else msim_route_back<D, 32><<<grid, 256, 0, st>>>(p);
+}
+
 template <typename D> void launch_dropout(const DropP &d, hipStream_t st)
 {
     const uint64_t n = d.rows * d.cols, per = 16 / sizeof(typename D::raw);
-    if (d.per_row) {
-        const uint32_t lwide = d.cols >= 256 ? 8 : 31 - __builtin_clz(pow2((uint32_t)d.cols));
-        const uint64_t rows = 256 >> lwide;
-        msim_dropout_rows<D><<<(uint32_t)std::min<uint64_t>((d.rows + rows - 1) / rows, 1u << 16), 256, 0, st>>>(d, lwide);
-    } else if ((d.rows == 1 || (d.xs == d.cols && d.ys == d.cols)) && (uintptr_t)d.x % 16 == 0 &&
-               (uintptr_t)d.y % 16 == 0 && d.limit >> 32 == 0) {
+    if (!d.per_row && (d.rows == 1 || (d.xs == d.cols && d.ys == d.cols)) && (uintptr_t)d.x % 16 == 0 &&
+        (uintptr_t)d.y % 16 == 0 && d.limit >> 32 == 0) {
         msim_dropout_flat<D><<<(uint32_t)std::min<uint64_t>((n + 256 * per - 1) / (256 * per), 1u << 16), 256, 0, st>>>(d);
-    } else {
-        msim_dropout_any<D><<<(uint32_t)std::min<uint64_t>((n + 255) / 256, 1u << 16), 256, 0, st>>>(d);
+        return;
     }
+    const uint64_t turns = d.per_row ? d.cols : d.cols / 2 + 1;
+    const uint32_t lwide = turns >= 256 ? 8 : __builtin_ctz(pow2((uint32_t)turns));
+    const uint64_t rows = 256 >> lwide;
+    const uint32_t grid = (uint32_t)std::min<uint64_t>((d.rows + rows - 1) / rows, 1u << 16);
+    if (d.per_row) msim_dropout_rows<D, true><<<grid, 256, 0, st>>>(d, lwide);
+    else msim_dropout_rows<D, false><<<grid, 256, 0, st>>>(d, lwide);
 }
 
 } // namespace
@@ -892,13 +1001,15 @@ extern "C" int msim_route_backward(const msim_route_spec *s, const void *logits,
     if (!logits || !ids || !grad || !grad_logits) return fail(MSIM_E_ARG, "route: null logits, ids or gradient");
     if (grad_stride < s->experts) return fail(MSIM_E_ARG, "route: grad_stride below experts");
     if (grad_stride >> 40) return fail(MSIM_E_LIMIT, "route: grad_stride of 2^40 or more");
+    const uint32_t size = s->dtype == MSIM_F32 ? 4 : 2;
+    const bool vec = s->experts * size % 16 == 0 && s->row_stride * size % 16 == 0 && grad_stride * size % 16 == 0 &&
+                     (uintptr_t)logits % 16 == 0 && (uintptr_t)grad_logits % 16 == 0;
     const BackP p = {logits, ids, grad, grad_logits, s->rows, s->row_stride, grad_stride, s->experts, s->top_k,
-                     s->renorm, s->score == MSIM_SCORE_SIGMOID, s->scale};
+                     s->renorm, s->score == MSIM_SCORE_SIGMOID, s->scale, vec};
     hipStream_t st = (hipStream_t)hip_stream;
-    const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + 3) / 4, 4096);
-    if (s->dtype == MSIM_F32) msim_route_back<F32><<<grid, 256, 0, st>>>(p);
-    else if (s->dtype == MSIM_F16) msim_route_back<F16><<<grid, 256, 0, st>>>(p);
-    else msim_route_back<BF16><<<grid, 256, 0, st>>>(p);
+    if (s->dtype == MSIM_F32) launch_back<F32>(p, st);
+    else if (s->dtype == MSIM_F16) launch_back<F16>(p, st);
+    else launch_back<BF16>(p, st);
     return launched("route backward launch");
 }
 
@@ -933,7 +1044,8 @@ extern "C" int msim_traffic(const msim_traffic_spec *s, const int32_t *ids, cons
     if (!s->token_bytes || !s->pkt_bytes) return fail(MSIM_E_ARG, "traffic: token_bytes and pkt_bytes must be at least 1");
     if (s->per_row > 1 || s->reserved) return fail(MSIM_E_ARG, "traffic: per_row must be 0 or 1, reserved 0");
     TrafficP p = {ids, token_off, home, place, packets, s->rows, s->n_seg, splitmix_base(s->seed, s->offset), 0,
-                  s->experts, s->top_k, s->hosts, s->token_bytes, s->pkt_bytes, s->per_row};
+                  s->experts, s->top_k, s->hosts, s->token_bytes, s->pkt_bytes, s->per_row,
+                  s->top_k % 4 == 0 && (uintptr_t)ids % 16 == 0, 0, 0xFFFFFFFFu / std::max(s->pkt_bytes, 1u)};
     if (!drop_limit(s->drop, &p.limit)) return fail(MSIM_E_ARG, "traffic: drop must be in [0, 1]");
     if (s->experts > (1u << 24)) return fail(MSIM_E_LIMIT, "traffic: more than 2^24 experts");
     if (s->top_k > MSIM_MAX_TOP_K) return fail(MSIM_E_LIMIT, "traffic: top_k above MSIM_MAX_TOP_K");
@@ -942,7 +1054,16 @@ extern "C" int msim_traffic(const msim_traffic_spec *s, const int32_t *ids, cons
     if (s->n_seg >> 32) return fail(MSIM_E_LIMIT, "traffic: 2^32 segments or more");
     if (s->n_seg == 0) return MSIM_OK;
     if (!token_off || !home || !place || !packets || (s->rows && !ids)) return fail(MSIM_E_ARG, "traffic: null array");
-    const uint32_t grid = (uint32_t)std::min<uint64_t>(s->n_seg, 1u << 16);
-    msim_traffic_segments<<<grid, 256, 4 * s->hosts, (hipStream_t)hip_stream>>>(p);
+    p.small = s->rows * s->token_bytes < (1ull << 31);
+    const uint32_t grid = (uint32_t)std::min<uint64_t>(s->n_seg, 1u << 20);
+    const uint64_t tokens = s->rows / s->n_seg;        /* of a segment, about */
+    const uint32_t block = tokens <= 128 ? 64 : tokens <= 512 ? 128 : tokens <= 2048 ? 256 : 1024;
+    const size_t lds = 4 * s->hosts;
+    hipStream_t st = (hipStream_t)hip_stream;
+    if (p.K <= 2) msim_traffic_segments<2><<<grid, block, lds, st>>>(p);
+    else if (p.K <= 4) msim_traffic_segments<4><<<grid, block, lds, st>>>(p);
+    else if (p.K <= 8) msim_traffic_segments<8><<<grid, block, lds, st>>>(p);
+    else if (p.K <= 16) msim_traffic_segments<16><<<grid, block, lds, st>>>(p);
+    else msim_traffic_segments<32><<<grid, block, lds, st>>>(p);
     return launched("traffic launch");
 }
