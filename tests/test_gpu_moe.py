@@ -138,7 +138,8 @@ SHAPES = [  # rows, experts, top_k, groups, top_groups, group_top
     (130, 128, 8, 1, 1, 1), (257, 160, 6, 8, 3, 1), (33, 161, 7, 7, 3, 2), (300, 256, 8, 8, 4, 2), (9, 256, 32, 4, 4, 2),
     (17, 257, 3, 1, 1, 1), (12, 384, 8, 1, 1, 1), (40, 512, 10, 16, 4, 2), (7, 1000, 16, 20, 2, 1), (21, 1024, 32, 64, 9, 2),
     (18, 192, 16, 64, 6, 2), (50, 256, 1, 8, 1, 1), (70, 96, 4, 2, 1, 2), (31, 256, 9, 8, 5, 2), (29, 32, 4, 4, 2, 2),
-    (19, 16, 4, 1, 1, 1), (27, 512, 8, 8, 4, 2), (23, 256, 16, 1, 1, 1), (26, 1024, 8, 1, 1, 1),
+    (19, 16, 4, 1, 1, 1), (27, 512, 8, 8, 4, 2), (23, 256, 16, 1, 1, 1), (26, 1024, 8, 1, 1, 1), (11, 510, 12, 5, 2, 1),
+    (13, 400, 16, 16, 4, 2), (45, 6, 3, 2, 2, 1), (20, 3, 2, 1, 1, 1), (36, 5, 5, 1, 1, 1), (34, 224, 16, 7, 2, 2),
 ]
 
 
@@ -197,6 +198,30 @@ def test_route_tells_keys_apart_that_32_bits_do_not(T, M):
     b = (0.5 - s).float()
     check_route(M, x, 8, score="softmax", bias=b, groups=8, top_groups=2, group_top=2)
     check_route(M, x, 8, score="softmax", bias=b)
+
+
+@pytest.mark.parametrize("k", [8, 16])
+@pytest.mark.parametrize("experts", [256, 512])
+def test_route_tells_the_first_left_out_from_the_last_chosen(T, M, experts, k):
+    """All choices are neighbours, and the first that is left out differs from
+    the last chosen by less than 32 bits tell, in either order."""
+    x = T.full((64, experts), -3.0, device=DEV)
+    x[:, :k] = 3.0 - 0.25 * T.arange(k, device=DEV)
+    x[:, k] = x[:, k - 1] + T.linspace(-1e-6, 1e-6, 64, device=DEV)
+    x[1::2, k - 1], x[1::2, k] = x[1::2, k].clone(), x[1::2, k - 1].clone()
+    for groups, top_groups in ((1, 1), (8, 2)):
+        check_route(M, x, k, score="sigmoid", bias=T.zeros(experts, device=DEV), groups=groups, top_groups=top_groups)
+        check_route(M, x, k, score="softmax", bias=T.full((experts,), 0.125, device=DEV), groups=groups,
+                    top_groups=top_groups, group_top=2)
+
+
+def test_route_of_large_biases(T, M):
+    """Keys whose biases are far larger than the scores: sums of two that nearly cancel among them."""
+    g = np.random.default_rng(4)
+    x = logits_of(T, 200, 64, T.float32, 12)
+    b = T.from_numpy(np.where(np.arange(64) % 8 == 0, 100.0, -100.0).astype(np.float32) + g.choice([0.0, 1e-5, 0.5], 64).astype(np.float32)).to(DEV)
+    check_route(M, x, 4, score="sigmoid", bias=b, groups=8, top_groups=3, group_top=2)
+    check_route(M, x, 8, score="softmax", bias=b * 1000, groups=4, top_groups=2, group_top=2)
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
