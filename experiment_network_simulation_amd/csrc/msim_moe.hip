@@ -83,16 +83,12 @@ struct RouteP {
                                               16-byte loads */
 };
 
-/* Exchange with another lane of the same 16 (M = 1, 2: lane ^ M; 7, 15: the
- * mirror of 8 and of 16), of the same 32 (16) or of the wavefront (32). */
+/* Exchange with another lane of the same 16: M = 1, 2: lane ^ M; 7, 15: the
+ * mirror of 8 and of 16. */
 template <int M> __device__ __forceinline__ uint32_t other(uint32_t v)
 {
-    if constexpr (M == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);
-    else if constexpr (M == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);
-    else if constexpr (M == 7) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);
-    else if constexpr (M == 15) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);
-    else if constexpr (M == 16) return __builtin_amdgcn_ds_swizzle(v, 0x401F);
-    else return __shfl_xor(v, 32);
+    constexpr int CTRL = M == 1 ? 0xB1 : M == 2 ? 0x4E : M == 7 ? 0x141 : 0x140;
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
 }
 template <int M> __device__ __forceinline__ float other(float v)
 {
@@ -104,6 +100,30 @@ template <int M> __device__ __forceinline__ double other(double v)
     return __builtin_bit_cast(double, (uint64_t)other<M>((uint32_t)(u >> 32)) << 32 | other<M>((uint32_t)u));
 }
 
+/* The values that lanes l and l ^ N (16 or 32) hold, in the same order on both:
+ * the swap of v with itself. */
+template <int N> __device__ __forceinline__ void both(uint32_t v, uint32_t &a, uint32_t &b)
+{
+    const auto r = N == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                           : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
+}
+template <int N, typename F> __device__ __forceinline__ float fold_far(float v, F f)
+{
+    uint32_t a, b;
+    both<N>(__builtin_bit_cast(uint32_t, v), a, b);
+    return f(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+template <int N, typename F> __device__ __forceinline__ double fold_far(double v, F f)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    uint32_t al, ah, bl, bh;
+    both<N>((uint32_t)u, al, bl);
+    both<N>((uint32_t)(u >> 32), ah, bh);
+    return f(__builtin_bit_cast(double, (uint64_t)ah << 32 | al), __builtin_bit_cast(double, (uint64_t)bh << 32 | bl));
+}
+
 /* Folds v over blocks of N lanes; every lane has the result. */
 template <int N, typename T, typename F> __device__ __forceinline__ T fold(T v, F f)
 {
@@ -111,13 +131,15 @@ template <int N, typename T, typename F> __device__ __forceinline__ T fold(T v, 
     v = f(v, other<2>(v));
     v = f(v, other<7>(v));
     if constexpr (N > 8) v = f(v, other<15>(v));
-    if constexpr (N > 16) v = f(v, other<16>(v));
-    if constexpr (N > 32) v = f(v, other<32>(v));
+    if constexpr (N > 16) v = fold_far<16>(v, f);
+    if constexpr (N > 32) v = fold_far<32>(v, f);
     return v;
 }
 struct Max { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 struct Min { __device__ float operator()(float a, float b) const { return fminf(a, b); } };
-struct Sum { __device__ float operator()(float a, float b) const { return a + b; } };
+struct Sum {
+    template <typename T> __device__ T operator()(T a, T b) const { return a + b; }
+};
 
 /* A key and its expert in one 64-bit number that v_max_f64 orders: the high
  * word is the key as a float, which orders as the high word of a double does
@@ -232,11 +254,12 @@ template <typename D, int VPL> __device__ void route_row(const RouteP &p, uint64
         bad |= v[i] != v[i] || (!p.sigmoid && v[i] == INFINITY);
         top = fmaxf(top, v[i]);
     }
-    const bool is_void = __any(bad);
-    top = fold<WAVE>(top, Max());
+    const bool is_void = __any(bad), in = __any(top > -INFINITY);
+    if (!p.sigmoid) top = fold<WAVE>(top, Max());
     int32_t my_id = -1;
+    float xs = -INFINITY;
     double inv = 1.0;
-    if (!is_void && top > -INFINITY) {
+    if (!is_void && in) {
         const bool scored = p.bias || p.gtop > 1;
         if (scored || (!p.sigmoid && !p.renorm)) {
             double sum = 0;
@@ -245,8 +268,7 @@ template <typename D, int VPL> __device__ void route_row(const RouteP &p, uint64
                 sum += key[i];
             }
             if (!p.sigmoid) {
-                for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
-                inv = 1.0 / sum;
+                inv = 1.0 / fold<WAVE>(sum, Sum());
             }
         }
         for (int i = 0; i < VPL; i++) {
@@ -302,13 +324,20 @@ template <typename D, int VPL> __device__ void route_row(const RouteP &p, uint64
                 win = min(win, __builtin_amdgcn_readlane(at, __builtin_ctzll(has)));
                 has &= has - 1;
             }
+            float won = 0.0f;
             for (int i = 0; i < VPL; i++)
-                if (i * WAVE + (int)lane == win) key[i] = -INFINITY;
-            if (lane == r) my_id = win;
+                if (i * WAVE + (int)lane == win) {
+                    key[i] = -INFINITY;
+                    won = v[i];
+                }
+            won = __shfl(won, win % WAVE);
+            if (lane == r) {
+                my_id = win;
+                xs = won;
+            }
         }
     }
     /* weights: lane j has slot j */
-    const float xs = my_id >= 0 ? D::get(x[my_id]) : -INFINITY;
     const float q = weight_of<WAVE>(p, xs, my_id >= 0, top, (float)inv);
     if (lane < p.K) {
         p.ids[row * p.K + lane] = my_id;

@@ -222,6 +222,31 @@ def test_route_of_large_biases(T, M):
     b = T.from_numpy(np.where(np.arange(64) % 8 == 0, 100.0, -100.0).astype(np.float32) + g.choice([0.0, 1e-5, 0.5], 64).astype(np.float32)).to(DEV)
     check_route(M, x, 4, score="sigmoid", bias=b, groups=8, top_groups=3, group_top=2)
     check_route(M, x, 8, score="softmax", bias=b * 1000, groups=4, top_groups=2, group_top=2)
+    # the lowest value as a mask: such an expert comes last, but before none
+    for low in (T.finfo(T.float32).min, -1e9, -3.5, -2.9):
+        b = bias_of(T, 64)
+        b[::3] = low
+        for score in ("softmax", "sigmoid"):
+            check_route(M, x, 8, score=score, bias=b)
+            check_route(M, x, 4, score=score, bias=b, groups=8, top_groups=3, group_top=2)
+            b[:60] = low
+            check_route(M, x, 8, score=score, bias=b)
+            check_route(M, x, 4, score=score, bias=b, groups=8, top_groups=3, group_top=1)
+    b = bias_of(T, 64)
+    b[5], b[9], b[40], b[41] = np.inf, np.inf, T.finfo(T.float32).max, 1e31
+    check_route(M, x, 8, score="sigmoid", bias=b)
+    check_route(M, x, 8, score="sigmoid", bias=b, groups=8, top_groups=2)
+
+
+@pytest.mark.parametrize("experts,k", [(256, 8), (64, 4), (512, 16)])
+def test_route_of_many_equal_keys(T, M, experts, k):
+    """A coarse grid of logits with a bias that is the same for all, or for runs of experts."""
+    x = (logits_of(T, 400, experts, T.float32, 13) * 2).round()
+    for b in (T.zeros(experts, device=DEV), T.full((experts,), -0.5, device=DEV),
+              (T.arange(experts, device=DEV) // 7 % 2).float() * 0.25):
+        for score in ("softmax", "sigmoid"):
+            check_route(M, x, k, score=score, bias=b)
+            check_route(M, x.bfloat16(), k, score=score, bias=b, groups=8, top_groups=4)
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
