@@ -200,9 +200,11 @@ def main():
     ap.add_argument("--chunk", type=int, default=0,
                     help="run the batch in chunks of this many experiments, compiling the next chunk while the "
                          "current one runs (default: whole batch; C5 beyond 2048 experiments: 2048)")
-    ap.add_argument("--dse", choices=["tune", "reshard"], default=None,
-                    help="time a design-space-exploration driver instead: AutoCCL tuning or AlpaComm schedules")
-    ap.add_argument("--dse-n", type=int, default=0, help="tuning tasks / resharding instances (default 256 / 64)")
+    ap.add_argument("--dse", choices=["tune", "reshard", "route"], default=None,
+                    help="time a design-space-exploration driver instead: AutoCCL tuning, AlpaComm schedules or "
+                         "expert-parallel router designs")
+    ap.add_argument("--dse-n", type=int, default=0,
+                    help="tuning tasks / resharding instances / router designs (default 256 / 64 / 64)")
     ap.add_argument("--copy-probe", type=int, default=0,
                     help="only run a plain device-to-device copy of this many bytes (calibrates HBM byte counters)")
     args = ap.parse_args()
@@ -503,6 +505,37 @@ def dse_bench(args):
             ok = sum(ref["ticks"] == res[t].ticks and ref["algo"] == res[t].algo for t, ref in zip(ids, refs))
             cpu = {"value": probes / dt, "unit": unit, "cores": min(threads, len(ids)), "kind": "oracle",
                    "sample": f"{len(ids)} of {n} tuning tasks, {probes} probes in {dt:.1f}s; same result on "
+                             f"{ok}/{len(ids)}", "parity_ok": ok, "parity_n": len(ids)}
+    elif args.dse == "route":
+        import torch
+        n = args.dse_n or 64
+        topo = I.fat_tree(8)
+        H, tokens, experts = topo.hosts().size, 128, 256
+        logits = torch.from_numpy(I.gate_logits(0x70C, H * tokens, experts)).to("cuda:0").bfloat16()
+        designs = [P.RouteDesign(**d) for d in I.route_design_space(n, H, experts)]
+        workload = (f"{n} router designs over {experts} experts on the {H} hosts of a k=8 fat-tree, {tokens} tokens a "
+                    "host with synthetic gate logits: top-k 2/4/8, groups, balance bias, dropped assignments; the "
+                    "dispatch all-to-all of each scored by simulation")
+        t0 = time.perf_counter()
+        res = P.route_designs(logits, np.arange(H + 1) * tokens, np.arange(H), designs, topo, ev, seed=7)
+        wall = time.perf_counter() - t0
+        detail = {"designs": n, "packets": [min(r.packets for r in res), max(r.packets for r in res)],
+                  "ticks": [min(r.ticks for r in res), max(r.ticks for r in res)],
+                  "busiest_expert_over_mean": [min(r.busiest for r in res), max(r.busiest for r in res)]}
+        unit = "designs/s"
+        cpu = None
+        if args.cpu_sample:
+            from oracle import oracle as O
+            m = min(args.cpu_sample, n)
+            ids = sorted(set(j * n // m for j in range(m)))
+            t1 = time.perf_counter()
+            with ThreadPoolExecutor(min(threads, len(ids))) as ex:
+                refs = list(ex.map(lambda k: O.run(O.OracleBatch(I.single_batch(topo, res[k].work, 16, 0).pack()), 0),
+                                   ids))
+            dt = time.perf_counter() - t1
+            ok = sum(r["t_end"] == res[k].ticks for k, r in zip(ids, refs))
+            cpu = {"value": len(ids) / dt, "unit": unit, "cores": min(threads, len(ids)), "kind": "oracle",
+                   "sample": f"{len(ids)} of {n} designs' all-to-alls simulated in {dt:.1f}s; same completion tick on "
                              f"{ok}/{len(ids)}", "parity_ok": ok, "parity_n": len(ids)}
     else:
         n = args.dse_n or 64

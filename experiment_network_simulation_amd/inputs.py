@@ -330,6 +330,8 @@ def traffic_flows(packets: np.ndarray, home: Optional[Sequence[int]] = None) -> 
     total = np.zeros((n, n), np.int64)
     np.add.at(total, src, pk)
     np.fill_diagonal(total, 0)
+    if (total < 0).any() or (total >> 32).any():
+        raise ValueError("a flow must have 0 .. 2^32 - 1 packets")
     a, b = np.nonzero(total)
     w = Workload()
     w.xsrc, w.xdst, w.xpkts = a.astype(np.uint32), b.astype(np.uint32), total[a, b].astype(np.uint32)
@@ -952,4 +954,22 @@ def greedy_keys(seed: int, n_tasks: int, n_rounds: int, n_stages: Optional[int] 
     flat = out.reshape(-1)
     for i in range(flat.size):
         flat[i] = g.next()
+    return out
+
+
+def route_design_space(n: int, hosts: int, experts: int, seed: int = 0xE9) -> List[dict]:
+    """n router designs (keyword arguments of dse.RouteDesign) over `experts`
+    experts spread evenly over `hosts` hosts in a seeded order: top-k in {2, 4,
+    8}, all experts or the 4 best of 8 groups, 0 or 20 steps of the balance
+    bias, and 0, 5 or 20 % of the assignments dropped."""
+    g = exp_rng(seed, experts)
+    out = []
+    for _ in range(n):
+        order = g.permutation(experts)
+        place = np.zeros(experts, np.int32)
+        place[order] = np.arange(experts) * hosts // experts
+        grouped = g.below(2)
+        out.append(dict(top_k=(2, 4, 8)[g.below(3)], place=place, groups=8 if grouped else 1,
+                        top_groups=4 if grouped else 1, group_top=2 if grouped else 1,
+                        balance_steps=20 * g.below(2), drop=(0.0, 0.05, 0.2)[g.below(3)]))
     return out

@@ -291,6 +291,17 @@ def test_route_masks(T, M, experts, groups, top_groups, score, dtype):
     check_route(M, x, 6, score=score, bias=b, groups=groups, top_groups=top_groups)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_route_of_tiny_logits(T, M, dtype):
+    """Logits below the smallest normal number, of both signs, keep their order."""
+    x = (T.arange(64, device=DEV) * 37 % 64 - 31).float().repeat(6, 1)
+    x = (x * T.tensor([1e-38, 1e-39, 2.0 ** -133, 2.0 ** -126, 1e-30, 1.0], device=DEV)[:, None]).to(getattr(T, dtype))
+    for score in ("softmax", "sigmoid"):
+        check_route(M, x, 8, score=score)
+        check_route(M, x, 16, score=score, groups=4, top_groups=2)
+        check_route(M, x, 20, score=score)
+
+
 def test_route_of_no_rows_and_given_outputs(T, M):
     x = logits_of(T, 50, 64, T.float32, 10)
     r = M.route(x[:0], 4)

@@ -145,6 +145,19 @@ def test_flows_of_a_traffic_matrix():
     for home in ([0, 1], [0, 1, 3], [0, 1, -1]):
         with pytest.raises(ValueError):
             I.traffic_flows(np.ones((3, 3)), home)
+    most = 0x7FFFFFFF
+    assert I.traffic_flows([[0, most], [0, 0], [0, most]], [0, 1, 0]).xpkts.tolist() == [2 * most]
+    with pytest.raises(ValueError):
+        I.traffic_flows([[0, most]] * 3 + [[1, 0]], [0, 0, 0, 1])
+
+
+def test_router_designs_are_seeded_and_valid():
+    a, b = I.route_design_space(40, 16, 64), I.route_design_space(40, 16, 64)
+    for x, y in zip(a, b):
+        assert all(np.array_equal(x[k], y[k]) for k in x)
+        assert np.array_equal(np.bincount(x["place"], minlength=16), np.full(16, 4))
+        assert x["top_k"] <= 64 // x["groups"] * x["top_groups"]
+    assert len({d["top_k"] for d in a}) == 3 and len({d["drop"] for d in a}) == 3
 
 
 def test_gate_logits_are_seeded_and_spread():
