@@ -429,6 +429,8 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
     typedef vec loose __attribute__((aligned(sizeof(typename D::raw))));
     __shared__ int32_t hist[MSIM_MAX_EXPERTS];
     __shared__ float lds_bias[BIAS ? LANES * (VPL + 4) : 1];
+    __shared__ double lds_list[256][KL + 1];                  /* each thread's list, and an end; 8 (KL + 1) bytes apart no
+                                                               * two lanes of a half-wavefront meet in a bank */
     constexpr uint32_t ROWS = WAVE / LANES;                   /* rows a wavefront */
     const uint32_t glanes = 1u << p.lglanes;
     const uint32_t lane = threadIdx.x & 63, l = lane % LANES, sub = l & (glanes - 1);
@@ -438,6 +440,7 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
     const uint32_t n0 = past > first0 ? past - first0 : 0;
     /* one workgroup that leaves no row undecided counts by itself */
     const bool count = p.load && gridDim.x == 1 && !(BIAS || p.gtop > 1);
+    lds_list[threadIdx.x][KL] = pack(-INFINITY, 0);
     if (count)
         for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
     else
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
             if (c) keep_list<KL>(a, b);
         }
         const float slack = sigmoid ? 0x1p-20f : 0x1p-22f + 0x1p-17f * inv;
-        bool near = false;
+        bool near = false, left_out = false;
         if (p.G > 1) {
             float t1 = key_of(a[0]), t2 = key_of(a[1]);
             _Pragma("unroll 1") for (uint32_t m = 1; m < glanes; m <<= 1) {
@@ -562,22 +565,25 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
                 const float size = fold<LANES>((t1 > -INFINITY ? fabsf(t1) : 0.0f) + (t2 > -INFINITY ? fabsf(t2) : 0.0f), Max());
                 near = out > -INFINITY && !(in - out > 2.0f * slack + 0x1p-20f * size);
             }
-            if (!stay)
-                for (int i = 0; i < KL; i++) a[i] = pack(-INFINITY, 0);
+            left_out = !stay;
         }
         double slot = pack(-INFINITY, 0), last = slot;
-        /* with bias one round more, for the difference to the first that is not chosen.  A loop: written out for
-         * each round, with lists that get shorter, it is a quarter slower (131,072 x 256 bf16) */
-        uint32_t won_all = 0;
+        const double *list = lds_list[threadIdx.x];
+        for (int i = 0; i < KL; i++) lds_list[threadIdx.x][i] = a[i];
+        double head = a[0];
+        if (left_out) {
+            head = slot;
+            list += KL;
+        }
+        /* with bias one round more, for the difference to the first that is not chosen */
         _Pragma("unroll 1") for (uint32_t r = 0; r < p.K + BIAS; r++) {
-            const double m = fold<LANES>(a[0], Max64());
+            const double m = fold<LANES>(head, Max64());
             if (l == r) slot = m;
             if (BIAS) last = m;
-            const bool won = __builtin_bit_cast(uint64_t, m) == __builtin_bit_cast(uint64_t, a[0]);
-            if (BIAS) won_all += won && key_of(m) > -INFINITY;
-            for (int i = 0; i < KL - 1; i++) a[i] = won ? a[i + 1] : a[i];
-            a[KL - 1] = won ? pack(-INFINITY, 0) : a[KL - 1];
+            if (__builtin_bit_cast(uint64_t, m) == __builtin_bit_cast(uint64_t, head) && list < lds_list[threadIdx.x] + KL) list++;
+            head = *list;
         }
+        const uint32_t won_all = left_out ? 0 : list - lds_list[threadIdx.x];
         /* a list that is used up hides what comes next to its last */
         if (BIAS && VPL > KL) near |= won_all >= KL;
         const bool got = l < p.K && key_of(slot) > -INFINITY && !is_void;
