@@ -424,11 +424,13 @@ template <typename D, int VPL> __global__ void __launch_bounds__(512) msim_route
  * sums of two scores) the keys here are 32-bit approximations with a known
  * error, and a row whose choice depends on a difference within twice that error
  * is left to msim_route_finish, which compares in 64 bits (1 row in 1,000 of
- * sigmoids with a bias).  Errors: a sigmoid is off by less than 2^-22 (v_exp_f32
- * and v_rcp_f32 are off by 2^-23 relative, the argument x log2 e by 1.5 2^-24
- * |x|, and |x| s (1 - s) < 0.23); a softmax score by less than 2^-24 (0.6 + 48 s)
- * (a sum of 32 terms a lane, six exchanges); the sum with the bias by 2^-24
- * |key| more.
+ * sigmoids with a bias).  Errors: v_exp_f32 and v_rcp_f32 are off by 2^-23
+ * relative.  A sigmoid is off by less than 2^-22: its exponential's argument by
+ * 1.4 2^-24 |x|, and |x| s (1 - s) < 0.23.  A softmax score is off by less than
+ * 2^-24 (0.9 + 54 s): the argument by 2.4 2^-24 |x - top|, and |x - top| e^(x -
+ * top) < 0.37 in the score and 4.5 of the sum for 1,024 experts; the sum by 36
+ * additions (32 terms a lane, five exchanges).  The sum with the bias adds 2^-24
+ * |key|.
  *
  * Bound by the issue of vector instructions, 1,087 for eight rows of 256 with
  * groups and bias: 42 us at 131,072 x 256 bf16, where its bytes would take 15.5.
@@ -595,7 +597,8 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
             const double m = fold<LANES>(head, Max64());
             if (l == r) slot = m;
             if (BIAS) last = m;
-            if (__builtin_bit_cast(uint64_t, m) == __builtin_bit_cast(uint64_t, head) && list < lds_list[threadIdx.x] + KL) list++;
+            /* (the end of a list is no key) */
+            if (__builtin_bit_cast(uint64_t, m) == __builtin_bit_cast(uint64_t, head) && key_of(m) > -INFINITY) list++;
             head = *list;
         }
         const uint32_t won_all = left_out ? 0 : list - lds_list[threadIdx.x];
@@ -958,7 +961,7 @@ const char *check_route(const msim_route_spec *s, bool backward, int *code)
     *code = MSIM_E_LIMIT;
     if (s->experts > MSIM_MAX_EXPERTS) return "route: more than MSIM_MAX_EXPERTS experts";
     if (s->top_k > MSIM_MAX_TOP_K) return "route: top_k above MSIM_MAX_TOP_K";
-    if (s->rows >> 40 || s->row_stride >> 40) return "route: rows or row_stride of 2^40 or more";
+    if (s->rows >> 31 || s->row_stride >> 40) return "route: 2^31 rows or more, or a row_stride of 2^40 or more";
     *code = MSIM_E_ARG;
     if (backward) return s->top_k > s->experts ? "route: top_k above experts" : nullptr;
     if (s->groups == 0 || s->experts % s->groups) return "route: groups must divide experts";

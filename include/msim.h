@@ -460,7 +460,7 @@ int msim_lds_probe(void *dev_out, uint64_t out_bytes, uint32_t blocks, uint32_t 
  *  - weight = scale * s, with renorm scale * s / (sum of the chosen s).
  * Limits: experts <= MSIM_MAX_EXPERTS, groups <= MSIM_MAX_EXPERT_GROUPS and a
  * divisor of experts, top_k <= MSIM_MAX_TOP_K and <= top_groups * experts /
- * groups.
+ * groups, rows < 2^31.
  */
 typedef struct msim_route_spec {
     uint32_t version;            /* MSIM_ABI_VERSION */
