@@ -853,19 +853,43 @@ struct TrafficP {
     uint64_t rows, n_seg, base, limit;
     uint32_t E, K, H, token_bytes, pkt_bytes, per_row;
     uint32_t vec, small, recip;            /* ids by 16 bytes; bytes below 2^31; floor((2^32 - 1) / pkt_bytes) */
+    uint64_t parts;                        /* workgroups a segment */
 };
+
+/* the packets of `count` tokens */
+__device__ __forceinline__ uint32_t packets_of(const TrafficP &p, uint32_t count)
+{
+    if (p.small) {
+        /* below 2^31 bytes: the quotient by the reciprocal is right or one short */
+        const uint32_t b = count * p.token_bytes;
+        uint32_t k = __umulhi(b, p.recip), rest = b - k * p.pkt_bytes;
+        if (rest >= p.pkt_bytes) { k++; rest -= p.pkt_bytes; }
+        return k + (rest != 0);
+    }
+    const uint64_t b = (uint64_t)count * p.token_bytes;
+    return (uint32_t)min(b / p.pkt_bytes + (b % p.pkt_bytes != 0), (uint64_t)0x7FFFFFFF);
+}
 
 /* A workgroup a segment: a count per host in LDS, a token a thread, its hosts
  * in registers where each is compared with those before it.  Bound by latency:
  * offsets, ids, hosts and counts follow from one another, so a segment has no
  * more threads than tokens and as many segments as fit run side by side.  64 x
- * 128 hosts, 8 choices: 11 us for 21 MB; 1,024 hosts with 128 tokens: 5.5 for 8. */
+ * 128 hosts, 8 choices: 11 us for 21 MB; 1,024 hosts with 128 tokens: 5.5 for 8.
+ * Few long segments are cut into `parts`, whose counts meet in the table, cleared
+ * before and turned into packets after: 8 segments of 131,072 tokens and 128
+ * hosts 227 -> 16 us, 64 of 16,384 32 -> 16. */
 template <int KMAX> __global__ void __launch_bounds__(1024) msim_traffic_segments(TrafficP p)
 {
     extern __shared__ uint32_t count[];
-    for (uint64_t s = blockIdx.x; s < p.n_seg; s += gridDim.x) {
-        const uint64_t lo = min((uint64_t)max(p.off[s], (int64_t)0), p.rows);
-        const uint64_t hi = min((uint64_t)max(p.off[s + 1], (int64_t)0), p.rows);
+    for (uint64_t w = blockIdx.x; w < p.n_seg * p.parts; w += gridDim.x) {
+        const uint64_t s = p.parts == 1 ? w : w / p.parts, part = w - s * p.parts;
+        uint64_t lo = min((uint64_t)max(p.off[s], (int64_t)0), p.rows);
+        uint64_t hi = min((uint64_t)max(p.off[s + 1], (int64_t)0), p.rows);
+        if (p.parts > 1 && hi > lo) {
+            const uint64_t each = (hi - lo + p.parts - 1) / p.parts;
+            lo = min(lo + part * each, hi);
+            hi = min(lo + each, hi);
+        }
         const uint32_t home = p.home[s];
         for (uint32_t h = threadIdx.x; h < p.H; h += blockDim.x) count[h] = 0;
         __syncthreads();
@@ -905,22 +929,25 @@ template <int KMAX> __global__ void __launch_bounds__(1024) msim_traffic_segment
         }
         __syncthreads();
         for (uint32_t h = threadIdx.x; h < p.H; h += blockDim.x) {
-            uint32_t k = 0;
-            if (h != home && p.small) {
-                /* b < 2^31: the quotient by the reciprocal is right or one short */
-                const uint32_t b = count[h] * p.token_bytes;
-                k = __umulhi(b, p.recip);
-                uint32_t rest = b - k * p.pkt_bytes;
-                if (rest >= p.pkt_bytes) { k++; rest -= p.pkt_bytes; }
-                k += rest != 0;
-            } else if (h != home) {
-                const uint64_t b = (uint64_t)count[h] * p.token_bytes;
-                k = (uint32_t)min(b / p.pkt_bytes + (b % p.pkt_bytes != 0), (uint64_t)0x7FFFFFFF);
-            }
-            p.out[s * p.H + h] = (int32_t)k;
+            int32_t *out = p.out + s * p.H + h;
+            if (p.parts == 1) *out = h == home ? 0 : (int32_t)packets_of(p, count[h]);
+            else if (h != home && count[h]) atomicAdd(out, (int32_t)count[h]);
         }
         __syncthreads();
     }
+}
+
+__global__ void __launch_bounds__(256) msim_traffic_clear(TrafficP p)
+{
+    const uint64_t n = p.n_seg * p.H, step = (uint64_t)gridDim.x * blockDim.x;
+    for (uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) p.out[i] = 0;
+}
+
+__global__ void __launch_bounds__(256) msim_traffic_packets(TrafficP p)
+{
+    const uint64_t n = p.n_seg * p.H, step = (uint64_t)gridDim.x * blockDim.x;
+    for (uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step)
+        p.out[i] = (int32_t)packets_of(p, (uint32_t)p.out[i]);
 }
 
 /* ------------------------------------------------------------------------ */
@@ -1137,7 +1164,7 @@ extern "C" int msim_traffic(const msim_traffic_spec *s, const int32_t *ids, cons
     if (s->per_row > 1 || s->reserved) return fail(MSIM_E_ARG, "traffic: per_row must be 0 or 1, reserved 0");
     TrafficP p = {ids, token_off, home, place, packets, s->rows, s->n_seg, splitmix_base(s->seed, s->offset), 0,
                   s->experts, s->top_k, s->hosts, s->token_bytes, s->pkt_bytes, s->per_row,
-                  s->top_k % 4 == 0 && (uintptr_t)ids % 16 == 0, 0, 0xFFFFFFFFu / std::max(s->pkt_bytes, 1u)};
+                  s->top_k % 4 == 0 && (uintptr_t)ids % 16 == 0, 0, 0xFFFFFFFFu / std::max(s->pkt_bytes, 1u), 1};
     if (!drop_limit(s->drop, &p.limit)) return fail(MSIM_E_ARG, "traffic: drop must be in [0, 1]");
     if (s->experts > (1u << 24)) return fail(MSIM_E_LIMIT, "traffic: more than 2^24 experts");
     if (s->top_k > MSIM_MAX_TOP_K) return fail(MSIM_E_LIMIT, "traffic: top_k above MSIM_MAX_TOP_K");
@@ -1147,7 +1174,6 @@ extern "C" int msim_traffic(const msim_traffic_spec *s, const int32_t *ids, cons
     if (s->n_seg == 0) return MSIM_OK;
     if (!token_off || !home || !place || !packets || (s->rows && !ids)) return fail(MSIM_E_ARG, "traffic: null array");
     p.small = s->rows * s->token_bytes < (1ull << 31);
-    const uint32_t grid = (uint32_t)std::min<uint64_t>(s->n_seg, 1u << 20);
     /* As many threads as a segment has tokens (about) or quarters of its hosts, while all segments' together fill
      * the card: 1,024 segments of 128 tokens and 1,024 hosts take 5.4 us with 256 threads, 7.6 with 64; 8,192 of 64
      * and 128 hosts 11.1 with 64, 16.5 with 256. */
@@ -1155,6 +1181,11 @@ extern "C" int msim_traffic(const msim_traffic_spec *s, const int32_t *ids, cons
     const uint64_t most = std::max<uint64_t>(64, 524288 / s->n_seg);
     uint32_t block = 64;
     while (block < 1024 && block < want && 2 * block <= most) block *= 2;
+    /* A workgroup for every 4,096 tokens of a segment, up to 1,024 in all. */
+    p.parts = std::max<uint64_t>(1, std::min((s->rows / s->n_seg) / 4096, 1024 / s->n_seg));
+    const uint32_t grid = (uint32_t)std::min<uint64_t>(s->n_seg * p.parts, 1u << 20);
+    const uint32_t every = (uint32_t)std::min<uint64_t>((s->n_seg * s->hosts + 255) / 256, 4096);
+    if (p.parts > 1) msim_traffic_clear<<<every, 256, 0, (hipStream_t)hip_stream>>>(p);
     const size_t lds = 4 * s->hosts;
     hipStream_t st = (hipStream_t)hip_stream;
     if (p.K <= 2) msim_traffic_segments<2><<<grid, block, lds, st>>>(p);
@@ -1162,5 +1193,6 @@ extern "C" int msim_traffic(const msim_traffic_spec *s, const int32_t *ids, cons
     else if (p.K <= 8) msim_traffic_segments<8><<<grid, block, lds, st>>>(p);
     else if (p.K <= 16) msim_traffic_segments<16><<<grid, block, lds, st>>>(p);
     else msim_traffic_segments<32><<<grid, block, lds, st>>>(p);
+    if (p.parts > 1) msim_traffic_packets<<<every, 256, 0, st>>>(p);
     return launched("traffic launch");
 }

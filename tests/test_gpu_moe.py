@@ -587,6 +587,23 @@ def test_traffic(T, M, segs, hosts, tokens, experts, k):
     check_traffic(T, M, ids, off, home, place, hosts, drop=0.4, seed=6, per_row=True, token_bytes=100, pkt_bytes=64)
 
 
+@pytest.mark.parametrize("segs,tokens,hosts,k", [(1, 20000, 40, 4), (3, 9000, 7, 8), (2, 30000, 300, 3)])
+def test_traffic_of_few_long_segments(T, M, segs, tokens, hosts, k):
+    """Segments that several workgroups share, of very different lengths."""
+    g = np.random.default_rng(hosts)
+    rows = segs * tokens
+    off = np.sort(np.concatenate([[0, rows - 11], g.integers(0, rows // 4, segs - 1)]))
+    ids = g.integers(-1, 50, (rows, k))
+    place = g.integers(0, hosts, 50)
+    out = T.full((segs, hosts), 77, dtype=T.int32, device=DEV)
+    check_traffic(T, M, ids, off, np.arange(segs), place, hosts, token_bytes=1000, pkt_bytes=4096)
+    got = check_traffic(T, M, ids, off, np.arange(segs), place, hosts, drop=0.5, seed=4)
+    dev = lambda a, dt: T.from_numpy(np.asarray(a, dt)).to(DEV)
+    assert T.equal(M.traffic(dev(ids, np.int32), dev(off, np.int64), dev(np.arange(segs), np.int32), dev(place, np.int32),
+                             hosts, drop=0.5, seed=4, out=out), got)
+    check_traffic(T, M, ids, [0] * segs + [rows], [-1] * segs, place, hosts, token_bytes=(1 << 32) - 1, pkt_bytes=3)
+
+
 def test_traffic_counts_a_host_once_and_never_itself(T, M):
     place = [0, 0, 1, 1, 2, 2]
     ids = [[0, 1, 2], [2, 3, 3], [4, 5, 0], [-1, -1, -1], [5, 5, 5]]
@@ -743,6 +760,60 @@ def test_on_another_stream(T, M):
     r = M.route(args[0], 4, score="sigmoid", bias=args[5], groups=4, top_groups=2, group_top=2, scale=2.5, stream=s.cuda_stream)
     s.synchronize()
     assert T.equal(r.ids, want[0])
+
+
+def test_past_32_bits_of_logits(T, M):
+    """4.7 x 10^9 logits, and a gradient of as many: rows behind element 2^32 are routed as they are by themselves."""
+    rows, experts = 9 << 20, 500
+    x = T.empty(rows, experts, dtype=T.bfloat16, device=DEV).normal_(0, 1.5, generator=T.Generator(DEV).manual_seed(3))
+    b = bias_of(T, experts)
+    how = dict(score="sigmoid", bias=b, groups=10, top_groups=4, group_top=2)
+    r = M.route(x, 6, **how)
+    g = T.ones(rows, 6, device=DEV) * T.arange(6, device=DEV)
+    dx = M.route_backward(x, r.ids, g, score="sigmoid")
+    assert int(r.load.sum(dtype=T.int64)) == 6 * rows
+    for lo in (0, (1 << 32) // experts - 20, rows - 40):
+        part = M.route(x[lo:lo + 40], 6, **how)
+        assert T.equal(part.ids, r.ids[lo:lo + 40])
+        np.testing.assert_allclose(part.weights.cpu(), r.weights[lo:lo + 40].cpu(), rtol=64 * U)
+        own = M.route_backward(x[lo:lo + 40], part.ids, g[:40], score="sigmoid")
+        # another number of rows adds the same terms in another order: 2^-8 is a step of bfloat16
+        np.testing.assert_allclose(own.float().cpu(), dx[lo:lo + 40].float().cpu(), rtol=2.0 ** -8, atol=1e-5)
+    del x, dx, r, g
+    T.cuda.empty_cache()
+
+
+def test_past_32_bits_of_ids(T, M):
+    """4.3 x 10^9 assignments: the last segment of tokens counts as it does by itself, with the same draws."""
+    rows, k = (1 << 27) + 5, 32
+    ids = T.arange(64, dtype=T.int32, device=DEV).repeat(rows * k // 64 + 1)[:rows * k].view(rows, k)
+    off = T.tensor([0, 7, rows - 300, rows], device=DEV)
+    home = T.tensor([1, 2, 3], dtype=T.int32, device=DEV)
+    place = T.arange(64, dtype=T.int32, device=DEV) % 20
+    got = M.traffic(ids, off, home, place, 20, drop=0.6, seed=8)
+    lo = rows - 300
+    keep = kept(300 * k, 0.6, 8, lo * k // 2).reshape(300, k)
+    part = np.where(keep, ids[lo:].cpu().numpy(), -1)
+    want = plain_traffic(part, [0, 300], [3], place.cpu().numpy(), 20)
+    assert np.array_equal(got[2].cpu().numpy(), want[0])
+    del ids
+    T.cuda.empty_cache()
+
+
+def test_on_two_streams_at_once(T, M):
+    """Calls that overlap on two streams, each with outputs of its own."""
+    a, b = pipeline_inputs(T, 100, rows=16 * 500), pipeline_inputs(T, 101, rows=16 * 700)
+    want = [[t.clone() for t in pipeline(T, M, *args)] for args in (a, b)]
+    T.cuda.synchronize()
+    streams = [T.cuda.Stream(), T.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for s, args in zip(streams, (a, b)):
+            with T.cuda.stream(s):
+                got.append(pipeline(T, M, *args))
+        T.cuda.synchronize()
+        for w, g in zip(want, got):
+            assert all(T.equal(p, q) for p, q in zip(w, g))
 
 
 def test_captured_and_replayed(T, M):
