@@ -649,7 +649,6 @@ struct BackP {
     uint64_t rows, stride, dstride;
     uint32_t E, K, renorm, sigmoid;
     float scale;
-    uint32_t vec;                          /* rows of whole 16 bytes, aligned */
 };
 
 /* The slots of a row on LANES lanes (at least top_k), 64 / LANES rows a
@@ -664,6 +663,7 @@ template <typename D, int LANES> __global__ void __launch_bounds__(256) msim_rou
     constexpr int PER = 16 / sizeof(typename D::raw), ROWS = WAVE / LANES;
     constexpr uint32_t CHUNK = 256;
     typedef typename D::raw vec __attribute__((ext_vector_type(PER)));
+    typedef vec loose __attribute__((aligned(sizeof(typename D::raw))));
     __shared__ float lds[4][ROWS][CHUNK + 4];
     const uint32_t lane = threadIdx.x & 63, l = lane % LANES;
     float (*const buf)[CHUNK + 4] = lds[threadIdx.x / WAVE];
@@ -684,24 +684,19 @@ template <typename D, int LANES> __global__ void __launch_bounds__(256) msim_rou
         if (!got) g = 0.0f;
         float top = -INFINITY, inv = 1.0f;
         if (every) {
-            if (p.vec) {
-                for (uint32_t e = l * PER; e < p.E; e += LANES * PER) {
-                    const vec t = *(const vec *)(x + e);
-                    for (int i = 0; i < PER; i++) top = fmaxf(top, D::get(t[i]));
-                }
-            } else {
-                for (uint32_t e = l; e < p.E; e += LANES) top = fmaxf(top, D::get(x[e]));
+            const uint32_t whole = p.E - p.E % PER;
+            for (uint32_t e = l * PER; e < whole; e += LANES * PER) {
+                const vec t = *(const loose *)(x + e);
+                for (int i = 0; i < PER; i++) top = fmaxf(top, D::get(t[i]));
             }
+            if (whole + l < p.E) top = fmaxf(top, D::get(x[whole + l]));
             top = fold<LANES>(top, Max());
             float sum = 0.0f;
-            if (p.vec) {
-                for (uint32_t e = l * PER; e < p.E; e += LANES * PER) {
-                    const vec t = *(const vec *)(x + e);
-                    for (int i = 0; i < PER; i++) sum += __builtin_amdgcn_exp2f((D::get(t[i]) - top) * LOG2E);
-                }
-            } else {
-                for (uint32_t e = l; e < p.E; e += LANES) sum += __builtin_amdgcn_exp2f((D::get(x[e]) - top) * LOG2E);
+            for (uint32_t e = l * PER; e < whole; e += LANES * PER) {
+                const vec t = *(const loose *)(x + e);
+                for (int i = 0; i < PER; i++) sum += __builtin_amdgcn_exp2f((D::get(t[i]) - top) * LOG2E);
             }
+            if (whole + l < p.E) sum += __builtin_amdgcn_exp2f((D::get(x[whole + l]) - top) * LOG2E);
             inv = 1.0f / fold<LANES>(sum, Sum());
         }
         /* the scores, renormalised or not, as msim_route has them */
@@ -739,33 +734,23 @@ template <typename D, int LANES> __global__ void __launch_bounds__(256) msim_rou
             if (in) buf[lane / LANES][id - e0] = total;
             wave_sync();
             const uint32_t end = min(CHUNK, p.E - e0);
-            if (p.vec) {
-                for (uint32_t e = l * PER; e < end; e += LANES * PER) {
-                    float v[PER];
-                    for (int i = 0; i < PER; i += 4) *(f32x4 *)&v[i] = *(const f32x4 *)&buf[lane / LANES][e + i];
-                    if (every && some) {
-                        const vec t = *(const vec *)(x + e0 + e);
-                        for (int i = 0; i < PER; i++)
-                            v[i] += base * (__builtin_amdgcn_exp2f((D::get(t[i]) - top) * LOG2E) * inv);
-                    }
-                    vec o;
-                    for (int i = 0; i < PER; i++) o[i] = D::put(v[i]);
-                    if (mine) *(vec *)(dx + e0 + e) = o;
+            const uint32_t whole = end - end % PER;
+            for (uint32_t e = l * PER; e < whole; e += LANES * PER) {
+                float v[PER];
+                for (int i = 0; i < PER; i += 4) *(f32x4 *)&v[i] = *(const f32x4 *)&buf[lane / LANES][e + i];
+                if (every && some) {
+                    const vec t = *(const loose *)(x + e0 + e);
+                    for (int i = 0; i < PER; i++)
+                        v[i] += base * (__builtin_amdgcn_exp2f((D::get(t[i]) - top) * LOG2E) * inv);
                 }
-            } else {
-                /* rows of any alignment, one after the other */
-                for (uint32_t r = 0; r < ROWS && rows + r < p.rows; r++) {
-                    const float rb = __shfl(base, (int)(r * LANES)), rt = __shfl(top, (int)(r * LANES));
-                    const float ri = __shfl(inv, (int)(r * LANES));
-                    const bool rs = every && __shfl(some, (int)(r * LANES));
-                    const typename D::raw *rx = (const typename D::raw *)p.x + (rows + r) * p.stride + e0;
-                    typename D::raw *ro = (typename D::raw *)p.dx + (rows + r) * p.dstride + e0;
-                    for (uint32_t e = lane; e < end; e += WAVE) {
-                        float v = buf[r][e];
-                        if (rs) v += rb * (__builtin_amdgcn_exp2f((D::get(rx[e]) - rt) * LOG2E) * ri);
-                        ro[e] = D::put(v);
-                    }
-                }
+                vec o;
+                for (int i = 0; i < PER; i++) o[i] = D::put(v[i]);
+                if (mine) *(loose *)(dx + e0 + e) = o;
+            }
+            if (whole + l < end) {
+                float v = buf[lane / LANES][whole + l];
+                if (every && some) v += base * (__builtin_amdgcn_exp2f((D::get(x[e0 + whole + l]) - top) * LOG2E) * inv);
+                if (mine) dx[e0 + whole + l] = D::put(v);
             }
             wave_sync();
             if (in) buf[lane / LANES][id - e0] = 0.0f;
@@ -793,7 +778,7 @@ struct DropP {
 template <typename D> __global__ void __launch_bounds__(256) msim_dropout_flat(DropP p)
 {
     constexpr int PER = 16 / sizeof(typename D::raw);
-    typedef typename D::raw vec __attribute__((ext_vector_type(PER)));
+    typedef typename D::raw vec __attribute__((ext_vector_type(PER), aligned(sizeof(typename D::raw))));
     const uint64_t n = p.rows * p.cols, step = (uint64_t)gridDim.x * blockDim.x * PER;
     const uint32_t limit = (uint32_t)p.limit;          /* p < 1 here */
     for (uint64_t i = ((uint64_t)blockIdx.x * blockDim.x + threadIdx.x) * PER; i < n; i += step) {
@@ -817,25 +802,42 @@ template <typename D> __global__ void __launch_bounds__(256) msim_dropout_flat(D
     }
 }
 
-/* Rows with a stride, or that stay or go whole: 2^lwide threads a row, two
- * elements of one mix a thread and turn (4,097 x 333 f16 by rows: 4.5 us). */
-template <typename D, bool WHOLE> __global__ void __launch_bounds__(256) msim_dropout_rows(DropP p, uint32_t lwide)
+/* Rows with a stride, or that stay or go whole: 2^lwide threads a row, PER
+ * elements (16 bytes, or 2 of rows shorter than that) a thread and turn.  Where a
+ * row begins on the second half of a mix, so does every thread's part. */
+template <typename D, int PER, bool WHOLE> __global__ void __launch_bounds__(256) msim_dropout_rows(DropP p, uint32_t lwide)
 {
+    typedef typename D::raw vec __attribute__((ext_vector_type(PER), aligned(sizeof(typename D::raw))));
     const uint32_t wide = 1u << lwide, me = threadIdx.x & (wide - 1);
     const uint64_t step = (uint64_t)gridDim.x * (blockDim.x >> lwide);
     for (uint64_t r = (uint64_t)blockIdx.x * (blockDim.x >> lwide) + (threadIdx.x >> lwide); r < p.rows; r += step) {
-        const typename D::raw *x = (const typename D::raw *)p.x + r * p.xs;
-        typename D::raw *y = (typename D::raw *)p.y + r * p.ys;
-        if (WHOLE) {
-            const bool keep = draw32(p.base, r) >= p.limit;
-            for (uint64_t c = me; c < p.cols; c += wide) y[c] = D::put(keep ? D::get(x[c]) * p.scale : 0.0f);
-        } else {
-            /* element i of the tensor is column i - i0; pairs begin at even i */
-            const uint64_t i0 = r * p.cols, i1 = i0 + p.cols;
-            for (uint64_t i = (i0 & ~1ull) + 2 * me; i < i1; i += 2 * wide) {
-                const uint64_t d = mix64(p.base + (i >> 1) * GAMMA);
-                if (i >= i0) y[i - i0] = D::put((uint32_t)d >= p.limit ? D::get(x[i - i0]) * p.scale : 0.0f);
-                if (i + 1 < i1) y[i + 1 - i0] = D::put((d >> 32) >= p.limit ? D::get(x[i + 1 - i0]) * p.scale : 0.0f);
+        const bool stays = !WHOLE || draw32(p.base, r) >= p.limit;
+        for (uint64_t c = me * PER; c < p.cols; c += wide * PER) {
+            const typename D::raw *x = (const typename D::raw *)p.x + r * p.xs + c;
+            typename D::raw *y = (typename D::raw *)p.y + r * p.ys + c;
+            bool keep[PER];
+            for (int j = 0; j < PER; j++) keep[j] = stays;
+            if (!WHOLE) {
+                const uint64_t i = r * p.cols + c;
+                uint64_t z = p.base + (i >> 1) * GAMMA;
+                const bool odd = i & 1;
+                uint32_t half[PER + 2];
+                for (int j = 0; j < PER; j += 2, z += GAMMA) {
+                    const uint64_t d = mix64(z);
+                    half[j] = (uint32_t)d;
+                    half[j + 1] = (uint32_t)(d >> 32);
+                }
+                half[PER] = odd ? (uint32_t)mix64(z) : 0;
+                for (int j = 0; j < PER; j++) keep[j] = (odd ? half[j + 1] : half[j]) >= p.limit;
+            }
+            if (c + PER <= p.cols) {
+                vec v = {};
+                if (stays) v = *(const vec *)x;
+                for (int j = 0; j < PER; j++) v[j] = D::put(keep[j] ? D::get(v[j]) * p.scale : 0.0f);
+                *(vec *)y = v;
+            } else {
+                for (int j = 0; j < PER; j++)
+                    if (c + j < p.cols) y[j] = D::put(keep[j] ? D::get(x[j]) * p.scale : 0.0f);
             }
         }
     }
@@ -1079,18 +1081,23 @@ template <typename D> void launch_back(const BackP &p, hipStream_t st)
 
 template <typename D> void launch_dropout(const DropP &d, hipStream_t st)
 {
-    const uint64_t n = d.rows * d.cols, per = 16 / sizeof(typename D::raw);
-    if (!d.per_row && (d.rows == 1 || (d.xs == d.cols && d.ys == d.cols)) && (uintptr_t)d.x % 16 == 0 &&
-        (uintptr_t)d.y % 16 == 0 && d.limit >> 32 == 0) {
+    constexpr uint64_t per = 16 / sizeof(typename D::raw);
+    const uint64_t n = d.rows * d.cols;
+    if (!d.per_row && (d.rows == 1 || (d.xs == d.cols && d.ys == d.cols)) && d.limit >> 32 == 0) {
         msim_dropout_flat<D><<<(uint32_t)std::min<uint64_t>((n + 256 * per - 1) / (256 * per), 1u << 16), 256, 0, st>>>(d);
         return;
     }
-    const uint64_t turns = d.per_row ? d.cols : d.cols / 2 + 1;
+    const uint64_t turns = (d.cols + (d.cols >= per ? per : 2) - 1) / (d.cols >= per ? per : 2);
     const uint32_t lwide = turns >= 256 ? 8 : __builtin_ctz(pow2((uint32_t)turns));
     const uint64_t rows = 256 >> lwide;
     const uint32_t grid = (uint32_t)std::min<uint64_t>((d.rows + rows - 1) / rows, 1u << 16);
-    if (d.per_row) msim_dropout_rows<D, true><<<grid, 256, 0, st>>>(d, lwide);
-    else msim_dropout_rows<D, false><<<grid, 256, 0, st>>>(d, lwide);
+    if (d.cols >= per) {
+        if (d.per_row) msim_dropout_rows<D, per, true><<<grid, 256, 0, st>>>(d, lwide);
+        else msim_dropout_rows<D, per, false><<<grid, 256, 0, st>>>(d, lwide);
+    } else {
+        if (d.per_row) msim_dropout_rows<D, 2, true><<<grid, 256, 0, st>>>(d, lwide);
+        else msim_dropout_rows<D, 2, false><<<grid, 256, 0, st>>>(d, lwide);
+    }
 }
 
 } // namespace
@@ -1120,11 +1127,8 @@ extern "C" int msim_route_backward(const msim_route_spec *s, const void *logits,
     if (!logits || !ids || !grad || !grad_logits) return fail(MSIM_E_ARG, "route: null logits, ids or gradient");
     if (grad_stride < s->experts) return fail(MSIM_E_ARG, "route: grad_stride below experts");
     if (grad_stride >> 40) return fail(MSIM_E_LIMIT, "route: grad_stride of 2^40 or more");
-    const uint32_t size = s->dtype == MSIM_F32 ? 4 : 2;
-    const bool vec = s->experts * size % 16 == 0 && s->row_stride * size % 16 == 0 && grad_stride * size % 16 == 0 &&
-                     (uintptr_t)logits % 16 == 0 && (uintptr_t)grad_logits % 16 == 0;
     const BackP p = {logits, ids, grad, grad_logits, s->rows, s->row_stride, grad_stride, s->experts, s->top_k,
-                     s->renorm, s->score == MSIM_SCORE_SIGMOID, s->scale, vec};
+                     s->renorm, s->score == MSIM_SCORE_SIGMOID, s->scale};
     hipStream_t st = (hipStream_t)hip_stream;
     if (s->dtype == MSIM_F32) launch_back<F32>(p, st);
     else if (s->dtype == MSIM_F16) launch_back<F16>(p, st);
