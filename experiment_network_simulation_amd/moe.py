@@ -14,7 +14,8 @@ All tensors are on one GPU, whichever is current.  A call enqueues on `stream`
 (a torch stream or a raw handle; default: the current stream of the tensors'
 device) and returns; results are allocated on that stream unless given as
 `out`.  Bad arguments raise ValueError or TypeError here, MsimError from the
-library; nothing is launched then.
+library; nothing is launched then.  Results carry no autograd history: gradients
+are calls of their own.
 """
 
 from __future__ import annotations
