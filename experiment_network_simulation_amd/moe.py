@@ -86,24 +86,9 @@ def _range(value, name: str, lo: int, hi: int) -> int:
     return v
 
 
-class _Here:
-    """The tensors' device is current and the call goes to its current stream:
-    nothing to switch (what torch's context managers cost is a multiple of the
-    call)."""
-
-    def __init__(self, ptr):
-        self.ptr = ptr
-
-    def __enter__(self):
-        return self.ptr
-
-    def __exit__(self, *exc):
-        return False
-
-
 class _There:
     """Makes the tensors' device and the given stream current, so that results
-    are allocated there."""
+    are allocated there; its value is the stream's handle."""
 
     def __init__(self, device, stream):
         if stream is None:
@@ -123,11 +108,14 @@ class _There:
         return self._ctx.__exit__(*exc)
 
 
-def _on(device, stream):
-    """Context of a call: its value is the handle of the stream."""
+def _run(device, stream, call):
+    """call(handle of the stream), with device and stream current.  Where they are
+    already, nothing is switched: torch's context managers cost as much as the
+    call."""
     if stream is None and device.index == torch._C._cuda_getDevice():
-        return _Here(torch._C._cuda_getCurrentRawStream(device.index))
-    return _There(device, stream)
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with _There(device, stream) as handle:
+        return call(handle)
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -163,19 +151,23 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Opt
     spec = RouteSpec(ABI_VERSION, _DTYPES[logits.dtype], _score(score), experts, k,
                      _range(groups, "groups", 1, 1 << 20), _range(top_groups, "top_groups", 1, 1 << 20),
                      _range(group_top, "group_top", 1, 2), 1 if renorm else 0, float(scale), rows, stride)
-    with _on(dev, stream) as on:
-        if out is None:
-            out = Routing(logits.new_empty((rows, k), dtype=torch.int32),
-                          logits.new_empty((rows, k), dtype=torch.float32),
-                          logits.new_empty(experts, dtype=torch.int32))
-        else:
-            _need(out.ids, "out.ids", torch.int32, dev, (rows, k))
-            _need(out.weights, "out.weights", torch.float32, dev, (rows, k))
-            if out.load is not None:
-                _need(out.load, "out.load", torch.int32, dev, (experts,))
-        _call(load_library().msim_route(C.byref(spec), _p(logits), _p(bias), _p(out.ids), _p(out.weights),
-                                        _p(out.load), on))
-    return out
+    if out is not None:
+        _need(out.ids, "out.ids", torch.int32, dev, (rows, k))
+        _need(out.weights, "out.weights", torch.float32, dev, (rows, k))
+        if out.load is not None:
+            _need(out.load, "out.load", torch.int32, dev, (experts,))
+
+    def call(on):
+        r = out
+        if r is None:
+            new = logits.new_empty
+            r = Routing(new((rows, k), dtype=torch.int32), new((rows, k), dtype=torch.float32),
+                        new(experts, dtype=torch.int32))
+        _call(load_library().msim_route(C.byref(spec), logits.data_ptr(), _p(bias), r.ids.data_ptr(),
+                                        r.weights.data_ptr(), _p(r.load), on))
+        return r
+
+    return _run(dev, stream, call)
 
 
 def route_backward(logits: torch.Tensor, ids: torch.Tensor, grad: torch.Tensor, *, score: str = "softmax",
@@ -193,14 +185,15 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, grad: torch.Tensor, 
     _need(grad, "grad", torch.float32, dev, (rows, k))
     spec = RouteSpec(ABI_VERSION, _DTYPES[logits.dtype], _score(score), experts, k, 1, 1, 1, 1 if renorm else 0,
                      float(scale), rows, stride)
-    with _on(dev, stream) as on:
-        if out is None:
-            out, out_stride = logits.new_empty((rows, experts)), experts
-        else:
-            out_stride = _out_rows(out, "out", logits)
-        _call(load_library().msim_route_backward(C.byref(spec), _p(logits), _p(ids), _p(grad), _p(out), out_stride,
-                                                 on))
-    return out
+    out_stride = experts if out is None else _out_rows(out, "out", logits)
+
+    def call(on):
+        dx = logits.new_empty((rows, experts)) if out is None else out
+        _call(load_library().msim_route_backward(C.byref(spec), logits.data_ptr(), ids.data_ptr(), grad.data_ptr(),
+                                                 dx.data_ptr(), out_stride, on))
+        return dx
+
+    return _run(dev, stream, call)
 
 
 def _out_rows(out, name: str, like) -> int:
@@ -220,14 +213,15 @@ def dropout(x: torch.Tensor, p: float, seed: int, *, offset: int = 0, per_row: b
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be in [0, 1], not {p!r}")
     seed, offset = _range(seed, "seed", 0, (1 << 64) - 1), _range(offset, "offset", 0, (1 << 64) - 1)
-    with _on(dev, stream) as on:
-        if out is None:
-            out, ys = x.new_empty((rows, cols)), max(cols, 1)
-        else:
-            ys = _out_rows(out, "out", x)
-        _call(load_library().msim_dropout(_DTYPES[x.dtype], _p(x), _p(out), rows, cols, xs, ys, float(p), seed,
-                                          offset, 1 if per_row else 0, on))
-    return out
+    ys = max(cols, 1) if out is None else _out_rows(out, "out", x)
+
+    def call(on):
+        y = x.new_empty((rows, cols)) if out is None else out
+        _call(load_library().msim_dropout(_DTYPES[x.dtype], x.data_ptr(), y.data_ptr(), rows, cols, xs, ys, float(p),
+                                          seed, offset, 1 if per_row else 0, on))
+        return y
+
+    return _run(dev, stream, call)
 
 
 def dropout_backward(grad: torch.Tensor, p: float, seed: int, *, offset: int = 0, per_row: bool = False,
@@ -271,10 +265,13 @@ def traffic(ids: torch.Tensor, token_off: torch.Tensor, home: torch.Tensor, plac
                        _range(pkt_bytes, "pkt_bytes", 1, (1 << 32) - 1), float(drop),
                        _range(seed, "seed", 0, (1 << 64) - 1), _range(offset, "offset", 0, (1 << 64) - 1),
                        1 if per_row else 0, 0)
-    with _on(dev, stream) as on:
-        if out is None:
-            out = ids.new_empty((n_seg, h))
-        else:
-            _need(out, "out", torch.int32, dev, (n_seg, h))
-        _call(load_library().msim_traffic(C.byref(spec), _p(ids), _p(token_off), _p(home), _p(place), _p(out), on))
-    return out
+    if out is not None:
+        _need(out, "out", torch.int32, dev, (n_seg, h))
+
+    def call(on):
+        packets = ids.new_empty((n_seg, h)) if out is None else out
+        _call(load_library().msim_traffic(C.byref(spec), ids.data_ptr(), token_off.data_ptr(), home.data_ptr(),
+                                          place.data_ptr(), packets.data_ptr(), on))
+        return packets
+
+    return _run(dev, stream, call)
