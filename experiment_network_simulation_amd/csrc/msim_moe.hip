@@ -25,6 +25,7 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int WAVE = 64;
 constexpr float LOG2E = 1.44269504f;
+constexpr uint32_t THREAD_EXPERTS = 32;    /* experts of msim_route_threads, at most */
 constexpr uint32_t FINISH_ROWS = 1024;     /* rows a workgroup of msim_route_finish, at most */
 constexpr int32_t UNDECIDED = INT32_MIN;   /* ids of a row that msim_route_lists leaves to the 64-bit path */
 
@@ -635,6 +636,125 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
     }
 }
 
+/* Few experts and many rows: a row a thread, which keeps the eight largest keys
+ * in order as msim_route_lists does, eight experts at a time, and has all slots
+ * of its row; no exchange and no rounds.  With bias top_k < 8, so that the first
+ * key that is not chosen is in the list.  Bound by latency until the rows fill
+ * the card, then by its instructions: with the counts 1,048,576 x 8 f32 take 27
+ * us here (floor 10) and 92 in msim_route_lists, 131,072 x 32 bf16 13 and 19,
+ * but 16,384 x 32 8.3 and 7.1, and 1,048,576 x 64 145 and 83, for the rows of a
+ * wavefront no longer fit the first-level cache. */
+template <typename D, bool BIAS> __global__ void __launch_bounds__(256) msim_route_threads(RouteP p)
+{
+    constexpr int PER16 = 16 / sizeof(typename D::raw);
+    typedef typename D::raw loose __attribute__((ext_vector_type(PER16), aligned(sizeof(typename D::raw))));
+    __shared__ float bias[THREAD_EXPERTS];
+    clear_load(p);
+    if (BIAS) {
+        if (threadIdx.x < THREAD_EXPERTS) {
+            const float b = threadIdx.x < p.E ? p.bias[threadIdx.x] : -INFINITY;
+            bias[threadIdx.x] = b == b ? b : -INFINITY;
+        }
+        __syncthreads();
+    }
+    const bool sigmoid = p.sigmoid;
+    const uint64_t step = (uint64_t)gridDim.x * blockDim.x;
+    for (uint64_t row = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; row < p.rows; row += step) {
+        const typename D::raw *x = (const typename D::raw *)p.x + row * p.stride;
+        /* eight values from expert c on, -inf where there are no more, and their experts */
+        auto eight = [&](uint32_t c, float *v, uint32_t *e) {
+            for (int h = 0; h < 8; h += PER16) {
+                if (p.vec != 2) {
+                    const uint32_t from = min(c + h, p.E - PER16);     /* the load stays within the row */
+                    const loose t = *(const loose *)(x + from);
+                    for (int i = 0; i < PER16; i++) {
+                        e[h + i] = from + i;
+                        v[h + i] = from + i >= c + h ? D::get(t[i]) : -INFINITY;
+                    }
+                } else {
+                    for (int i = 0; i < PER16; i++) {
+                        e[h + i] = c + h + i;
+                        v[h + i] = c + h + i < p.E ? D::get(x[c + h + i]) : -INFINITY;
+                    }
+                }
+            }
+        };
+        float v[8];
+        uint32_t e[8];
+        float top = 0.0f, inv = 1.0f;
+        if (!sigmoid && (BIAS || !p.renorm)) {
+            top = -INFINITY;
+            for (uint32_t c = 0; c < p.E; c += 8) {
+                eight(c, v, e);
+                for (int i = 0; i < 8; i++) top = fmaxf(top, v[i]);
+            }
+            if (!(top > -INFINITY && top < INFINITY)) top = 0.0f;
+            float sum = 0.0f;
+            for (uint32_t c = 0; c < p.E; c += 8) {
+                eight(c, v, e);
+                for (int i = 0; i < 8; i++) sum += __builtin_amdgcn_exp2f((v[i] - top) * LOG2E);
+            }
+            inv = 1.0f / sum;
+        }
+        bool bad = false;
+        double a[8], b[8];
+        for (uint32_t c = 0; c < p.E; c += 8) {
+            eight(c, v, e);
+            for (int i = 0; i < 8; i++) {
+                bad |= sigmoid ? v[i] != v[i] : !(v[i] < INFINITY);
+                float k = v[i] + 0.0f;
+                if (BIAS) {
+                    k = sigmoid ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v[i] * -LOG2E))
+                                : __builtin_amdgcn_exp2f((v[i] - top) * LOG2E) * inv;
+                    k = v[i] > -INFINITY ? k + bias[e[i]] : -INFINITY;
+                }
+                b[i] = BIAS ? pack_approx(k, e[i]) : pack(k, e[i]);
+            }
+            sort8(b);
+            if (c == 0)
+                for (int i = 0; i < 8; i++) a[i] = b[i];
+            else
+                keep_list<8>(a, b);
+        }
+        int32_t id[8];
+        float xs[8], most = -INFINITY, sum = 0.0f;
+        for (int j = 0; j < 8; j++) {
+            const bool got = j < (int)p.K && key_of(a[j]) > -INFINITY && !bad;
+            id[j] = got ? (int32_t)(BIAS ? ~(uint32_t)__builtin_bit_cast(uint64_t, a[j]) : expert_of(a[j])) : -1;
+            xs[j] = got ? (BIAS ? D::get(x[id[j]]) : key_of(a[j])) : -INFINITY;
+            most = fmaxf(most, xs[j]);
+        }
+        bool again = false;
+        if (BIAS) {
+            const float slack = sigmoid ? 0x1p-20f : 0x1p-22f + 0x1p-17f * inv;
+            for (int j = 0; j < 7; j++) {
+                const float k0 = key_of(a[j]), k1 = key_of(a[j + 1]);
+                if (id[j] >= 0 && !(k0 - k1 > slack + 0x1p-22f * fabsf(k0)))
+                    again |= !(id[j + 1] >= 0 && xs[j] == xs[j + 1] && bias[id[j]] == bias[id[j + 1]] && k0 >= 0.0f);
+            }
+        }
+        /* the weights, as weight_of has them */
+        const float c = p.renorm ? (sigmoid ? fminf(most, 0.0f) : most) : sigmoid ? 0.0f : top;
+        for (int j = 0; j < 8; j++) {
+            float q = 0.0f;
+            if (id[j] >= 0) {
+                q = expf((sigmoid ? fminf(xs[j], 0.0f) : xs[j]) - c);
+                if (sigmoid) q /= 1.0f + expf(-fabsf(xs[j]));
+                else if (!p.renorm) q *= inv;
+            }
+            xs[j] = q;
+            sum += q;
+        }
+        for (int j = 0; j < 8; j++)
+            if (j < (int)p.K) {
+                float q = xs[j];
+                if (p.renorm && id[j] >= 0) q /= sum;
+                p.ids[row * p.K + j] = again ? UNDECIDED : id[j];
+                p.w[row * p.K + j] = bad ? NAN : p.scale * q;
+            }
+    }
+}
+
 __global__ void msim_route_nothing(RouteP p) { clear_load(p); }
 
 /* ------------------------------------------------------------------------ */
@@ -1044,8 +1164,16 @@ template <typename D> void launch_route(RouteP p, hipStream_t st)
     uint32_t glanes = std::max(1u, kl / g2);
     while ((size + glanes - 1) / glanes > 32) glanes *= 2;
     const uint32_t lanes = g2 * glanes;
+    const size_t sz = sizeof(typename D::raw);
+    if (p.G == 1 && p.E <= THREAD_EXPERTS && p.K <= (p.bias ? 7u : 8u) && p.rows >= 2048 * p.E) {
+        const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + 255) / 256, 4096);
+        p.vec = p.E * sz >= 16 ? 0 : 2;
+        if (p.bias) msim_route_threads<D, true><<<grid, 256, 0, st>>>(p);
+        else msim_route_threads<D, false><<<grid, 256, 0, st>>>(p);
+        launch_finish<D>(p, p.bias != nullptr, st);
+        return;
+    }
     if (p.K <= 16 && lanes <= 32) {
-        const size_t sz = sizeof(typename D::raw);
         p.size = size;
         p.lglanes = __builtin_ctz(glanes);
         p.part = (size + glanes - 1) / glanes;

@@ -315,6 +315,56 @@ def test_route_of_no_rows_and_given_outputs(T, M):
     assert got.load is None and T.equal(got.ids, want.ids)
 
 
+def many_rows(T, experts, dtype, seed, pad=0):
+    """More than 2,048 rows an expert, among them masked, tied, void and empty ones."""
+    rows = 2048 * experts + 77
+    x = logits_of(T, rows, experts, T.float32, seed, pad=pad).to(dtype) if not pad else logits_of(T, rows, experts, dtype, seed, pad=pad)
+    k = T.arange(rows, device=DEV) % 300
+    x[k == 3] = -np.inf
+    x[k == 5, ::2] = -np.inf
+    x[k == 7, experts // 2] = np.nan
+    x[k == 9, experts // 3] = np.inf
+    x[k == 11] = 0.25
+    x[k == 13] = T.finfo(dtype).min
+    x[k == 15] = -0.0
+    x[k == 17, 1:] = -np.inf
+    x[(k >= 20) & (k < 120)] = (x[(k >= 20) & (k < 120)] * 2).round()
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,k", [(1, 1), (3, 2), (5, 5), (8, 2), (8, 8), (13, 4), (16, 7), (31, 8), (32, 6)])
+def test_route_of_many_rows_of_few_experts(T, M, experts, k, score, dtype):
+    """Sampled rows against the plain implementation, and all against calls of fewer rows, which go another way."""
+    for pad, renorm, bias in ((0, True, False), (3, False, True), (0, True, True), (1, False, False)):
+        x = many_rows(T, experts, getattr(T, dtype), 14, pad)
+        b = None
+        if bias:
+            b = bias_of(T, experts, size=0.05)
+            b[0] = b[experts - 1]                  # equal keys where the logits are
+        how = dict(score=score, bias=b, renorm=renorm, scale=1.5)
+        r = M.route(x, k, **how)
+        few = [M.route(x[lo:lo + 2000], k, **how) for lo in range(0, x.shape[0], 2000)]
+        assert T.equal(r.ids, T.cat([f.ids for f in few]))
+        assert T.equal(r.load, T.stack([f.load for f in few]).sum(0).to(T.int32))
+        np.testing.assert_allclose(r.weights.cpu(), T.cat([f.weights for f in few]).cpu(), equal_nan=True,
+                                   rtol=2 * rtol_weights(x.cpu().double().numpy(), experts), atol=2.0 ** -125)
+        ids, w, _ = plain_route(x[:300], k, **how)
+        assert np.array_equal(r.ids[:300].cpu().numpy(), ids)
+        n = k if renorm else experts
+        np.testing.assert_allclose(r.weights[:300].cpu().numpy().astype(np.float64), w, equal_nan=True,
+                                   rtol=rtol_weights(x[:300].cpu().double().numpy(), n), atol=2.0 ** -125)
+
+
+def test_many_rows_tell_keys_apart_that_32_bits_do_not(T, M):
+    g = np.random.default_rng(21)
+    x = T.from_numpy(g.uniform(18.0, 24.0, (2048 * 8 + 5, 8)).astype(np.float32)).to(DEV)
+    r = M.route(x, 4, score="sigmoid", bias=T.zeros(8, device=DEV))
+    order = x.cpu().double().numpy()
+    assert np.array_equal(r.ids.cpu().numpy(), np.argsort(-order, axis=1, kind="stable")[:, :4])
+
+
 def test_route_is_deterministic(T, M):
     x = logits_of(T, 20000, 128, T.bfloat16, 11)
     a, b = M.route(x, 8, score="sigmoid"), M.route(x, 8, score="sigmoid")
