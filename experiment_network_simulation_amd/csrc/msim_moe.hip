@@ -537,7 +537,9 @@ __global__ void __launch_bounds__(256) msim_route_lists(RouteP p)
                     if (p.vec) {
                         for (int i = 0; i < 8; i++) k[i] += (*(const f32x4 *)&t[h + (i & 4)])[i & 3];
                     } else {
-                        for (int i = 0; i < 8; i++) k[i] += t[from[(h + i) / PER16] + i % PER16 - first];
+                        /* a load moved back begins before the lane's part: an index below zero, but not below lds_bias, for
+                         * first is at most VPL experts for each lane before this one */
+                        for (int i = 0; i < 8; i++) k[i] += t[(int32_t)(from[(h + i) / PER16] + i % PER16 - first)];
                     }
                     if (any_odd || !p.vec)
                         for (int i = 0; i < 8; i++) k[i] = v(h + i) > -INFINITY ? k[i] : -INFINITY;
