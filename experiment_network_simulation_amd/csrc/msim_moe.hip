@@ -376,7 +376,7 @@ template <typename D, int VPL> __global__ void __launch_bounds__(256) msim_route
  * 256 bf16).  Counted here, few workgroups add to the same few addresses, at
  * about 13 ns each (4,096 that counted by themselves took 41 us longer than
  * 1,024).  Every workgroup has `part` rows, at most FINISH_ROWS, whose undecided
- * ones its wavefronts share.  Bound by latency: 3.8 us at 10,007 rows, 11.6 at
+ * ones its wavefronts share.  Bound by latency: 3.1 us at 10,007 rows, 11.6 at
  * 131,072 of which about 4 are an undecided row's. */
 template <typename D, int VPL> __global__ void __launch_bounds__(512) msim_route_finish(RouteP p, uint64_t part)
 {
