@@ -454,7 +454,8 @@ int msim_lds_probe(void *dev_out, uint64_t out_bytes, uint32_t blocks, uint32_t 
  *  - groups > 1: the experts in groups of experts / groups consecutive ones; a
  *    group is worth the sum of its group_top (1 or 2) largest values of s + b
  *    among its experts still in (group_top 1 without bias: its largest logit);
- *    only the top_groups best groups with an expert still in stay;
+ *    only the top_groups best groups with an expert still in stay, of groups
+ *    worth the same (s(x) + s(-x) is 1 for every x) the lower;
  *  - the top_k largest keys are chosen, in descending order; slots that find no
  *    expert get id -1 and weight 0;
  *  - weight = scale * s, with renorm scale * s / (sum of the chosen s).
