@@ -1107,10 +1107,21 @@ __global__ void __launch_bounds__(256) msim_traffic_packets(TrafficP p)
 
 int fail(int code, const char *what) { msim_set_error(what); return code; }
 
-int launched(const char *what)
+/* Enqueues a kernel.  The result is the launch's own: an error that another call
+ * left pending on this thread neither fails it nor is taken from its owner. */
+template <typename... P, typename... A>
+hipError_t launch(void (*kernel)(P...), uint32_t grid, uint32_t block, size_t lds, hipStream_t st, A... args)
 {
-    const hipError_t e = hipGetLastError();
+    return [&](P... p) {
+        void *at[] = {&p...};
+        return hipLaunchKernel((const void *)kernel, dim3(grid), dim3(block), at, lds, st);
+    }(args...);
+}
+
+int launched(hipError_t e, const char *what)
+{
     if (e == hipSuccess) return MSIM_OK;
+    (void)hipGetLastError();               /* it is reported here */
     msim_set_error2(what, hipGetErrorString(e));
     return MSIM_E_HIP;
 }
@@ -1158,34 +1169,30 @@ uint32_t pow2(uint32_t v)
     return p;
 }
 
-template <typename D> void launch_finish(const RouteP &p, bool undecided, hipStream_t st)
+template <typename D> hipError_t launch_finish(const RouteP &p, bool undecided, hipStream_t st)
 {
-    if (!undecided && !p.load) return;
+    if (!undecided && !p.load) return hipSuccess;
     /* 256 workgroups, which is few enough to add to the same counts, while they can take the rows */
     const uint64_t part = std::min<uint64_t>(std::max<uint64_t>(256, (p.rows + 255) / 256), FINISH_ROWS);
     const uint32_t grid = (uint32_t)((p.rows + part - 1) / part);
     const uint32_t block = p.E <= 256 ? 512 : 256;            /* LDS: at most 32 KiB of keys */
     const size_t lds = undecided && p.G > 1 ? block / WAVE * p.E * sizeof(double) : 0;
-    if (p.E <= 256) msim_route_finish<D, 4><<<grid, block, lds, st>>>(p, part);
-    else msim_route_finish<D, 16><<<grid, block, lds, st>>>(p, part);
+    return launch(p.E <= 256 ? msim_route_finish<D, 4> : msim_route_finish<D, 16>, grid, block, lds, st, p, part);
 }
 
-template <typename D, int VPL, int LANES, int KL> void launch_lists(const RouteP &p, hipStream_t st)
+template <typename D, int VPL, int LANES, int KL> hipError_t launch_lists(const RouteP &p, hipStream_t st)
 {
     const uint32_t rows = 4 * WAVE / LANES;
     const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + rows - 1) / rows, 1024);
     const bool undecided = p.bias || p.gtop > 1;
-    if (p.bias) msim_route_lists<D, VPL, LANES, KL, true><<<grid, 256, 0, st>>>(p);
-    else msim_route_lists<D, VPL, LANES, KL, false><<<grid, 256, 0, st>>>(p);
-    if (grid > 1 || undecided) launch_finish<D>(p, undecided, st);
+    const hipError_t e = launch(p.bias ? msim_route_lists<D, VPL, LANES, KL, true> : msim_route_lists<D, VPL, LANES, KL, false>,
+                                grid, 256, 0, st, p);
+    return e == hipSuccess && (grid > 1 || undecided) ? launch_finish<D>(p, undecided, st) : e;
 }
 
-template <typename D> void launch_route(RouteP p, hipStream_t st)
+template <typename D> hipError_t launch_route(RouteP p, hipStream_t st)
 {
-    if (p.rows == 0) {
-        if (p.load) msim_route_nothing<<<1, 256, 0, st>>>(p);
-        return;
-    }
+    if (p.rows == 0) return p.load ? launch(msim_route_nothing, 1, 256, 0, st, p) : hipSuccess;
     /* lists: lanes for every group and every choice, at most 32 experts a lane */
     const uint32_t size = p.E / p.G, g2 = pow2(p.G), kl = p.K <= 8 ? 8 : 16;
     uint32_t glanes = std::max(1u, kl / g2);
@@ -1195,10 +1202,8 @@ template <typename D> void launch_route(RouteP p, hipStream_t st)
     if (p.G == 1 && p.E <= THREAD_EXPERTS && p.K <= (p.bias ? 7u : 8u) && p.rows >= 2048 * p.E) {
         const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + 255) / 256, 4096);
         p.vec = p.E * sz >= 16 ? 0 : 2;
-        if (p.bias) msim_route_threads<D, true><<<grid, 256, 0, st>>>(p);
-        else msim_route_threads<D, false><<<grid, 256, 0, st>>>(p);
-        launch_finish<D>(p, p.bias != nullptr, st);
-        return;
+        const hipError_t e = launch(p.bias ? msim_route_threads<D, true> : msim_route_threads<D, false>, grid, 256, 0, st, p);
+        return e == hipSuccess ? launch_finish<D>(p, p.bias != nullptr, st) : e;
     }
     if (p.K <= 16 && lanes <= 32) {
         p.size = size;
@@ -1207,54 +1212,46 @@ template <typename D> void launch_route(RouteP p, hipStream_t st)
         const uint32_t vpl = std::max(lanes == 8 ? 8u : lanes == 16 ? 16u : 32u, pow2(p.part));
         p.vec = p.part == vpl && p.part * glanes == size && (size * sz) % 16 == 0 && (p.stride * sz) % 16 == 0 &&
                 (uintptr_t)p.x % 16 == 0 ? 1 : p.E * sz >= 16 ? 0 : 2;
-        if (kl == 16 && lanes == 32) launch_lists<D, 32, 32, 16>(p, st);
-        else if (kl == 16 && vpl == 32) launch_lists<D, 32, 16, 16>(p, st);
-        else if (kl == 16) launch_lists<D, 16, 16, 16>(p, st);
-        else if (lanes == 32) launch_lists<D, 32, 32, 8>(p, st);
-        else if (lanes == 16 && vpl == 32) launch_lists<D, 32, 16, 8>(p, st);
-        else if (lanes == 16) launch_lists<D, 16, 16, 8>(p, st);
-        else if (vpl == 32) launch_lists<D, 32, 8, 8>(p, st);
-        else if (vpl == 16) launch_lists<D, 16, 8, 8>(p, st);
-        else launch_lists<D, 8, 8, 8>(p, st);
-        return;
+        if (kl == 16 && lanes == 32) return launch_lists<D, 32, 32, 16>(p, st);
+        if (kl == 16 && vpl == 32) return launch_lists<D, 32, 16, 16>(p, st);
+        if (kl == 16) return launch_lists<D, 16, 16, 16>(p, st);
+        if (lanes == 32) return launch_lists<D, 32, 32, 8>(p, st);
+        if (lanes == 16 && vpl == 32) return launch_lists<D, 32, 16, 8>(p, st);
+        if (lanes == 16) return launch_lists<D, 16, 16, 8>(p, st);
+        if (vpl == 32) return launch_lists<D, 32, 8, 8>(p, st);
+        if (vpl == 16) return launch_lists<D, 16, 8, 8>(p, st);
+        return launch_lists<D, 8, 8, 8>(p, st);
     }
     const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + 3) / 4, 2048);
     const size_t lds = p.G > 1 ? 4 * p.E * sizeof(double) : 0;
-    if (p.E <= 256) msim_route_rows<D, 4><<<grid, 256, lds, st>>>(p);
-    else msim_route_rows<D, 16><<<grid, 256, lds, st>>>(p);
-    launch_finish<D>(p, false, st);
+    const hipError_t e = launch(p.E <= 256 ? msim_route_rows<D, 4> : msim_route_rows<D, 16>, grid, 256, lds, st, p);
+    return e == hipSuccess ? launch_finish<D>(p, false, st) : e;
 }
 
-template <typename D> void launch_back(const BackP &p, hipStream_t st)
+template <typename D> hipError_t launch_back(const BackP &p, hipStream_t st)
 {
     /* few rows: fewer of them a wavefront, and more wavefronts */
     const uint32_t lanes = p.K <= 8 && p.rows > 16384 ? 8 : p.K <= 16 && p.rows > 4096 ? 16 : 32;
     const uint64_t rows = 4 * WAVE / lanes;
     const uint32_t grid = (uint32_t)std::min<uint64_t>((p.rows + rows - 1) / rows, 2048);
-    if (lanes == 8) msim_route_back<D, 8><<<grid, 256, 0, st>>>(p);
-    else if (lanes == 16) msim_route_back<D, 16><<<grid, 256, 0, st>>>(p);
-    else msim_route_back<D, 32><<<grid, 256, 0, st>>>(p);
+    return launch(lanes == 8 ? msim_route_back<D, 8> : lanes == 16 ? msim_route_back<D, 16> : msim_route_back<D, 32>, grid, 256,
+                  0, st, p);
 }
 
-template <typename D> void launch_dropout(const DropP &d, hipStream_t st)
+template <typename D> hipError_t launch_dropout(const DropP &d, hipStream_t st)
 {
     constexpr uint64_t per = 16 / sizeof(typename D::raw);
     const uint64_t n = d.rows * d.cols;
-    if (!d.per_row && (d.rows == 1 || (d.xs == d.cols && d.ys == d.cols)) && d.limit >> 32 == 0) {
-        msim_dropout_flat<D><<<(uint32_t)std::min<uint64_t>((n + 256 * per - 1) / (256 * per), 1u << 16), 256, 0, st>>>(d);
-        return;
-    }
+    if (!d.per_row && (d.rows == 1 || (d.xs == d.cols && d.ys == d.cols)) && d.limit >> 32 == 0)
+        return launch(msim_dropout_flat<D>, (uint32_t)std::min<uint64_t>((n + 256 * per - 1) / (256 * per), 1u << 16), 256, 0,
+                      st, d);
     const uint64_t turns = (d.cols + (d.cols >= per ? per : 2) - 1) / (d.cols >= per ? per : 2);
     const uint32_t lwide = turns >= 256 ? 8 : __builtin_ctz(pow2((uint32_t)turns));
     const uint64_t rows = 256 >> lwide;
     const uint32_t grid = (uint32_t)std::min<uint64_t>((d.rows + rows - 1) / rows, 1u << 16);
-    if (d.cols >= per) {
-        if (d.per_row) msim_dropout_rows<D, per, true><<<grid, 256, 0, st>>>(d, lwide);
-        else msim_dropout_rows<D, per, false><<<grid, 256, 0, st>>>(d, lwide);
-    } else {
-        if (d.per_row) msim_dropout_rows<D, 2, true><<<grid, 256, 0, st>>>(d, lwide);
-        else msim_dropout_rows<D, 2, false><<<grid, 256, 0, st>>>(d, lwide);
-    }
+    if (d.cols >= per)
+        return launch(d.per_row ? msim_dropout_rows<D, per, true> : msim_dropout_rows<D, per, false>, grid, 256, 0, st, d, lwide);
+    return launch(d.per_row ? msim_dropout_rows<D, 2, true> : msim_dropout_rows<D, 2, false>, grid, 256, 0, st, d, lwide);
 }
 
 } // namespace
@@ -1269,10 +1266,9 @@ extern "C" int msim_route(const msim_route_spec *s, const void *logits, const fl
                 s->top_groups, s->group_top, s->renorm, s->score == MSIM_SCORE_SIGMOID, s->scale, 0, 0, 0, 0};
     if (p.TG == p.G) p.G = p.TG = p.gtop = 1;       /* every group stays */
     hipStream_t st = (hipStream_t)hip_stream;
-    if (s->dtype == MSIM_F32) launch_route<F32>(p, st);
-    else if (s->dtype == MSIM_F16) launch_route<F16>(p, st);
-    else launch_route<BF16>(p, st);
-    return launched("route launch");
+    const hipError_t e = s->dtype == MSIM_F32 ? launch_route<F32>(p, st)
+        : s->dtype == MSIM_F16 ? launch_route<F16>(p, st) : launch_route<BF16>(p, st);
+    return launched(e, "route launch");
 }
 
 extern "C" int msim_route_backward(const msim_route_spec *s, const void *logits, const int32_t *ids,
@@ -1287,10 +1283,9 @@ extern "C" int msim_route_backward(const msim_route_spec *s, const void *logits,
     const BackP p = {logits, ids, grad, grad_logits, s->rows, s->row_stride, grad_stride, s->experts, s->top_k,
                      s->renorm, s->score == MSIM_SCORE_SIGMOID, s->scale};
     hipStream_t st = (hipStream_t)hip_stream;
-    if (s->dtype == MSIM_F32) launch_back<F32>(p, st);
-    else if (s->dtype == MSIM_F16) launch_back<F16>(p, st);
-    else launch_back<BF16>(p, st);
-    return launched("route backward launch");
+    const hipError_t e = s->dtype == MSIM_F32 ? launch_back<F32>(p, st)
+        : s->dtype == MSIM_F16 ? launch_back<F16>(p, st) : launch_back<BF16>(p, st);
+    return launched(e, "route backward launch");
 }
 
 extern "C" int msim_dropout(uint32_t dtype, const void *x, void *y, uint64_t rows, uint64_t cols, uint64_t x_stride,
@@ -1309,10 +1304,9 @@ extern "C" int msim_dropout(uint32_t dtype, const void *x, void *y, uint64_t row
         return fail(MSIM_E_LIMIT, "dropout: more than 2^44 elements");
     d.scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.0f;
     hipStream_t st = (hipStream_t)hip_stream;
-    if (dtype == MSIM_F32) launch_dropout<F32>(d, st);
-    else if (dtype == MSIM_F16) launch_dropout<F16>(d, st);
-    else launch_dropout<BF16>(d, st);
-    return launched("dropout launch");
+    const hipError_t e = dtype == MSIM_F32 ? launch_dropout<F32>(d, st)
+        : dtype == MSIM_F16 ? launch_dropout<F16>(d, st) : launch_dropout<BF16>(d, st);
+    return launched(e, "dropout launch");
 }
 
 extern "C" int msim_traffic(const msim_traffic_spec *s, const int32_t *ids, const int64_t *token_off,
@@ -1346,14 +1340,12 @@ extern "C" int msim_traffic(const msim_traffic_spec *s, const int32_t *ids, cons
     p.parts = std::max<uint64_t>(1, std::min((s->rows / s->n_seg) / 4096, 1024 / s->n_seg));
     const uint32_t grid = (uint32_t)std::min<uint64_t>(s->n_seg * p.parts, 1u << 20);
     const uint32_t every = (uint32_t)std::min<uint64_t>((s->n_seg * s->hosts + 255) / 256, 4096);
-    if (p.parts > 1) msim_traffic_clear<<<every, 256, 0, (hipStream_t)hip_stream>>>(p);
     const size_t lds = 4 * s->hosts;
     hipStream_t st = (hipStream_t)hip_stream;
-    if (p.K <= 2) msim_traffic_segments<2><<<grid, block, lds, st>>>(p);
-    else if (p.K <= 4) msim_traffic_segments<4><<<grid, block, lds, st>>>(p);
-    else if (p.K <= 8) msim_traffic_segments<8><<<grid, block, lds, st>>>(p);
-    else if (p.K <= 16) msim_traffic_segments<16><<<grid, block, lds, st>>>(p);
-    else msim_traffic_segments<32><<<grid, block, lds, st>>>(p);
-    if (p.parts > 1) msim_traffic_packets<<<every, 256, 0, st>>>(p);
-    return launched("traffic launch");
+    void (*const segments)(TrafficP) = p.K <= 2 ? msim_traffic_segments<2> : p.K <= 4 ? msim_traffic_segments<4>
+        : p.K <= 8 ? msim_traffic_segments<8> : p.K <= 16 ? msim_traffic_segments<16> : msim_traffic_segments<32>;
+    hipError_t e = p.parts > 1 ? launch(msim_traffic_clear, every, 256, 0, st, p) : hipSuccess;
+    if (e == hipSuccess) e = launch(segments, grid, block, lds, st, p);
+    if (e == hipSuccess && p.parts > 1) e = launch(msim_traffic_packets, every, 256, 0, st, p);
+    return launched(e, "traffic launch");
 }

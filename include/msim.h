@@ -422,8 +422,11 @@ int msim_lds_probe(void *dev_out, uint64_t out_bytes, uint32_t blocks, uint32_t 
  * return at once; they allocate nothing, keep nothing between calls and may be
  * captured into a graph.  The device that holds the arrays must be current.
  * Calls on different streams may overlap when their outputs do not.  On error
- * nothing is launched, the return code says why (MSIM_E_ARG, MSIM_E_LIMIT,
- * MSIM_E_HIP) and msim_last_error(NULL) gives the message on the same thread.
+ * the return code says why and msim_last_error(NULL) gives the message on the
+ * same thread: MSIM_E_ARG and MSIM_E_LIMIT, nothing was launched; MSIM_E_HIP, a
+ * launch was refused, nothing was launched after it, and the outputs are
+ * undefined.  HIP errors of other calls that are pending on the thread change
+ * nothing and stay pending.
  */
 
 /* element types of logits, gradients and dropout's tensors */
