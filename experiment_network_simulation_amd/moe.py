@@ -13,9 +13,12 @@ every value is computed by the HIP library.
 All tensors are on one GPU, whichever is current.  A call enqueues on `stream`
 (a torch stream or a raw handle; default: the current stream of the tensors'
 device) and returns; results are allocated on that stream unless given as
-`out`.  Bad arguments raise ValueError or TypeError here, MsimError from the
-library; nothing is launched then.  Results carry no autograd history: gradients
-are calls of their own.
+`out`.  The caller orders the streams: a given `stream` has to wait for what made
+the inputs, and what reads the results for `stream`; inputs and `out` may be
+dropped at once, their memory stays until `stream` is past the call.  `out` must
+not overlap an input (dropout's may be the input itself).  Bad arguments raise
+ValueError or TypeError here, MsimError from the library; nothing is launched
+then.  Results carry no autograd history: gradients are calls of their own.
 """
 
 from __future__ import annotations
@@ -88,15 +91,22 @@ def _range(value, name: str, lo: int, hi: int) -> int:
 
 class _There:
     """Makes the tensors' device and the given stream current, so that results
-    are allocated there; its value is the stream's handle."""
+    are allocated there; its value is the stream's handle.  On a stream that is
+    given the tensors are recorded: the allocator does not hand their memory out
+    again before the stream is past this point."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, tensors):
+        given = stream is not None
         if stream is None:
             stream = torch.cuda.current_stream(device)
         elif isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        if given:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
         self.ptr = stream.cuda_stream
         self._ctx = torch.cuda.stream(stream)
 
@@ -108,13 +118,13 @@ class _There:
         return self._ctx.__exit__(*exc)
 
 
-def _run(device, stream, call):
-    """call(handle of the stream), with device and stream current.  Where they are
-    already, nothing is switched: torch's context managers cost as much as the
-    call."""
+def _run(device, stream, call, *tensors):
+    """call(handle of the stream), with device and stream current; tensors: those
+    the call is given, or None.  Where device and stream are current already,
+    nothing is switched: torch's context managers cost as much as the call."""
     if stream is None and device.index == torch._C._cuda_getDevice():
         return call(torch._C._cuda_getCurrentRawStream(device.index))
-    with _There(device, stream) as handle:
+    with _There(device, stream, tensors) as handle:
         return call(handle)
 
 
@@ -167,7 +177,7 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Opt
                                         r.weights.data_ptr(), _p(r.load), on))
         return r
 
-    return _run(dev, stream, call)
+    return _run(dev, stream, call, logits, bias, *(() if out is None else (out.ids, out.weights, out.load)))
 
 
 def route_backward(logits: torch.Tensor, ids: torch.Tensor, grad: torch.Tensor, *, score: str = "softmax",
@@ -193,7 +203,7 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, grad: torch.Tensor, 
                                                  dx.data_ptr(), out_stride, on))
         return dx
 
-    return _run(dev, stream, call)
+    return _run(dev, stream, call, logits, ids, grad, out)
 
 
 def _out_rows(out, name: str, like) -> int:
@@ -221,7 +231,7 @@ def dropout(x: torch.Tensor, p: float, seed: int, *, offset: int = 0, per_row: b
                                           seed, offset, 1 if per_row else 0, on))
         return y
 
-    return _run(dev, stream, call)
+    return _run(dev, stream, call, x, out)
 
 
 def dropout_backward(grad: torch.Tensor, p: float, seed: int, *, offset: int = 0, per_row: bool = False,
@@ -274,4 +284,4 @@ def traffic(ids: torch.Tensor, token_off: torch.Tensor, home: torch.Tensor, plac
                                           place.data_ptr(), packets.data_ptr(), on))
         return packets
 
-    return _run(dev, stream, call)
+    return _run(dev, stream, call, ids, token_off, home, place, out)
