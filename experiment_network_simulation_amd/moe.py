@@ -28,7 +28,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .sim import ABI_VERSION, MsimError, RouteSpec, TrafficSpec, load_library
+from .sim import ABI_VERSION, MAX_TRAFFIC_HOSTS, MsimError, RouteSpec, TrafficSpec, load_library
 
 __all__ = ["Routing", "route", "route_backward", "dropout", "dropout_backward", "traffic"]
 
@@ -279,6 +279,8 @@ def traffic(ids: torch.Tensor, token_off: torch.Tensor, home: torch.Tensor, plac
         _need(out, "out", torch.int32, dev, (n_seg, h))
 
     def call(on):
+        if h > MAX_TRAFFIC_HOSTS:          # refused before memory for such a table is asked for
+            _call(load_library().msim_traffic(C.byref(spec), None, None, None, None, None, on))
         packets = ids.new_empty((n_seg, h)) if out is None else out
         _call(load_library().msim_traffic(C.byref(spec), ids.data_ptr(), token_off.data_ptr(), home.data_ptr(),
                                           place.data_ptr(), packets.data_ptr(), on))

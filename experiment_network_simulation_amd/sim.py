@@ -17,6 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmsim.so")
 
 ABI_VERSION = 5
+MAX_TRAFFIC_HOSTS = 16384                # MSIM_MAX_TRAFFIC_HOSTS
 OK, S_INCOMPLETE, S_DEADLOCK = 0, 1, 2
 E_INVALID_SPEC, E_UNROUTABLE, E_WORKSPACE, E_HIP, E_ARG, E_STATE, E_LIMIT = -1, -2, -3, -4, -5, -6, -7
 EXP_DONE, EXP_INCOMPLETE, EXP_DEADLOCK = 0, 1, 2
