@@ -83,8 +83,11 @@ def _need_rows(t, name: str):
 def _range(value, name: str, lo: int, hi: int) -> int:
     if type(value) is int and lo <= value <= hi:
         return value
-    v = int(value)
-    if v != value or not lo <= v <= hi:
+    try:
+        v = int(value)
+    except OverflowError:                  # an infinity
+        v = None
+    if v is None or v != value or not lo <= v <= hi:
         raise ValueError(f"{name} must be a whole number in {lo} .. {hi}, not {value!r}")
     return v
 

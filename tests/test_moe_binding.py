@@ -23,3 +23,12 @@ def test_traffic_refuses_hosts_before_it_asks_for_their_memory(M, monkeypatch, s
     with pytest.raises(MsimError, match="HOSTS"):
         M.traffic(i32(4, 2), gpu(segs + 1, dtype=torch.int64), i32(segs), i32(8), hosts)
     assert not asked
+
+
+def test_numbers_that_are_not_whole_are_refused(M):
+    x = gpu(4, 8)
+    for bad in (float("inf"), -float("inf"), float("nan"), 2.5, "2", 1 << 70):
+        for call in (lambda: M.route(x, bad), lambda: M.route(x, 2, groups=bad), lambda: M.dropout(x, 0.5, bad),
+                     lambda: M.dropout(x, 0.5, 1, offset=bad)):
+            with pytest.raises(ValueError):
+                call()
