@@ -18,7 +18,8 @@ the inputs, and what reads the results for `stream`; inputs and `out` may be
 dropped at once, their memory stays until `stream` is past the call.  `out` must
 not overlap an input (dropout's may be the input itself).  Bad arguments raise
 ValueError or TypeError here, MsimError from the library; nothing is launched
-then.  Results carry no autograd history: gradients are calls of their own.
+then.  Results carry no autograd history: gradients are calls of their own; what
+is written to `out` counts as a change in place.
 """
 
 from __future__ import annotations
@@ -131,6 +132,12 @@ def _run(device, stream, call, *tensors):
         return call(handle)
 
 
+def _changed(*tensors):
+    """Tells autograd that the library wrote to them: where one was kept for a
+    backward pass, that raises instead of using the new values."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -178,6 +185,8 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: Opt
                         new(experts, dtype=torch.int32))
         _call(load_library().msim_route(C.byref(spec), logits.data_ptr(), _p(bias), r.ids.data_ptr(),
                                         r.weights.data_ptr(), _p(r.load), on))
+        if out is not None:
+            _changed(out.ids, out.weights, out.load)
         return r
 
     return _run(dev, stream, call, logits, bias, *(() if out is None else (out.ids, out.weights, out.load)))
@@ -204,6 +213,8 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, grad: torch.Tensor, 
         dx = logits.new_empty((rows, experts)) if out is None else out
         _call(load_library().msim_route_backward(C.byref(spec), logits.data_ptr(), ids.data_ptr(), grad.data_ptr(),
                                                  dx.data_ptr(), out_stride, on))
+        if out is not None:
+            _changed(out)
         return dx
 
     return _run(dev, stream, call, logits, ids, grad, out)
@@ -232,6 +243,8 @@ def dropout(x: torch.Tensor, p: float, seed: int, *, offset: int = 0, per_row: b
         y = x.new_empty((rows, cols)) if out is None else out
         _call(load_library().msim_dropout(_DTYPES[x.dtype], x.data_ptr(), y.data_ptr(), rows, cols, xs, ys, float(p),
                                           seed, offset, 1 if per_row else 0, on))
+        if out is not None:
+            _changed(out)
         return y
 
     return _run(dev, stream, call, x, out)
@@ -287,6 +300,8 @@ def traffic(ids: torch.Tensor, token_off: torch.Tensor, home: torch.Tensor, plac
         packets = ids.new_empty((n_seg, h)) if out is None else out
         _call(load_library().msim_traffic(C.byref(spec), ids.data_ptr(), token_off.data_ptr(), home.data_ptr(),
                                           place.data_ptr(), packets.data_ptr(), on))
+        if out is not None:
+            _changed(out)
         return packets
 
     return _run(dev, stream, call, ids, token_off, home, place, out)
