@@ -471,6 +471,9 @@ def route_designs(logits, token_off: Sequence[int], home: Sequence[int], designs
     token_off[s + 1] - 1, lie on host home[s].  evaluate(probes) -> ticks."""
     import torch
     from . import moe
+    for d in designs:
+        if np.shape(d.place) != (logits.shape[1],):
+            raise ValueError(f"place must name a host for each of the {logits.shape[1]} experts (-1: none)")
     dev = logits.device
     hosts = int(topo.hosts().size)
     off = torch.as_tensor(np.asarray(token_off, np.int64)).to(dev)
