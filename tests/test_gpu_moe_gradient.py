@@ -1,4 +1,6 @@
-"""The router's gradient against its formula in 64 bits, element by element.
+"""The router's gradient against its formula in 64 bits, element by element, in
+every variant: 8, 16 and 32 lanes a row (more than 16,384 rows, more than 4,096,
+and fewer), chosen logits only and all of them.
 
 Bound of an element, u = 2^-24, K choices, E experts, A the largest argument of
 an exponential (at most 104: below e^-104 float32 has nothing):
@@ -217,3 +219,25 @@ def test_gradient(M, shape, renorm, score, dtype):
             odd_rows(x, ids, score, rows - 10)
         dx = M.route_backward(x, ids, g, score=score, renorm=renorm, scale=2.5)
         assert dx.dtype == x.dtype and off(dx, x, ids, g, score, renorm, 2.5) <= 1, pad
+
+
+LARGE = [(61, 1), (61, 8), (61, 9), (161, 8), (161, 16), (256, 8), (257, 5), (257, 9), (1000, 8), (1000, 16), (1000, 20), (9, 9)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("rows", [4097, 16385])
+def test_gradient_of_many_rows(M, rows, renorm, score, dtype):
+    """The variants of 16 and of 8 lanes a row; odd rows at both ends, the last of a workgroup that is not full."""
+    for n, (experts, k) in enumerate(LARGE):
+        x, ids, g = inputs(rows, experts, k, getattr(torch, dtype), 40 + n, (0, 3, 8, 1)[n % 4], "cuda:0")
+        odd_rows(x, ids, score, 0)
+        odd_rows(x, ids, score, rows // 2)
+        odd_rows(x, ids, score, rows - 10)
+        dx = M.route_backward(x, ids, g, score=score, renorm=renorm, scale=0.5)
+        assert off(dx, x, ids, g, score, renorm, 0.5) <= 1, (experts, k)
+        wide = torch.full((rows, experts + 7), 9.0, dtype=x.dtype, device=x.device)
+        out = M.route_backward(x, ids, g, score=score, renorm=renorm, scale=0.5, out=wide[:, 3:3 + experts])
+        assert torch.equal(out, dx) and bool((wide[:, :3] == 9).all()) and bool((wide[:, 3 + experts:] == 9).all()), (experts, k)
