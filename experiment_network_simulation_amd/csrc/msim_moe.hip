@@ -243,19 +243,21 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_wave_barrier();
 }
 
-/* A score as n + z, of which z alone is rounded: a sigmoid is e / (1 + e) with
- * e = e^-|x| for x < 0 and 1 less that for x > 0.  Sums of two scores and their
- * biases are equal as real numbers where the terms of z are the same or cancel
- * and the rest is equal (s(x) + s(-x) and 1; the same logits and biases in
- * another order); z summed by itself, and n and the biases by themselves, are
- * then equal too, and the tie goes to the lower group.  Scores added one by one
- * gave 1 - 2^-53 or 1 + 2^-52 for 14 % of such pairs. */
-struct Score { double z, n; };
-__device__ __forceinline__ Score score_of(double x, bool sigmoid, float top, double inv)
+/* A score is n + z, z alone being rounded: a softmax's has n = 0, a sigmoid's z =
+ * e / (1 + e), e = e^-|x|, for x < 0, and n = 1 with that negative for x > 0.
+ * Sums of two scores and their biases are equal as real numbers where the terms
+ * of z are the same or cancel and the rest is equal (s(x) + s(-x) and 1; the same
+ * logits and biases in another order); z summed by itself, and n and the biases by
+ * themselves, are then equal too, and the tie goes to the lower group.  Scores
+ * added one by one gave 1 - 2^-53 or 1 + 2^-52 for 14 % of such pairs.  Takes n
+ * off z: n is 1/2 at x = 0. */
+__device__ __forceinline__ double exact_part(double &z)
 {
-    if (!sigmoid) return {exp(x - top) * inv, 0.0};
-    const double e = exp(-fabs(x)), q = e / (1.0 + e);
-    return {x < 0 ? q : x > 0 ? -q : 0.0, x < 0 ? 0.0 : x > 0 ? 1.0 : 0.5};
+    if (fabs(z) == 0.5) {
+        z = 0.0;
+        return 0.5;
+    }
+    return __builtin_signbit(z) ? 1.0 : 0.0;
 }
 
 /* One row by one wavefront, keys in 64 bits.  Lane l has experts l, l + 64, ...:
@@ -281,11 +283,13 @@ template <typename D, int VPL> __device__ void route_row(const RouteP &p, uint64
     float xs = -INFINITY;
     double inv = 1.0;
     if (!is_void && in) {
-        if (p.bias || (!p.sigmoid && !p.renorm)) {
+        const bool sums = p.G > 1 && p.gtop > 1;
+        double z[VPL];
+        if (p.bias || sums || (!p.sigmoid && !p.renorm)) {
             double sum = 0;
             for (int i = 0; i < VPL; i++) {
-                key[i] = exp(p.sigmoid ? -fabs((double)v[i]) : (double)v[i] - top);
-                sum += key[i];
+                z[i] = exp(p.sigmoid ? -fabs((double)v[i]) : (double)v[i] - top);
+                sum += z[i];
             }
             if (!p.sigmoid) {
                 inv = 1.0 / fold<WAVE>(sum, Sum());
@@ -294,10 +298,14 @@ template <typename D, int VPL> __device__ void route_row(const RouteP &p, uint64
         for (int i = 0; i < VPL; i++) {
             const uint32_t e = i * WAVE + lane;
             double k = v[i];
-            if (p.bias) {
-                const float b = e < p.E ? p.bias[e] : 0.0f;
-                k = p.sigmoid ? (v[i] >= 0 ? 1.0 : key[i]) / (1.0 + key[i]) : key[i] * inv;
-                k = v[i] > -INFINITY && b > -INFINITY ? k + b : -INFINITY;
+            if (p.bias || sums) {
+                z[i] = p.sigmoid ? z[i] / (1.0 + z[i]) : z[i] * inv;
+                if (p.bias) {
+                    const float b = e < p.E ? p.bias[e] : 0.0f;
+                    k = p.sigmoid && v[i] > 0 ? 1.0 - z[i] : z[i];
+                    k = v[i] > -INFINITY && b > -INFINITY ? k + b : -INFINITY;
+                }
+                if (p.sigmoid && v[i] > 0) z[i] = -z[i];
             }
             key[i] = k;
         }
@@ -307,26 +315,28 @@ template <typename D, int VPL> __device__ void route_row(const RouteP &p, uint64
             for (int i = 0; i < VPL; i++)
                 if (i * WAVE + lane < p.E) lds[i * WAVE + lane] = key[i];
             wave_sync();
-            double worth = -INFINITY;
+            double worth = -INFINITY, c = -INFINITY;
+            uint32_t ea = 0, ec = 0;
             if (lane < p.G) {
-                double a = -INFINITY, c = -INFINITY;
-                uint32_t ea = 0, ec = 0;
                 _Pragma("unroll 4") for (uint32_t e = lane * size; e < (lane + 1) * size; e++) {
                     const double k = lds[e];
-                    const bool first = k > a, second = k > c;
+                    const bool first = k > worth, second = k > c;
                     ec = first ? ea : second ? e : ec;
-                    c = fmax(c, fmin(a, k));
+                    c = fmax(c, fmin(worth, k));
                     ea = first ? e : ea;
-                    a = fmax(a, k);
+                    worth = fmax(worth, k);
                 }
-                worth = a;
-                if (p.gtop > 1 && a > -INFINITY) {
-                    const bool two = c > -INFINITY;
-                    const Score sa = score_of(p.bias ? (double)D::get(x[ea]) : a, p.sigmoid, top, inv);
-                    const Score sc = score_of(two ? p.bias ? (double)D::get(x[ec]) : c : -INFINITY, p.sigmoid, top, inv);
-                    double rest = sa.n + sc.n;
-                    if (p.bias) rest += (double)p.bias[ea] + (two ? (double)p.bias[ec] : 0.0);
-                    worth = sa.z + sc.z + rest;
+            }
+            if (sums) {
+                wave_sync();
+                for (int i = 0; i < VPL; i++)
+                    if (i * WAVE + lane < p.E) lds[i * WAVE + lane] = z[i];
+                wave_sync();
+                if (worth > -INFINITY) {
+                    double za = lds[ea], zc = c > -INFINITY ? lds[ec] : 0.0;
+                    double rest = p.sigmoid ? exact_part(za) + exact_part(zc) : 0.0;
+                    if (p.bias) rest += (double)p.bias[ea] + (c > -INFINITY ? (double)p.bias[ec] : 0.0);
+                    worth = za + zc + rest;
                 }
             }
             wave_sync();
