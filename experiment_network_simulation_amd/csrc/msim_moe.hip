@@ -220,7 +220,11 @@ template <int KL> __device__ __forceinline__ void keep_list(double *a, const dou
 /* The weight of the slot this lane has (got: it has one), logit xs, over the
  * row's N lanes.  s = e^min(x,0) / (1 + e^-|x|) for a sigmoid, e^(x - top) inv
  * for a softmax; renormalised, the exponentials are taken relative to the
- * largest chosen one, so that no sum vanishes. */
+ * largest chosen one, so that no sum vanishes.  All in 32 bits: inv comes from
+ * v_exp_f32 of (x - top) times a rounded log2(e), off by 2.4 2^-24 |x - top|
+ * relative where expf of the difference is off by 2^-24 |x - top|.  Terms count by
+ * their size, so of 1,024 experts inv is off by at most 2^-24 x 17 from there, 2
+ * from the function and 36 from the additions. */
 template <int N> __device__ __forceinline__ float weight_of(const RouteP &p, float xs, bool got, float top, float inv)
 {
     const float t = p.sigmoid ? fminf(xs, 0.0f) : xs;
@@ -394,7 +398,12 @@ __device__ __forceinline__ void clear_load(const RouteP &p)
         for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) p.load[e] = 0;
 }
 
-/* A wavefront a row: more than 16 choices, or more than 32 groups. */
+/* A wavefront a row: more than 16 choices, or more than 32 groups.  Bound by the
+ * latency of the rounds, each an exchange over all lanes: 131,072 x 256 bf16 take
+ * 335 us with 17 choices and 384 with 20, where msim_route_lists takes 62 for 16;
+ * 337 with 8 choices in 64 groups (190 in 32, there); 8 rows 11 us.  A lane's
+ * registers hold no longer lists, and 64 groups have no lanes of their own for a
+ * row's half-wavefront. */
 template <typename D, int VPL> __global__ void __launch_bounds__(256) msim_route_rows(RouteP p)
 {
     extern __shared__ double keys[];
@@ -411,7 +420,7 @@ template <typename D, int VPL> __global__ void __launch_bounds__(256) msim_route
  * 256 bf16).  Counted here, few workgroups add to the same few addresses, at
  * about 13 ns each (4,096 that counted by themselves took 41 us longer than
  * 1,024).  Every workgroup has `part` rows, at most FINISH_ROWS, whose undecided
- * ones its wavefronts share.  Bound by latency: 3.1 us at 10,007 rows, 11.6 at
+ * ones its wavefronts share.  Bound by latency: 3.0 us at 10,007 rows, 12.3 at
  * 131,072 of which about 4 are an undecided row's. */
 template <typename D, int VPL> __global__ void __launch_bounds__(512) msim_route_finish(RouteP p, uint64_t part)
 {
@@ -459,9 +468,13 @@ template <typename D, int VPL> __global__ void __launch_bounds__(512) msim_route
  * Without bias keys are the logits and the choice is exact.  With bias (and for
  * sums of two scores) the keys here are 32-bit approximations with a known
  * error, and a row whose choice depends on a difference within twice that error
- * is left to msim_route_finish, which compares in 64 bits (1 row in 1,000 of
- * sigmoids with a bias).  Errors: v_exp_f32 and v_rcp_f32 are off by 2^-23
- * relative.  A sigmoid is off by less than 2^-22: its exponential's argument by
+ * is left to msim_route_finish, which compares in 64 bits.  Of normal logits with
+ * sigmoids and a normal bias that is 1 row in 1,000, with one bias for all or in
+ * steps more: at 256 experts and top 8 bf16 9 % and 4 %, for the last chosen and
+ * the first left out often have the same logit and bias, and f32 0.2 %.  131,072 x
+ * 256 bf16 take 45 us with a normal bias, 66 in steps, 81 with one for all, and 387
+ * where logits on a coarse grid leave nearly all rows undecided.  Errors:
+ * v_exp_f32 and v_rcp_f32 are off by 2^-23 relative.  A sigmoid is off by less than 2^-22: its exponential's argument by
  * 1.4 2^-24 |x|, and |x| s (1 - s) < 0.23.  A softmax score is off by less than
  * 2^-24 (0.9 + 54 s): the argument by 2.4 2^-24 |x - top|, and |x - top| e^(x -
  * top) < 0.37 in the score and 4.5 of the sum for 1,024 experts; the sum by 36
@@ -814,7 +827,11 @@ struct BackP {
  * a time, and leave it in 16-byte stores.  What was put there is taken out again
  * afterwards, so the rest stays zero.  Bound by the memory: 25 us at 131,072 x
  * 256 bf16, which writes 67 MB and, a chosen logit bringing its whole cache line,
- * reads about as much (5.4 TB/s).  2,048 workgroups: 1,280 take 29 us, 4,096 27. */
+ * reads about as much (5.4 TB/s).  2,048 workgroups: 1,280 take 29 us, 4,096 27.
+ * With all experts (softmax, not renormalised) the row is read three times, its
+ * exponentials taken twice: 39 us at 131,072 x 256 bf16 where the memory allows 27,
+ * 71 f32.  Scores as weight_of has them, in 32 bits; a lane's part of a
+ * denominator is up to 128 additions long. */
 template <typename D, int LANES> __global__ void __launch_bounds__(256) msim_route_back(BackP p)
 {
     constexpr int PER = 16 / sizeof(typename D::raw), ROWS = WAVE / LANES;
@@ -1038,7 +1055,11 @@ __device__ __forceinline__ uint32_t packets_of(const TrafficP &p, uint32_t count
  * 128 hosts, 8 choices: 11 us for 21 MB; 1,024 hosts with 128 tokens: 5.5 for 8.
  * Few long segments are cut into `parts`, whose counts meet in the table, cleared
  * before and turned into packets after: 8 segments of 131,072 tokens and 128
- * hosts 227 -> 16 us, 64 of 16,384 32 -> 16. */
+ * hosts 227 -> 16 us, 64 of 16,384 32 -> 16.  All segments in the same number, by
+ * their mean length: a long one among many short ones is one workgroup's work (one
+ * of 1,048,576 tokens among 1,024 of 128: 3.9 ms, where 1,025 of the same sum take
+ * 14 us).  More than 16 choices: 64 registers spill, 166 us for the 64 x 128
+ * segments of 128 tokens that take 13 with 8 choices and 24 with 16. */
 template <int KMAX> __global__ void __launch_bounds__(1024) msim_traffic_segments(TrafficP p)
 {
     extern __shared__ uint32_t count[];
@@ -1346,7 +1367,8 @@ extern "C" int msim_traffic(const msim_traffic_spec *s, const int32_t *ids, cons
     const uint64_t most = std::max<uint64_t>(64, 524288 / s->n_seg);
     uint32_t block = 64;
     while (block < 1024 && block < want && 2 * block <= most) block *= 2;
-    /* A workgroup for every 4,096 tokens of a segment, up to 1,024 in all. */
+    /* A workgroup for every 4,096 tokens of a segment of mean length (rows behind the last segment counted in), up
+     * to 1,024 in all: token_off is on the device, so the host knows no other length. */
     p.parts = std::max<uint64_t>(1, std::min((s->rows / s->n_seg) / 4096, 1024 / s->n_seg));
     const uint32_t grid = (uint32_t)std::min<uint64_t>(s->n_seg * p.parts, 1u << 20);
     const uint32_t every = (uint32_t)std::min<uint64_t>((s->n_seg * s->hosts + 255) / 256, 4096);
