@@ -13,7 +13,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmsim.so")
 SOURCES = [os.path.join(CSRC, "msim_kernel.hip"), os.path.join(CSRC, "msim_probe.hip"),
-           os.path.join(CSRC, "msim_moe.hip"), os.path.join(CSRC, "msim_host.cpp")]
+           os.path.join(CSRC, "msim_moe.hip"), os.path.join(CSRC, "msim_gemm.hip"),
+           os.path.join(CSRC, "msim_host.cpp")]
 ARCH = os.environ.get("MSIM_OFFLOAD_ARCH", "gfx950")
 
 
@@ -28,13 +29,19 @@ def build(verbose: bool = False) -> str:
     common = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", os.path.join(ROOT, "include"),
               "-I", CSRC, "-Wall", "-Wno-unused-result",
               "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+    running = []
     for src in SOURCES:
         obj = os.path.join(CSRC, os.path.basename(src) + ".o")
         cmd = [hipcc()] + common + ["-x", "hip", "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.check_call(cmd)
+        running.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    for cmd, p in running:
+        p.wait()
+    for cmd, p in running:
+        if p.returncode:
+            raise subprocess.CalledProcessError(p.returncode, cmd)
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp] + objs + ["-lpthread"]
     if verbose:

@@ -1,0 +1,57 @@
+/* What the kernels of msim_moe.hip, msim_gemm.hip and msim_layer.hip share:
+ * element types and how a call launches and reports. */
+#ifndef MSIM_DEVICE_H
+#define MSIM_DEVICE_H
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "msim.h"
+#include "msim_error.h"
+
+namespace {
+
+constexpr int WAVE = 64;
+
+struct F32 {
+    typedef float raw;
+    static __device__ float get(raw v) { return v; }
+    static __device__ raw put(float v) { return v; }
+};
+struct F16 {
+    typedef uint16_t raw;
+    static __device__ float get(raw v) { return (float)__builtin_bit_cast(_Float16, v); }
+    static __device__ raw put(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+};
+struct BF16 {
+    typedef uint16_t raw;
+    static __device__ float get(raw v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
+    /* to nearest, ties to even; a NaN stays one */
+    static __device__ raw put(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+};
+
+[[maybe_unused]] inline int fail(int code, const char *what) { msim_set_error(what); return code; }
+
+/* Enqueues a kernel.  The result is the launch's own: an error that another call
+ * left pending on this thread neither fails it nor is taken from its owner. */
+template <typename... P, typename... A>
+hipError_t launch(void (*kernel)(P...), uint32_t grid, uint32_t block, size_t lds, hipStream_t st, A... args)
+{
+    return [&](P... p) {
+        void *at[] = {&p...};
+        return hipLaunchKernel((const void *)kernel, dim3(grid), dim3(block), at, lds, st);
+    }(args...);
+}
+
+[[maybe_unused]] inline int launched(hipError_t e, const char *what)
+{
+    if (e == hipSuccess) return MSIM_OK;
+    (void)hipGetLastError();               /* it is reported here */
+    msim_set_error2(what, hipGetErrorString(e));
+    return MSIM_E_HIP;
+}
+
+} // namespace
+
+#endif

@@ -14,8 +14,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "msim.h"
-#include "msim_error.h"
+#include "msim_device.h"
 
 namespace {
 
@@ -23,32 +22,10 @@ typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int WAVE = 64;
 constexpr float LOG2E = 1.44269504f;
 constexpr uint32_t THREAD_EXPERTS = 32;    /* experts of msim_route_threads, at most */
 constexpr uint32_t FINISH_ROWS = 1024;     /* rows a workgroup of msim_route_finish, at most */
 constexpr int32_t UNDECIDED = INT32_MIN;   /* ids of a row that msim_route_lists leaves to the 64-bit path */
-
-/* ------------------------------------------------------------------------ */
-/* element types                                                             */
-/* ------------------------------------------------------------------------ */
-
-struct F32 {
-    typedef float raw;
-    static __device__ float get(raw v) { return v; }
-    static __device__ raw put(float v) { return v; }
-};
-struct F16 {
-    typedef uint16_t raw;
-    static __device__ float get(raw v) { return (float)__builtin_bit_cast(_Float16, v); }
-    static __device__ raw put(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
-};
-struct BF16 {
-    typedef uint16_t raw;
-    static __device__ float get(raw v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
-    /* to nearest, ties to even; a NaN stays one */
-    static __device__ raw put(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
-};
 
 /* ------------------------------------------------------------------------ */
 /* the generator                                                             */
@@ -1135,27 +1112,6 @@ __global__ void __launch_bounds__(256) msim_traffic_packets(TrafficP p)
 /* ------------------------------------------------------------------------ */
 /* host                                                                      */
 /* ------------------------------------------------------------------------ */
-
-int fail(int code, const char *what) { msim_set_error(what); return code; }
-
-/* Enqueues a kernel.  The result is the launch's own: an error that another call
- * left pending on this thread neither fails it nor is taken from its owner. */
-template <typename... P, typename... A>
-hipError_t launch(void (*kernel)(P...), uint32_t grid, uint32_t block, size_t lds, hipStream_t st, A... args)
-{
-    return [&](P... p) {
-        void *at[] = {&p...};
-        return hipLaunchKernel((const void *)kernel, dim3(grid), dim3(block), at, lds, st);
-    }(args...);
-}
-
-int launched(hipError_t e, const char *what)
-{
-    if (e == hipSuccess) return MSIM_OK;
-    (void)hipGetLastError();               /* it is reported here */
-    msim_set_error2(what, hipGetErrorString(e));
-    return MSIM_E_HIP;
-}
 
 uint64_t splitmix_base(uint64_t seed, uint64_t offset) { return seed + (offset + 1) * GAMMA; }
 

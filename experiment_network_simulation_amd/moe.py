@@ -29,12 +29,15 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .sim import ABI_VERSION, MAX_TRAFFIC_HOSTS, MsimError, RouteSpec, TrafficSpec, load_library
+from .sim import (ABI_VERSION, MAX_TRAFFIC_HOSTS, LinearSpec, MsimError, OrthogonalizeSpec, RouteSpec, TrafficSpec,
+                  load_library)
 
-__all__ = ["Routing", "route", "route_backward", "dropout", "dropout_backward", "traffic"]
+__all__ = ["Routing", "route", "route_backward", "dropout", "dropout_backward", "traffic", "LinearGrads", "linear",
+           "linear_backward", "orthogonalize"]
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class Routing(NamedTuple):
@@ -305,3 +308,156 @@ def traffic(ids: torch.Tensor, token_off: torch.Tensor, home: torch.Tensor, plac
         return packets
 
     return _run(dev, stream, call, ids, token_off, home, place, out)
+
+
+class LinearGrads(NamedTuple):
+    """What linear_backward() returns: the gradients of x [rows, cols] and weight
+    [outs, cols] in their type, of bias float32 [outs]; None where not asked for."""
+    x: Optional[torch.Tensor]
+    weight: Optional[torch.Tensor]
+    bias: Optional[torch.Tensor]
+
+
+def _act(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, not {act!r}")
+    return _ACTS[act]
+
+
+def _like(t, name: str, dtype, device, shape) -> int:
+    """Checks for a tensor of that type, device and shape with contiguous rows; its row stride."""
+    stride = _need_rows(t, name)[3]
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return stride
+
+
+def _weights(x, weight):
+    """Checks of x and weight; device, rows, columns, outs and the two row strides."""
+    dev, rows, cols, xs = _need_rows(x, "x")
+    _, outs, wide, ws = _need_rows(weight, "weight")
+    if weight.device != dev or weight.dtype != x.dtype:
+        raise ValueError(f"weight must be {x.dtype} on {dev}, not {weight.dtype} on {weight.device}")
+    if wide != cols:
+        raise ValueError(f"weight has {wide} columns, x has {cols}")
+    if not 1 <= cols <= 1 << 20 or not 1 <= outs <= 1 << 20:
+        raise ValueError(f"weight must have 1 .. {1 << 20} rows and columns, not {tuple(weight.shape)}")
+    return dev, rows, cols, outs, xs, ws
+
+
+def _workspace(like, query, *args):
+    """Device memory of the size that the library asks for, and its size."""
+    n = C.c_uint64()
+    _call(query(*args, C.byref(n)))
+    return (like.new_empty(n.value, dtype=torch.uint8) if n.value else None), n.value
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *, act: str = "none",
+           residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+           pre: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """act(x weight^T + bias) + residual, rounded once: x [rows, cols], weight
+    [outs, cols], bias float32 [outs], residual [rows, outs] of the result's type.
+
+    act: "none", "relu", "gelu", "gelu_tanh" or "silu".  out_dtype: x's type or
+    float32 (a router's logits).  pre, a [rows, outs] tensor of x's type, gets
+    what goes into the activation, for linear_backward.  out may be residual."""
+    dev, rows, cols, outs, xs, ws = _weights(x, weight)
+    to = x.dtype if out_dtype is None else out_dtype
+    if to != x.dtype and to != torch.float32:
+        raise TypeError(f"out_dtype must be {x.dtype} or torch.float32, not {to}")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, dev, (outs,))
+    shape = (rows, outs)
+    rs = outs if residual is None else _like(residual, "residual", to, dev, shape)
+    ps = outs if pre is None else _like(pre, "pre", x.dtype, dev, shape)
+    os = outs if out is None else _like(out, "out", to, dev, shape)
+    spec = LinearSpec(ABI_VERSION, _DTYPES[x.dtype], _DTYPES[to], _act(act), cols, outs, rows, xs, ws, os, rs, ps, 0, 0)
+
+    def call(on):
+        lib = load_library()
+        y = x.new_empty(shape, dtype=to) if out is None else out
+        mem, size = _workspace(x, lib.msim_linear_workspace, C.byref(spec), x.data_ptr(), weight.data_ptr())
+        _call(lib.msim_linear(C.byref(spec), x.data_ptr(), weight.data_ptr(), _p(bias), _p(residual), y.data_ptr(), _p(pre),
+                              _p(mem), size, on))
+        if out is not None or pre is not None:
+            _changed(out, pre)
+        return y
+
+    return _run(dev, stream, call, x, weight, bias, residual, pre, out)
+
+
+def linear_backward(x: torch.Tensor, weight: torch.Tensor, grad: torch.Tensor, *, act: str = "none",
+                    pre: Optional[torch.Tensor] = None, need_x: bool = True, need_weight: bool = True,
+                    need_bias: bool = True, out: Optional[LinearGrads] = None, stream=None) -> LinearGrads:
+    """The gradients of linear()'s x, weight and bias, given that of its result
+    (float32 or x's type [rows, outs]; the residual's gradient is grad itself) and
+    for an activation what the forward pass kept in pre.  With out, those of its
+    tensors that are not None are written, whatever the need flags say."""
+    dev, rows, cols, outs, xs, ws = _weights(x, weight)
+    if not isinstance(grad, torch.Tensor) or grad.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"grad must be a tensor of {x.dtype} or torch.float32")
+    shape = (rows, outs)
+    gs = _like(grad, "grad", grad.dtype, dev, shape)
+    a = _act(act)
+    if a and pre is None:
+        raise ValueError(f"the gradient through {act} needs pre")
+    ps = outs if pre is None else _like(pre, "pre", x.dtype, dev, shape)
+    dxs = dws = cols
+    if out is not None:
+        dxs = cols if out.x is None else _like(out.x, "out.x", x.dtype, dev, (rows, cols))
+        dws = cols if out.weight is None else _like(out.weight, "out.weight", x.dtype, dev, (outs, cols))
+        if out.bias is not None:
+            _need(out.bias, "out.bias", torch.float32, dev, (outs,))
+    spec = LinearSpec(ABI_VERSION, _DTYPES[x.dtype], _DTYPES[grad.dtype], a, cols, outs, rows, xs, ws, gs, 0, ps, dxs, dws)
+
+    def call(on):
+        lib = load_library()
+        new = x.new_empty
+        g = out if out is not None else LinearGrads(new((rows, cols)) if need_x else None, new((outs, cols)) if need_weight else None,
+                                                    new(outs, dtype=torch.float32) if need_bias else None)
+        mem, size = _workspace(x, lib.msim_linear_backward_workspace, C.byref(spec), x.data_ptr(), weight.data_ptr(),
+                               grad.data_ptr(), g.x is not None, g.weight is not None, g.bias is not None)
+        _call(lib.msim_linear_backward(C.byref(spec), x.data_ptr(), weight.data_ptr(), _p(pre), grad.data_ptr(), _p(g.x),
+                                       _p(g.weight), _p(g.bias), _p(mem), size, on))
+        if out is not None:
+            _changed(*out)
+        return g
+
+    return _run(dev, stream, call, x, weight, grad, pre, *(() if out is None else out))
+
+
+def orthogonalize(update: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """update, a matrix [rows, cols] or a stack of them [count, rows, cols]
+    (contiguous), each with its singular values moved towards 1: X = update /
+    (norm + eps), then `steps` times X = a X + (b X X^T + c (X X^T)^2) X.  With
+    the default coefficients singular values from about 0.01 of the norm on end
+    within 0.7 .. 1.2.  out may be update."""
+    if not isinstance(update, torch.Tensor):
+        raise TypeError("update must be a tensor")
+    if update.dtype not in _DTYPES:
+        raise TypeError(f"update must be float32, float16 or bfloat16, not {update.dtype}")
+    if update.dim() not in (2, 3):
+        raise ValueError(f"update must have two or three dimensions, not {update.dim()}")
+    dev = update.device
+    _need(update, "update", update.dtype, dev)
+    rows, cols = update.shape[-2:]
+    count = update.shape[0] if update.dim() == 3 else 1
+    if not 1 <= rows <= 1 << 20 or not 1 <= cols <= 1 << 20 or count > 65536:
+        raise ValueError(f"update must hold at most 65536 matrices of 1 .. {1 << 20} rows and columns, not {tuple(update.shape)}")
+    a, b, c = (float(v) for v in coefficients)
+    spec = OrthogonalizeSpec(ABI_VERSION, _DTYPES[update.dtype], count, _range(steps, "steps", 0, 64), rows, cols, float(eps),
+                             a, b, c, 0)
+    if out is not None:
+        _need(out, "out", update.dtype, dev, update.shape)
+
+    def call(on):
+        lib = load_library()
+        mem, size = _workspace(update, lib.msim_orthogonalize_workspace, C.byref(spec))
+        y = torch.empty_like(update) if out is None else out
+        _call(lib.msim_orthogonalize(C.byref(spec), update.data_ptr(), y.data_ptr(), _p(mem), size, on))
+        if out is not None:
+            _changed(out)
+        return y
+
+    return _run(dev, stream, call, update, out)

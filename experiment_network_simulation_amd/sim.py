@@ -32,7 +32,9 @@ EXPORTED = ["msim_create", "msim_workspace_size", "msim_bind", "msim_run", "msim
             "msim_results",
             "msim_flow_count", "msim_flow_ticks", "msim_task_count", "msim_task_ticks", "msim_get_info",
             "msim_last_error", "msim_destroy", "msim_lds_probe",
-            "msim_route", "msim_route_backward", "msim_dropout", "msim_traffic"]
+            "msim_route", "msim_route_backward", "msim_dropout", "msim_traffic",
+            "msim_linear", "msim_linear_workspace", "msim_linear_backward", "msim_linear_backward_workspace",
+            "msim_orthogonalize", "msim_orthogonalize_workspace"]
 
 _P8, _P32, _P64 = C.POINTER(C.c_uint8), C.POINTER(C.c_uint32), C.POINTER(C.c_uint64)
 
@@ -79,6 +81,20 @@ class TrafficSpec(C.Structure):
                 ("per_row", C.c_uint32), ("reserved", C.c_uint32)]
 
 
+class LinearSpec(C.Structure):
+    _fields_ = [("version", C.c_uint32), ("dtype", C.c_uint32), ("out_dtype", C.c_uint32), ("act", C.c_uint32),
+                ("cols", C.c_uint32), ("outs", C.c_uint32), ("rows", C.c_uint64),
+                ("x_stride", C.c_uint64), ("weight_stride", C.c_uint64), ("out_stride", C.c_uint64),
+                ("residual_stride", C.c_uint64), ("pre_stride", C.c_uint64),
+                ("dx_stride", C.c_uint64), ("dweight_stride", C.c_uint64)]
+
+
+class OrthogonalizeSpec(C.Structure):
+    _fields_ = [("version", C.c_uint32), ("dtype", C.c_uint32), ("count", C.c_uint32), ("steps", C.c_uint32),
+                ("rows", C.c_uint64), ("cols", C.c_uint64), ("eps", C.c_double),
+                ("a", C.c_float), ("b", C.c_float), ("c", C.c_float), ("reserved", C.c_uint32)]
+
+
 class _Info(C.Structure):
     _fields_ = [("n_exp", C.c_uint32), ("block_threads", C.c_uint32), ("grid_blocks", C.c_uint32),
                 ("lds_bytes", C.c_uint32), ("n_lds_exp", C.c_uint32), ("n_compact", C.c_uint32),
@@ -122,6 +138,13 @@ def load_library():
     lib.msim_dropout.argtypes = [C.c_uint32, vp, vp, C.c_uint64, C.c_uint64, C.c_uint64, C.c_uint64, C.c_double,
                                  C.c_uint64, C.c_uint64, C.c_uint32, vp]
     lib.msim_traffic.argtypes = [C.POINTER(TrafficSpec), vp, vp, vp, vp, vp, vp]
+    lib.msim_linear_workspace.argtypes = [C.POINTER(LinearSpec), vp, vp, _P64]
+    lib.msim_linear.argtypes = [C.POINTER(LinearSpec), vp, vp, vp, vp, vp, vp, vp, C.c_uint64, vp]
+    lib.msim_linear_backward_workspace.argtypes = [C.POINTER(LinearSpec), vp, vp, vp, C.c_uint32, C.c_uint32, C.c_uint32,
+                                                   _P64]
+    lib.msim_linear_backward.argtypes = [C.POINTER(LinearSpec), vp, vp, vp, vp, vp, vp, vp, vp, C.c_uint64, vp]
+    lib.msim_orthogonalize_workspace.argtypes = [C.POINTER(OrthogonalizeSpec), _P64]
+    lib.msim_orthogonalize.argtypes = [C.POINTER(OrthogonalizeSpec), vp, vp, vp, C.c_uint64, vp]
     for name in EXPORTED:
         if name not in ("msim_last_error", "msim_destroy"):
             getattr(lib, name).restype = C.c_int

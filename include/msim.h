@@ -434,6 +434,13 @@ int msim_lds_probe(void *dev_out, uint64_t out_bytes, uint32_t blocks, uint32_t 
 #define MSIM_F16 1
 #define MSIM_BF16 2
 
+/* activations */
+#define MSIM_ACT_NONE 0
+#define MSIM_ACT_RELU 1
+#define MSIM_ACT_GELU 2          /* z times the share of a normal distribution below z */
+#define MSIM_ACT_GELU_TANH 3     /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define MSIM_ACT_SILU 4          /* z / (1 + e^-z) */
+
 /* scores of the router */
 #define MSIM_SCORE_SOFTMAX 0     /* over all experts of the row */
 #define MSIM_SCORE_SIGMOID 1     /* each expert by itself */
@@ -535,6 +542,81 @@ typedef struct msim_traffic_spec {
 
 int msim_traffic(const msim_traffic_spec *spec, const int32_t *ids, const int64_t *token_off,
                  const int32_t *home, const int32_t *place, int32_t *packets, void *hip_stream);
+
+/*
+ * The products around the router: a gate's logits and the gradient of its
+ * weights, a dense block, the update of trained weights, a layer of experts.  As
+ * the calls above, with a workspace where they need one: device memory of the
+ * caller on 256 bytes, of the size that the call's own *_workspace function gives
+ * for the same arguments; its contents need not be kept, and calls that may
+ * overlap (two streams, two captured graphs) need one each.  MSIM_E_WORKSPACE,
+ * nothing launched, if it is missing or too small.  Sums are made in 32 bits or
+ * more, in an order that depends on sizes and alignment alone.  Strides are in
+ * elements.
+ */
+#define MSIM_MAX_LINEAR (1u << 20)
+
+/*
+ * z = x weight^T + bias, out = act(z) + residual.  x: rows x cols, weight: outs x
+ * cols, of type dtype; out and residual: rows x outs of out_dtype (dtype or
+ * MSIM_F32); bias: outs floats or NULL; residual may be NULL, or out itself.  pre,
+ * unless NULL, gets z in type dtype, for the backward pass of an activation.
+ * Limits: rows < 2^31, cols and outs <= MSIM_MAX_LINEAR.
+ */
+typedef struct msim_linear_spec {
+    uint32_t version;            /* MSIM_ABI_VERSION */
+    uint32_t dtype, out_dtype, act;
+    uint32_t cols, outs;
+    uint64_t rows;
+    uint64_t x_stride, weight_stride, out_stride, residual_stride, pre_stride;
+    uint64_t dx_stride, dweight_stride;       /* of the backward pass */
+} msim_linear_spec;
+
+/* x and weight: the arrays of the call (their alignment counts, they are not read) */
+int msim_linear_workspace(const msim_linear_spec *spec, const void *x, const void *weight, uint64_t *bytes);
+int msim_linear(const msim_linear_spec *spec, const void *x, const void *weight, const float *bias,
+                const void *residual, void *out, void *pre, void *workspace, uint64_t workspace_bytes,
+                void *hip_stream);
+
+/*
+ * The gradients of msim_linear: with d = grad act'(pre), dx = d weight, dweight =
+ * d^T x, dbias = the sums of d's columns; that of the residual is grad itself.
+ * grad: rows x outs of out_dtype at out_stride; pre: what the forward pass kept
+ * (not read without an activation).  dx (at dx_stride) and dweight (at
+ * dweight_stride) are of type dtype.  Any of dx, dweight and dbias may be NULL; x
+ * may be without dweight, weight without dx.  d is rounded to dtype where it is
+ * not there already (an activation, or a grad of 32 bits).  rows = 0: dweight and
+ * dbias are zeros.
+ */
+int msim_linear_backward_workspace(const msim_linear_spec *spec, const void *x, const void *weight, const void *grad,
+                                   uint32_t dx, uint32_t dweight, uint32_t dbias, uint64_t *bytes);
+int msim_linear_backward(const msim_linear_spec *spec, const void *x, const void *weight, const void *pre,
+                         const void *grad, void *dx, void *dweight, float *dbias, void *workspace,
+                         uint64_t workspace_bytes, void *hip_stream);
+
+/*
+ * The update of a weight matrix with its singular values moved towards 1, by
+ * Newton-Schulz products: X = update / (Frobenius norm + eps), then `steps` times
+ * X <- a X + (b X X^T + c (X X^T)^2) X; of a tall matrix on its transpose, which is
+ * the same.  count matrices of rows x cols (contiguous) in one call, each by
+ * itself.  out may be update.  Products are made from numbers of 22 bits (the sum
+ * of two f16) with sums in 32; steps whose numbers would leave their range are
+ * refused (MSIM_E_ARG), as singular values beyond 24 are.  A matrix that is not
+ * finite gives NaN.  Limits: rows and cols <= MSIM_MAX_LINEAR, count <= 65,536,
+ * steps <= 64, 2^36 elements.
+ */
+typedef struct msim_orthogonalize_spec {
+    uint32_t version;            /* MSIM_ABI_VERSION */
+    uint32_t dtype, count, steps;
+    uint64_t rows, cols;
+    double eps;
+    float a, b, c;
+    uint32_t reserved;           /* 0 */
+} msim_orthogonalize_spec;
+
+int msim_orthogonalize_workspace(const msim_orthogonalize_spec *spec, uint64_t *bytes);
+int msim_orthogonalize(const msim_orthogonalize_spec *spec, const void *update, void *out, void *workspace,
+                       uint64_t workspace_bytes, void *hip_stream);
 
 #ifdef __cplusplus
 }
