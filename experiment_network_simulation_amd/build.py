@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmsim.so")
 SOURCES = [os.path.join(CSRC, "msim_kernel.hip"), os.path.join(CSRC, "msim_probe.hip"),
            os.path.join(CSRC, "msim_moe.hip"), os.path.join(CSRC, "msim_gemm.hip"),
-           os.path.join(CSRC, "msim_host.cpp")]
+           os.path.join(CSRC, "msim_layer.hip"), os.path.join(CSRC, "msim_host.cpp")]
 ARCH = os.environ.get("MSIM_OFFLOAD_ARCH", "gfx950")
 
 

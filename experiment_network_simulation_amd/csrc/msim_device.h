@@ -10,6 +10,9 @@
 #include "msim.h"
 #include "msim_error.h"
 
+/* What is wrong with a router (and the code for it), or NULL; msim_route makes the same checks. */
+__attribute__((visibility("hidden"))) const char *msim_check_route(const msim_route_spec *s, bool backward, int *code) noexcept;
+
 namespace {
 
 constexpr int WAVE = 64;

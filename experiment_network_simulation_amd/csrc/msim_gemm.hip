@@ -11,15 +11,11 @@
 #include <algorithm>
 #include <cmath>
 
-#include "msim_device.h"
+#include "msim_stream.h"
 
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 
 /* element types of a product: the three of the library, and a number as the sum
@@ -196,17 +192,6 @@ struct Epilogue {
     uint64_t out_batch;          /* bytes between matrices of out and src */
     float alpha, beta;
 };
-
-__device__ __forceinline__ float act_of(float z, uint32_t act)
-{
-    switch (act) {
-    case MSIM_ACT_RELU: return z < 0 ? 0.0f : z;                 /* a NaN stays one */
-    case MSIM_ACT_SILU: return z / (1.0f + expf(-z));
-    case MSIM_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case MSIM_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
-    default: return z;
-    }
-}
 
 __device__ __forceinline__ float slope_of(float z, uint32_t act)
 {
@@ -479,6 +464,52 @@ template <int MODE> __global__ void __launch_bounds__(256) msim_gemm_join(GemmP 
 }
 
 /* ------------------------------------------------------------------------ */
+/* few rows                                                                  */
+/* ------------------------------------------------------------------------ */
+
+/* A linear layer of up to 16 MT rows: 16 NT outs a workgroup, whose wavefronts
+ * share k.  The weights are read once, from where they lie on any element. */
+struct FewP {
+    const void *x, *w;
+    uint64_t x_ld, w_ld;
+    uint32_t K;
+    Epilogue e;
+};
+
+template <int MODE, int MT, int NT, int WAVES> __global__ void __launch_bounds__(64 * WAVES) msim_linear_few(FewP p)
+{
+    typedef typename Type<MODE>::D D;
+    typedef typename D::raw raw;
+    __shared__ f32x4 sums[WAVES * MT * NT * 64];
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = lane & 15;
+    const uint32_t n0 = blockIdx.x * 16 * NT;
+    const raw *w[NT], *x[MT];
+    for (int j = 0; j < NT; j++) w[j] = (const raw *)p.w + min(n0 + j * 16 + l, p.e.N - 1) * p.w_ld;
+    for (int i = 0; i < MT; i++) x[i] = (const raw *)p.x + min(i * 16 + l, p.e.M - 1) * p.x_ld;
+    f32x4 acc[MT][NT];
+    for (int i = 0; i < MT; i++)
+        for (int j = 0; j < NT; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+    stream<D, MT, NT>(w, x, p.K, wave, WAVES, acc);
+    join<MT, NT, WAVES>(sums, wave, acc);
+    _Pragma("unroll") for (int i = 0; i < MT; i++) {
+        const uint32_t m = i * 16 + l;
+        if (i % WAVES != (int)wave || m >= p.e.M) continue;
+        for (int j = 0; j < NT; j++)
+            for (uint32_t k = 0; k < 4; k++) {
+                const uint32_t n = n0 + j * 16 + (lane >> 4) * 4 + k;
+                if (n >= p.e.N) continue;
+                float v = acc[i][j][k];
+                if (p.e.bias) v += p.e.bias[n];
+                if (p.e.pre) ((raw *)p.e.pre)[m * p.e.pre_ld + n] = D::put(v);
+                v = act_of(v, p.e.act);
+                if (p.e.res) v += p.e.out32 ? ((const float *)p.e.res)[m * p.e.res_ld + n] : D::get(((const raw *)p.e.res)[m * p.e.res_ld + n]);
+                if (p.e.out32) ((float *)p.e.out)[m * p.e.out_ld + n] = v;
+                else ((raw *)p.e.out)[m * p.e.out_ld + n] = D::put(v);
+            }
+    }
+}
+
+/* ------------------------------------------------------------------------ */
 /* operands that do not lie as the product reads them                        */
 /* ------------------------------------------------------------------------ */
 
@@ -679,18 +710,23 @@ const char *check_linear(const msim_linear_spec *s, int *code)
     return nullptr;
 }
 
+constexpr uint64_t FEW_ROWS = 64;          /* rows of msim_linear_few, at most */
+
 struct Forward {
     Matrix x, w;
     Plan plan;
     uint64_t bytes;
+    bool few;
 };
 
 Forward forward_of(const msim_linear_spec *s, const void *x, const void *weight)
 {
-    Forward f;
+    Forward f = {};
     const uint32_t size = size_of(s->dtype);
     f.x = matrix_of(x, s->rows, s->cols, s->x_stride, size);
     f.w = matrix_of(weight, s->outs, s->cols, s->weight_stride, size);
+    f.few = s->rows <= FEW_ROWS;
+    if (f.few) return f;
     f.plan = plan_of(s->dtype, s->rows, s->outs, f.x.wide(), 1);
     f.bytes = f.x.bytes() + f.w.bytes() + f.plan.part_bytes;
     return f;
@@ -699,6 +735,16 @@ Forward forward_of(const msim_linear_spec *s, const void *x, const void *weight)
 template <int MODE>
 int run_forward(const msim_linear_spec *s, const Forward &f, const Epilogue &e, char *ws, hipStream_t st)
 {
+    if (f.few) {
+        const FewP q = {f.x.at, f.w.at, f.x.ld, f.w.ld, s->cols, e};
+        /* one row of tiles and 8 wavefronts where there are few outs, so that the card is filled */
+        const uint32_t wide = (s->outs + 31) / 32, thin = (s->outs + 15) / 16;
+        const hipError_t r = s->rows > 32 ? launch(msim_linear_few<MODE, 4, 2, 4>, wide, 256, 0, st, q)
+            : s->rows > 16 ? launch(msim_linear_few<MODE, 2, 2, 4>, wide, 256, 0, st, q)
+            : wide >= 256 ? launch(msim_linear_few<MODE, 1, 2, 4>, wide, 256, 0, st, q)
+                          : launch(msim_linear_few<MODE, 1, 1, 8>, thin, 512, 0, st, q);
+        return launched(r, "linear launch");
+    }
     GemmP p = {};
     char *wx = ws, *ww = wx + f.x.bytes();
     p.a = f.x.operand(wx);

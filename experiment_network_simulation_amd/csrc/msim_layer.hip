@@ -1,0 +1,286 @@
+/* A whole mixture-of-experts layer for a few tokens (msim_layer of include/msim.h,
+ * which has the definition): gate logits, msim_route, the experts' two products,
+ * and the weighted sum of what the chosen experts answer.
+ *
+ * What bounds it is reading the chosen experts' weights once; each of the two
+ * products has a workgroup for an expert that some token chose and a few of its
+ * rows of weights, and that workgroup has all of the expert's tokens.
+ */
+
+#include <algorithm>
+
+#include "msim_stream.h"
+
+namespace {
+
+constexpr int WAVES = 4;                   /* wavefronts of a workgroup: k is shared among them */
+constexpr uint32_t MAX_ROWS = MSIM_MAX_LAYER_ROWS;
+
+struct LayerP {
+    const void *x, *gate, *w_in, *w_out, *res;
+    const uint8_t *mask;
+    void *out;
+    float *logits;
+    const int32_t *ids;
+    const float *weights;
+    void *h;                     /* [rows * top_k][h_ld], of the layer's type */
+    float *part;                 /* [rows * top_k][part_ld] */
+    uint64_t x_ld, out_ld, res_ld, h_ld, part_ld;
+    uint32_t rows, E, K, C, F, act, gated;
+    uint32_t slots, tiles, chunks;         /* of a product: experts, tiles of weight rows, runs of tokens */
+};
+
+/* Logits in 64 bits, rounded to 32: of 16-bit inputs every product is exact, and
+ * the choice of experts follows from the inputs, not from an order of additions.
+ * One expert and TT tokens a workgroup.  Rows that are masked out route nowhere. */
+template <typename D, int TT> __global__ void __launch_bounds__(256) msim_layer_gate(LayerP p)
+{
+    typedef typename D::raw raw;
+    constexpr uint32_t PER = 16 / sizeof(raw);
+    typedef raw vec __attribute__((ext_vector_type(PER)));
+    __shared__ double part[4][TT];
+    const uint32_t e = blockIdx.x % p.E, t0 = blockIdx.x / p.E * TT;
+    const raw *g = (const raw *)p.gate + (uint64_t)e * p.C;
+    double sum[TT];
+    for (int t = 0; t < TT; t++) sum[t] = 0;
+    for (uint32_t c = threadIdx.x * PER; c < p.C; c += 256 * PER) {
+        const vec w = __builtin_bit_cast(vec, piece<D>(g, c, p.C));
+        vec x[TT];
+        for (int t = 0; t < TT; t++)
+            x[t] = __builtin_bit_cast(vec, piece<D>((const raw *)p.x + min(t0 + t, p.rows - 1) * p.x_ld, c, p.C));
+        for (uint32_t i = 0; i < PER; i++) {
+            const double v = D::get(w[i]);
+            for (int t = 0; t < TT; t++) sum[t] = __builtin_fma(v, (double)D::get(x[t][i]), sum[t]);
+        }
+    }
+    for (int t = 0; t < TT; t++) {
+        for (int d = 1; d < 64; d *= 2) sum[t] += __shfl_xor(sum[t], d);
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][t] = sum[t];
+    }
+    __syncthreads();
+    const uint32_t t = t0 + threadIdx.x;
+    if (threadIdx.x < TT && t < p.rows) {
+        const double s = part[0][threadIdx.x] + part[1][threadIdx.x] + part[2][threadIdx.x] + part[3][threadIdx.x];
+        p.logits[(uint64_t)t * p.E + e] = p.mask && !p.mask[t] ? -INFINITY : (float)s;
+    }
+}
+
+/* The expert of a slot and the list of its assignments (row * K + choice), in
+ * order.  Where there are fewer assignments than experts a slot is an assignment,
+ * and the first that names an expert has it; otherwise a slot is an expert.  The
+ * number of assignments, 0 where another slot has the expert. */
+__device__ __forceinline__ uint32_t tokens_of(const LayerP &p, uint32_t slot, uint32_t *list, uint32_t *counts, int32_t &expert)
+{
+    const uint32_t n = p.rows * p.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool by_choice = p.slots == n;
+    expert = by_choice ? p.ids[slot] : (int32_t)slot;
+    if (expert < 0) return 0;
+    uint32_t have = 0;
+    for (uint32_t j0 = 0; j0 < n; j0 += 64 * WAVES) {
+        const uint32_t j = j0 + threadIdx.x;
+        const bool mine = j < n && p.ids[j] == expert;
+        const uint64_t all = __ballot(mine);
+        if (lane == 0) counts[wave] = __popcll(all);
+        __syncthreads();
+        uint32_t at = have + __popcll(all & ((1ull << lane) - 1));
+        for (uint32_t w = 0; w < WAVES; w++) {
+            if (w < wave) at += counts[w];
+            have += counts[w];
+        }
+        if (mine && at < MAX_ROWS) list[at] = j;
+        __syncthreads();
+    }
+    return by_choice && list[0] != slot ? 0 : min(have, MAX_ROWS);
+}
+
+/* h = act(gate rows x) (up rows x), or act(rows x): 16 hidden units (32 without a
+ * gate) of one expert for up to 16 MT of its tokens.  h is rounded to the layer's
+ * type, as the second product's matrix instructions read it. */
+template <typename D, int MT>
+__device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, f32x4 *lds)
+{
+    typedef typename D::raw raw;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
+    const uint32_t f0 = tile * (p.gated ? 16 : 32);
+    const raw *w[2], *x[MT];
+    const raw *base = (const raw *)p.w_in + (uint64_t)expert * (p.gated ? 2 : 1) * p.F * p.C;
+    w[0] = base + (uint64_t)min(f0 + l, p.F - 1) * p.C;
+    w[1] = base + (uint64_t)(p.gated ? p.F + min(f0 + l, p.F - 1) : min(f0 + 16 + l, p.F - 1)) * p.C;
+    for (int i = 0; i < MT; i++) x[i] = (const raw *)p.x + list[min(i * 16 + l, n - 1)] / p.K * p.x_ld;
+    f32x4 acc[MT][2];
+    for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+    stream<D, MT, 2>(w, x, p.C, wave, WAVES, acc);
+    join<MT, 2, WAVES>(lds, wave, acc);
+    _Pragma("unroll") for (int i = 0; i < MT; i++) {
+        if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
+        raw *h = (raw *)p.h + (uint64_t)list[i * 16 + l] * p.h_ld;
+        for (int j = 0; j < (p.gated ? 1 : 2); j++) {
+            const uint32_t f = f0 + j * 16 + (lane >> 4) * 4;
+            if (f >= p.F) continue;        /* rows of h have room to a multiple of 8 */
+            for (int k = 0; k < 4; k++) {
+                const float v = act_of(j ? acc[i][1][k] : acc[i][0][k], p.act);
+                h[f + k] = D::put(p.gated ? v * acc[i][1][k] : v);
+            }
+        }
+    }
+}
+
+/* 32 columns of what one expert answers to up to 16 MT of its tokens, in 32 bits */
+template <typename D, int MT>
+__device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, f32x4 *lds)
+{
+    typedef typename D::raw raw;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
+    const uint32_t c0 = tile * 32;
+    const raw *w[2], *x[MT];
+    const raw *base = (const raw *)p.w_out + (uint64_t)expert * p.C * p.F;
+    for (int j = 0; j < 2; j++) w[j] = base + (uint64_t)min(c0 + j * 16 + l, p.C - 1) * p.F;
+    for (int i = 0; i < MT; i++) x[i] = (const raw *)p.h + (uint64_t)list[min(i * 16 + l, n - 1)] * p.h_ld;
+    f32x4 acc[MT][2];
+    for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+    stream<D, MT, 2>(w, x, p.F, wave, WAVES, acc);
+    join<MT, 2, WAVES>(lds, wave, acc);
+    _Pragma("unroll") for (int i = 0; i < MT; i++) {
+        if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
+        float *to = p.part + (uint64_t)list[i * 16 + l] * p.part_ld;
+        for (int j = 0; j < 2; j++) {
+            const uint32_t c = c0 + j * 16 + (lane >> 4) * 4;
+            if (c < p.C) *(f32x4 *)(to + c) = acc[i][j];       /* rows of part have room to a multiple of 4 */
+        }
+    }
+}
+
+/* MT: tokens of a run, in 16; runs of at most 16 take the leaner code */
+template <typename D, int MT, bool DOWN> __global__ void __launch_bounds__(64 * WAVES) msim_layer_product(LayerP p)
+{
+    __shared__ uint32_t list[MAX_ROWS], counts[WAVES];
+    __shared__ f32x4 sums[WAVES * MT * 2 * 64];
+    const uint32_t tile = blockIdx.x % p.tiles, rest = blockIdx.x / p.tiles, chunk = rest % p.chunks, slot = rest / p.chunks;
+    int32_t expert;
+    const uint32_t all = tokens_of(p, slot, list, counts, expert), first = chunk * 16 * MT;
+    if (first >= all) return;
+    const uint32_t n = min(all - first, 16u * MT);
+    if (n <= 16) DOWN ? down_tokens<D, 1>(p, expert, tile, list + first, n, sums) : up_tokens<D, 1>(p, expert, tile, list + first, n, sums);
+    else DOWN ? down_tokens<D, MT>(p, expert, tile, list + first, n, sums) : up_tokens<D, MT>(p, expert, tile, list + first, n, sums);
+}
+
+/* The weighted sum over a token's choices, in their order, and the residual.  A
+ * row that the router voids (weights NaN) answers NaN. */
+template <typename D> __global__ void __launch_bounds__(256) msim_layer_sum(LayerP p)
+{
+    typedef typename D::raw raw;
+    const uint32_t turns = (p.C + 3) / 4;
+    const uint64_t id = blockIdx.x * 256ull + threadIdx.x;
+    const uint32_t t = (uint32_t)(id / turns), c = (uint32_t)(id - (uint64_t)t * turns) * 4;
+    if (t >= p.rows) return;
+    f32x4 y = {0, 0, 0, 0};
+    for (uint32_t k = 0; k < p.K; k++) {
+        const uint32_t j = t * p.K + k;
+        const float w = p.weights[j];
+        if (p.ids[j] >= 0) y += w * *(const f32x4 *)(p.part + (uint64_t)j * p.part_ld + c);
+        else if (w != w) y += w;
+    }
+    for (uint32_t i = 0; i < 4 && c + i < p.C; i++) {
+        const float r = p.res ? D::get(((const raw *)p.res)[t * p.res_ld + c + i]) : 0.0f;
+        ((raw *)p.out)[t * p.out_ld + c + i] = D::put(y[i] + r);
+    }
+}
+
+/* ------------------------------------------------------------------------ */
+/* host                                                                      */
+/* ------------------------------------------------------------------------ */
+
+uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+
+struct Layout { uint64_t logits, h, part, bytes, h_ld, part_ld; };
+
+Layout layout_of(const msim_layer_spec *s)
+{
+    const uint64_t n = s->route.rows * s->route.top_k;
+    Layout l;
+    l.h_ld = up(s->hidden, 8);
+    l.part_ld = up(s->cols, 4);
+    l.logits = up(s->route.rows * s->route.experts * 4, 256);
+    l.h = up(n * l.h_ld * (s->dtype == MSIM_F32 ? 4 : 2), 256);
+    l.part = up(n * l.part_ld * 4, 256);
+    l.bytes = l.logits + l.h + l.part;
+    return l;
+}
+
+const char *check_layer(const msim_layer_spec *s, int *code)
+{
+    *code = MSIM_E_ARG;
+    if (!s) return "layer: null spec";
+    if (s->version != MSIM_ABI_VERSION) return "layer: spec version mismatch";
+    if (s->dtype > MSIM_BF16) return "layer: unknown dtype";
+    if (s->act > MSIM_ACT_SILU) return "layer: unknown activation";
+    if (s->gated > 1) return "layer: gated must be 0 or 1";
+    if (!s->cols || !s->hidden) return "layer: cols and hidden must be at least 1";
+    if (s->route.dtype != MSIM_F32 || s->route.row_stride != s->route.experts)
+        return "layer: the router's logits are 32-bit and contiguous";
+    if (s->route.rows > 1 && (s->x_stride < s->cols || s->out_stride < s->cols)) return "layer: x_stride or out_stride below cols";
+    if (const char *why = msim_check_route(&s->route, false, code)) return why;
+    *code = MSIM_E_LIMIT;
+    if (s->route.rows > MAX_ROWS) return "layer: more than MSIM_MAX_LAYER_ROWS rows";
+    if (s->cols > MSIM_MAX_LINEAR || s->hidden > MSIM_MAX_LINEAR) return "layer: cols or hidden above MSIM_MAX_LINEAR";
+    if ((uint64_t)s->route.experts * std::max(s->cols, s->hidden) >> 24) return "layer: experts * cols or experts * hidden of 2^24 or more";
+    if (s->x_stride >> 40 || s->out_stride >> 40 || s->residual_stride >> 40) return "layer: a stride of 2^40 or more";
+    return nullptr;
+}
+
+template <typename D, int MT, bool DOWN> hipError_t launch_product(LayerP p, uint64_t tiles, hipStream_t st)
+{
+    p.tiles = (uint32_t)tiles;
+    p.chunks = (p.rows + 16 * MT - 1) / (16 * MT);
+    return launch(msim_layer_product<D, MT, DOWN>, p.slots * p.chunks * p.tiles, 64 * WAVES, 0, st, p);
+}
+
+template <typename D> int run_layer(const msim_layer_spec *s, LayerP p, const float *bias, int32_t *ids, float *weights, int32_t *load, hipStream_t st)
+{
+    hipError_t e = p.rows == 1 ? launch(msim_layer_gate<D, 1>, p.E, 256, 0, st, p)
+                               : launch(msim_layer_gate<D, 4>, p.E * ((p.rows + 3) / 4), 256, 0, st, p);
+    if (e != hipSuccess) return launched(e, "layer launch");
+    if (int rc = msim_route(&s->route, p.logits, bias, ids, weights, load, st)) return rc;
+    p.slots = std::min(p.rows * p.K, p.E);
+    const uint64_t in = (p.F + (p.gated ? 15 : 31)) / (p.gated ? 16 : 32), out = (p.C + 31) / 32;
+    e = p.rows <= 16 ? launch_product<D, 1, false>(p, in, st)
+        : p.rows <= 32 ? launch_product<D, 2, false>(p, in, st) : launch_product<D, 4, false>(p, in, st);
+    if (e == hipSuccess)
+        e = p.rows <= 16 ? launch_product<D, 1, true>(p, out, st)
+            : p.rows <= 32 ? launch_product<D, 2, true>(p, out, st) : launch_product<D, 4, true>(p, out, st);
+    if (e == hipSuccess) e = launch(msim_layer_sum<D>, (uint32_t)(((uint64_t)p.rows * ((p.C + 3) / 4) + 255) / 256), 256, 0, st, p);
+    return launched(e, "layer launch");
+}
+
+} // namespace
+
+extern "C" int msim_layer_workspace(const msim_layer_spec *s, uint64_t *bytes)
+{
+    int code;
+    if (const char *why = check_layer(s, &code)) return fail(code, why);
+    if (!bytes) return fail(MSIM_E_ARG, "layer: null bytes");
+    *bytes = s->route.rows ? layout_of(s).bytes : 0;
+    return MSIM_OK;
+}
+
+extern "C" int msim_layer(const msim_layer_spec *s, const void *x, const void *gate, const float *bias, const void *w_in,
+                          const void *w_out, const uint8_t *mask, const void *residual, void *out, int32_t *ids,
+                          float *weights, int32_t *load, void *workspace, uint64_t workspace_bytes, void *hip_stream)
+{
+    int code;
+    if (const char *why = check_layer(s, &code)) return fail(code, why);
+    if (s->route.rows == 0) return msim_route(&s->route, nullptr, bias, ids, weights, load, hip_stream);
+    if (!x || !gate || !w_in || !w_out || !out || !ids || !weights) return fail(MSIM_E_ARG, "layer: null array");
+    if (residual && s->route.rows > 1 && s->residual_stride < s->cols) return fail(MSIM_E_ARG, "layer: residual_stride below cols");
+    const Layout l = layout_of(s);
+    if (!workspace || workspace_bytes < l.bytes || (uintptr_t)workspace % 256)
+        return fail(MSIM_E_WORKSPACE, "layer: workspace missing, too small or not on 256 bytes");
+    char *ws = (char *)workspace;
+    const LayerP p = {x, gate, w_in, w_out, residual, mask, out, (float *)ws, ids, weights, ws + l.logits,
+                      (float *)(ws + l.logits + l.h), s->x_stride, s->out_stride, s->residual_stride, l.h_ld, l.part_ld,
+                      (uint32_t)s->route.rows, s->route.experts, s->route.top_k, s->cols, s->hidden, s->act, s->gated, 0, 0, 0};
+    hipStream_t st = (hipStream_t)hip_stream;
+    return s->dtype == MSIM_F32 ? run_layer<F32>(s, p, bias, ids, weights, load, st)
+        : s->dtype == MSIM_F16 ? run_layer<F16>(s, p, bias, ids, weights, load, st)
+                               : run_layer<BF16>(s, p, bias, ids, weights, load, st);
+}

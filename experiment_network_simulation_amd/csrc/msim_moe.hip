@@ -1123,32 +1123,6 @@ bool drop_limit(double p, uint64_t *limit)
     return true;
 }
 
-const char *check_route(const msim_route_spec *s, bool backward, int *code)
-{
-    *code = MSIM_E_ARG;
-    if (!s) return "route: null spec";
-    if (s->version != MSIM_ABI_VERSION) return "route: spec version mismatch";
-    if (s->dtype > MSIM_BF16) return "route: unknown dtype";
-    if (s->score > MSIM_SCORE_SIGMOID) return "route: unknown score";
-    if (s->experts == 0 || s->top_k == 0) return "route: experts and top_k must be at least 1";
-    if (s->renorm > 1) return "route: renorm must be 0 or 1";
-    if (!std::isfinite(s->scale)) return "route: scale must be finite";
-    if (s->rows && s->row_stride < s->experts) return "route: row_stride below experts";
-    *code = MSIM_E_LIMIT;
-    if (s->experts > MSIM_MAX_EXPERTS) return "route: more than MSIM_MAX_EXPERTS experts";
-    if (s->top_k > MSIM_MAX_TOP_K) return "route: top_k above MSIM_MAX_TOP_K";
-    if (s->rows >> 31 || s->row_stride >> 40) return "route: 2^31 rows or more, or a row_stride of 2^40 or more";
-    *code = MSIM_E_ARG;
-    if (backward) return s->top_k > s->experts ? "route: top_k above experts" : nullptr;
-    if (s->groups == 0 || s->experts % s->groups) return "route: groups must divide experts";
-    if (s->top_groups == 0 || s->top_groups > s->groups) return "route: top_groups must be 1 .. groups";
-    if (s->group_top < 1 || s->group_top > 2) return "route: group_top must be 1 or 2";
-    if (s->top_k > s->experts / s->groups * s->top_groups) return "route: top_k above the experts of top_groups groups";
-    *code = MSIM_E_LIMIT;
-    if (s->groups > MSIM_MAX_EXPERT_GROUPS) return "route: more than MSIM_MAX_EXPERT_GROUPS groups";
-    return nullptr;
-}
-
 uint32_t pow2(uint32_t v)
 {
     uint32_t p = 1;
@@ -1243,11 +1217,37 @@ template <typename D> hipError_t launch_dropout(const DropP &d, hipStream_t st)
 
 } // namespace
 
+const char *msim_check_route(const msim_route_spec *s, bool backward, int *code) noexcept
+{
+    *code = MSIM_E_ARG;
+    if (!s) return "route: null spec";
+    if (s->version != MSIM_ABI_VERSION) return "route: spec version mismatch";
+    if (s->dtype > MSIM_BF16) return "route: unknown dtype";
+    if (s->score > MSIM_SCORE_SIGMOID) return "route: unknown score";
+    if (s->experts == 0 || s->top_k == 0) return "route: experts and top_k must be at least 1";
+    if (s->renorm > 1) return "route: renorm must be 0 or 1";
+    if (!std::isfinite(s->scale)) return "route: scale must be finite";
+    if (s->rows && s->row_stride < s->experts) return "route: row_stride below experts";
+    *code = MSIM_E_LIMIT;
+    if (s->experts > MSIM_MAX_EXPERTS) return "route: more than MSIM_MAX_EXPERTS experts";
+    if (s->top_k > MSIM_MAX_TOP_K) return "route: top_k above MSIM_MAX_TOP_K";
+    if (s->rows >> 31 || s->row_stride >> 40) return "route: 2^31 rows or more, or a row_stride of 2^40 or more";
+    *code = MSIM_E_ARG;
+    if (backward) return s->top_k > s->experts ? "route: top_k above experts" : nullptr;
+    if (s->groups == 0 || s->experts % s->groups) return "route: groups must divide experts";
+    if (s->top_groups == 0 || s->top_groups > s->groups) return "route: top_groups must be 1 .. groups";
+    if (s->group_top < 1 || s->group_top > 2) return "route: group_top must be 1 or 2";
+    if (s->top_k > s->experts / s->groups * s->top_groups) return "route: top_k above the experts of top_groups groups";
+    *code = MSIM_E_LIMIT;
+    if (s->groups > MSIM_MAX_EXPERT_GROUPS) return "route: more than MSIM_MAX_EXPERT_GROUPS groups";
+    return nullptr;
+}
+
 extern "C" int msim_route(const msim_route_spec *s, const void *logits, const float *bias, int32_t *ids,
                           float *weights, int32_t *load, void *hip_stream)
 {
     int code;
-    if (const char *why = check_route(s, false, &code)) return fail(code, why);
+    if (const char *why = msim_check_route(s, false, &code)) return fail(code, why);
     if (s->rows && (!logits || !ids || !weights)) return fail(MSIM_E_ARG, "route: null logits, ids or weights");
     RouteP p = {logits, bias, ids, weights, load, s->rows, s->row_stride, s->experts, s->top_k, s->groups,
                 s->top_groups, s->group_top, s->renorm, s->score == MSIM_SCORE_SIGMOID, s->scale, 0, 0, 0, 0};
@@ -1262,7 +1262,7 @@ extern "C" int msim_route_backward(const msim_route_spec *s, const void *logits,
                                    const float *grad, void *grad_logits, uint64_t grad_stride, void *hip_stream)
 {
     int code;
-    if (const char *why = check_route(s, true, &code)) return fail(code, why);
+    if (const char *why = msim_check_route(s, true, &code)) return fail(code, why);
     if (s->rows == 0) return MSIM_OK;
     if (!logits || !ids || !grad || !grad_logits) return fail(MSIM_E_ARG, "route: null logits, ids or gradient");
     if (grad_stride < s->experts) return fail(MSIM_E_ARG, "route: grad_stride below experts");

@@ -29,11 +29,11 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .sim import (ABI_VERSION, MAX_TRAFFIC_HOSTS, LinearSpec, MsimError, OrthogonalizeSpec, RouteSpec, TrafficSpec,
+from .sim import (ABI_VERSION, MAX_TRAFFIC_HOSTS, LayerSpec, LinearSpec, MsimError, OrthogonalizeSpec, RouteSpec, TrafficSpec,
                   load_library)
 
 __all__ = ["Routing", "route", "route_backward", "dropout", "dropout_backward", "traffic", "LinearGrads", "linear",
-           "linear_backward", "orthogonalize"]
+           "linear_backward", "Layer", "layer", "orthogonalize"]
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -424,6 +424,78 @@ def linear_backward(x: torch.Tensor, weight: torch.Tensor, grad: torch.Tensor, *
         return g
 
     return _run(dev, stream, call, x, weight, grad, pre, *(() if out is None else out))
+
+
+class Layer(NamedTuple):
+    """What layer() returns: y [rows, cols] in x's type, and the Routing it used."""
+    y: torch.Tensor
+    routing: Routing
+
+
+def layer(x: torch.Tensor, gate: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, top_k: int, *, act: str = "silu",
+          gated: bool = True, score: str = "softmax", bias: Optional[torch.Tensor] = None, groups: int = 1,
+          top_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+          mask: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None, out: Optional[Layer] = None,
+          stream=None) -> Layer:
+    """A whole mixture-of-experts layer for a few tokens (at most 512): routes
+    every row of x [rows, cols] by its logits x gate^T as route() does, and sums
+    what the chosen experts answer, by their weights, onto residual.
+
+    gate [experts, cols]; an expert answers w_out[e] h with h = act(a) * b, a and
+    b the two halves of w_in[e] x; without gated, h = act(w_in[e] x).  w_in
+    [experts, 2 hidden (or hidden), cols], w_out [experts, cols, hidden]; all of
+    x's type.  act as in linear().  mask (bool [rows]): False for rows of padding,
+    which route nowhere and get the residual alone, whatever x holds there.
+    out.y may be residual."""
+    dev, rows, cols, xs = _need_rows(x, "x")
+    if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
+        raise ValueError("gate must be a tensor of two dimensions")
+    if not isinstance(w_out, torch.Tensor) or w_out.dim() != 3:
+        raise ValueError("w_out must be a tensor of three dimensions")
+    experts, hidden = gate.shape[0], w_out.shape[2]
+    if cols < 1 or hidden < 1 or experts < 1:
+        raise ValueError("cols, hidden and experts must be at least 1")
+    _need(gate, "gate", x.dtype, dev, (experts, cols))
+    _need(w_in, "w_in", x.dtype, dev, (experts, 2 * hidden if gated else hidden, cols))
+    _need(w_out, "w_out", x.dtype, dev, (experts, cols, hidden))
+    k = _range(top_k, "top_k", 1, experts)
+    if bias is not None:
+        _need(bias, "bias", torch.float32, dev, (experts,))
+    if mask is not None:
+        _need(mask, "mask", torch.bool, dev, (rows,))
+    rs = cols if residual is None else _like(residual, "residual", x.dtype, dev, (rows, cols))
+    ys, load = cols, None
+    if out is not None:
+        ys = _like(out.y, "out.y", x.dtype, dev, (rows, cols))
+        load = out.routing.load
+        _need(out.routing.ids, "out.routing.ids", torch.int32, dev, (rows, k))
+        _need(out.routing.weights, "out.routing.weights", torch.float32, dev, (rows, k))
+        if load is not None:
+            _need(load, "out.routing.load", torch.int32, dev, (experts,))
+    limit = 1 << 20
+    spec = LayerSpec(ABI_VERSION, _DTYPES[x.dtype], _act(act), 1 if gated else 0, _range(cols, "cols", 1, limit),
+                     _range(hidden, "hidden", 1, limit), xs, ys, rs,
+                     RouteSpec(ABI_VERSION, 0, _score(score), _range(experts, "experts", 1, limit), k, _range(groups, "groups", 1, limit),
+                               _range(top_groups, "top_groups", 1, limit), _range(group_top, "group_top", 1, 2),
+                               1 if renorm else 0, float(scale), rows, experts))
+
+    def call(on):
+        lib = load_library()
+        mem, size = _workspace(x, lib.msim_layer_workspace, C.byref(spec))
+        r = out
+        if r is None:
+            new = x.new_empty
+            r = Layer(new((rows, cols)), Routing(new((rows, k), dtype=torch.int32), new((rows, k), dtype=torch.float32),
+                                                 new(experts, dtype=torch.int32)))
+        _call(lib.msim_layer(C.byref(spec), x.data_ptr(), gate.data_ptr(), _p(bias), w_in.data_ptr(), w_out.data_ptr(),
+                             _p(mask), _p(residual), r.y.data_ptr(), r.routing.ids.data_ptr(), r.routing.weights.data_ptr(),
+                             _p(r.routing.load), _p(mem), size, on))
+        if out is not None:
+            _changed(out.y, *out.routing)
+        return r
+
+    return _run(dev, stream, call, x, gate, w_in, w_out, bias, mask, residual,
+                *(() if out is None else (out.y, *out.routing)))
 
 
 def orthogonalize(update: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,

@@ -34,7 +34,7 @@ EXPORTED = ["msim_create", "msim_workspace_size", "msim_bind", "msim_run", "msim
             "msim_last_error", "msim_destroy", "msim_lds_probe",
             "msim_route", "msim_route_backward", "msim_dropout", "msim_traffic",
             "msim_linear", "msim_linear_workspace", "msim_linear_backward", "msim_linear_backward_workspace",
-            "msim_orthogonalize", "msim_orthogonalize_workspace"]
+            "msim_orthogonalize", "msim_orthogonalize_workspace", "msim_layer", "msim_layer_workspace"]
 
 _P8, _P32, _P64 = C.POINTER(C.c_uint8), C.POINTER(C.c_uint32), C.POINTER(C.c_uint64)
 
@@ -87,6 +87,12 @@ class LinearSpec(C.Structure):
                 ("x_stride", C.c_uint64), ("weight_stride", C.c_uint64), ("out_stride", C.c_uint64),
                 ("residual_stride", C.c_uint64), ("pre_stride", C.c_uint64),
                 ("dx_stride", C.c_uint64), ("dweight_stride", C.c_uint64)]
+
+
+class LayerSpec(C.Structure):
+    _fields_ = [("version", C.c_uint32), ("dtype", C.c_uint32), ("act", C.c_uint32), ("gated", C.c_uint32),
+                ("cols", C.c_uint32), ("hidden", C.c_uint32), ("x_stride", C.c_uint64), ("out_stride", C.c_uint64),
+                ("residual_stride", C.c_uint64), ("route", RouteSpec)]
 
 
 class OrthogonalizeSpec(C.Structure):
@@ -143,6 +149,8 @@ def load_library():
     lib.msim_linear_backward_workspace.argtypes = [C.POINTER(LinearSpec), vp, vp, vp, C.c_uint32, C.c_uint32, C.c_uint32,
                                                    _P64]
     lib.msim_linear_backward.argtypes = [C.POINTER(LinearSpec), vp, vp, vp, vp, vp, vp, vp, vp, C.c_uint64, vp]
+    lib.msim_layer_workspace.argtypes = [C.POINTER(LayerSpec), _P64]
+    lib.msim_layer.argtypes = [C.POINTER(LayerSpec), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, C.c_uint64, vp]
     lib.msim_orthogonalize_workspace.argtypes = [C.POINTER(OrthogonalizeSpec), _P64]
     lib.msim_orthogonalize.argtypes = [C.POINTER(OrthogonalizeSpec), vp, vp, vp, C.c_uint64, vp]
     for name in EXPORTED:

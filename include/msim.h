@@ -595,6 +595,36 @@ int msim_linear_backward(const msim_linear_spec *spec, const void *x, const void
                          uint64_t workspace_bytes, void *hip_stream);
 
 /*
+ * A whole mixture-of-experts layer for a few tokens, as a decoding step has them:
+ * logits = x gate^T, formed in 64 bits and rounded to 32; ids, weights and load of
+ * msim_route on them; y = the sum over a token's choices of weight * w_out[e]
+ * h, h = act(w_in[e] x), or with gated = 1 act(first half of w_in[e] x) * (second
+ * half of it); out = y + residual.  x, out, residual: rows x cols of type dtype;
+ * gate: experts x cols, w_in: experts x (hidden, gated: 2 hidden) x cols, w_out:
+ * experts x cols x hidden, all of type dtype and contiguous.  h is rounded to
+ * dtype.  mask (may be NULL): one byte a row; a row with 0 is padding, whatever x
+ * holds there: ids -1, weights 0, y 0.  A row that the router voids (a NaN logit)
+ * has y NaN.  bias is msim_route's.  route.dtype is MSIM_F32 and route.row_stride
+ * is route.experts.  Only chosen experts' weights are read.  residual may be out.
+ * Limits: msim_route's, rows <= MSIM_MAX_LAYER_ROWS, cols and hidden <=
+ * MSIM_MAX_LINEAR, experts times either below 2^24.
+ */
+#define MSIM_MAX_LAYER_ROWS 512
+
+typedef struct msim_layer_spec {
+    uint32_t version;            /* MSIM_ABI_VERSION */
+    uint32_t dtype, act, gated;
+    uint32_t cols, hidden;
+    uint64_t x_stride, out_stride, residual_stride;
+    msim_route_spec route;
+} msim_layer_spec;
+
+int msim_layer_workspace(const msim_layer_spec *spec, uint64_t *bytes);
+int msim_layer(const msim_layer_spec *spec, const void *x, const void *gate, const float *bias, const void *w_in,
+               const void *w_out, const uint8_t *mask, const void *residual, void *out, int32_t *ids,
+               float *weights, int32_t *load, void *workspace, uint64_t workspace_bytes, void *hip_stream);
+
+/*
  * The update of a weight matrix with its singular values moved towards 1, by
  * Newton-Schulz products: X = update / (Frobenius norm + eps), then `steps` times
  * X <- a X + (b X X^T + c (X X^T)^2) X; of a tall matrix on its transpose, which is
