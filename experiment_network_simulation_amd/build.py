@@ -12,9 +12,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmsim.so")
-SOURCES = [os.path.join(CSRC, "msim_kernel.hip"), os.path.join(CSRC, "msim_probe.hip"),
-           os.path.join(CSRC, "msim_moe.hip"), os.path.join(CSRC, "msim_gemm.hip"),
-           os.path.join(CSRC, "msim_layer.hip"), os.path.join(CSRC, "msim_host.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in
+           ("msim_gemm_split.hip", "msim_gemm_bf16.hip", "msim_gemm_f16.hip", "msim_gemm_f32.hip", "msim_kernel.hip",
+            "msim_probe.hip", "msim_moe.hip", "msim_linear.hip", "msim_layer.hip", "msim_host.cpp")]
 ARCH = os.environ.get("MSIM_OFFLOAD_ARCH", "gfx950")
 
 

@@ -1,0 +1,10 @@
+/* The products of bf16. */
+#include "msim_gemm_kernel.h"
+
+namespace msim {
+
+template hipError_t launch_gemm<M_BF16, false, false>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_gemm<M_BF16, false, true>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_gemm<M_BF16, true, true>(GemmP, const Plan &, hipStream_t);
+
+} // namespace msim

@@ -1,0 +1,10 @@
+/* The products of 32-bit numbers. */
+#include "msim_gemm_kernel.h"
+
+namespace msim {
+
+template hipError_t launch_gemm<M_F32, false, false>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_gemm<M_F32, false, true>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_gemm<M_F32, true, true>(GemmP, const Plan &, hipStream_t);
+
+} // namespace msim

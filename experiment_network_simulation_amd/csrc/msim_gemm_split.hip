@@ -1,0 +1,9 @@
+/* The products of numbers that are the sum of two f16. */
+#include "msim_gemm_kernel.h"
+
+namespace msim {
+
+template hipError_t launch_gemm<M_SPLIT, false, false>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_gemm<M_SPLIT, false, true>(GemmP, const Plan &, hipStream_t);
+
+} // namespace msim

@@ -117,10 +117,10 @@ __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint3
         for (int j = 0; j < (p.gated ? 1 : 2); j++) {
             const uint32_t f = f0 + j * 16 + (lane >> 4) * 4;
             if (f >= p.F) continue;        /* rows of h have room to a multiple of 8 */
-            for (int k = 0; k < 4; k++) {
-                const float v = act_of(j ? acc[i][1][k] : acc[i][0][k], p.act);
-                h[f + k] = D::put(p.gated ? v * acc[i][1][k] : v);
-            }
+            float v[4];
+            for (int k = 0; k < 4; k++) v[k] = j ? acc[i][1][k] : acc[i][0][k];
+            act_of<4>(v, p.act);
+            for (int k = 0; k < 4; k++) h[f + k] = D::put(p.gated ? v[k] * acc[i][1][k] : v[k]);
         }
     }
 }

@@ -1,467 +1,15 @@
-/* Matrix products: a linear layer with bias, activation and residual, its
- * gradient, and the orthogonal update of a weight matrix by Newton-Schulz products
- * (msim_linear, msim_linear_backward and msim_orthogonalize of include/msim.h,
- * which has the definitions).
- *
- * One kernel makes every product, C[m][n] = sum over k of A[m][k] B[n][k], from
- * operands that are contiguous along k or along m (n); what becomes of the sums
- * is its epilogue.  Sums are 32-bit, their order depends on the sizes alone.
+/* A linear layer with bias, activation and residual, its gradient, and the
+ * orthogonal update of a weight matrix by Newton-Schulz products (msim_linear,
+ * msim_linear_backward and msim_orthogonalize of include/msim.h, which has the
+ * definitions).
  */
 
 #include <algorithm>
 #include <cmath>
 
-#include "msim_stream.h"
+#include "msim_gemm.h"
 
 namespace {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
-
-/* element types of a product: the three of the library, and a number as the sum
- * of two f16, of which 32 columns lie as 32 high parts and 32 low ones */
-enum { M_F32 = MSIM_F32, M_F16 = MSIM_F16, M_BF16 = MSIM_BF16, M_SPLIT = 3 };
-
-constexpr uint32_t OUTSIDE = 0x80000000u;  /* an offset past every buffer: the load gives zeros */
-
-/* what the wavefront's lanes wrote to LDS is there for its other lanes */
-__device__ __forceinline__ void wave_sync()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
-/* ------------------------------------------------------------------------ */
-/* operands                                                                  */
-/* ------------------------------------------------------------------------ */
-
-struct Operand {
-    const char *at;
-    uint64_t extent;             /* bytes that may be read from `at` on */
-    uint64_t ld, batch;          /* bytes between rows, between matrices */
-};
-
-/* BT rows (m or n) by 128 bytes of k (64 columns of 16 bits, 32 of 32 bits or of
- * two halves) in LDS.
- *
- * Contiguous along k: LDS rows are the operand's, 128 bytes each.  A wavefront's
- * fragments are 16 bytes of each of 32 rows; the 16-byte pieces of a row are
- * exchanged by (row / 2) mod 8, so that 16 rows cover all banks.
- * Contiguous along m (MC): LDS rows are those of k, BT columns each.  16-bit
- * fragments are read with a transposition, 32 bytes of 4 rows by 16 lanes; pieces
- * of 64 bytes are exchanged by the row, so that those 4 rows lie in different
- * banks.  32-bit fragments are one element of two rows; pieces of 128 bytes are
- * exchanged between rows that are 4 apart.
- *
- * Tiles go from memory to LDS without registers; the exchange is made in the
- * addresses that the lanes read.  Rows and columns outside the operand are read
- * as zeros, through an offset outside the buffer. */
-template <int MODE, bool MC, int BT, int THREADS> struct Tile {
-    static constexpr int ES = MODE == M_F16 || MODE == M_BF16 ? 2 : 4;   /* bytes of a column */
-    static constexpr int BK = 128 / ES;                                  /* columns of k */
-    static constexpr int W = MC ? BT * ES : 128, R = MC ? BK : BT;       /* bytes of an LDS row, rows */
-    static constexpr int BYTES = R * W, LOADS = BYTES / 16 / THREADS;
-    static_assert(R * W == BT * 128 && LOADS * 16 * THREADS == BYTES, "whole loads");
-
-    const char *at;
-    uint64_t extent, step;
-    uint32_t off[LOADS];
-    uint32_t k_end;              /* MC: rows of k; otherwise bytes of a row */
-
-    /* the source of LDS byte b of row r, and the other way round */
-    static __device__ __forceinline__ uint32_t exchange(uint32_t r, uint32_t b)
-    {
-        if constexpr (!MC) return b ^ ((r >> 1 & 7) << 4);
-        else if constexpr (MODE == M_F32) return b ^ ((r >> 2 & 1) << 7);
-        else if constexpr (W >= 256) return b ^ ((r & 3) << 6);
-        else return b ^ ((r >> 1 & 1) << 6);
-    }
-
-    __device__ __forceinline__ void init(const Operand &o, uint32_t batch, uint32_t row0, uint32_t rows, uint32_t K)
-    {
-        const uint64_t first = MC ? (uint64_t)row0 * ES : row0 * o.ld;
-        at = o.at + batch * o.batch + first;
-        extent = o.extent > first ? o.extent - first : 0;
-        step = MC ? BK * o.ld : 128;
-        k_end = MC ? K : K * ES;
-        _Pragma("unroll") for (int i = 0; i < LOADS; i++) {
-            const uint32_t c = i * THREADS + threadIdx.x, r = c / (W / 16), b = exchange(r, c % (W / 16) * 16);
-            /* of a split matrix 32 columns lie together, high parts and low ones */
-            const uint32_t col = MODE == M_SPLIT ? b / 128 * 32 : b / ES;
-            const bool in = MC ? row0 + col < rows : row0 + r < rows;
-            off[i] = in ? (uint32_t)(r * o.ld) + b : OUTSIDE;
-        }
-    }
-
-    /* tile kt of k; every lane of the workgroup takes part */
-    __device__ __forceinline__ void load(uint32_t kt, char *lds) const
-    {
-        const uint64_t done = kt * step, left = extent > done ? extent - done : 0;
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(at + done), 0, (int)(left < 0x7FFFFFFF ? left : 0x7FFFFFFF), 0x00020000);
-        const uint32_t k0 = kt * (MC ? BK : 128);
-        const bool whole = k0 + (MC ? BK : 128) <= k_end;
-        _Pragma("unroll") for (int i = 0; i < LOADS; i++) {
-            uint32_t o = off[i];
-            if (!whole) {
-                const uint32_t c = i * THREADS + threadIdx.x, r = c / (W / 16);
-                const uint32_t k = k0 + (MC ? r : exchange(r, c % (W / 16) * 16));
-                o = k < k_end ? o : OUTSIDE;
-            }
-            const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)(lds + (i * THREADS + wave * WAVE) * 16),
-                                                     16, o, 0, 0, 0);
-        }
-    }
-};
-
-/* Fragments of 32 rows by 16 bytes of k (in each half of the wavefront) out of a Tile. */
-template <int MODE, bool MC, int BT> struct Reader {
-    typedef Tile<MODE, MC, BT, 64> T;
-    uint32_t base, x;
-
-    __device__ __forceinline__ void init(uint32_t row0)
-    {
-        const uint32_t lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5, l = lane & 15;
-        if constexpr (!MC) {
-            base = (row0 + l32) * 128;
-            x = half << 4 ^ (l32 >> 1 & 7) << 4;
-        } else if constexpr (MODE == M_F32) {
-            base = half * 4 * T::W + l32 * 4;
-            x = (row0 * 4) ^ half << 7;
-        } else {
-            const uint32_t r = half * 8 + (l >> 2);
-            base = r * T::W + (l & 3) * 8;
-            x = T::exchange(r, (MODE == M_SPLIT ? row0 * 4 : row0 * 2) + (lane >> 4 & 1) * 32);
-        }
-    }
-
-    /* Block i of 32 rows, step s of k (4, or 2 with parts: low 0 or 1).  Rows of k 4
-     * apart have the same exchange; row0 is a multiple of the wavefront's rows, so
-     * blocks are other bits of x. */
-    __device__ __forceinline__ u32x4 get(const char *lds, int i, int s, int low) const
-    {
-        if constexpr (!MC) {
-            return *(const u32x4 *)(lds + base + i * (32 * 128) + (x ^ ((low * 4 + s * 2) << 4)));
-        } else if constexpr (MODE == M_F32) {
-            u32x4 v;
-            for (int e = 0; e < 4; e++) v[e] = *(const uint32_t *)(lds + base + (s * 8 + e) * T::W + (x ^ (i * 128)));
-            return v;
-        } else {
-            const uint32_t b = base + s * 16 * T::W + (MODE == M_SPLIT ? x ^ (i * 128 + low * 64) : x ^ (i * 64));
-            typedef __attribute__((address_space(3))) i16x4 *at;
-            const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)(lds + b));
-            const i16x4 c = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)(lds + b + 4 * T::W));
-            return __builtin_bit_cast(u32x4, __builtin_shufflevector(a, c, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
-    }
-};
-
-template <int MODE> __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c)
-{
-    if constexpr (MODE == M_BF16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    else if constexpr (MODE == M_F32) {
-        const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
-        for (int e = 0; e < 4; e++) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], y[e], c, 0, 0, 0);
-        return c;
-    } else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
-/* ------------------------------------------------------------------------ */
-/* what becomes of a sum                                                     */
-/* ------------------------------------------------------------------------ */
-
-template <int MODE> struct Type { typedef F16 D; };
-template <> struct Type<M_F32> { typedef F32 D; };
-template <> struct Type<M_BF16> { typedef BF16 D; };
-
-struct Epilogue {
-    uint32_t M, N;
-    void *out;                   /* 32 bits (out32) or the operands' type, as res */
-    uint64_t out_ld;             /* elements, as the others */
-    const float *bias;
-    const void *res;
-    uint64_t res_ld;
-    void *pre;                   /* of the operands' type */
-    uint64_t pre_ld;
-    uint32_t act, out32, vec;    /* vec: rows of out, res and pre on 16 bytes */
-    /* orthogonal update: out = alpha src + beta sum, split matrices of out_ld columns (a multiple of 32) */
-    const void *src;
-    uint64_t out_batch;          /* bytes between matrices of out and src */
-    float alpha, beta;
-};
-
-__device__ __forceinline__ float slope_of(float z, uint32_t act)
-{
-    switch (act) {
-    case MSIM_ACT_RELU: return z > 0 ? 1.0f : z != z ? z : 0.0f;
-    case MSIM_ACT_SILU: {
-        const float s = 1.0f / (1.0f + expf(-z));
-        return s * (1.0f + z * (1.0f - s));
-    }
-    case MSIM_ACT_GELU: return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z);
-    case MSIM_ACT_GELU_TANH: {
-        const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
-        return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
-    }
-    default: return 1.0f;
-    }
-}
-
-/* eight elements from p on, n of them there; vec: p is on 16 bytes */
-template <typename D> __device__ __forceinline__ void load8(float *v, const void *p, uint64_t at, uint32_t n, bool vec)
-{
-    typedef typename D::raw raw;
-    typedef raw part __attribute__((ext_vector_type(16 / sizeof(raw))));
-    const raw *q = (const raw *)p + at;
-    if (vec && n == 8) {
-        _Pragma("unroll") for (uint32_t i = 0; i < 8; i += 16 / sizeof(raw)) {
-            const part w = *(const part *)(q + i);
-            for (uint32_t j = 0; j < 16 / sizeof(raw); j++) v[i + j] = D::get(w[j]);
-        }
-    } else {
-        _Pragma("unroll") for (uint32_t i = 0; i < 8; i++) v[i] = i < n ? D::get(q[i]) : 0.0f;
-    }
-}
-template <typename D> __device__ __forceinline__ void store8(const float *v, void *p, uint64_t at, uint32_t n, bool vec)
-{
-    typedef typename D::raw raw;
-    typedef raw part __attribute__((ext_vector_type(16 / sizeof(raw))));
-    raw *q = (raw *)p + at;
-    if (vec && n == 8) {
-        _Pragma("unroll") for (uint32_t i = 0; i < 8; i += 16 / sizeof(raw)) {
-            part w;
-            for (uint32_t j = 0; j < 16 / sizeof(raw); j++) w[j] = D::put(v[i + j]);
-            *(part *)(q + i) = w;
-        }
-    } else {
-        _Pragma("unroll") for (uint32_t i = 0; i < 8; i++)
-            if (i < n) q[i] = D::put(v[i]);
-    }
-}
-
-/* A number as the sum of two f16: 22 bits of it, for what is not below 2^-14. */
-__device__ __forceinline__ void split_of(float v, uint16_t &hi, uint16_t &lo)
-{
-    const _Float16 h = (_Float16)v;
-    hi = __builtin_bit_cast(uint16_t, h);
-    lo = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)h));
-}
-
-typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-
-/* eight columns from n (a multiple of 8) on of row m of a split matrix: where the high parts begin */
-__device__ __forceinline__ uint64_t split_at(uint64_t ld, uint32_t m, uint32_t n)
-{
-    return ((uint64_t)m * ld + (n & ~31u)) * 2 + (n & 31);
-}
-__device__ __forceinline__ void load_split(float *v, const void *p, uint64_t at)
-{
-    const u16x8 h = *(const u16x8 *)((const uint16_t *)p + at), l = *(const u16x8 *)((const uint16_t *)p + at + 32);
-    for (int i = 0; i < 8; i++) v[i] = F16::get(h[i]) + F16::get(l[i]);
-}
-__device__ __forceinline__ void store_split(const float *v, void *p, uint64_t at)
-{
-    u16x8 h, l;
-    for (int i = 0; i < 8; i++) {
-        uint16_t a, b;
-        split_of(v[i], a, b);
-        h[i] = a;
-        l[i] = b;
-    }
-    *(u16x8 *)((uint16_t *)p + at) = h;
-    *(u16x8 *)((uint16_t *)p + at + 32) = l;
-}
-
-/* the sums v of row m, columns n .. n + 7 (n a multiple of 8) */
-template <int MODE> __device__ __forceinline__ void finish(const Epilogue &e, uint32_t batch, uint32_t m, uint32_t n, float *v)
-{
-    if (m >= e.M) return;
-    if constexpr (MODE == M_SPLIT) {
-        if (n >= e.out_ld) return;         /* columns behind N: sums of zeros, which keep them zero */
-        const uint64_t at = split_at(e.out_ld, m, n);
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (e.src) load_split(x, (const char *)e.src + batch * e.out_batch, at);
-        for (int i = 0; i < 8; i++) v[i] = e.alpha * x[i] + e.beta * v[i];
-        store_split(v, (char *)e.out + batch * e.out_batch, at);
-    } else {
-        typedef typename Type<MODE>::D D;
-        if (n >= e.N) return;
-        const uint32_t k = min(8u, e.N - n);
-        float x[8];
-        if (e.bias) {
-            load8<F32>(x, e.bias, n, k, false);
-            for (int i = 0; i < 8; i++) v[i] += x[i];
-        }
-        if (e.pre) store8<D>(v, e.pre, m * e.pre_ld + n, k, e.vec);
-        if (e.act) {
-            _Pragma("unroll 1") for (int i = 0; i < 8; i++) v[i] = act_of(v[i], e.act);
-        }
-        if (e.res) {
-            if (e.out32) load8<F32>(x, e.res, m * e.res_ld + n, k, e.vec);
-            else load8<D>(x, e.res, m * e.res_ld + n, k, e.vec);
-            for (int i = 0; i < 8; i++) v[i] += x[i];
-        }
-        if (e.out32) store8<F32>(v, e.out, m * e.out_ld + n, k, e.vec);
-        else store8<D>(v, e.out, m * e.out_ld + n, k, e.vec);
-    }
-}
-
-/* ------------------------------------------------------------------------ */
-/* the product                                                               */
-/* ------------------------------------------------------------------------ */
-
-struct GemmP {
-    Operand a, b;
-    uint32_t M, N, K, batch;
-    uint32_t tm, tn, nk, parts, per;       /* tiles of m, n and k; parts of k, tiles of k a part */
-    uint32_t mirror;                       /* C is symmetric: tiles below the diagonal are written on both sides */
-    float *part;                           /* parts > 1: sums of the parts, [batch][parts][M][part_ld] */
-    uint64_t part_ld;
-    Epilogue e;
-};
-
-template <int MODE, bool AMC, bool BMC, int BT, int THREADS>
-__global__ void __launch_bounds__(THREADS, 2) msim_gemm(GemmP p)
-{
-    constexpr int WAVES = THREADS / WAVE, WM = 2, WN = WAVES / WM;      /* wavefronts along m and n */
-    constexpr int RM = BT / WM, RN = BT / WN, IM = RM / 32, IN = RN / 32;
-    constexpr int STEPS = MODE == M_SPLIT ? 2 : 4;
-    typedef Tile<MODE, AMC, BT, THREADS> TA;
-    typedef Tile<MODE, BMC, BT, THREADS> TB;
-    __shared__ __attribute__((aligned(256))) char lds0[TA::BYTES + TB::BYTES];
-    __shared__ __attribute__((aligned(256))) char lds1[TA::BYTES + TB::BYTES];
-
-    /* Workgroups go to the 8 dies in turn: each die takes consecutive tiles, and
-     * those walk along m within bands of 8 tiles of n, so that what a die reads
-     * together stays in its cache. */
-    const uint32_t total = gridDim.x, q = total >> 3, r = total & 7, die = blockIdx.x & 7;
-    uint32_t id = die * q + min(die, r) + (blockIdx.x >> 3);
-    const uint32_t tiles = p.tm * p.tn;
-    const uint32_t group = id / tiles;
-    id -= group * tiles;
-    const uint32_t batch = group / p.parts, part = group - batch * p.parts;
-    const uint32_t band = id / (8 * p.tm), width = min(8u, p.tn - band * 8), in = id - band * 8 * p.tm;
-    const uint32_t bm = in / width, bn = band * 8 + in - bm * width;
-    if (p.mirror && bm < bn) return;
-    const uint32_t m0 = bm * BT, n0 = bn * BT;
-
-    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const uint32_t wm = wave % WM, wn = wave / WM;
-    TA ta;
-    TB tb;
-    ta.init(p.a, batch, m0, p.M, p.K);
-    tb.init(p.b, batch, n0, p.N, p.K);
-    Reader<MODE, AMC, BT> ra;
-    Reader<MODE, BMC, BT> rb;
-    ra.init(wm * RM);
-    rb.init(wn * RN);
-    f32x16 acc[IM][IN];
-    _Pragma("unroll") for (int i = 0; i < IM; i++)
-        _Pragma("unroll") for (int j = 0; j < IN; j++) acc[i][j] = f32x16{};
-
-    const uint32_t first = part * p.per, last = min(first + p.per, p.nk);
-    /* The tile at kt is in `cur` when all wavefronts have passed the barrier, and
-     * none of them reads `next` any more: the next tile goes there meanwhile. */
-    const auto turn = [&](uint32_t kt, const char *cur, char *next) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);          /* this wavefront's loads to LDS */
-        __syncthreads();
-        if (kt + 1 < last) {
-            ta.load(kt + 1, next);
-            tb.load(kt + 1, next + TA::BYTES);
-        }
-        _Pragma("unroll") for (int s = 0; s < STEPS; s++) {
-            u32x4 a[IM], b[IN];
-            _Pragma("unroll") for (int i = 0; i < IM; i++) a[i] = ra.get(cur, i, s, 0);
-            _Pragma("unroll") for (int j = 0; j < IN; j++) b[j] = rb.get(cur + TA::BYTES, j, s, 0);
-            _Pragma("unroll") for (int i = 0; i < IM; i++)
-                _Pragma("unroll") for (int j = 0; j < IN; j++) acc[i][j] = mma<MODE>(b[j], a[i], acc[i][j]);
-            if constexpr (MODE == M_SPLIT) {
-                u32x4 al[IM], bl[IN];
-                _Pragma("unroll") for (int i = 0; i < IM; i++) al[i] = ra.get(cur, i, s, 1);
-                _Pragma("unroll") for (int j = 0; j < IN; j++) bl[j] = rb.get(cur + TA::BYTES, j, s, 1);
-                _Pragma("unroll") for (int i = 0; i < IM; i++)
-                    _Pragma("unroll") for (int j = 0; j < IN; j++) acc[i][j] = mma<MODE>(bl[j], a[i], acc[i][j]);
-                _Pragma("unroll") for (int i = 0; i < IM; i++)
-                    _Pragma("unroll") for (int j = 0; j < IN; j++) acc[i][j] = mma<MODE>(b[j], al[i], acc[i][j]);
-            }
-        }
-    };
-    if (first < last) {
-        ta.load(first, lds0);
-        tb.load(first, lds0 + TA::BYTES);
-        for (uint32_t kt = first; kt < last; kt += 2) {
-            turn(kt, lds0, lds1);
-            if (kt + 1 < last) turn(kt + 1, lds1, lds0);
-        }
-    }
-
-    /* Through LDS to rows: a lane has, of row l32 of a block, four columns next to
-     * each other; it gets eight of one row, next to those of the lanes beside it. */
-    __syncthreads();
-    constexpr int C = RN / 4;                        /* 16-byte pieces of a row */
-    float *stage = (float *)(lds0 + wave * (32 * RN * 4));
-    static_assert(WAVES * 32 * RN * 4 <= TA::BYTES + TB::BYTES, "room for a block of 32 rows a wavefront");
-    const uint32_t l32 = lane & 31, half = lane >> 5;
-    _Pragma("unroll") for (int i = 0; i < IM; i++) {
-        _Pragma("unroll") for (int j = 0; j < IN; j++)
-            _Pragma("unroll") for (int g = 0; g < 4; g++) {
-                const f32x4 v = {acc[i][j][g * 4], acc[i][j][g * 4 + 1], acc[i][j][g * 4 + 2], acc[i][j][g * 4 + 3]};
-                *(f32x4 *)(stage + l32 * RN + ((j * 8 + g * 2 + half) ^ (l32 & (C - 1))) * 4) = v;
-            }
-        wave_sync();
-        const uint32_t mi = m0 + wm * RM + i * 32, ni = n0 + wn * RN;
-        _Pragma("unroll 1") for (uint32_t id = lane; id < 32 * RN / 8; id += 64) {
-            const uint32_t row = id / (RN / 8), c = id % (RN / 8) * 2;
-            const f32x4 x = *(const f32x4 *)(stage + row * RN + (c ^ (row & (C - 1))) * 4);
-            const f32x4 y = *(const f32x4 *)(stage + row * RN + ((c + 1) ^ (row & (C - 1))) * 4);
-            float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            if (p.parts > 1) {
-                if (mi + row < p.M && ni + c * 4 < p.part_ld) {
-                    f32x4 *to = (f32x4 *)(p.part + ((uint64_t)group * p.M + mi + row) * p.part_ld + ni + c * 4);
-                    to[0] = x;
-                    to[1] = y;
-                }
-            } else {
-                finish<MODE>(p.e, batch, mi + row, ni + c * 4, v);
-            }
-        }
-        if constexpr (MODE == M_SPLIT) {
-            if (p.mirror && bm != bn) {
-                _Pragma("unroll 1") for (uint32_t id = lane; id < 4 * RN; id += 64) {
-                    const uint32_t col = id % RN, r8 = id / RN * 8;
-                    float v[8];
-                    for (uint32_t k = 0; k < 8; k++)
-                        v[k] = stage[(r8 + k) * RN + ((col / 4) ^ ((r8 + k) & (C - 1))) * 4 + col % 4];
-                    finish<MODE>(p.e, batch, ni + col, mi + r8, v);
-                }
-            }
-        }
-        wave_sync();
-    }
-}
-
-/* The parts' sums together, in order, and what becomes of them. */
-template <int MODE> __global__ void __launch_bounds__(256) msim_gemm_join(GemmP p)
-{
-    const uint32_t wide = (uint32_t)(p.part_ld / 8);
-    const uint64_t n = (uint64_t)p.batch * p.M * wide, size = (uint64_t)p.M * p.part_ld;
-    for (uint64_t id = blockIdx.x * 256ull + threadIdx.x; id < n; id += gridDim.x * 256ull) {
-        const uint64_t row = id / wide;
-        const uint32_t c = (uint32_t)(id - row * wide) * 8, batch = (uint32_t)(row / p.M), m = (uint32_t)(row - (uint64_t)batch * p.M);
-        const float *q = p.part + (uint64_t)batch * p.parts * size + (uint64_t)m * p.part_ld + c;
-        f32x4 x = *(const f32x4 *)q, y = *(const f32x4 *)(q + 4);
-        for (uint32_t k = 1; k < p.parts; k++) {
-            q += size;
-            x += *(const f32x4 *)q;
-            y += *(const f32x4 *)(q + 4);
-        }
-        float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        finish<MODE>(p.e, batch, m, c, v);
-    }
-}
 
 /* ------------------------------------------------------------------------ */
 /* few rows                                                                  */
@@ -494,18 +42,23 @@ template <int MODE, int MT, int NT, int WAVES> __global__ void __launch_bounds__
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         const uint32_t m = i * 16 + l;
         if (i % WAVES != (int)wave || m >= p.e.M) continue;
-        for (int j = 0; j < NT; j++)
+        for (int j = 0; j < NT; j++) {
+            float u[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+            const uint32_t nj = n0 + j * 16 + (lane >> 4) * 4;
             for (uint32_t k = 0; k < 4; k++) {
-                const uint32_t n = n0 + j * 16 + (lane >> 4) * 4 + k;
+                if (p.e.bias && nj + k < p.e.N) u[k] += p.e.bias[nj + k];
+                if (p.e.pre && nj + k < p.e.N) ((raw *)p.e.pre)[m * p.e.pre_ld + nj + k] = D::put(u[k]);
+            }
+            act_of<4>(u, p.e.act);
+            for (uint32_t k = 0; k < 4; k++) {
+                const uint32_t n = nj + k;
                 if (n >= p.e.N) continue;
-                float v = acc[i][j][k];
-                if (p.e.bias) v += p.e.bias[n];
-                if (p.e.pre) ((raw *)p.e.pre)[m * p.e.pre_ld + n] = D::put(v);
-                v = act_of(v, p.e.act);
+                float v = u[k];
                 if (p.e.res) v += p.e.out32 ? ((const float *)p.e.res)[m * p.e.res_ld + n] : D::get(((const raw *)p.e.res)[m * p.e.res_ld + n]);
                 if (p.e.out32) ((float *)p.e.out)[m * p.e.out_ld + n] = v;
                 else ((raw *)p.e.out)[m * p.e.out_ld + n] = D::put(v);
             }
+        }
     }
 }
 
@@ -533,11 +86,30 @@ msim_pack(const void *from, uint64_t ld, void *to, uint32_t rows, uint32_t cols,
     }
 }
 
+/* v[i] = the activation's slope at v[i] */
+template <int N> __device__ __forceinline__ void slope_of(float *v, uint32_t act)
+{
+    switch (act) {
+    case MSIM_ACT_RELU: return each<N>(v, [](float z) { return z > 0 ? 1.0f : z != z ? z : 0.0f; });
+    case MSIM_ACT_SILU:
+        return each<N>(v, [](float z) {
+            const float s = 1.0f / (1.0f + expf(-z));
+            return s * (1.0f + z * (1.0f - s));
+        });
+    case MSIM_ACT_GELU:
+        return each<N>(v, [](float z) { return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z); });
+    case MSIM_ACT_GELU_TANH:
+        return each<N>(v, [](float z) {
+            const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
+            return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
+        });
+    }
+}
+
 /* The gradient in front of the activation, d = grad act'(pre), as the products
  * read it, and the sums of its columns over each workgroup's rows.  A workgroup
- * has GRAD_ROWS rows and 8 * lanes columns.  d is rounded to the operands' type,
+ * has `part` rows and 8 * lanes columns.  d is rounded to the operands' type,
  * as a matrix instruction reads it; the sums are of what is not rounded. */
-constexpr uint32_t GRAD_ROWS = 128;
 
 struct GradP {
     const void *grad, *pre;
@@ -545,7 +117,7 @@ struct GradP {
     void *d;                     /* NULL: grad itself is read by the products */
     float *sums;                 /* [blocks of rows][outs], or NULL */
     uint32_t rows, outs, wide;   /* wide: columns of d */
-    uint32_t act, grad32, lglanes, vec;
+    uint32_t act, grad32, lglanes, vec, part;
 };
 
 template <typename D> __global__ void __launch_bounds__(256) msim_linear_grad(GradP p)
@@ -554,16 +126,17 @@ template <typename D> __global__ void __launch_bounds__(256) msim_linear_grad(Gr
     const uint32_t lanes = 1u << p.lglanes, cols = 8 * lanes;
     const uint32_t across = (p.wide + cols - 1) / cols, by = blockIdx.x / across, bx = blockIdx.x - by * across;
     const uint32_t n = bx * cols + (threadIdx.x & (lanes - 1)) * 8, k = n < p.outs ? min(8u, p.outs - n) : 0;
-    const uint32_t end = min(p.rows, (by + 1) * GRAD_ROWS);
+    const uint32_t end = min(p.rows, (by + 1) * p.part);
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (n < p.wide)
-        for (uint32_t m = by * GRAD_ROWS + (threadIdx.x >> p.lglanes); m < end; m += 256u >> p.lglanes) {
+        for (uint32_t m = by * p.part + (threadIdx.x >> p.lglanes); m < end; m += 256u >> p.lglanes) {
             float g[8], z[8];
             if (p.grad32) load8<F32>(g, p.grad, m * p.grad_ld + n, k, p.vec);
             else load8<D>(g, p.grad, m * p.grad_ld + n, k, p.vec);
             if (p.act) {
                 load8<D>(z, p.pre, m * p.pre_ld + n, k, p.vec);
-                _Pragma("unroll 1") for (uint32_t i = 0; i < 8; i++) g[i] = i < k ? g[i] * slope_of(z[i], p.act) : 0.0f;
+                slope_of<8>(z, p.act);
+                for (uint32_t i = 0; i < 8; i++) g[i] = i < k ? g[i] * z[i] : 0.0f;
             }
             for (int i = 0; i < 8; i++) sum[i] += g[i];
             if (p.d) store8<D>(g, p.d, (uint64_t)m * p.wide + n, 8, true);
@@ -578,18 +151,18 @@ template <typename D> __global__ void __launch_bounds__(256) msim_linear_grad(Gr
     }
 }
 
-/* column sums of the workgroups together: 32 columns and 8 runs of rows a workgroup */
-__global__ void __launch_bounds__(256) msim_linear_bias_grad(const float *sums, uint32_t blocks, uint32_t outs, float *out)
+/* column sums of the workgroups together: 32 columns and 32 runs of rows a workgroup */
+__global__ void __launch_bounds__(1024) msim_linear_bias_grad(const float *sums, uint32_t blocks, uint32_t outs, float *out)
 {
-    __shared__ double part[256];
+    __shared__ double part[1024];
     const uint32_t c = blockIdx.x * 32 + (threadIdx.x & 31);
     double s = 0;
     if (c < outs)
-        for (uint32_t b = threadIdx.x >> 5; b < blocks; b += 8) s += sums[(uint64_t)b * outs + c];
+        _Pragma("unroll 4") for (uint32_t b = threadIdx.x >> 5; b < blocks; b += 32) s += sums[(uint64_t)b * outs + c];
     part[threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.x < 32 && c < outs) {
-        for (int i = 1; i < 8; i++) s += part[i * 32 + threadIdx.x];
+        for (int i = 1; i < 32; i++) s += part[i * 32 + threadIdx.x];
         out[c] = (float)s;
     }
 }
@@ -598,57 +171,45 @@ __global__ void __launch_bounds__(256) msim_linear_bias_grad(const float *sums, 
 /* host: products                                                            */
 /* ------------------------------------------------------------------------ */
 
+uint32_t size_of(uint32_t dtype) { return dtype == MSIM_F32 ? 4 : 2; }
 constexpr uint64_t MAX_LD = 8000000;       /* bytes: the offsets of a tile's 256 rows stay below 2^31 */
 
-uint32_t size_of(uint32_t dtype) { return dtype == MSIM_F32 ? 4 : 2; }
-uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
-
-/* How a product is cut: tiles of 256, 128 or 64 and parts of k. */
-struct Plan { uint32_t bt, parts, per, nk; uint64_t part_bytes; };
-
+/* The cheapest by an estimate in us.  Workgroups of a kind are on the card `slots`
+ * at a time; one takes `more`, and for a stage `low` where it has a compute unit to
+ * itself, `high` where the card is full (measured with sizes of 1,024 and 8,192);
+ * parts of k add the time of their sums through memory. */
 Plan plan_of(uint32_t mode, uint64_t M, uint64_t N, uint64_t K, uint64_t batch)
 {
-    const uint32_t bk = mode == M_F16 || mode == M_BF16 ? 64 : 32;
-    const uint64_t nk = (K + bk - 1) / bk;
-    Plan best = {64, 1, (uint32_t)std::max<uint64_t>(nk, 1), (uint32_t)nk, 0};
+    static const struct { double slots, more, low[3], high[3]; } times[] = {         /* 16 bits, 32 bits, split */
+        {256, 9, {1.15, 8.0, 1.7}, {1.6, 8.0, 2.2}}, {512, 4, {0.53, 1.8, 0.6}, {1.0, 3.6, 1.3}}, {512, 2, {0.25, 0.5, 0.3}, {0.41, 0.95, 0.5}},
+#ifdef TUNE
+        {512, 2}, {512, 2}, {512, 2}, {512, 2}, {512, 2},
+#endif
+    };
+    const uint32_t bk = mode == M_F16 || mode == M_BF16 ? 64 : 32, t = bk == 64 ? 0 : mode == M_F32 ? 1 : 2;
+    const uint64_t nk = (K + bk - 1) / bk, n = std::max<uint64_t>(nk, 1);
+    Plan best = {};
     double least = INFINITY;
-    const struct { uint32_t bt; double slots, turn; } kinds[] = {{256, 256, 1.0}, {128, 512, 0.65}, {64, 1024, 0.5}};
-    for (const auto &k : kinds) {
+    for (uint32_t i = 0; i < N_KINDS; i++) {
+        const Kind k = KINDS[i];
+        const auto &c = times[i];
+        if (mode == M_F32 && k.bt == 256) continue;        /* 32-bit products are so slow that tiles of 128 feed them as well */
         const uint64_t tiles = ((M + k.bt - 1) / k.bt) * ((N + k.bt - 1) / k.bt) * batch;
-        for (uint64_t parts = 1; parts <= 64 && parts <= std::max<uint64_t>(nk, 1); parts++) {
-            const uint64_t per = (std::max<uint64_t>(nk, 1) + parts - 1) / parts;
-            if ((std::max<uint64_t>(nk, 1) + per - 1) / per != parts) continue;
-            const double rounds = std::ceil((double)(tiles * parts) / k.slots);
-            double cost = rounds * k.turn * (per + 3.0);
-            if (parts > 1) cost += 6.0 + (double)batch * M * N * parts * 8.0 / 4e6;     /* us about: 4 TB/s, a launch */
+        for (uint64_t parts = 1; parts <= 64 && parts <= n; parts++) {
+            const uint64_t per = (n + parts - 1) / parts;
+            if ((n + per - 1) / per != parts) continue;
+            const double groups = (double)(tiles * parts), rounds = std::floor(groups / c.slots), rest = groups - rounds * c.slots;
+            double cost = rounds * (c.more + c.high[t] * per);
+            if (rest > 0) cost += c.more + (rest <= 256 && c.slots > 256 ? c.low[t] : rest > 128 ? c.high[t] : c.low[t]) * per;
+            if (parts > 1) cost += 4.0 + (double)batch * M * N * parts * 8.0 / 4e6;
             if (cost < least) {
                 least = cost;
-                best = {k.bt, (uint32_t)parts, (uint32_t)per, (uint32_t)nk, parts > 1 ? batch * parts * M * up(N, mode == M_SPLIT ? 32 : 8) * 4 : 0};
+                best = {i, (uint32_t)parts, (uint32_t)per, (uint32_t)nk,
+                        parts > 1 ? batch * parts * M * up(N, mode == M_SPLIT ? 32 : 8) * 4 : 0};
             }
         }
     }
     return best;
-}
-
-template <int MODE, bool AMC, bool BMC> hipError_t launch_gemm(GemmP p, const Plan &c, hipStream_t st)
-{
-    p.tm = (p.M + c.bt - 1) / c.bt;
-    p.tn = (p.N + c.bt - 1) / c.bt;
-    p.nk = c.nk;
-    p.parts = c.parts;
-    p.per = c.per;
-    p.part_ld = up(p.N, 8);
-    if (MODE == M_SPLIT) p.part_ld = up(p.N, 32);
-    if (p.parts > 1) p.mirror = 0;
-    const uint64_t grid = (uint64_t)p.tm * p.tn * p.parts * p.batch;
-    if (!grid) return hipSuccess;
-    hipError_t e;
-    if (c.bt == 256) e = launch(msim_gemm<MODE, AMC, BMC, 256, 512>, (uint32_t)grid, 512, 0, st, p);
-    else if (c.bt == 128) e = launch(msim_gemm<MODE, AMC, BMC, 128, 256>, (uint32_t)grid, 256, 0, st, p);
-    else e = launch(msim_gemm<MODE, AMC, BMC, 64, 256>, (uint32_t)grid, 256, 0, st, p);
-    if (e != hipSuccess || p.parts == 1) return e;
-    const uint64_t n = (uint64_t)p.batch * p.M * (p.part_ld / 8);
-    return launch(msim_gemm_join<MODE>, (uint32_t)std::min<uint64_t>((n + 255) / 256, 1u << 16), 256, 0, st, p);
 }
 
 /* Whether the products can read rows of `cols` elements as they lie: 16 bytes at a time. */
@@ -767,7 +328,7 @@ struct Backward {
     bool own;                    /* d is made: an activation, another type, or a grad that does not lie as it is read */
     uint64_t wide;               /* columns of d */
     uint64_t d_bytes, sum_bytes;
-    uint32_t blocks;
+    uint32_t blocks, part;       /* of rows, for the sums: about 1,024, of at least 8 rows */
     Plan px, pw;
     uint64_t bytes;
 };
@@ -781,7 +342,8 @@ Backward backward_of(const msim_linear_spec *s, const void *x, const void *weigh
     const bool need = dx || dw;
     b.own = need && (s->act || s->out_dtype != s->dtype || !ready(grad, s->rows, s->outs, s->out_stride, size));
     b.wide = b.own ? up(s->outs, 16 / size * (size == 4 ? 2 : 1)) : s->outs;
-    b.blocks = (uint32_t)((s->rows + GRAD_ROWS - 1) / GRAD_ROWS);
+    b.part = (uint32_t)std::max<uint64_t>(8, (s->rows + 1023) / 1024);
+    b.blocks = (uint32_t)((s->rows + b.part - 1) / b.part);
     b.d_bytes = b.own ? up(s->rows * b.wide * size, 256) : 0;
     b.sum_bytes = db ? up((uint64_t)b.blocks * s->outs * 4, 256) : 0;
     if (dx) b.px = plan_of(s->dtype, s->rows, s->cols, b.wide, 1);
@@ -801,7 +363,7 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
     if ((b.own || dbias) && s->rows) {
         const uint32_t gsize = size_of(s->out_dtype);
         GradP g = {grad, pre, s->out_stride, s->pre_stride, b.own ? wd : nullptr, dbias ? (float *)wsum : nullptr,
-                   (uint32_t)s->rows, s->outs, (uint32_t)up(s->outs, 8), s->act, s->out_dtype == MSIM_F32, 0, 0};
+                   (uint32_t)s->rows, s->outs, (uint32_t)up(s->outs, 8), s->act, s->out_dtype == MSIM_F32, 0, 0, b.part};
         if (b.own) g.wide = (uint32_t)b.wide;
         while (g.lglanes < 5 && (8u << g.lglanes) < g.wide) g.lglanes++;
         g.vec = on16(grad, s->out_stride, gsize) && (!s->act || on16(pre, s->pre_stride, size));
@@ -809,7 +371,7 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
         r = launch(msim_linear_grad<D>, (uint32_t)(b.blocks * across), 256, 0, st, g);
     }
     if (r == hipSuccess && dbias)
-        r = launch(msim_linear_bias_grad, (s->outs + 31) / 32, 256, 0, st, (const float *)wsum, s->rows ? b.blocks : 0, s->outs, dbias);
+        r = launch(msim_linear_bias_grad, (s->outs + 31) / 32, 1024, 0, st, (const float *)wsum, s->rows ? b.blocks : 0, s->outs, dbias);
     Operand d = {wd, s->rows * b.wide * size, b.wide * size, 0};
     if (!b.own) d = Matrix{grad, s->rows, s->outs, s->out_stride, size, false}.operand(nullptr);
     GemmP p = {};
@@ -853,18 +415,23 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
 /* X is held times this: its singular values stay near 1, so high parts are well
  * inside f16 and low parts above its subnormal numbers where they matter. */
 constexpr float ORTH_SCALE = 2048.0f;
-constexpr uint32_t NORM_PARTS = 64;
+constexpr uint32_t NORM_PARTS = 256;
 
 /* sums of squares in 64 bits: NORM_PARTS workgroups a matrix */
 template <typename D> __global__ void __launch_bounds__(256) msim_orth_norm(const void *from, uint64_t size, double *part)
 {
+    constexpr uint32_t PER = 16 / sizeof(typename D::raw);
+    typedef typename D::raw vec __attribute__((ext_vector_type(PER)));
     __shared__ double sums[4];
     const uint32_t batch = blockIdx.x / NORM_PARTS, k = blockIdx.x % NORM_PARTS;
     const typename D::raw *x = (const typename D::raw *)from + batch * size;
     double s = 0;
-    for (uint64_t i = k * 256 + threadIdx.x; i < size; i += NORM_PARTS * 256) {
-        const double v = D::get(x[i]);
-        s += v * v;
+    _Pragma("unroll 2") for (uint64_t i = (k * 256 + threadIdx.x) * PER; i < size; i += NORM_PARTS * 256 * PER) {
+        const vec v = __builtin_bit_cast(vec, i + PER <= size ? piece<D>(x + i) : piece<D>(x + i, 0, (uint32_t)(size - i)));
+        for (uint32_t j = 0; j < PER; j++) {
+            const double d = D::get(v[j]);
+            s += d * d;
+        }
     }
     for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
@@ -896,7 +463,8 @@ template <typename D, bool BEGIN> __global__ void __launch_bounds__(256) msim_or
     const uint64_t base = batch * p.rows * p.cols;
     if constexpr (BEGIN) {
         if (threadIdx.x < 64) {
-            double s = p.part[batch * NORM_PARTS + threadIdx.x];
+            const double *q = p.part + batch * NORM_PARTS + threadIdx.x;
+            double s = q[0] + q[64] + q[128] + q[192];
             for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
             if (threadIdx.x == 0) factor = s < INFINITY ? ORTH_SCALE / (sqrt(s) + p.eps) : NAN;
         }

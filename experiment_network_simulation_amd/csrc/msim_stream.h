@@ -105,14 +105,19 @@ template <int MT, int NT, int WAVES> __device__ __forceinline__ void join(f32x4 
             }
 }
 
-__device__ __forceinline__ float act_of(float z, uint32_t act)
+/* v[i] = f(v[i]) with the activation's function, chosen once for all N */
+template <int N, typename F> __device__ __forceinline__ void each(float *v, F f)
+{
+    _Pragma("unroll") for (int i = 0; i < N; i++) v[i] = f(v[i]);
+}
+template <int N> __device__ __forceinline__ void act_of(float *v, uint32_t act)
 {
     switch (act) {
-    case MSIM_ACT_RELU: return z < 0 ? 0.0f : z;                 /* a NaN stays one */
-    case MSIM_ACT_SILU: return z / (1.0f + expf(-z));
-    case MSIM_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case MSIM_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
-    default: return z;
+    case MSIM_ACT_RELU: return each<N>(v, [](float z) { return z < 0 ? 0.0f : z; });      /* a NaN stays one */
+    case MSIM_ACT_SILU: return each<N>(v, [](float z) { return z / (1.0f + expf(-z)); });
+    case MSIM_ACT_GELU: return each<N>(v, [](float z) { return 0.5f * z * (1.0f + erff(z * 0.70710678f)); });
+    case MSIM_ACT_GELU_TANH:
+        return each<N>(v, [](float z) { return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z))); });
     }
 }
 
