@@ -1,5 +1,5 @@
-/* What the kernels of msim_moe.hip, msim_gemm.hip and msim_layer.hip share:
- * element types and how a call launches and reports. */
+/* What the kernels of the calls without a context share: element types and how a
+ * call launches and reports. */
 #ifndef MSIM_DEVICE_H
 #define MSIM_DEVICE_H
 
@@ -33,6 +33,13 @@ struct BF16 {
     /* to nearest, ties to even; a NaN stays one */
     static __device__ raw put(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 };
+
+/* what the wavefront's lanes wrote to LDS is there for its other lanes */
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 [[maybe_unused]] inline int fail(int code, const char *what) { msim_set_error(what); return code; }
 

@@ -18,13 +18,6 @@ enum { M_F32 = MSIM_F32, M_F16 = MSIM_F16, M_BF16 = MSIM_BF16, M_SPLIT = 3 };
 
 constexpr uint32_t OUTSIDE = 0x80000000u;  /* an offset past every buffer: the load gives zeros */
 
-/* what the wavefront's lanes wrote to LDS is there for its other lanes */
-__device__ __forceinline__ void wave_sync()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 struct Operand {
     const char *at;
     uint64_t extent;             /* bytes that may be read from `at` on */

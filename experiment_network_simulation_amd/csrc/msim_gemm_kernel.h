@@ -12,13 +12,6 @@ typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t OUTSIDE = 0x80000000u;  /* an offset past every buffer: the load gives zeros */
 
-/* what the wavefront's lanes wrote to LDS is there for its other lanes */
-__device__ __forceinline__ void wave_sync()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 /* BT rows (m or n) by 128 bytes of k (64 columns of 16 bits, 32 of 32 bits or of
  * two halves) in LDS.
  *
@@ -175,9 +168,19 @@ template <int MODE> __device__ __forceinline__ void early_of(const Epilogue &e, 
     }
 }
 
-/* the sums v of row m, columns n .. n + 7 (n a multiple of 8) */
+/* The sums v of row m, columns n .. n + 7 (n a multiple of 8), the bias added: the activation, */
+template <int MODE> __device__ __forceinline__ void before(const Epilogue &e, uint32_t m, uint32_t n, float *v)
+{
+    typedef typename Type<MODE>::D D;
+    if (m >= e.M || n >= e.N) return;
+    const uint32_t k = min(8u, e.N - n);
+    if (e.pre) store8<D>(v, e.pre, m * e.pre_ld + n, k, e.vec);
+    act_of<8>(v, e.act);
+}
+
+/* and residual and result, or the next split matrix */
 template <int MODE>
-__device__ __forceinline__ void finish(const Epilogue &e, uint32_t batch, uint32_t m, uint32_t n, float *v, const typename Early<MODE>::T &x)
+__device__ __forceinline__ void after(const Epilogue &e, uint32_t batch, uint32_t m, uint32_t n, float *v, const typename Early<MODE>::T &x)
 {
     if (m >= e.M) return;
     if constexpr (MODE == M_SPLIT) {
@@ -194,13 +197,6 @@ __device__ __forceinline__ void finish(const Epilogue &e, uint32_t batch, uint32
         if (n >= e.N) return;
         const uint32_t k = min(8u, e.N - n);
         const bool vec = e.vec && k == 8;
-        if (e.bias) {
-            float b[8];
-            load8<F32>(b, e.bias, n, k, false);
-            for (int i = 0; i < 8; i++) v[i] += b[i];
-        }
-        if (e.pre) store8<D>(v, e.pre, m * e.pre_ld + n, k, vec);
-        act_of<8>(v, e.act);
         if (e.res) {
             float r[8];
             if (vec && (MODE == M_F32 || e.out32)) {
@@ -357,11 +353,20 @@ __global__ void __launch_bounds__(THREADS, 2) msim_gemm(GemmP p)
             return;
         }
     constexpr int HR = RM < 64 ? RM : 64, C = RN / 4, BLOCK = HR * RN * 4;      /* rows at a time; 16-byte pieces of a row */
-    constexpr int FIT = STAGE / BLOCK, G = HR * RN / 512 < 4 ? HR * RN / 512 : 4;
+    constexpr int FIT = STAGE / BLOCK, TURNS = HR * RN / 512;
     static_assert(WAVES <= DEPTH * FIT, "room for a block of every wavefront");
     float *const stage = (float *)(room(wave / FIT) + wave % FIT * BLOCK);
+    /* the lane's eight columns, and its row among those of a turn */
+    const uint32_t c8 = lane % (RN / 8), n8 = ni + c8 * 8, r8 = lane / (RN / 8);
+    const auto at = [&](uint32_t row, uint32_t half) { return (f32x4 *)(stage + row * RN + ((c8 * 2 + half) ^ (row & 15 & (C - 1))) * 4); };
+    float bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (p.e.bias && p.parts == 1 && n8 < p.N) load8<F32>(bias, p.e.bias, n8, min(8u, p.N - n8), false);
     _Pragma("unroll") for (int h = 0; h < RM / HR; h++) {
         const uint32_t mi = m0 + wm * RM + h * HR;
+        /* what is read of memory is asked for first */
+        typename Early<MODE>::T early[TURNS];
+        if (!p.plain)
+            _Pragma("unroll") for (int t = 0; t < TURNS; t++) early_of<MODE>(p.e, batch, mi + t * (512 / RN) + r8, n8, early[t]);
         _Pragma("unroll") for (int i = 0; i < HR / 32; i++)
             _Pragma("unroll") for (int j = 0; j < IN; j++)
                 _Pragma("unroll") for (int g = 0; g < 4; g++) {             /* columns 8 g + 4 (lane / 32) of a block */
@@ -381,30 +386,40 @@ __global__ void __launch_bounds__(THREADS, 2) msim_gemm(GemmP p)
                 if (r < rows) *(f32x4 *)(to + r * ld) = v;
             }
         } else {
-            /* what is read of memory for four pieces is asked for before */
-            _Pragma("unroll 1") for (uint32_t id = lane; id < HR * RN / 8; id += G * 64) {
-                typename Early<MODE>::T early[G];
-                _Pragma("unroll") for (int t = 0; t < G; t++)
-                    early_of<MODE>(p.e, batch, mi + (id + t * 64) / (RN / 8), ni + (id + t * 64) % (RN / 8) * 8, early[t]);
-                _Pragma("unroll") for (int t = 0; t < G; t++) {
-                    const uint32_t row = (id + t * 64) / (RN / 8), c = (id + t * 64) % (RN / 8) * 2, z = row & 15 & (C - 1);
-                    const f32x4 x = *(const f32x4 *)(stage + row * RN + (c ^ z) * 4);
-                    const f32x4 y = *(const f32x4 *)(stage + row * RN + ((c + 1) ^ z) * 4);
-                    float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-                    finish<MODE>(p.e, batch, mi + row, ni + c * 4, v, early[t]);
+            /* bias and activation, whose code is there once; then, in LDS until what is read of memory has
+             * come, the residual */
+            if constexpr (MODE != M_SPLIT) {
+                _Pragma("unroll 1") for (uint32_t row = r8; row < HR; row += 512 / RN) {
+                    const f32x4 x = *at(row, 0), y = *at(row, 1);
+                    float v[8];
+                    for (int i = 0; i < 8; i++) v[i] = (i < 4 ? x[i] : y[i - 4]) + bias[i];
+                    before<MODE>(p.e, mi + row, n8, v);
+                    if (p.e.res) {
+                        *at(row, 0) = f32x4{v[0], v[1], v[2], v[3]};
+                        *at(row, 1) = f32x4{v[4], v[5], v[6], v[7]};
+                    } else {
+                        after<MODE>(p.e, batch, mi + row, n8, v, early[0]);
+                    }
                 }
             }
+            if (MODE == M_SPLIT || p.e.res)
+                _Pragma("unroll") for (int t = 0; t < TURNS; t++) {
+                    const uint32_t row = t * (512 / RN) + r8;
+                    const f32x4 x = *at(row, 0), y = *at(row, 1);
+                    float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+                    after<MODE>(p.e, batch, mi + row, n8, v, early[t]);
+                }
         }
         if constexpr (MODE == M_SPLIT) {
             if (p.mirror && bm != bn) {
                 _Pragma("unroll 1") for (uint32_t id = lane; id < HR / 8 * RN; id += 64) {
-                    const uint32_t col = id % RN, r8 = id / RN * 8;
+                    const uint32_t col = id % RN, up8 = id / RN * 8;
                     float v[8];
                     for (uint32_t k = 0; k < 8; k++)
-                        v[k] = stage[(r8 + k) * RN + ((col / 4) ^ ((r8 + k) & 15 & (C - 1))) * 4 + col % 4];
+                        v[k] = stage[(up8 + k) * RN + ((col / 4) ^ ((up8 + k) & 15 & (C - 1))) * 4 + col % 4];
                     typename Early<MODE>::T e;
-                    early_of<MODE>(p.e, batch, ni + col, mi + r8, e);
-                    finish<MODE>(p.e, batch, ni + col, mi + r8, v, e);
+                    early_of<MODE>(p.e, batch, ni + col, mi + up8, e);
+                    after<MODE>(p.e, batch, ni + col, mi + up8, v, e);
                 }
             }
         }
@@ -430,7 +445,13 @@ template <int MODE> __global__ void __launch_bounds__(256) msim_gemm_join(GemmP 
             y += *(const f32x4 *)(q + 4);
         }
         float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        finish<MODE>(p.e, batch, m, c, v, early);
+        if constexpr (MODE != M_SPLIT) {
+            float bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (p.e.bias && c < p.N) load8<F32>(bias, p.e.bias, c, min(8u, p.N - c), false);
+            for (int i = 0; i < 8; i++) v[i] += bias[i];
+            before<MODE>(p.e, m, c, v);
+        }
+        after<MODE>(p.e, batch, m, c, v, early);
     }
 }
 

@@ -9,6 +9,7 @@
 
 #include <algorithm>
 
+#include "msim_route.h"
 #include "msim_stream.h"
 
 namespace {
@@ -93,9 +94,22 @@ __device__ __forceinline__ uint32_t tokens_of(const LayerP &p, uint32_t slot, ui
     return by_choice && list[0] != slot ? 0 : min(have, MAX_ROWS);
 }
 
+/* Four hidden units from f on (16 more of them 16 further, without a gate) of what
+ * goes into a token's row h of the second product, rounded to the layer's type, as
+ * its matrix instructions read it.  h has room to a multiple of 8. */
+template <typename D> __device__ __forceinline__ void hidden_of(const LayerP &p, const f32x4 *sums, uint32_t f, typename D::raw *h)
+{
+    for (uint32_t j = 0; j < (p.gated ? 1 : 2); j++, f += 16) {
+        if (f >= p.F) continue;
+        float v[4];
+        for (int k = 0; k < 4; k++) v[k] = j ? sums[1][k] : sums[0][k];
+        act_of<4>(v, p.act);
+        for (int k = 0; k < 4; k++) h[f + k] = D::put(p.gated ? v[k] * sums[1][k] : v[k]);
+    }
+}
+
 /* h = act(gate rows x) (up rows x), or act(rows x): 16 hidden units (32 without a
- * gate) of one expert for up to 16 MT of its tokens.  h is rounded to the layer's
- * type, as the second product's matrix instructions read it. */
+ * gate) of one expert for up to 16 MT of its tokens */
 template <typename D, int MT>
 __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, f32x4 *lds)
 {
@@ -113,15 +127,7 @@ __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint3
     join<MT, 2, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
-        raw *h = (raw *)p.h + (uint64_t)list[i * 16 + l] * p.h_ld;
-        for (int j = 0; j < (p.gated ? 1 : 2); j++) {
-            const uint32_t f = f0 + j * 16 + (lane >> 4) * 4;
-            if (f >= p.F) continue;        /* rows of h have room to a multiple of 8 */
-            float v[4];
-            for (int k = 0; k < 4; k++) v[k] = j ? acc[i][1][k] : acc[i][0][k];
-            act_of<4>(v, p.act);
-            for (int k = 0; k < 4; k++) h[f + k] = D::put(p.gated ? v[k] * acc[i][1][k] : v[k]);
-        }
+        hidden_of<D>(p, acc[i], f0 + (lane >> 4) * 4, (raw *)p.h + (uint64_t)list[i * 16 + l] * p.h_ld);
     }
 }
 
@@ -147,6 +153,91 @@ __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uin
             const uint32_t c = c0 + j * 16 + (lane >> 4) * 4;
             if (c < p.C) *(f32x4 *)(to + c) = acc[i][j];       /* rows of part have room to a multiple of 4 */
         }
+    }
+}
+
+/* One or a few tokens (rows <= FEW_ROWS): three launches.  Every choice of every
+ * token is a product of its own, and an expert that two tokens chose is read twice.
+ *
+ * The first product routes, too: every workgroup all rows, by route_row, which
+ * takes 1 to 2 us where msim_route would be a launch or two more. */
+constexpr uint32_t FEW_ROWS = 4;
+constexpr int FEW_WAVES = 16;
+
+template <typename D, int VPL> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_layer_up_few(LayerP p, RouteP r, int32_t *ids, float *weights, int32_t *load)
+{
+    typedef typename D::raw raw;
+    extern __shared__ double keys[];
+    __shared__ int32_t chosen[FEW_ROWS * MSIM_MAX_TOP_K];
+    __shared__ float shares[FEW_ROWS * MSIM_MAX_TOP_K];
+    __shared__ f32x4 sums[FEW_WAVES * 2 * 64];
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15, n = p.rows * p.K;
+    r.ids = chosen;
+    r.w = shares;
+    if (wave < p.rows) route_row<F32, VPL>(r, wave, keys + wave * p.E, nullptr);
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (uint32_t j = threadIdx.x; j < n; j += blockDim.x) {
+            ids[j] = chosen[j];
+            weights[j] = shares[j];
+        }
+        if (load)
+            for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
+                int32_t c = 0;
+                for (uint32_t j = 0; j < n; j++) c += chosen[j] == (int32_t)e;
+                load[e] = c;
+            }
+    }
+    const uint32_t tile = blockIdx.x % p.tiles, j = blockIdx.x / p.tiles, f0 = tile * (p.gated ? 16 : 32);
+    const int32_t expert = chosen[j];
+    if (expert < 0) return;
+    const raw *base = (const raw *)p.w_in + (uint64_t)expert * (p.gated ? 2 : 1) * p.F * p.C;
+    const raw *w[2] = {base + (uint64_t)min(f0 + l, p.F - 1) * p.C,
+                       base + (uint64_t)(p.gated ? p.F + min(f0 + l, p.F - 1) : min(f0 + 16 + l, p.F - 1)) * p.C};
+    const raw *x[1] = {(const raw *)p.x + j / p.K * p.x_ld};
+    f32x4 acc[1][2] = {};
+    stream<D, 1, 2>(w, x, p.C, wave, FEW_WAVES, acc);
+    join<1, 2, FEW_WAVES>(sums, wave, acc);
+    if (wave == 0 && l == 0) hidden_of<D>(p, acc[0], f0 + (lane >> 4) * 4, (raw *)p.h + (uint64_t)j * p.h_ld);
+}
+
+/* 32 columns of a token's result a workgroup, whose wavefronts share all runs of k of all its choices */
+template <typename D> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_layer_down_few(LayerP p)
+{
+    typedef typename D::raw raw;
+    __shared__ f32x4 sums[FEW_WAVES * 2 * 64];
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15;
+    const uint32_t t = blockIdx.x / p.tiles, c0 = blockIdx.x % p.tiles * 32, runs = (p.F + RUN<D> - 1) / RUN<D>;
+    /* lane k has choice k; the residual is asked for now */
+    const bool mine = lane < p.K;
+    const int32_t id = mine ? p.ids[t * p.K + lane] : -1;
+    const float share = mine ? p.weights[t * p.K + lane] : 0.0f;
+    const uint32_t c = c0 + (lane >> 4) * 4;
+    float res[8];
+    for (uint32_t i = 0; i < 8; i++) {
+        const uint32_t at = c + i / 4 * 16 + i % 4;
+        res[i] = wave == 0 && l == 0 && p.res && at < p.C ? D::get(((const raw *)p.res)[t * p.res_ld + at]) : 0.0f;
+    }
+    f32x4 y[1][2] = {};
+    for (uint32_t i = wave; i < p.K * runs; i += FEW_WAVES) {
+        const uint32_t k = i / runs;
+        const int32_t expert = __builtin_amdgcn_readlane(id, k);
+        if (expert < 0) continue;
+        const raw *base = (const raw *)p.w_out + (uint64_t)expert * p.C * p.F;
+        const raw *w[2] = {base + (uint64_t)min(c0 + l, p.C - 1) * p.F, base + (uint64_t)min(c0 + 16 + l, p.C - 1) * p.F};
+        const raw *x[1] = {(const raw *)p.h + (uint64_t)(t * p.K + k) * p.h_ld};
+        f32x4 acc[1][2] = {};
+        stream_run<D, 1, 2>(w, x, i % runs * RUN<D>, p.F, acc);
+        const float s = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, share), k));
+        for (int m = 0; m < 2; m++) y[0][m] += s * acc[0][m];
+    }
+    join<1, 2, FEW_WAVES>(sums, wave, y);
+    const bool is_void = __any(share != share);        /* by the router */
+    if (wave != 0 || l != 0) return;
+    for (uint32_t i = 0; i < 8; i++) {
+        const uint32_t at = c + i / 4 * 16 + i % 4;
+        const float v = is_void ? NAN : y[0][i / 4][i % 4];
+        if (at < p.C) ((raw *)p.out)[t * p.out_ld + at] = D::put(v + res[i]);
     }
 }
 
@@ -240,9 +331,21 @@ template <typename D> int run_layer(const msim_layer_spec *s, LayerP p, const fl
     hipError_t e = p.rows == 1 ? launch(msim_layer_gate<D, 1>, p.E, 256, 0, st, p)
                                : launch(msim_layer_gate<D, 4>, p.E * ((p.rows + 3) / 4), 256, 0, st, p);
     if (e != hipSuccess) return launched(e, "layer launch");
+    const uint64_t in = (p.F + (p.gated ? 15 : 31)) / (p.gated ? 16 : 32), out = (p.C + 31) / 32;
+    if (p.rows <= FEW_ROWS) {
+        const msim_route_spec &r = s->route;
+        RouteP q = {p.logits, bias, nullptr, nullptr, nullptr, r.rows, r.experts, r.experts, r.top_k, r.groups, r.top_groups,
+                    r.group_top, r.renorm, r.score == MSIM_SCORE_SIGMOID, r.scale, 0, 0, 0, 0};
+        if (q.TG == q.G) q.G = q.TG = q.gtop = 1;       /* every group stays */
+        const size_t lds = q.G > 1 ? p.rows * p.E * sizeof(double) : 0;
+        p.tiles = (uint32_t)in;
+        e = launch(p.E <= 256 ? msim_layer_up_few<D, 4> : msim_layer_up_few<D, 16>, p.rows * p.K * p.tiles, 64 * FEW_WAVES, lds, st, p, q, ids, weights, load);
+        p.tiles = (uint32_t)out;
+        if (e == hipSuccess) e = launch(msim_layer_down_few<D>, p.rows * p.tiles, 64 * FEW_WAVES, 0, st, p);
+        return launched(e, "layer launch");
+    }
     if (int rc = msim_route(&s->route, p.logits, bias, ids, weights, load, st)) return rc;
     p.slots = std::min(p.rows * p.K, p.E);
-    const uint64_t in = (p.F + (p.gated ? 15 : 31)) / (p.gated ? 16 : 32), out = (p.C + 31) / 32;
     e = p.rows <= 16 ? launch_product<D, 1, false>(p, in, st)
         : p.rows <= 32 ? launch_product<D, 2, false>(p, in, st) : launch_product<D, 4, false>(p, in, st);
     if (e == hipSuccess)

@@ -93,15 +93,15 @@ template <int N> __device__ __forceinline__ void slope_of(float *v, uint32_t act
     case MSIM_ACT_RELU: return each<N>(v, [](float z) { return z > 0 ? 1.0f : z != z ? z : 0.0f; });
     case MSIM_ACT_SILU:
         return each<N>(v, [](float z) {
-            const float s = 1.0f / (1.0f + expf(-z));
+            const float s = logistic(z);
             return s * (1.0f + z * (1.0f - s));
         });
     case MSIM_ACT_GELU:
-        return each<N>(v, [](float z) { return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z); });
+        return each<N>(v, [](float z) { return normal_below(z) + z * 0.39894228f * expf(-0.5f * z * z); });
     case MSIM_ACT_GELU_TANH:
         return each<N>(v, [](float z) {
-            const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
-            return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
+            const float s = logistic(z * (TANH_A + TANH_B * z * z));
+            return s * (1.0f + (1.0f - s) * z * (TANH_A + 3.0f * TANH_B * z * z));
         });
     }
 }
