@@ -63,8 +63,12 @@ constexpr uint32_t N_KINDS = sizeof(KINDS) / sizeof(Kind);
 /* How a product is cut: the kernel, and parts of k. */
 struct Plan { uint32_t kind, parts, per, nk; uint64_t part_bytes; };
 
-/* Enqueues a product; p.part has room for the plan's parts. */
-template <int MODE, bool AMC, bool BMC> __attribute__((visibility("hidden"))) hipError_t launch_gemm(GemmP p, const Plan &c, hipStream_t st);
+/* Enqueues a product of A contiguous along k and B along k (BMC: along n); p.part
+ * has room for the plan's parts.  launch_pair: of a backward pass, x of A along k
+ * and B along n, w of both along m and n, in one launch and with plans of one
+ * kind; either may be left out (batch 0). */
+template <int MODE, bool BMC> __attribute__((visibility("hidden"))) hipError_t launch_gemm(GemmP p, const Plan &c, hipStream_t st);
+template <int MODE> __attribute__((visibility("hidden"))) hipError_t launch_pair(GemmP x, const Plan &cx, GemmP w, const Plan &cw, hipStream_t st);
 
 inline uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 

@@ -3,8 +3,7 @@
 
 namespace msim {
 
-template hipError_t launch_gemm<M_BF16, false, false>(GemmP, const Plan &, hipStream_t);
-template hipError_t launch_gemm<M_BF16, false, true>(GemmP, const Plan &, hipStream_t);
-template hipError_t launch_gemm<M_BF16, true, true>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_gemm<M_BF16, false>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_pair<M_BF16>(GemmP, const Plan &, GemmP, const Plan &, hipStream_t);
 
 } // namespace msim

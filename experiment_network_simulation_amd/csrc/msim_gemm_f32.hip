@@ -3,8 +3,7 @@
 
 namespace msim {
 
-template hipError_t launch_gemm<M_F32, false, false>(GemmP, const Plan &, hipStream_t);
-template hipError_t launch_gemm<M_F32, false, true>(GemmP, const Plan &, hipStream_t);
-template hipError_t launch_gemm<M_F32, true, true>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_gemm<M_F32, false>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_pair<M_F32>(GemmP, const Plan &, GemmP, const Plan &, hipStream_t);
 
 } // namespace msim

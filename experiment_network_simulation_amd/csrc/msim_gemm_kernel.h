@@ -221,24 +221,24 @@ __device__ __forceinline__ void after(const Epilogue &e, uint32_t batch, uint32_
 /* the product                                                               */
 /* ------------------------------------------------------------------------ */
 
-/* BT x BT of C a workgroup, DEPTH stages in LDS. */
+/* BT x BT of C a workgroup, which is number `block` of `total`; DEPTH stages in LDS,
+ * in arrays of their own, so that the compiler knows which of them a load to LDS
+ * writes. */
 template <int MODE, bool AMC, bool BMC, int BT, int DEPTH, int THREADS>
-__global__ void __launch_bounds__(THREADS, 2) msim_gemm(GemmP p)
+__device__ __forceinline__ void product(const GemmP &p, uint32_t total, uint32_t block, char *lds0, char *lds1, char *lds2, char *lds3)
 {
     constexpr int WAVES = THREADS / WAVE, WM = 2, WN = WAVES / WM;      /* wavefronts along m and n */
     constexpr int RM = BT / WM, RN = BT / WN, IM = RM / 32, IN = RN / 32;
     constexpr int STEPS = MODE == M_SPLIT ? 2 : 4;
     typedef Tile<MODE, AMC, BT, THREADS> TA;
     typedef Tile<MODE, BMC, BT, THREADS> TB;
-    /* separate arrays, so that the compiler knows which of them a load to LDS writes */
     constexpr int STAGE = TA::BYTES + TB::BYTES;
-    __shared__ __attribute__((aligned(256))) char lds0[STAGE], lds1[STAGE], lds2[DEPTH > 2 ? STAGE : 16], lds3[DEPTH > 2 ? STAGE : 16];
 
     /* Workgroups go to the 8 dies in turn: each die takes consecutive tiles, and
      * those walk along m within bands of 8 tiles of n, so that what a die reads
      * together stays in its cache. */
-    const uint32_t total = gridDim.x, q = total >> 3, r = total & 7, die = blockIdx.x & 7;
-    uint32_t id = die * q + min(die, r) + (blockIdx.x >> 3);
+    const uint32_t q = total >> 3, r = total & 7, die = block & 7;
+    uint32_t id = die * q + min(die, r) + (block >> 3);
     const uint32_t tiles = p.tm * p.tn;
     const uint32_t group = id / tiles;
     id -= group * tiles;
@@ -427,31 +427,61 @@ __global__ void __launch_bounds__(THREADS, 2) msim_gemm(GemmP p)
     }
 }
 
-/* The parts' sums together, in order, and what becomes of them. */
-template <int MODE> __global__ void __launch_bounds__(256) msim_gemm_join(GemmP p)
+template <int BT, int DEPTH> struct Room {
+    static constexpr int STAGE = 2 * BT * 128;
+    static constexpr int SPARE = DEPTH > 2 ? STAGE : 16;
+};
+#define MSIM_ROOM(BT, DEPTH)                                                                        \
+    typedef Room<BT, DEPTH> R_;                                                                     \
+    __shared__ __attribute__((aligned(256))) char lds0[R_::STAGE], lds1[R_::STAGE], lds2[R_::SPARE], lds3[R_::SPARE]
+
+template <int MODE, bool BMC, int BT, int DEPTH, int THREADS> __global__ void __launch_bounds__(THREADS, 2) msim_gemm(GemmP p)
+{
+    MSIM_ROOM(BT, DEPTH);
+    product<MODE, false, BMC, BT, DEPTH, THREADS>(p, gridDim.x, blockIdx.x, lds0, lds1, lds2, lds3);
+}
+
+/* The two products of a backward pass in one launch: n of the first, and from the
+ * next multiple of 8 on, so that dies are numbered alike, those of the second. */
+template <int MODE, int BT, int DEPTH, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2) msim_gemm_pair(GemmP x, GemmP w, uint32_t n)
+{
+    MSIM_ROOM(BT, DEPTH);
+    const uint32_t n8 = (n + 7) & ~7u;
+    if (blockIdx.x < n) product<MODE, false, true, BT, DEPTH, THREADS>(x, n, blockIdx.x, lds0, lds1, lds2, lds3);
+    else if (blockIdx.x >= n8) product<MODE, true, true, BT, DEPTH, THREADS>(w, gridDim.x - n8, blockIdx.x - n8, lds0, lds1, lds2, lds3);
+}
+
+/* The parts' sums together, in order, and what becomes of them: of one product, or of two. */
+template <int MODE> __device__ __forceinline__ void join_parts(const GemmP &p, uint64_t id)
 {
     const uint32_t wide = (uint32_t)(p.part_ld / 8);
-    const uint64_t n = (uint64_t)p.batch * p.M * wide, size = (uint64_t)p.M * p.part_ld;
-    for (uint64_t id = blockIdx.x * 256ull + threadIdx.x; id < n; id += gridDim.x * 256ull) {
-        const uint64_t row = id / wide;
-        const uint32_t c = (uint32_t)(id - row * wide) * 8, batch = (uint32_t)(row / p.M), m = (uint32_t)(row - (uint64_t)batch * p.M);
-        typename Early<MODE>::T early;
-        early_of<MODE>(p.e, batch, m, c, early);
-        const float *q = p.part + (uint64_t)batch * p.parts * size + (uint64_t)m * p.part_ld + c;
-        f32x4 x = *(const f32x4 *)q, y = *(const f32x4 *)(q + 4);
-        _Pragma("unroll 8") for (uint32_t k = 1; k < p.parts; k++) {
-            q += size;
-            x += *(const f32x4 *)q;
-            y += *(const f32x4 *)(q + 4);
-        }
-        float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        if constexpr (MODE != M_SPLIT) {
-            float bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (p.e.bias && c < p.N) load8<F32>(bias, p.e.bias, c, min(8u, p.N - c), false);
-            for (int i = 0; i < 8; i++) v[i] += bias[i];
-            before<MODE>(p.e, m, c, v);
-        }
-        after<MODE>(p.e, batch, m, c, v, early);
+    const uint64_t size = (uint64_t)p.M * p.part_ld, row = id / wide;
+    const uint32_t c = (uint32_t)(id - row * wide) * 8, batch = (uint32_t)(row / p.M), m = (uint32_t)(row - (uint64_t)batch * p.M);
+    typename Early<MODE>::T early;
+    early_of<MODE>(p.e, batch, m, c, early);
+    const float *q = p.part + (uint64_t)batch * p.parts * size + (uint64_t)m * p.part_ld + c;
+    f32x4 x = *(const f32x4 *)q, y = *(const f32x4 *)(q + 4);
+    _Pragma("unroll 8") for (uint32_t k = 1; k < p.parts; k++) {
+        q += size;
+        x += *(const f32x4 *)q;
+        y += *(const f32x4 *)(q + 4);
+    }
+    float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    if constexpr (MODE != M_SPLIT) {
+        float bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (p.e.bias && c < p.N) load8<F32>(bias, p.e.bias, c, min(8u, p.N - c), false);
+        for (int i = 0; i < 8; i++) v[i] += bias[i];
+        before<MODE>(p.e, m, c, v);
+    }
+    after<MODE>(p.e, batch, m, c, v, early);
+}
+
+template <int MODE> __global__ void __launch_bounds__(256) msim_gemm_join(GemmP a, uint64_t na, GemmP b, uint64_t nb)
+{
+    for (uint64_t id = blockIdx.x * 256ull + threadIdx.x; id < na + nb; id += gridDim.x * 256ull) {
+        if (id < na) join_parts<MODE>(a, id);
+        else join_parts<MODE>(b, id - na);
     }
 }
 
@@ -459,18 +489,8 @@ template <int MODE> __global__ void __launch_bounds__(256) msim_gemm_join(GemmP 
 
 namespace msim {
 
-template <int MODE, bool AMC, bool BMC, uint32_t I = 0> hipError_t launch_kind(uint32_t kind, uint32_t grid, const GemmP &p, hipStream_t st)
-{
-    if constexpr (I < N_KINDS) {
-        constexpr Kind k = KINDS[I];
-        if (kind != I) return launch_kind<MODE, AMC, BMC, I + 1>(kind, grid, p, st);
-        if constexpr (!(MODE == M_F32 && k.bt == 256))
-            return launch(msim_gemm<MODE, AMC, BMC, k.bt, k.depth, k.threads>, grid, k.threads, 0, st, p);
-    }
-    return hipErrorInvalidValue;
-}
-
-template <int MODE, bool AMC, bool BMC> hipError_t launch_gemm(GemmP p, const Plan &c, hipStream_t st)
+/* what the plan and the epilogue make of a product; its workgroups */
+template <int MODE> uint64_t ready(GemmP &p, const Plan &c)
 {
     const uint32_t bt = KINDS[c.kind].bt;
     p.tm = (p.M + bt - 1) / bt;
@@ -478,18 +498,57 @@ template <int MODE, bool AMC, bool BMC> hipError_t launch_gemm(GemmP p, const Pl
     p.nk = c.nk;
     p.parts = c.parts;
     p.per = c.per;
-    p.part_ld = up(p.N, 8);
-    if (MODE == M_SPLIT) p.part_ld = up(p.N, 32);
+    p.part_ld = up(p.N, MODE == M_SPLIT ? 32 : 8);
     if (p.parts > 1) p.mirror = 0;
     const Epilogue &e = p.e;
     const bool only = MODE != M_SPLIT && !e.bias && !e.res && !e.pre && !e.act && e.vec && p.N % 8 == 0;
     p.plain = p.parts > 1 || (only && (MODE == M_F32 || e.out32)) ? 1 : only ? 2 : 0;
-    const uint64_t grid = (uint64_t)p.tm * p.tn * p.parts * p.batch;
+    return (uint64_t)p.tm * p.tn * p.parts * p.batch;
+}
+
+template <int MODE> hipError_t launch_join(const GemmP &a, const GemmP &b, hipStream_t st)
+{
+    const uint64_t na = a.parts > 1 ? (uint64_t)a.batch * a.M * (a.part_ld / 8) : 0, nb = b.parts > 1 ? (uint64_t)b.batch * b.M * (b.part_ld / 8) : 0;
+    if (na + nb == 0) return hipSuccess;
+    return launch(msim_gemm_join<MODE>, (uint32_t)std::min<uint64_t>((na + nb + 255) / 256, 1u << 16), 256, 0, st, a, na, b, nb);
+}
+
+template <int MODE, bool BMC, uint32_t I = 0> hipError_t launch_kind(uint32_t kind, uint32_t grid, const GemmP &p, hipStream_t st)
+{
+    if constexpr (I < N_KINDS) {
+        constexpr Kind k = KINDS[I];
+        if (kind != I) return launch_kind<MODE, BMC, I + 1>(kind, grid, p, st);
+        if constexpr (!(MODE == M_F32 && k.bt == 256))
+            return launch(msim_gemm<MODE, BMC, k.bt, k.depth, k.threads>, grid, k.threads, 0, st, p);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <int MODE, bool BMC> hipError_t launch_gemm(GemmP p, const Plan &c, hipStream_t st)
+{
+    const uint64_t grid = ready<MODE>(p, c);
     if (!grid) return hipSuccess;
-    const hipError_t r = launch_kind<MODE, AMC, BMC>(c.kind, (uint32_t)grid, p, st);
-    if (r != hipSuccess || p.parts == 1) return r;
-    const uint64_t n = (uint64_t)p.batch * p.M * (p.part_ld / 8);
-    return launch(msim_gemm_join<MODE>, (uint32_t)std::min<uint64_t>((n + 255) / 256, 1u << 16), 256, 0, st, p);
+    const hipError_t r = launch_kind<MODE, BMC>(c.kind, (uint32_t)grid, p, st);
+    return r == hipSuccess ? launch_join<MODE>(p, GemmP{}, st) : r;
+}
+
+template <int MODE, uint32_t I = 0> hipError_t launch_pair_kind(uint32_t kind, uint32_t nx, uint32_t nw, const GemmP &x, const GemmP &w, hipStream_t st)
+{
+    if constexpr (I < N_KINDS) {
+        constexpr Kind k = KINDS[I];
+        if (kind != I) return launch_pair_kind<MODE, I + 1>(kind, nx, nw, x, w, st);
+        if constexpr (!(MODE == M_F32 && k.bt == 256))
+            return launch(msim_gemm_pair<MODE, k.bt, k.depth, k.threads>, (nx + 7) / 8 * 8 + nw, k.threads, 0, st, x, w, nx);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <int MODE> hipError_t launch_pair(GemmP x, const Plan &cx, GemmP w, const Plan &cw, hipStream_t st)
+{
+    const uint64_t nx = x.batch ? ready<MODE>(x, cx) : 0, nw = w.batch ? ready<MODE>(w, cw) : 0;
+    if (nx + nw == 0) return hipSuccess;
+    const hipError_t r = launch_pair_kind<MODE>(x.batch ? cx.kind : cw.kind, (uint32_t)nx, (uint32_t)nw, x, w, st);
+    return r == hipSuccess ? launch_join<MODE>(x, w, st) : r;
 }
 
 } // namespace msim

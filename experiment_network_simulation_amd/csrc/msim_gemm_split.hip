@@ -3,7 +3,7 @@
 
 namespace msim {
 
-template hipError_t launch_gemm<M_SPLIT, false, false>(GemmP, const Plan &, hipStream_t);
-template hipError_t launch_gemm<M_SPLIT, false, true>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_gemm<M_SPLIT, false>(GemmP, const Plan &, hipStream_t);
+template hipError_t launch_gemm<M_SPLIT, true>(GemmP, const Plan &, hipStream_t);
 
 } // namespace msim

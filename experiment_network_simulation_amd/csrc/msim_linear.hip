@@ -67,22 +67,22 @@ template <int MODE, int MT, int NT, int WAVES> __global__ void __launch_bounds__
 /* ------------------------------------------------------------------------ */
 
 /* rows x cols of a strided matrix to rows of `wide` columns, zeros behind the last */
-template <typename D> __global__ void __launch_bounds__(256)
-msim_pack(const void *from, uint64_t ld, void *to, uint32_t rows, uint32_t cols, uint32_t wide)
+struct PackP {
+    const void *from;
+    uint64_t ld;
+    void *to;
+    uint32_t rows, cols, wide, blocks;
+};
+
+template <typename D> __device__ __forceinline__ void pack_rows(const PackP &p, uint32_t block)
 {
     constexpr uint32_t PER = 16 / sizeof(typename D::raw);
-    typedef typename D::raw vec __attribute__((ext_vector_type(PER)));
-    typedef typename D::raw loose __attribute__((ext_vector_type(PER), aligned(sizeof(typename D::raw))));
-    const uint32_t turns = wide / PER;
-    const uint64_t n = (uint64_t)rows * turns;
-    for (uint64_t id = blockIdx.x * 256ull + threadIdx.x; id < n; id += gridDim.x * 256ull) {
+    const uint32_t turns = p.wide / PER;
+    const uint64_t n = (uint64_t)p.rows * turns;
+    _Pragma("unroll 2") for (uint64_t id = block * 256ull + threadIdx.x; id < n; id += p.blocks * 256ull) {
         const uint64_t r = id / turns;
         const uint32_t c = (uint32_t)(id - r * turns) * PER;
-        const typename D::raw *x = (const typename D::raw *)from + r * ld + c;
-        vec v;
-        if (c + PER <= cols) v = *(const loose *)x;
-        else for (uint32_t i = 0; i < PER; i++) v[i] = c + i < cols ? x[i] : 0;
-        *(vec *)((typename D::raw *)to + r * wide + c) = v;
+        *(u32x4 *)((typename D::raw *)p.to + r * p.wide + c) = piece<D>((const typename D::raw *)p.from + r * p.ld, c, p.cols);
     }
 }
 
@@ -115,16 +115,15 @@ struct GradP {
     const void *grad, *pre;
     uint64_t grad_ld, pre_ld;
     void *d;                     /* NULL: grad itself is read by the products */
-    float *sums;                 /* [blocks of rows][outs], or NULL */
+    float *sums;                 /* [blocks of rows][outs] (dbias itself, of one block), or NULL */
     uint32_t rows, outs, wide;   /* wide: columns of d */
-    uint32_t act, grad32, lglanes, vec, part;
+    uint32_t act, grad32, lglanes, vec, part, blocks;
 };
 
-template <typename D> __global__ void __launch_bounds__(256) msim_linear_grad(GradP p)
+template <typename D> __device__ __forceinline__ void grad_rows(const GradP &p, uint32_t block, float *part)
 {
-    __shared__ float part[256 * 8];
     const uint32_t lanes = 1u << p.lglanes, cols = 8 * lanes;
-    const uint32_t across = (p.wide + cols - 1) / cols, by = blockIdx.x / across, bx = blockIdx.x - by * across;
+    const uint32_t across = (p.wide + cols - 1) / cols, by = block / across, bx = block - by * across;
     const uint32_t n = bx * cols + (threadIdx.x & (lanes - 1)) * 8, k = n < p.outs ? min(8u, p.outs - n) : 0;
     const uint32_t end = min(p.rows, (by + 1) * p.part);
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -149,6 +148,15 @@ template <typename D> __global__ void __launch_bounds__(256) msim_linear_grad(Gr
         for (uint32_t t = c / 8; t < 256; t += lanes) s += part[(c & 7) * 256 + t];
         if (bx * cols + c < p.outs) p.sums[(uint64_t)by * p.outs + bx * cols + c] = s;
     }
+}
+
+/* What the products of a call need first: x and weight packed, and the gradient. */
+template <typename D> __global__ void __launch_bounds__(256) msim_linear_prepare(PackP x, PackP w, GradP g)
+{
+    __shared__ float part[256 * 8];
+    if (blockIdx.x < x.blocks) pack_rows<D>(x, blockIdx.x);
+    else if (blockIdx.x < x.blocks + w.blocks) pack_rows<D>(w, blockIdx.x - x.blocks);
+    else grad_rows<D>(g, blockIdx.x - x.blocks - w.blocks, part);
 }
 
 /* column sums of the workgroups together: 32 columns and 32 runs of rows a workgroup */
@@ -178,38 +186,65 @@ constexpr uint64_t MAX_LD = 8000000;       /* bytes: the offsets of a tile's 256
  * at a time; one takes `more`, and for a stage `low` where it has a compute unit to
  * itself, `high` where the card is full (measured with sizes of 1,024 and 8,192);
  * parts of k add the time of their sums through memory. */
-Plan plan_of(uint32_t mode, uint64_t M, uint64_t N, uint64_t K, uint64_t batch)
-{
-    static const struct { double slots, more, low[3], high[3]; } times[] = {         /* 16 bits, 32 bits, split */
-        {256, 9, {1.15, 8.0, 1.7}, {1.6, 8.0, 2.2}}, {512, 4, {0.53, 1.8, 0.6}, {1.0, 3.6, 1.3}}, {512, 2, {0.25, 0.5, 0.3}, {0.41, 0.95, 0.5}},
+constexpr struct { double slots, more, low[3], high[3]; } TIMES[] = {         /* 16 bits, 32 bits, split */
+    {256, 9, {1.15, 8.0, 1.7}, {1.6, 8.0, 2.2}}, {512, 4, {0.53, 1.8, 0.6}, {1.0, 3.6, 1.3}}, {512, 2, {0.25, 0.5, 0.3}, {0.41, 0.95, 0.5}},
 #ifdef TUNE
-        {512, 2}, {512, 2}, {512, 2}, {512, 2}, {512, 2},
+    {512, 2}, {512, 2}, {512, 2}, {512, 2}, {512, 2},
 #endif
-    };
-    const uint32_t bk = mode == M_F16 || mode == M_BF16 ? 64 : 32, t = bk == 64 ? 0 : mode == M_F32 ? 1 : 2;
-    const uint64_t nk = (K + bk - 1) / bk, n = std::max<uint64_t>(nk, 1);
-    Plan best = {};
+};
+
+struct Product { uint64_t M, N, K, batch; };
+
+/* the best parts for a kernel; `share` of the card is this product's; the estimate */
+double plan_kind(uint32_t mode, const Product &q, uint32_t kind, double share, Plan *best)
+{
+    const auto &c = TIMES[kind];
+    const uint32_t bt = KINDS[kind].bt, bk = mode == M_F16 || mode == M_BF16 ? 64 : 32, t = bk == 64 ? 0 : mode == M_F32 ? 1 : 2;
+    const uint64_t nk = (q.K + bk - 1) / bk, n = std::max<uint64_t>(nk, 1), tiles = ((q.M + bt - 1) / bt) * ((q.N + bt - 1) / bt) * q.batch;
+    const double slots = c.slots * share;
     double least = INFINITY;
-    for (uint32_t i = 0; i < N_KINDS; i++) {
-        const Kind k = KINDS[i];
-        const auto &c = times[i];
-        if (mode == M_F32 && k.bt == 256) continue;        /* 32-bit products are so slow that tiles of 128 feed them as well */
-        const uint64_t tiles = ((M + k.bt - 1) / k.bt) * ((N + k.bt - 1) / k.bt) * batch;
-        for (uint64_t parts = 1; parts <= 64 && parts <= n; parts++) {
-            const uint64_t per = (n + parts - 1) / parts;
-            if ((n + per - 1) / per != parts) continue;
-            const double groups = (double)(tiles * parts), rounds = std::floor(groups / c.slots), rest = groups - rounds * c.slots;
-            double cost = rounds * (c.more + c.high[t] * per);
-            if (rest > 0) cost += c.more + (rest <= 256 && c.slots > 256 ? c.low[t] : rest > 128 ? c.high[t] : c.low[t]) * per;
-            if (parts > 1) cost += 4.0 + (double)batch * M * N * parts * 8.0 / 4e6;
-            if (cost < least) {
-                least = cost;
-                best = {i, (uint32_t)parts, (uint32_t)per, (uint32_t)nk,
-                        parts > 1 ? batch * parts * M * up(N, mode == M_SPLIT ? 32 : 8) * 4 : 0};
-            }
+    for (uint64_t parts : {1, 2, 3, 4, 6, 8, 9, 12, 16, 24, 32, 48, 64}) {
+        if (parts > n) break;
+        const uint64_t per = (n + parts - 1) / parts;
+        if ((n + per - 1) / per != parts) continue;
+        const double groups = (double)(tiles * parts), rounds = std::floor(groups / slots), rest = groups - rounds * slots;
+        double cost = rounds * (c.more + c.high[t] * per);
+        if (rest > 0) cost += c.more + (rest <= slots / 2 ? c.low[t] : c.high[t]) * per;
+        if (parts > 1) cost += 4.0 + (double)q.batch * q.M * q.N * parts * 8.0 / 4e6;
+        if (cost < least) {
+            least = cost;
+            *best = {kind, (uint32_t)parts, (uint32_t)per, (uint32_t)nk,
+                     parts > 1 ? up(q.batch * parts * q.M * up(q.N, mode == M_SPLIT ? 32 : 8) * 4, 256) : 0};
         }
     }
+    return least;
+}
+
+/* the kernels that a type has: 32-bit products are so slow that tiles of 128 feed them as well as larger ones */
+bool has_kind(uint32_t mode, uint32_t kind) { return mode != M_F32 || KINDS[kind].bt < 256; }
+
+Plan plan_of(uint32_t mode, const Product &q)
+{
+    Plan best = {}, p;
+    double least = INFINITY;
+    for (uint32_t i = 0; i < N_KINDS; i++) {
+        if (!has_kind(mode, i)) continue;
+        const double cost = plan_kind(mode, q, i, 1.0, &p);
+        if (cost < least) least = cost, best = p;
+    }
     return best;
+}
+
+/* two products in one launch, each on half of the card (their operations are as many) */
+void plan_pair(uint32_t mode, const Product &a, const Product &b, Plan *pa, Plan *pb)
+{
+    Plan x, y;
+    double least = INFINITY;
+    for (uint32_t i = 0; i < N_KINDS; i++) {
+        if (!has_kind(mode, i)) continue;
+        const double cost = std::max(plan_kind(mode, a, i, 0.5, &x), plan_kind(mode, b, i, 0.5, &y));
+        if (cost < least) least = cost, *pa = x, *pb = y;
+    }
 }
 
 /* Whether the products can read rows of `cols` elements as they lie: 16 bytes at a time. */
@@ -238,13 +273,17 @@ Matrix matrix_of(const void *at, uint64_t rows, uint64_t cols, uint64_t ld, uint
     return {at, rows, cols, ld, size, !ready(at, rows, cols, ld, size)};
 }
 
-hipError_t pack(const Matrix &m, char *ws, hipStream_t st)
+PackP pack_of(const Matrix &m, char *ws)
 {
-    if (!m.packed || !m.rows) return hipSuccess;
+    if (!m.packed || !m.rows) return {};
     const uint64_t n = m.rows * m.wide() * m.size / 16;
-    const uint32_t grid = (uint32_t)std::min<uint64_t>((n + 255) / 256, 1u << 16);
-    return m.size == 4 ? launch(msim_pack<F32>, grid, 256, 0, st, m.at, m.ld, (void *)ws, (uint32_t)m.rows, (uint32_t)m.cols, (uint32_t)m.wide())
-                       : launch(msim_pack<F16>, grid, 256, 0, st, m.at, m.ld, (void *)ws, (uint32_t)m.rows, (uint32_t)m.cols, (uint32_t)m.wide());
+    return {m.at, m.ld, ws, (uint32_t)m.rows, (uint32_t)m.cols, (uint32_t)m.wide(), (uint32_t)std::min<uint64_t>((n + 511) / 512, 1u << 14)};
+}
+
+template <typename D> hipError_t prepare(const PackP &x, const PackP &w, const GradP &g, hipStream_t st)
+{
+    const uint32_t grid = x.blocks + w.blocks + g.blocks;
+    return grid ? launch(msim_linear_prepare<D>, grid, 256, 0, st, x, w, g) : hipSuccess;
 }
 
 bool on16(const void *at, uint64_t ld, uint32_t size) { return (uintptr_t)at % 16 == 0 && ld * size % 16 == 0; }
@@ -288,7 +327,7 @@ Forward forward_of(const msim_linear_spec *s, const void *x, const void *weight)
     f.w = matrix_of(weight, s->outs, s->cols, s->weight_stride, size);
     f.few = s->rows <= FEW_ROWS;
     if (f.few) return f;
-    f.plan = plan_of(s->dtype, s->rows, s->outs, f.x.wide(), 1);
+    f.plan = plan_of(s->dtype, {s->rows, s->outs, f.x.wide(), 1});
     f.bytes = f.x.bytes() + f.w.bytes() + f.plan.part_bytes;
     return f;
 }
@@ -316,9 +355,8 @@ int run_forward(const msim_linear_spec *s, const Forward &f, const Epilogue &e, 
     p.batch = 1;
     p.part = (float *)(ww + f.w.bytes());
     p.e = e;
-    hipError_t r = pack(f.x, wx, st);
-    if (r == hipSuccess) r = pack(f.w, ww, st);
-    if (r == hipSuccess) r = launch_gemm<MODE, false, false>(p, f.plan, st);
+    hipError_t r = prepare<typename Type<MODE>::D>(pack_of(f.x, wx), pack_of(f.w, ww), GradP{}, st);
+    if (r == hipSuccess) r = launch_gemm<MODE, false>(p, f.plan, st);
     return launched(r, "linear launch");
 }
 
@@ -328,7 +366,7 @@ struct Backward {
     bool own;                    /* d is made: an activation, another type, or a grad that does not lie as it is read */
     uint64_t wide;               /* columns of d */
     uint64_t d_bytes, sum_bytes;
-    uint32_t blocks, part;       /* of rows, for the sums: about 1,024, of at least 8 rows */
+    uint32_t blocks, part;       /* of rows, for the sums: one of up to 256, or about 1,024 of at least 8 */
     Plan px, pw;
     uint64_t bytes;
 };
@@ -342,13 +380,15 @@ Backward backward_of(const msim_linear_spec *s, const void *x, const void *weigh
     const bool need = dx || dw;
     b.own = need && (s->act || s->out_dtype != s->dtype || !ready(grad, s->rows, s->outs, s->out_stride, size));
     b.wide = b.own ? up(s->outs, 16 / size * (size == 4 ? 2 : 1)) : s->outs;
-    b.part = (uint32_t)std::max<uint64_t>(8, (s->rows + 1023) / 1024);
+    b.part = s->rows <= 256 ? 256 : (uint32_t)std::max<uint64_t>(8, (s->rows + 1023) / 1024);
     b.blocks = (uint32_t)((s->rows + b.part - 1) / b.part);
     b.d_bytes = b.own ? up(s->rows * b.wide * size, 256) : 0;
     b.sum_bytes = db ? up((uint64_t)b.blocks * s->outs * 4, 256) : 0;
-    if (dx) b.px = plan_of(s->dtype, s->rows, s->cols, b.wide, 1);
-    if (dw) b.pw = plan_of(s->dtype, s->outs, s->cols, s->rows, 1);
-    b.bytes = b.x.bytes() + b.w.bytes() + b.d_bytes + b.sum_bytes + std::max(b.px.part_bytes, b.pw.part_bytes);
+    const Product x1 = {s->rows, s->cols, b.wide, 1}, w1 = {s->outs, s->cols, s->rows, 1};
+    if (dx && dw) plan_pair(s->dtype, x1, w1, &b.px, &b.pw);
+    else if (dx) b.px = plan_of(s->dtype, x1);
+    else if (dw) b.pw = plan_of(s->dtype, w1);
+    b.bytes = b.x.bytes() + b.w.bytes() + b.d_bytes + b.sum_bytes + b.px.part_bytes + b.pw.part_bytes;
     return b;
 }
 
@@ -359,52 +399,46 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
     typedef typename Type<MODE>::D D;
     const uint32_t size = size_of(s->dtype);
     char *wx = ws, *ww = wx + b.x.bytes(), *wd = ww + b.w.bytes(), *wsum = wd + b.d_bytes, *wpart = wsum + b.sum_bytes;
-    hipError_t r = hipSuccess;
+    GradP g = {};
     if ((b.own || dbias) && s->rows) {
         const uint32_t gsize = size_of(s->out_dtype);
-        GradP g = {grad, pre, s->out_stride, s->pre_stride, b.own ? wd : nullptr, dbias ? (float *)wsum : nullptr,
-                   (uint32_t)s->rows, s->outs, (uint32_t)up(s->outs, 8), s->act, s->out_dtype == MSIM_F32, 0, 0, b.part};
-        if (b.own) g.wide = (uint32_t)b.wide;
+        g = {grad, pre, s->out_stride, s->pre_stride, b.own ? wd : nullptr, !dbias ? nullptr : b.blocks == 1 ? dbias : (float *)wsum,
+             (uint32_t)s->rows, s->outs, b.own ? (uint32_t)b.wide : (uint32_t)up(s->outs, 8), s->act, s->out_dtype == MSIM_F32, 0, 0, b.part, 0};
         while (g.lglanes < 5 && (8u << g.lglanes) < g.wide) g.lglanes++;
         g.vec = on16(grad, s->out_stride, gsize) && (!s->act || on16(pre, s->pre_stride, size));
-        const uint64_t across = (g.wide + (8u << g.lglanes) - 1) / (8u << g.lglanes);
-        r = launch(msim_linear_grad<D>, (uint32_t)(b.blocks * across), 256, 0, st, g);
+        g.blocks = b.blocks * ((g.wide + (8u << g.lglanes) - 1) / (8u << g.lglanes));
     }
-    if (r == hipSuccess && dbias)
-        r = launch(msim_linear_bias_grad, (s->outs + 31) / 32, 1024, 0, st, (const float *)wsum, s->rows ? b.blocks : 0, s->outs, dbias);
-    Operand d = {wd, s->rows * b.wide * size, b.wide * size, 0};
-    if (!b.own) d = Matrix{grad, s->rows, s->outs, s->out_stride, size, false}.operand(nullptr);
-    GemmP p = {};
-    p.a = d;
-    p.batch = 1;
-    p.N = s->cols;
-    p.part = (float *)wpart;
-    if (r == hipSuccess && dx) {
-        r = pack(b.w, ww, st);
-        p.b = b.w.operand(ww);
-        p.M = (uint32_t)s->rows;
-        p.K = (uint32_t)b.wide;
-        p.e = {};
-        p.e.M = p.M;
-        p.e.N = p.N;
-        p.e.out = dx;
-        p.e.out_ld = s->dx_stride;
-        p.e.vec = on16(dx, s->dx_stride, size);
-        if (r == hipSuccess) r = launch_gemm<MODE, false, true>(p, b.px, st);
+    hipError_t r = prepare<D>(dweight ? pack_of(b.x, wx) : PackP{}, dx ? pack_of(b.w, ww) : PackP{}, g, st);
+    if (r == hipSuccess && dbias && b.blocks != 1)
+        r = launch(msim_linear_bias_grad, (s->outs + 31) / 32, 1024, 0, st, (const float *)wsum, b.blocks, s->outs, dbias);
+    const Operand d = b.own ? Operand{wd, s->rows * b.wide * size, b.wide * size, 0}
+                            : Matrix{grad, s->rows, s->outs, s->out_stride, size, false}.operand(nullptr);
+    GemmP px = {}, pw = {};
+    if (dx) {
+        px.a = d;
+        px.b = b.w.operand(ww);
+        px.M = px.e.M = (uint32_t)s->rows;
+        px.N = px.e.N = s->cols;
+        px.K = (uint32_t)b.wide;
+        px.batch = 1;
+        px.part = (float *)wpart;
+        px.e.out = dx;
+        px.e.out_ld = s->dx_stride;
+        px.e.vec = on16(dx, s->dx_stride, size);
     }
-    if (r == hipSuccess && dweight) {
-        r = pack(b.x, wx, st);
-        p.b = b.x.operand(wx);
-        p.M = s->outs;
-        p.K = (uint32_t)s->rows;
-        p.e = {};
-        p.e.M = p.M;
-        p.e.N = p.N;
-        p.e.out = dweight;
-        p.e.out_ld = s->dweight_stride;
-        p.e.vec = on16(dweight, s->dweight_stride, size);
-        if (r == hipSuccess) r = launch_gemm<MODE, true, true>(p, b.pw, st);
+    if (dweight) {
+        pw.a = d;
+        pw.b = b.x.operand(wx);
+        pw.M = pw.e.M = s->outs;
+        pw.N = pw.e.N = s->cols;
+        pw.K = (uint32_t)s->rows;
+        pw.batch = 1;
+        pw.part = (float *)(wpart + b.px.part_bytes);
+        pw.e.out = dweight;
+        pw.e.out_ld = s->dweight_stride;
+        pw.e.vec = on16(dweight, s->dweight_stride, size);
     }
+    if (r == hipSuccess) r = launch_pair<MODE>(px, b.px, pw, b.pw, st);
     return launched(r, "linear backward launch");
 }
 
@@ -516,9 +550,9 @@ Orth orth_of(const msim_orthogonalize_spec *s)
     o.norm_bytes = up((uint64_t)s->count * NORM_PARTS * 8, 256);
     o.x_bytes = up(s->count * o.m * o.lx * 4, 256);
     o.p_bytes = up(s->count * o.m * o.lp * 4, 256);
-    o.square = plan_of(M_SPLIT, o.m, o.lp, o.lx, s->count);
-    o.poly = plan_of(M_SPLIT, o.m, o.lp, o.lp, s->count);
-    o.update = plan_of(M_SPLIT, o.m, o.lx, o.lp, s->count);
+    o.square = plan_of(M_SPLIT, {o.m, o.lp, o.lx, s->count});
+    o.poly = plan_of(M_SPLIT, {o.m, o.lp, o.lp, s->count});
+    o.update = plan_of(M_SPLIT, {o.m, o.lx, o.lp, s->count});
     o.bytes = o.norm_bytes + 2 * o.x_bytes + 2 * o.p_bytes +
               std::max(o.square.part_bytes, std::max(o.poly.part_bytes, o.update.part_bytes));
     return o;
@@ -583,7 +617,7 @@ hipError_t run_orth(const msim_orthogonalize_spec *s, const Orth &o, const void 
         p.e.out_ld = o.lp;
         p.e.out_batch = o.m * o.lp * 4;
         p.e.beta = 1.0f / ORTH_SCALE;
-        e = launch_gemm<M_SPLIT, false, false>(p, o.square, st);
+        e = launch_gemm<M_SPLIT, false>(p, o.square, st);
         if (e != hipSuccess) break;
         p.a = p.b = osq;
         p.K = (uint32_t)o.lp;
@@ -591,7 +625,7 @@ hipError_t run_orth(const msim_orthogonalize_spec *s, const Orth &o, const void 
         p.e.src = sq;
         p.e.alpha = s->b;
         p.e.beta = s->c / ORTH_SCALE;
-        e = launch_gemm<M_SPLIT, false, false>(p, o.poly, st);
+        e = launch_gemm<M_SPLIT, false>(p, o.poly, st);
         if (e != hipSuccess) break;
         p.mirror = 0;
         p.a = opoly;
@@ -603,7 +637,7 @@ hipError_t run_orth(const msim_orthogonalize_spec *s, const Orth &o, const void 
         p.e.src = x;
         p.e.alpha = s->a;
         p.e.beta = 1.0f / ORTH_SCALE;
-        e = launch_gemm<M_SPLIT, false, true>(p, o.update, st);
+        e = launch_gemm<M_SPLIT, true>(p, o.update, st);
         std::swap(x, y);
     }
     q.x = x;
