@@ -564,6 +564,7 @@ const char *check_steps(const msim_orthogonalize_spec *s)
 {
     const double a = s->a, b = s->b, c = s->c;
     double top = 1.0;
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return "orthogonalize: coefficients out of range";
     for (uint32_t k = 0; k < s->steps; k++) {
         double x = 0, poly = 0;
         for (int i = 0; i <= 4096; i++) {
