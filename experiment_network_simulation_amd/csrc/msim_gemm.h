@@ -33,7 +33,7 @@ struct Epilogue {
     uint64_t res_ld;
     void *pre;                   /* of the operands' type */
     uint64_t pre_ld;
-    uint32_t act, out32, vec;    /* vec: rows of out, res and pre on 16 bytes */
+    uint32_t act, out32;
     /* orthogonal update: out = alpha src + beta sum, split matrices of out_ld columns (a multiple of 32) */
     const void *src;
     uint64_t out_batch;          /* bytes between matrices of out and src */
@@ -53,11 +53,7 @@ struct GemmP {
 
 /* A kernel: tiles of bt x bt, stages in LDS, threads. */
 struct Kind { uint32_t bt, depth, threads; };
-constexpr Kind KINDS[] = {{256, 2, 512}, {128, 2, 256}, {64, 4, 256},
-#ifdef TUNE
-    {128, 4, 256}, {128, 2, 512}, {128, 4, 512}, {64, 2, 256}, {256, 2, 256},
-#endif
-};
+constexpr Kind KINDS[] = {{256, 2, 512}, {128, 2, 256}, {64, 4, 256}};
 constexpr uint32_t N_KINDS = sizeof(KINDS) / sizeof(Kind);
 
 /* How a product is cut: the kernel, and parts of k. */
@@ -83,31 +79,34 @@ template <> struct Type<M_F32> { typedef F32 D; };
 template <> struct Type<M_BF16> { typedef BF16 D; };
 
 
-/* eight elements from p on, n of them there; vec: p is on 16 bytes */
-template <typename D> __device__ __forceinline__ void load8(float *v, const void *p, uint64_t at, uint32_t n, bool vec)
+/* eight elements, n of them there; on any element, which costs an access or two more than on 16 bytes */
+template <typename D> __device__ __forceinline__ void load8(float *v, const void *p, uint64_t at, uint32_t n)
 {
     typedef typename D::raw raw;
-    typedef raw part __attribute__((ext_vector_type(16 / sizeof(raw))));
+    constexpr uint32_t PER = 16 / sizeof(raw);
+    typedef raw part __attribute__((ext_vector_type(PER)));
     const raw *q = (const raw *)p + at;
-    if (vec && n == 8) {
-        _Pragma("unroll") for (uint32_t i = 0; i < 8; i += 16 / sizeof(raw)) {
-            const part w = *(const part *)(q + i);
-            for (uint32_t j = 0; j < 16 / sizeof(raw); j++) v[i + j] = D::get(w[j]);
+    if (n == 8) {
+        _Pragma("unroll") for (uint32_t i = 0; i < 8; i += PER) {
+            const part w = __builtin_bit_cast(part, piece<D>(q + i));
+            for (uint32_t j = 0; j < PER; j++) v[i + j] = D::get(w[j]);
         }
     } else {
         _Pragma("unroll") for (uint32_t i = 0; i < 8; i++) v[i] = i < n ? D::get(q[i]) : 0.0f;
     }
 }
-template <typename D> __device__ __forceinline__ void store8(const float *v, void *p, uint64_t at, uint32_t n, bool vec)
+template <typename D> __device__ __forceinline__ void store8(const float *v, void *p, uint64_t at, uint32_t n)
 {
     typedef typename D::raw raw;
-    typedef raw part __attribute__((ext_vector_type(16 / sizeof(raw))));
+    constexpr uint32_t PER = 16 / sizeof(raw);
+    typedef raw part __attribute__((ext_vector_type(PER)));
+    typedef raw loose __attribute__((ext_vector_type(PER), aligned(sizeof(raw))));
     raw *q = (raw *)p + at;
-    if (vec && n == 8) {
-        _Pragma("unroll") for (uint32_t i = 0; i < 8; i += 16 / sizeof(raw)) {
+    if (n == 8) {
+        _Pragma("unroll") for (uint32_t i = 0; i < 8; i += PER) {
             part w;
-            for (uint32_t j = 0; j < 16 / sizeof(raw); j++) w[j] = D::put(v[i + j]);
-            *(part *)(q + i) = w;
+            for (uint32_t j = 0; j < PER; j++) w[j] = D::put(v[i + j]);
+            *(loose *)(q + i) = w;
         }
     } else {
         _Pragma("unroll") for (uint32_t i = 0; i < 8; i++)

@@ -157,13 +157,13 @@ template <int MODE> __device__ __forceinline__ void early_of(const Epilogue &e, 
         x.a = *(const u32x4 *)q;
         x.b = *(const u32x4 *)(q + 32);
     } else {
-        if (!e.res || !e.vec || m >= e.M || n + 8 > e.N) return;
+        if (!e.res || m >= e.M || n + 8 > e.N) return;
         if (MODE == M_F32 || e.out32) {
-            const u32x4 *q = (const u32x4 *)((const float *)e.res + m * e.res_ld + n);
-            x.a = q[0];
-            x.b = q[1];
+            const float *q = (const float *)e.res + m * e.res_ld + n;
+            x.a = piece<F32>(q);
+            x.b = piece<F32>(q + 4);
         } else {
-            x.a = *(const u32x4 *)((const uint16_t *)e.res + m * e.res_ld + n);
+            x.a = piece<F16>((const uint16_t *)e.res + m * e.res_ld + n);
         }
     }
 }
@@ -174,7 +174,7 @@ template <int MODE> __device__ __forceinline__ void before(const Epilogue &e, ui
     typedef typename Type<MODE>::D D;
     if (m >= e.M || n >= e.N) return;
     const uint32_t k = min(8u, e.N - n);
-    if (e.pre) store8<D>(v, e.pre, m * e.pre_ld + n, k, e.vec);
+    if (e.pre) store8<D>(v, e.pre, m * e.pre_ld + n, k);
     act_of<8>(v, e.act);
 }
 
@@ -196,24 +196,23 @@ __device__ __forceinline__ void after(const Epilogue &e, uint32_t batch, uint32_
         typedef typename Type<MODE>::D D;
         if (n >= e.N) return;
         const uint32_t k = min(8u, e.N - n);
-        const bool vec = e.vec && k == 8;
         if (e.res) {
             float r[8];
-            if (vec && (MODE == M_F32 || e.out32)) {
+            if (k == 8 && (MODE == M_F32 || e.out32)) {
                 const f32x4 a = __builtin_bit_cast(f32x4, x.a), b = __builtin_bit_cast(f32x4, x.b);
                 for (int i = 0; i < 8; i++) r[i] = i < 4 ? a[i] : b[i - 4];
-            } else if (vec) {
+            } else if (k == 8) {
                 const u16x8 a = __builtin_bit_cast(u16x8, x.a);
                 for (int i = 0; i < 8; i++) r[i] = Type<MODE == M_F32 ? M_F16 : MODE>::D::get(a[i]);
             } else if (e.out32) {
-                load8<F32>(r, e.res, m * e.res_ld + n, k, false);
+                load8<F32>(r, e.res, m * e.res_ld + n, k);
             } else {
-                load8<D>(r, e.res, m * e.res_ld + n, k, false);
+                load8<D>(r, e.res, m * e.res_ld + n, k);
             }
             for (int i = 0; i < 8; i++) v[i] += r[i];
         }
-        if (e.out32) store8<F32>(v, e.out, m * e.out_ld + n, k, vec);
-        else store8<D>(v, e.out, m * e.out_ld + n, k, vec);
+        if (e.out32) store8<F32>(v, e.out, m * e.out_ld + n, k);
+        else store8<D>(v, e.out, m * e.out_ld + n, k);
     }
 }
 
@@ -332,6 +331,7 @@ __device__ __forceinline__ void product(const GemmP &p, uint32_t total, uint32_t
             /* nothing but a rounding: all rows of the wavefront at once, 16 bits each */
             typedef typename Type<MODE>::D D;
             typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+            typedef u32x4 loose16 __attribute__((aligned(2)));
             constexpr int C = RN / 8, BLOCK = RM * RN * 2, FIT = STAGE / BLOCK;
             static_assert(WAVES <= DEPTH * FIT, "room for the rows of every wavefront");
             char *const stage = room(wave / FIT) + wave % FIT * BLOCK;
@@ -348,7 +348,7 @@ __device__ __forceinline__ void product(const GemmP &p, uint32_t total, uint32_t
             const uint32_t rows = ni + c * 8 < p.N ? p.M - min(p.M, m0 + wm * RM + lane / C) : 0;
             _Pragma("unroll 8") for (uint32_t r = 0; r < RM; r += 64 / C) {
                 const u32x4 v = *(const u32x4 *)(stage + (r + lane / C) * RN * 2 + (c ^ ((r + lane / C) & (C - 1))) * 16);
-                if (r < rows) *(u32x4 *)(to + r * p.e.out_ld) = v;
+                if (r < rows) *(loose16 *)(to + r * p.e.out_ld) = v;
             }
             return;
         }
@@ -360,7 +360,7 @@ __device__ __forceinline__ void product(const GemmP &p, uint32_t total, uint32_t
     const uint32_t c8 = lane % (RN / 8), n8 = ni + c8 * 8, r8 = lane / (RN / 8);
     const auto at = [&](uint32_t row, uint32_t half) { return (f32x4 *)(stage + row * RN + ((c8 * 2 + half) ^ (row & 15 & (C - 1))) * 4); };
     float bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (p.e.bias && p.parts == 1 && n8 < p.N) load8<F32>(bias, p.e.bias, n8, min(8u, p.N - n8), false);
+    if (p.e.bias && p.parts == 1 && n8 < p.N) load8<F32>(bias, p.e.bias, n8, min(8u, p.N - n8));
     _Pragma("unroll") for (int h = 0; h < RM / HR; h++) {
         const uint32_t mi = m0 + wm * RM + h * HR;
         /* what is read of memory is asked for first */
@@ -377,13 +377,14 @@ __device__ __forceinline__ void product(const GemmP &p, uint32_t total, uint32_t
         wave_sync();
         if (p.plain) {
             /* 32 bits as they are: parts of a sum, or results */
+            typedef f32x4 loose32 __attribute__((aligned(4)));
             const uint32_t c = lane % C, wide = p.parts > 1 ? (uint32_t)p.part_ld : p.N, r0 = lane / C;
             const uint64_t ld = p.parts > 1 ? p.part_ld : p.e.out_ld;
             float *to = (p.parts > 1 ? p.part + (uint64_t)group * p.M * ld : (float *)p.e.out) + (mi + r0) * ld + ni + c * 4;
             const uint32_t rows = ni + c * 4 < wide ? p.M - min(p.M, mi + r0) : 0;
             _Pragma("unroll 8") for (uint32_t r = 0; r < HR; r += 64 / C) {
                 const f32x4 v = *(const f32x4 *)(stage + (r + r0) * RN + (c ^ ((r + r0) & 15 & (C - 1))) * 4);
-                if (r < rows) *(f32x4 *)(to + r * ld) = v;
+                if (r < rows) *(loose32 *)(to + r * ld) = v;
             }
         } else {
             /* bias and activation, whose code is there once; then, in LDS until what is read of memory has
@@ -470,7 +471,7 @@ template <int MODE> __device__ __forceinline__ void join_parts(const GemmP &p, u
     float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     if constexpr (MODE != M_SPLIT) {
         float bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (p.e.bias && c < p.N) load8<F32>(bias, p.e.bias, c, min(8u, p.N - c), false);
+        if (p.e.bias && c < p.N) load8<F32>(bias, p.e.bias, c, min(8u, p.N - c));
         for (int i = 0; i < 8; i++) v[i] += bias[i];
         before<MODE>(p.e, m, c, v);
     }
@@ -501,7 +502,7 @@ template <int MODE> uint64_t ready(GemmP &p, const Plan &c)
     p.part_ld = up(p.N, MODE == M_SPLIT ? 32 : 8);
     if (p.parts > 1) p.mirror = 0;
     const Epilogue &e = p.e;
-    const bool only = MODE != M_SPLIT && !e.bias && !e.res && !e.pre && !e.act && e.vec && p.N % 8 == 0;
+    const bool only = MODE != M_SPLIT && !e.bias && !e.res && !e.pre && !e.act && p.N % 8 == 0;
     p.plain = p.parts > 1 || (only && (MODE == M_F32 || e.out32)) ? 1 : only ? 2 : 0;
     return (uint64_t)p.tm * p.tn * p.parts * p.batch;
 }

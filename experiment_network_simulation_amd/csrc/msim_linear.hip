@@ -117,7 +117,7 @@ struct GradP {
     void *d;                     /* NULL: grad itself is read by the products */
     float *sums;                 /* [blocks of rows][outs] (dbias itself, of one block), or NULL */
     uint32_t rows, outs, wide;   /* wide: columns of d */
-    uint32_t act, grad32, lglanes, vec, part, blocks;
+    uint32_t act, grad32, lglanes, part, blocks;
 };
 
 template <typename D> __device__ __forceinline__ void grad_rows(const GradP &p, uint32_t block, float *part)
@@ -130,15 +130,15 @@ template <typename D> __device__ __forceinline__ void grad_rows(const GradP &p, 
     if (n < p.wide)
         for (uint32_t m = by * p.part + (threadIdx.x >> p.lglanes); m < end; m += 256u >> p.lglanes) {
             float g[8], z[8];
-            if (p.grad32) load8<F32>(g, p.grad, m * p.grad_ld + n, k, p.vec);
-            else load8<D>(g, p.grad, m * p.grad_ld + n, k, p.vec);
+            if (p.grad32) load8<F32>(g, p.grad, m * p.grad_ld + n, k);
+            else load8<D>(g, p.grad, m * p.grad_ld + n, k);
             if (p.act) {
-                load8<D>(z, p.pre, m * p.pre_ld + n, k, p.vec);
+                load8<D>(z, p.pre, m * p.pre_ld + n, k);
                 slope_of<8>(z, p.act);
                 for (uint32_t i = 0; i < 8; i++) g[i] = i < k ? g[i] * z[i] : 0.0f;
             }
             for (int i = 0; i < 8; i++) sum[i] += g[i];
-            if (p.d) store8<D>(g, p.d, (uint64_t)m * p.wide + n, 8, true);
+            if (p.d) store8<D>(g, p.d, (uint64_t)m * p.wide + n, 8);
         }
     if (!p.sums) return;
     for (int i = 0; i < 8; i++) part[i * 256 + threadIdx.x] = sum[i];
@@ -187,20 +187,24 @@ constexpr uint64_t MAX_LD = 8000000;       /* bytes: the offsets of a tile's 256
  * itself, `high` where the card is full (measured with sizes of 1,024 and 8,192);
  * parts of k add the time of their sums through memory. */
 constexpr struct { double slots, more, low[3], high[3]; } TIMES[] = {         /* 16 bits, 32 bits, split */
-    {256, 9, {1.15, 8.0, 1.7}, {1.6, 8.0, 2.2}}, {512, 4, {0.53, 1.8, 0.6}, {1.0, 3.6, 1.3}}, {512, 2, {0.25, 0.5, 0.3}, {0.41, 0.95, 0.5}},
-#ifdef TUNE
-    {512, 2}, {512, 2}, {512, 2}, {512, 2}, {512, 2},
-#endif
+    {256, 9, {1.15, 8.0, 1.7}, {1.6, 8.0, 2.2}}, {512, 4, {0.53, 2.0, 0.6}, {1.0, 3.6, 1.3}}, {512, 2, {0.25, 0.63, 0.3}, {0.41, 1.2, 0.5}},
 };
 
 struct Product { uint64_t M, N, K, batch; };
 
-/* the best parts for a kernel; `share` of the card is this product's; the estimate */
-double plan_kind(uint32_t mode, const Product &q, uint32_t kind, double share, Plan *best)
+uint64_t tiles_of(const Product &q, uint32_t kind)
+{
+    const uint32_t bt = KINDS[kind].bt;
+    return ((q.M + bt - 1) / bt) * ((q.N + bt - 1) / bt) * q.batch;
+}
+
+/* The best parts for a kernel, and the estimate.  `share` of the card is this
+ * product's; it is crowded where another one fills the rest. */
+double plan_kind(uint32_t mode, const Product &q, uint32_t kind, double share, bool crowded, Plan *best)
 {
     const auto &c = TIMES[kind];
-    const uint32_t bt = KINDS[kind].bt, bk = mode == M_F16 || mode == M_BF16 ? 64 : 32, t = bk == 64 ? 0 : mode == M_F32 ? 1 : 2;
-    const uint64_t nk = (q.K + bk - 1) / bk, n = std::max<uint64_t>(nk, 1), tiles = ((q.M + bt - 1) / bt) * ((q.N + bt - 1) / bt) * q.batch;
+    const uint32_t bk = mode == M_F16 || mode == M_BF16 ? 64 : 32, t = bk == 64 ? 0 : mode == M_F32 ? 1 : 2;
+    const uint64_t nk = (q.K + bk - 1) / bk, n = std::max<uint64_t>(nk, 1), tiles = tiles_of(q, kind);
     const double slots = c.slots * share;
     double least = INFINITY;
     for (uint64_t parts : {1, 2, 3, 4, 6, 8, 9, 12, 16, 24, 32, 48, 64}) {
@@ -209,7 +213,7 @@ double plan_kind(uint32_t mode, const Product &q, uint32_t kind, double share, P
         if ((n + per - 1) / per != parts) continue;
         const double groups = (double)(tiles * parts), rounds = std::floor(groups / slots), rest = groups - rounds * slots;
         double cost = rounds * (c.more + c.high[t] * per);
-        if (rest > 0) cost += c.more + (rest <= slots / 2 ? c.low[t] : c.high[t]) * per;
+        if (rest > 0) cost += c.more + (rest <= slots / 2 && !crowded ? c.low[t] : c.high[t]) * per;
         if (parts > 1) cost += 4.0 + (double)q.batch * q.M * q.N * parts * 8.0 / 4e6;
         if (cost < least) {
             least = cost;
@@ -229,7 +233,7 @@ Plan plan_of(uint32_t mode, const Product &q)
     double least = INFINITY;
     for (uint32_t i = 0; i < N_KINDS; i++) {
         if (!has_kind(mode, i)) continue;
-        const double cost = plan_kind(mode, q, i, 1.0, &p);
+        const double cost = plan_kind(mode, q, i, 1.0, false, &p);
         if (cost < least) least = cost, best = p;
     }
     return best;
@@ -242,15 +246,17 @@ void plan_pair(uint32_t mode, const Product &a, const Product &b, Plan *pa, Plan
     double least = INFINITY;
     for (uint32_t i = 0; i < N_KINDS; i++) {
         if (!has_kind(mode, i)) continue;
-        const double cost = std::max(plan_kind(mode, a, i, 0.5, &x), plan_kind(mode, b, i, 0.5, &y));
+        const bool crowded = tiles_of(a, i) + tiles_of(b, i) > 256;
+        const double cost = std::max(plan_kind(mode, a, i, 0.5, crowded, &x), plan_kind(mode, b, i, 0.5, crowded, &y));
         if (cost < least) least = cost, *pa = x, *pb = y;
     }
 }
 
-/* Whether the products can read rows of `cols` elements as they lie: 16 bytes at a time. */
+/* Whether the products read rows of `cols` elements as they lie: 16 bytes at a time,
+ * which end with the row and lie on 4. */
 bool ready(const void *at, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t size)
 {
-    return (uintptr_t)at % 16 == 0 && cols * size % 16 == 0 && (rows <= 1 || (ld * size % 16 == 0 && ld * size <= MAX_LD));
+    return (uintptr_t)at % 4 == 0 && cols * size % 16 == 0 && (rows <= 1 || (ld * size % 4 == 0 && ld * size <= MAX_LD));
 }
 
 /* A rows x cols matrix as an operand: as it lies, or packed at ws. */
@@ -285,8 +291,6 @@ template <typename D> hipError_t prepare(const PackP &x, const PackP &w, const G
     const uint32_t grid = x.blocks + w.blocks + g.blocks;
     return grid ? launch(msim_linear_prepare<D>, grid, 256, 0, st, x, w, g) : hipSuccess;
 }
-
-bool on16(const void *at, uint64_t ld, uint32_t size) { return (uintptr_t)at % 16 == 0 && ld * size % 16 == 0; }
 
 const char *check_linear(const msim_linear_spec *s, int *code)
 {
@@ -401,11 +405,9 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
     char *wx = ws, *ww = wx + b.x.bytes(), *wd = ww + b.w.bytes(), *wsum = wd + b.d_bytes, *wpart = wsum + b.sum_bytes;
     GradP g = {};
     if ((b.own || dbias) && s->rows) {
-        const uint32_t gsize = size_of(s->out_dtype);
         g = {grad, pre, s->out_stride, s->pre_stride, b.own ? wd : nullptr, !dbias ? nullptr : b.blocks == 1 ? dbias : (float *)wsum,
-             (uint32_t)s->rows, s->outs, b.own ? (uint32_t)b.wide : (uint32_t)up(s->outs, 8), s->act, s->out_dtype == MSIM_F32, 0, 0, b.part, 0};
+             (uint32_t)s->rows, s->outs, b.own ? (uint32_t)b.wide : (uint32_t)up(s->outs, 8), s->act, s->out_dtype == MSIM_F32, 0, b.part, 0};
         while (g.lglanes < 5 && (8u << g.lglanes) < g.wide) g.lglanes++;
-        g.vec = on16(grad, s->out_stride, gsize) && (!s->act || on16(pre, s->pre_stride, size));
         g.blocks = b.blocks * ((g.wide + (8u << g.lglanes) - 1) / (8u << g.lglanes));
     }
     hipError_t r = prepare<D>(dweight ? pack_of(b.x, wx) : PackP{}, dx ? pack_of(b.w, ww) : PackP{}, g, st);
@@ -424,7 +426,6 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
         px.part = (float *)wpart;
         px.e.out = dx;
         px.e.out_ld = s->dx_stride;
-        px.e.vec = on16(dx, s->dx_stride, size);
     }
     if (dweight) {
         pw.a = d;
@@ -436,7 +437,6 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
         pw.part = (float *)(wpart + b.px.part_bytes);
         pw.e.out = dweight;
         pw.e.out_ld = s->dweight_stride;
-        pw.e.vec = on16(dweight, s->dweight_stride, size);
     }
     if (r == hipSuccess) r = launch_pair<MODE>(px, b.px, pw, b.pw, st);
     return launched(r, "linear backward launch");
@@ -678,7 +678,6 @@ extern "C" int msim_linear(const msim_linear_spec *s, const void *x, const void 
         return fail(MSIM_E_ARG, "linear: residual is out, with two strides");
     const Forward f = forward_of(s, x, weight);
     if (int rc = check_workspace(workspace, workspace_bytes, f.bytes, "linear: workspace missing, too small or not on 256 bytes")) return rc;
-    const uint32_t size = size_of(s->dtype), osize = size_of(s->out_dtype);
     Epilogue e = {};
     e.M = (uint32_t)s->rows;
     e.N = s->outs;
@@ -691,8 +690,6 @@ extern "C" int msim_linear(const msim_linear_spec *s, const void *x, const void 
     e.pre_ld = s->pre_stride;
     e.act = s->act;
     e.out32 = s->out_dtype == MSIM_F32 && s->dtype != MSIM_F32;
-    e.vec = on16(out, s->out_stride, osize) && (!residual || on16(residual, s->residual_stride, osize)) &&
-            (!pre || on16(pre, s->pre_stride, size));
     char *ws = (char *)workspace;
     hipStream_t st = (hipStream_t)hip_stream;
     return s->dtype == MSIM_F32 ? run_forward<M_F32>(s, f, e, ws, st)
