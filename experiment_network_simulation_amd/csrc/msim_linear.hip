@@ -246,8 +246,9 @@ void plan_pair(uint32_t mode, const Product &a, const Product &b, Plan *pa, Plan
     double least = INFINITY;
     for (uint32_t i = 0; i < N_KINDS; i++) {
         if (!has_kind(mode, i)) continue;
-        const bool crowded = tiles_of(a, i) + tiles_of(b, i) > 256;
-        const double cost = std::max(plan_kind(mode, a, i, 0.5, crowded, &x), plan_kind(mode, b, i, 0.5, crowded, &y));
+        double cost = std::max(plan_kind(mode, a, i, 0.5, false, &x), plan_kind(mode, b, i, 0.5, false, &y));
+        if (tiles_of(a, i) * x.parts + tiles_of(b, i) * y.parts > 256)
+            cost = std::max(plan_kind(mode, a, i, 0.5, true, &x), plan_kind(mode, b, i, 0.5, true, &y));
         if (cost < least) least = cost, *pa = x, *pb = y;
     }
 }
