@@ -62,6 +62,14 @@ hipError_t launch(void (*kernel)(P...), uint32_t grid, uint32_t block, size_t ld
     return MSIM_E_HIP;
 }
 
+/* an answer for a workspace that the call cannot use, or MSIM_OK */
+[[maybe_unused]] inline int check_workspace(const void *ws, uint64_t have, uint64_t need, const char *what)
+{
+    if (!need) return MSIM_OK;
+    if (!ws || have < need || (uintptr_t)ws % 256) return fail(MSIM_E_WORKSPACE, what);
+    return MSIM_OK;
+}
+
 } // namespace
 
 #endif

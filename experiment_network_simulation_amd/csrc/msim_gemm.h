@@ -59,6 +59,11 @@ constexpr uint32_t N_KINDS = sizeof(KINDS) / sizeof(Kind);
 /* How a product is cut: the kernel, and parts of k. */
 struct Plan { uint32_t kind, parts, per, nk; uint64_t part_bytes; };
 
+/* The plan of a product, and those of two in one launch, each on half of the card (their operations are as many). */
+struct Product { uint64_t M, N, K, batch; };
+__attribute__((visibility("hidden"))) Plan plan_of(uint32_t mode, const Product &q);
+__attribute__((visibility("hidden"))) void plan_pair(uint32_t mode, const Product &a, const Product &b, Plan *pa, Plan *pb);
+
 /* Enqueues a product of A contiguous along k and B along k (BMC: along n); p.part
  * has room for the plan's parts.  launch_pair: of a backward pass, x of A along k
  * and B along n, w of both along m and n, in one launch and with plans of one

@@ -1,6 +1,5 @@
-/* A linear layer with bias, activation and residual, its gradient, and the
- * orthogonal update of a weight matrix by Newton-Schulz products (msim_linear,
- * msim_linear_backward and msim_orthogonalize of include/msim.h, which has the
+/* A linear layer with bias, activation and residual, and its gradient
+ * (msim_linear and msim_linear_backward of include/msim.h, which has the
  * definitions).
  */
 
@@ -15,7 +14,7 @@ namespace {
 /* few rows                                                                  */
 /* ------------------------------------------------------------------------ */
 
-/* A linear layer of up to 16 MT rows: 16 NT outs a workgroup, whose wavefronts
+/* A linear layer of up to 16 MT rows: 16 outs a workgroup, whose wavefronts
  * share k.  The weights are read once, from where they lie on any element. */
 struct FewP {
     const void *x, *w;
@@ -24,40 +23,33 @@ struct FewP {
     Epilogue e;
 };
 
-template <int MODE, int MT, int NT, int WAVES> __global__ void __launch_bounds__(64 * WAVES) msim_linear_few(FewP p)
+template <int MODE, int MT, int WAVES> __global__ void __launch_bounds__(64 * WAVES) msim_linear_few(FewP p)
 {
     typedef typename Type<MODE>::D D;
     typedef typename D::raw raw;
-    __shared__ f32x4 sums[WAVES * MT * NT * 64];
+    __shared__ f32x4 sums[WAVES * MT * 64];
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = lane & 15;
-    const uint32_t n0 = blockIdx.x * 16 * NT;
-    const raw *w[NT], *x[MT];
-    for (int j = 0; j < NT; j++) w[j] = (const raw *)p.w + min(n0 + j * 16 + l, p.e.N - 1) * p.w_ld;
+    const uint32_t n0 = blockIdx.x * 16;
+    const raw *w[1] = {(const raw *)p.w + min(n0 + l, p.e.N - 1) * p.w_ld}, *x[MT];
     for (int i = 0; i < MT; i++) x[i] = (const raw *)p.x + min(i * 16 + l, p.e.M - 1) * p.x_ld;
-    f32x4 acc[MT][NT];
-    for (int i = 0; i < MT; i++)
-        for (int j = 0; j < NT; j++) acc[i][j] = f32x4{0, 0, 0, 0};
-    stream<D, MT, NT>(w, x, p.K, wave, WAVES, acc);
-    join<MT, NT, WAVES>(sums, wave, acc);
+    f32x4 acc[MT][1];
+    for (int i = 0; i < MT; i++) acc[i][0] = f32x4{0, 0, 0, 0};
+    stream<D, MT, 1>(w, x, p.K, wave, WAVES, acc);
+    join<MT, 1, WAVES>(sums, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
-        const uint32_t m = i * 16 + l;
+        const uint32_t m = i * 16 + l, n = n0 + (lane >> 4) * 4, have = n < p.e.N ? min(4u, p.e.N - n) : 0;
         if (i % WAVES != (int)wave || m >= p.e.M) continue;
-        for (int j = 0; j < NT; j++) {
-            float u[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-            const uint32_t nj = n0 + j * 16 + (lane >> 4) * 4;
-            for (uint32_t k = 0; k < 4; k++) {
-                if (p.e.bias && nj + k < p.e.N) u[k] += p.e.bias[nj + k];
-                if (p.e.pre && nj + k < p.e.N) ((raw *)p.e.pre)[m * p.e.pre_ld + nj + k] = D::put(u[k]);
-            }
-            act_of<4>(u, p.e.act);
-            for (uint32_t k = 0; k < 4; k++) {
-                const uint32_t n = nj + k;
-                if (n >= p.e.N) continue;
-                float v = u[k];
-                if (p.e.res) v += p.e.out32 ? ((const float *)p.e.res)[m * p.e.res_ld + n] : D::get(((const raw *)p.e.res)[m * p.e.res_ld + n]);
-                if (p.e.out32) ((float *)p.e.out)[m * p.e.out_ld + n] = v;
-                else ((raw *)p.e.out)[m * p.e.out_ld + n] = D::put(v);
-            }
+        float v[4];
+        for (uint32_t k = 0; k < 4; k++) {
+            v[k] = acc[i][0][k] + (p.e.bias && k < have ? p.e.bias[n + k] : 0.0f);
+            if (p.e.pre && k < have) ((raw *)p.e.pre)[m * p.e.pre_ld + n + k] = D::put(v[k]);
+        }
+        act_of<4>(v, p.e.act);
+        for (uint32_t k = 0; k < have; k++) {
+            const uint64_t at = m * p.e.res_ld + n + k;
+            if (p.e.res) v[k] += p.e.out32 ? ((const float *)p.e.res)[at] : D::get(((const raw *)p.e.res)[at]);
+            if (p.e.out32) ((float *)p.e.out)[m * p.e.out_ld + n + k] = v[k];
+            else ((raw *)p.e.out)[m * p.e.out_ld + n + k] = D::put(v[k]);
         }
     }
 }
@@ -182,77 +174,6 @@ __global__ void __launch_bounds__(1024) msim_linear_bias_grad(const float *sums,
 uint32_t size_of(uint32_t dtype) { return dtype == MSIM_F32 ? 4 : 2; }
 constexpr uint64_t MAX_LD = 8000000;       /* bytes: the offsets of a tile's 256 rows stay below 2^31 */
 
-/* The cheapest by an estimate in us.  Workgroups of a kind are on the card `slots`
- * at a time; one takes `more`, and for a stage `low` where it has a compute unit to
- * itself, `high` where the card is full (measured with sizes of 1,024 and 8,192);
- * parts of k add the time of their sums through memory. */
-constexpr struct { double slots, more, low[3], high[3]; } TIMES[] = {         /* 16 bits, 32 bits, split */
-    {256, 9, {1.15, 8.0, 1.7}, {1.6, 8.0, 2.2}}, {512, 4, {0.53, 2.0, 0.6}, {1.0, 3.6, 1.3}}, {512, 2, {0.25, 0.63, 0.3}, {0.41, 1.2, 0.5}},
-};
-
-struct Product { uint64_t M, N, K, batch; };
-
-uint64_t tiles_of(const Product &q, uint32_t kind)
-{
-    const uint32_t bt = KINDS[kind].bt;
-    return ((q.M + bt - 1) / bt) * ((q.N + bt - 1) / bt) * q.batch;
-}
-
-/* The best parts for a kernel, and the estimate.  `share` of the card is this
- * product's; it is crowded where another one fills the rest. */
-double plan_kind(uint32_t mode, const Product &q, uint32_t kind, double share, bool crowded, Plan *best)
-{
-    const auto &c = TIMES[kind];
-    const uint32_t bk = mode == M_F16 || mode == M_BF16 ? 64 : 32, t = bk == 64 ? 0 : mode == M_F32 ? 1 : 2;
-    const uint64_t nk = (q.K + bk - 1) / bk, n = std::max<uint64_t>(nk, 1), tiles = tiles_of(q, kind);
-    const double slots = c.slots * share;
-    double least = INFINITY;
-    for (uint64_t parts : {1, 2, 3, 4, 6, 8, 9, 12, 16, 24, 32, 48, 64}) {
-        if (parts > n) break;
-        const uint64_t per = (n + parts - 1) / parts;
-        if ((n + per - 1) / per != parts) continue;
-        const double groups = (double)(tiles * parts), rounds = std::floor(groups / slots), rest = groups - rounds * slots;
-        double cost = rounds * (c.more + c.high[t] * per);
-        if (rest > 0) cost += c.more + (rest <= slots / 2 && !crowded ? c.low[t] : c.high[t]) * per;
-        if (parts > 1) cost += 4.0 + (double)q.batch * q.M * q.N * parts * 8.0 / 4e6;
-        if (cost < least) {
-            least = cost;
-            *best = {kind, (uint32_t)parts, (uint32_t)per, (uint32_t)nk,
-                     parts > 1 ? up(q.batch * parts * q.M * up(q.N, mode == M_SPLIT ? 32 : 8) * 4, 256) : 0};
-        }
-    }
-    return least;
-}
-
-/* the kernels that a type has: 32-bit products are so slow that tiles of 128 feed them as well as larger ones */
-bool has_kind(uint32_t mode, uint32_t kind) { return mode != M_F32 || KINDS[kind].bt < 256; }
-
-Plan plan_of(uint32_t mode, const Product &q)
-{
-    Plan best = {}, p;
-    double least = INFINITY;
-    for (uint32_t i = 0; i < N_KINDS; i++) {
-        if (!has_kind(mode, i)) continue;
-        const double cost = plan_kind(mode, q, i, 1.0, false, &p);
-        if (cost < least) least = cost, best = p;
-    }
-    return best;
-}
-
-/* two products in one launch, each on half of the card (their operations are as many) */
-void plan_pair(uint32_t mode, const Product &a, const Product &b, Plan *pa, Plan *pb)
-{
-    Plan x, y;
-    double least = INFINITY;
-    for (uint32_t i = 0; i < N_KINDS; i++) {
-        if (!has_kind(mode, i)) continue;
-        double cost = std::max(plan_kind(mode, a, i, 0.5, false, &x), plan_kind(mode, b, i, 0.5, false, &y));
-        if (tiles_of(a, i) * x.parts + tiles_of(b, i) * y.parts > 256)
-            cost = std::max(plan_kind(mode, a, i, 0.5, true, &x), plan_kind(mode, b, i, 0.5, true, &y));
-        if (cost < least) least = cost, *pa = x, *pb = y;
-    }
-}
-
 /* Whether the products read rows of `cols` elements as they lie: 16 bytes at a time,
  * which end with the row and lie on 4. */
 bool ready(const void *at, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t size)
@@ -315,7 +236,14 @@ const char *check_linear(const msim_linear_spec *s, int *code)
     return nullptr;
 }
 
-constexpr uint64_t FEW_ROWS = 64;          /* rows of msim_linear_few, at most */
+/* Few rows are streamed while that is faster than tiles: 16 x 4,096 -> 4,096 bf16 10.0
+ * us (12.2 in tiles), -> 16,384 31 (21); 24 x 1,000 -> 1,000 5.2 (6.7), 64 rows of
+ * them 6.5 (6.8), 40 x 4,096 -> 4,096 16.4 (11.7). */
+bool few_rows(const msim_linear_spec *s)
+{
+    if (s->rows <= MSIM_LINEAR_FEW) return s->outs <= MSIM_LINEAR_FEW_OUTS;
+    return s->rows <= 64 && s->cols <= 1024 && s->outs <= 1024;
+}
 
 struct Forward {
     Matrix x, w;
@@ -328,9 +256,9 @@ Forward forward_of(const msim_linear_spec *s, const void *x, const void *weight)
 {
     Forward f = {};
     const uint32_t size = size_of(s->dtype);
+    f.few = few_rows(s);
     f.x = matrix_of(x, s->rows, s->cols, s->x_stride, size);
     f.w = matrix_of(weight, s->outs, s->cols, s->weight_stride, size);
-    f.few = s->rows <= FEW_ROWS;
     if (f.few) return f;
     f.plan = plan_of(s->dtype, {s->rows, s->outs, f.x.wide(), 1});
     f.bytes = f.x.bytes() + f.w.bytes() + f.plan.part_bytes;
@@ -342,12 +270,9 @@ int run_forward(const msim_linear_spec *s, const Forward &f, const Epilogue &e, 
 {
     if (f.few) {
         const FewP q = {f.x.at, f.w.at, f.x.ld, f.w.ld, s->cols, e};
-        /* one row of tiles and 8 wavefronts where there are few outs, so that the card is filled */
-        const uint32_t wide = (s->outs + 31) / 32, thin = (s->outs + 15) / 16;
-        const hipError_t r = s->rows > 32 ? launch(msim_linear_few<MODE, 4, 2, 4>, wide, 256, 0, st, q)
-            : s->rows > 16 ? launch(msim_linear_few<MODE, 2, 2, 4>, wide, 256, 0, st, q)
-            : wide >= 256 ? launch(msim_linear_few<MODE, 1, 2, 4>, wide, 256, 0, st, q)
-                          : launch(msim_linear_few<MODE, 1, 1, 8>, thin, 512, 0, st, q);
+        const uint32_t grid = (s->outs + 15) / 16;
+        const hipError_t r = s->rows > 32 ? launch(msim_linear_few<MODE, 4, 8>, grid, 512, 0, st, q)
+            : s->rows > 16 ? launch(msim_linear_few<MODE, 2, 16>, grid, 1024, 0, st, q) : launch(msim_linear_few<MODE, 1, 16>, grid, 1024, 0, st, q);
         return launched(r, "linear launch");
     }
     GemmP p = {};
@@ -443,217 +368,6 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
     return launched(r, "linear backward launch");
 }
 
-/* ------------------------------------------------------------------------ */
-/* orthogonal update                                                         */
-/* ------------------------------------------------------------------------ */
-
-/* X is held times this: its singular values stay near 1, so high parts are well
- * inside f16 and low parts above its subnormal numbers where they matter. */
-constexpr float ORTH_SCALE = 2048.0f;
-constexpr uint32_t NORM_PARTS = 256;
-
-/* sums of squares in 64 bits: NORM_PARTS workgroups a matrix */
-template <typename D> __global__ void __launch_bounds__(256) msim_orth_norm(const void *from, uint64_t size, double *part)
-{
-    constexpr uint32_t PER = 16 / sizeof(typename D::raw);
-    typedef typename D::raw vec __attribute__((ext_vector_type(PER)));
-    __shared__ double sums[4];
-    const uint32_t batch = blockIdx.x / NORM_PARTS, k = blockIdx.x % NORM_PARTS;
-    const typename D::raw *x = (const typename D::raw *)from + batch * size;
-    double s = 0;
-    _Pragma("unroll 2") for (uint64_t i = (k * 256 + threadIdx.x) * PER; i < size; i += NORM_PARTS * 256 * PER) {
-        const vec v = __builtin_bit_cast(vec, i + PER <= size ? piece<D>(x + i) : piece<D>(x + i, 0, (uint32_t)(size - i)));
-        for (uint32_t j = 0; j < PER; j++) {
-            const double d = D::get(v[j]);
-            s += d * d;
-        }
-    }
-    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) part[blockIdx.x] = sums[0] + sums[1] + sums[2] + sums[3];
-}
-
-struct OrthP {
-    const void *in;
-    void *out;
-    char *x;                     /* split, m rows of ld columns */
-    const double *part;
-    uint64_t rows, cols, ld, batch;        /* rows <= cols unless `flip`; batch: bytes between matrices of x */
-    double eps;
-    uint32_t count, flip;
-};
-
-/* Tiles of 32 x 64 between the caller's matrices and X (flip: its transpose).
- * BEGIN: X = scale in / (norm + eps); otherwise out = X / scale. */
-template <typename D, bool BEGIN> __global__ void __launch_bounds__(256) msim_orth_move(OrthP p)
-{
-    __shared__ float tile[32][65];
-    __shared__ double factor;
-    const uint64_t m = p.flip ? p.cols : p.rows, n = p.flip ? p.rows : p.cols;
-    const uint64_t tn = (p.ld + 63) / 64, tm = (m + 31) / 32;
-    const uint32_t batch = (uint32_t)(blockIdx.x / (tm * tn)), at = (uint32_t)(blockIdx.x - batch * tm * tn);
-    const uint64_t m0 = at / tn * 32, n0 = at % tn * 64;
-    char *x = p.x + batch * p.batch;
-    const uint64_t base = batch * p.rows * p.cols;
-    if constexpr (BEGIN) {
-        if (threadIdx.x < 64) {
-            const double *q = p.part + batch * NORM_PARTS + threadIdx.x;
-            double s = q[0] + q[64] + q[128] + q[192];
-            for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-            if (threadIdx.x == 0) factor = s < INFINITY ? ORTH_SCALE / (sqrt(s) + p.eps) : NAN;
-        }
-        __syncthreads();
-        const double f = factor;
-        for (uint32_t i = threadIdx.x; i < 2048; i += 256) {
-            const uint32_t r = p.flip ? i % 32 : i / 64, c = p.flip ? i / 32 : i % 64;
-            const uint64_t mm = m0 + r, nn = n0 + c;
-            float v = 0;
-            if (mm < m && nn < n) v = (float)(f * (double)D::get(((const typename D::raw *)p.in)[base + (p.flip ? nn * p.cols + mm : mm * p.cols + nn)]));
-            tile[r][c] = v;
-        }
-        __syncthreads();
-        const uint32_t r = threadIdx.x / 8, c = threadIdx.x % 8 * 8;
-        if (m0 + r < m && n0 + c < p.ld) {
-            float v[8];
-            for (int i = 0; i < 8; i++) v[i] = tile[r][c + i];
-            store_split(v, x, split_at(p.ld, (uint32_t)(m0 + r), (uint32_t)(n0 + c)));
-        }
-    } else {
-        const uint32_t r = threadIdx.x / 8, c = threadIdx.x % 8 * 8;
-        if (m0 + r < m && n0 + c < p.ld) {
-            float v[8];
-            load_split(v, x, split_at(p.ld, (uint32_t)(m0 + r), (uint32_t)(n0 + c)));
-            for (int i = 0; i < 8; i++) tile[r][c + i] = v[i] * (1.0f / ORTH_SCALE);
-        }
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < 2048; i += 256) {
-            const uint32_t rr = p.flip ? i % 32 : i / 64, cc = p.flip ? i / 32 : i % 64;
-            const uint64_t mm = m0 + rr, nn = n0 + cc;
-            if (mm < m && nn < n) ((typename D::raw *)p.out)[base + (p.flip ? nn * p.cols + mm : mm * p.cols + nn)] = D::put(tile[rr][cc]);
-        }
-    }
-}
-
-struct Orth {
-    uint64_t m, n, lx, lp;       /* of X: rows, columns, columns as held; of P: as held */
-    uint64_t norm_bytes, x_bytes, p_bytes, bytes;
-    Plan square, poly, update;
-};
-
-Orth orth_of(const msim_orthogonalize_spec *s)
-{
-    Orth o;
-    o.m = std::min(s->rows, s->cols);
-    o.n = std::max(s->rows, s->cols);
-    o.lx = up(o.n, 32);
-    o.lp = up(o.m, 32);
-    o.norm_bytes = up((uint64_t)s->count * NORM_PARTS * 8, 256);
-    o.x_bytes = up(s->count * o.m * o.lx * 4, 256);
-    o.p_bytes = up(s->count * o.m * o.lp * 4, 256);
-    o.square = plan_of(M_SPLIT, {o.m, o.lp, o.lx, s->count});
-    o.poly = plan_of(M_SPLIT, {o.m, o.lp, o.lp, s->count});
-    o.update = plan_of(M_SPLIT, {o.m, o.lx, o.lp, s->count});
-    o.bytes = o.norm_bytes + 2 * o.x_bytes + 2 * o.p_bytes +
-              std::max(o.square.part_bytes, std::max(o.poly.part_bytes, o.update.part_bytes));
-    return o;
-}
-
-/* The largest singular value and |B| that the steps can meet, from any in 0 .. 1:
- * both have to fit f16 times ORTH_SCALE. */
-const char *check_steps(const msim_orthogonalize_spec *s)
-{
-    const double a = s->a, b = s->b, c = s->c;
-    double top = 1.0;
-    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return "orthogonalize: coefficients out of range";
-    for (uint32_t k = 0; k < s->steps; k++) {
-        double x = 0, poly = 0;
-        for (int i = 0; i <= 4096; i++) {
-            const double v = top * i / 4096, q = v * v;
-            x = std::max(x, std::fabs(v * (a + q * (b + c * q))));
-            poly = std::max(poly, std::fabs(q * (b + c * q)));
-        }
-        if (!(poly <= 24.0 && top * top <= 24.0)) return "orthogonalize: steps with these coefficients leave the range of the products";
-        top = x * 1.001;
-        if (!(top <= 24.0)) return "orthogonalize: steps with these coefficients leave the range of the products";
-    }
-    return nullptr;
-}
-
-const char *check_orth(const msim_orthogonalize_spec *s, int *code)
-{
-    *code = MSIM_E_ARG;
-    if (!s) return "orthogonalize: null spec";
-    if (s->version != MSIM_ABI_VERSION) return "orthogonalize: spec version mismatch";
-    if (s->dtype > MSIM_BF16) return "orthogonalize: unknown dtype";
-    if (!s->rows || !s->cols) return "orthogonalize: rows and cols must be at least 1";
-    if (s->reserved) return "orthogonalize: reserved must be 0";
-    if (!(s->eps >= 0) || !std::isfinite(s->eps)) return "orthogonalize: eps must be finite and not negative";
-    *code = MSIM_E_LIMIT;
-    if (s->rows > MSIM_MAX_LINEAR || s->cols > MSIM_MAX_LINEAR) return "orthogonalize: rows or cols above MSIM_MAX_LINEAR";
-    if (s->count > 65536 || (uint64_t)s->count * s->rows * s->cols >> 36) return "orthogonalize: more than 65,536 matrices or 2^36 elements";
-    if (s->steps > 64) return "orthogonalize: more than 64 steps";
-    *code = MSIM_E_ARG;
-    return check_steps(s);
-}
-
-template <typename D>
-hipError_t run_orth(const msim_orthogonalize_spec *s, const Orth &o, const void *in, void *out, char *ws, hipStream_t st)
-{
-    char *norms = ws, *x = norms + o.norm_bytes, *y = x + o.x_bytes, *sq = y + o.x_bytes, *poly = sq + o.p_bytes, *part = poly + o.p_bytes;
-    OrthP q = {in, out, x, (const double *)norms, s->rows, s->cols, o.lx, o.m * o.lx * 4, s->eps, s->count, s->rows > s->cols};
-    const uint32_t moves = (uint32_t)((o.lx + 63) / 64 * ((o.m + 31) / 32) * s->count);
-    hipError_t e = launch(msim_orth_norm<D>, s->count * NORM_PARTS, 256, 0, st, in, s->rows * s->cols, (double *)norms);
-    if (e == hipSuccess) e = launch(msim_orth_move<D, true>, moves, 256, 0, st, q);
-    for (uint32_t k = 0; k < s->steps && e == hipSuccess; k++) {
-        const Operand ox = {x, o.m * o.lx * 4, o.lx * 4, o.m * o.lx * 4};
-        const Operand osq = {sq, o.m * o.lp * 4, o.lp * 4, o.m * o.lp * 4}, opoly = {poly, o.m * o.lp * 4, o.lp * 4, o.m * o.lp * 4};
-        GemmP p = {};
-        p.batch = s->count;
-        p.part = (float *)part;
-        p.M = p.N = p.e.M = p.e.N = (uint32_t)o.m;
-        p.mirror = 1;
-        p.a = p.b = ox;
-        p.K = (uint32_t)o.lx;
-        p.e.out = sq;
-        p.e.out_ld = o.lp;
-        p.e.out_batch = o.m * o.lp * 4;
-        p.e.beta = 1.0f / ORTH_SCALE;
-        e = launch_gemm<M_SPLIT, false>(p, o.square, st);
-        if (e != hipSuccess) break;
-        p.a = p.b = osq;
-        p.K = (uint32_t)o.lp;
-        p.e.out = poly;
-        p.e.src = sq;
-        p.e.alpha = s->b;
-        p.e.beta = s->c / ORTH_SCALE;
-        e = launch_gemm<M_SPLIT, false>(p, o.poly, st);
-        if (e != hipSuccess) break;
-        p.mirror = 0;
-        p.a = opoly;
-        p.b = ox;
-        p.N = p.e.N = (uint32_t)o.n;
-        p.e.out = y;
-        p.e.out_ld = o.lx;
-        p.e.out_batch = o.m * o.lx * 4;
-        p.e.src = x;
-        p.e.alpha = s->a;
-        p.e.beta = 1.0f / ORTH_SCALE;
-        e = launch_gemm<M_SPLIT, true>(p, o.update, st);
-        std::swap(x, y);
-    }
-    q.x = x;
-    if (e == hipSuccess) e = launch(msim_orth_move<D, false>, moves, 256, 0, st, q);
-    return e;
-}
-
-int check_workspace(const void *ws, uint64_t have, uint64_t need, const char *what)
-{
-    if (!need) return MSIM_OK;
-    if (!ws || have < need || (uintptr_t)ws % 256) return fail(MSIM_E_WORKSPACE, what);
-    return MSIM_OK;
-}
-
 }   // namespace
 
 extern "C" int msim_linear_workspace(const msim_linear_spec *s, const void *x, const void *weight, uint64_t *bytes)
@@ -725,29 +439,4 @@ extern "C" int msim_linear_backward(const msim_linear_spec *s, const void *x, co
     return s->dtype == MSIM_F32 ? run_backward<M_F32>(s, b, grad, pre, dx, dweight, dbias, ws, st)
         : s->dtype == MSIM_F16 ? run_backward<M_F16>(s, b, grad, pre, dx, dweight, dbias, ws, st)
                                : run_backward<M_BF16>(s, b, grad, pre, dx, dweight, dbias, ws, st);
-}
-
-extern "C" int msim_orthogonalize_workspace(const msim_orthogonalize_spec *s, uint64_t *bytes)
-{
-    int code;
-    if (const char *why = check_orth(s, &code)) return fail(code, why);
-    if (!bytes) return fail(MSIM_E_ARG, "orthogonalize: null bytes");
-    *bytes = s->count ? orth_of(s).bytes : 0;
-    return MSIM_OK;
-}
-
-extern "C" int msim_orthogonalize(const msim_orthogonalize_spec *s, const void *update, void *out, void *workspace,
-                                  uint64_t workspace_bytes, void *hip_stream)
-{
-    int code;
-    if (const char *why = check_orth(s, &code)) return fail(code, why);
-    if (s->count == 0) return MSIM_OK;
-    if (!update || !out) return fail(MSIM_E_ARG, "orthogonalize: null update or out");
-    const Orth o = orth_of(s);
-    if (int rc = check_workspace(workspace, workspace_bytes, o.bytes, "orthogonalize: workspace missing, too small or not on 256 bytes")) return rc;
-    hipStream_t st = (hipStream_t)hip_stream;
-    const hipError_t e = s->dtype == MSIM_F32 ? run_orth<F32>(s, o, update, out, (char *)workspace, st)
-        : s->dtype == MSIM_F16 ? run_orth<F16>(s, o, update, out, (char *)workspace, st)
-                               : run_orth<BF16>(s, o, update, out, (char *)workspace, st);
-    return launched(e, "orthogonalize launch");
 }

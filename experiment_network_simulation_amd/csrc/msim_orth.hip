@@ -1,0 +1,483 @@
+/* The orthogonal update of a weight matrix by Newton-Schulz products
+ * (msim_orthogonalize of include/msim.h, which has the definition).
+ *
+ * X, P = X X^T and B = b P + c P P are held as sums of two f16, 22 bits, and a
+ * product is three of f16: their rate leaves it three times as fast as one of 32
+ * bits, and its error near that.  Only one side of P and B, which are
+ * symmetric, is computed.
+ */
+
+#include <algorithm>
+#include <cmath>
+
+#include "msim_gemm.h"
+
+namespace {
+
+/* X is held times this: its singular values stay near 1, so high parts are well
+ * inside f16 and low parts above its subnormal numbers where they matter. */
+constexpr float ORTH_SCALE = 2048.0f;
+constexpr uint32_t NORM_PARTS = 256;
+
+/* sums of squares in 64 bits: NORM_PARTS workgroups a matrix */
+template <typename D> __global__ void __launch_bounds__(256) msim_orth_norm(const void *from, uint64_t size, double *part)
+{
+    constexpr uint32_t PER = 16 / sizeof(typename D::raw);
+    typedef typename D::raw vec __attribute__((ext_vector_type(PER)));
+    __shared__ double sums[4];
+    const uint32_t batch = blockIdx.x / NORM_PARTS, k = blockIdx.x % NORM_PARTS;
+    const typename D::raw *x = (const typename D::raw *)from + batch * size;
+    double s = 0;
+    _Pragma("unroll 2") for (uint64_t i = (k * 256 + threadIdx.x) * PER; i < size; i += NORM_PARTS * 256 * PER) {
+        const vec v = __builtin_bit_cast(vec, i + PER <= size ? piece<D>(x + i) : piece<D>(x + i, 0, (uint32_t)(size - i)));
+        for (uint32_t j = 0; j < PER; j++) {
+            const double d = D::get(v[j]);
+            s += d * d;
+        }
+    }
+    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) part[blockIdx.x] = sums[0] + sums[1] + sums[2] + sums[3];
+}
+
+/* what X is the update times: one wavefront asks, all its lanes know.  A norm that is not finite makes it NaN. */
+__device__ __forceinline__ double scale_of(const double *part, double eps)
+{
+    const uint32_t lane = threadIdx.x & 63;
+    double s = part[lane] + part[lane + 64] + part[lane + 128] + part[lane + 192];
+    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+    return s < INFINITY ? ORTH_SCALE / (sqrt(s) + eps) : NAN;
+}
+
+struct OrthP {
+    const void *in;
+    void *out;
+    char *x;                     /* split, m rows of ld columns */
+    const double *part;
+    uint64_t rows, cols, ld, batch;        /* rows <= cols unless `flip`; batch: bytes between matrices of x */
+    double eps;
+    uint32_t count, flip;
+};
+
+/* Tiles of 32 x 64 between the caller's matrices and X (flip: its transpose).
+ * BEGIN: X = scale in / (norm + eps); otherwise out = X / scale. */
+template <typename D, bool BEGIN> __global__ void __launch_bounds__(256) msim_orth_move(OrthP p)
+{
+    __shared__ float tile[32][65];
+    __shared__ double factor;
+    const uint64_t m = p.flip ? p.cols : p.rows, n = p.flip ? p.rows : p.cols;
+    const uint64_t tn = (p.ld + 63) / 64, tm = (m + 31) / 32;
+    const uint32_t batch = (uint32_t)(blockIdx.x / (tm * tn)), at = (uint32_t)(blockIdx.x - batch * tm * tn);
+    const uint64_t m0 = at / tn * 32, n0 = at % tn * 64;
+    char *x = p.x + batch * p.batch;
+    const uint64_t base = batch * p.rows * p.cols;
+    if constexpr (BEGIN) {
+        if (threadIdx.x < 64) {
+            const double f = scale_of(p.part + batch * NORM_PARTS, p.eps);
+            if (threadIdx.x == 0) factor = f;
+        }
+        __syncthreads();
+        const double f = factor;
+        for (uint32_t i = threadIdx.x; i < 2048; i += 256) {
+            const uint32_t r = p.flip ? i % 32 : i / 64, c = p.flip ? i / 32 : i % 64;
+            const uint64_t mm = m0 + r, nn = n0 + c;
+            float v = 0;
+            if (mm < m && nn < n) v = (float)(f * (double)D::get(((const typename D::raw *)p.in)[base + (p.flip ? nn * p.cols + mm : mm * p.cols + nn)]));
+            tile[r][c] = v;
+        }
+        __syncthreads();
+        const uint32_t r = threadIdx.x / 8, c = threadIdx.x % 8 * 8;
+        if (m0 + r < m && n0 + c < p.ld) {
+            float v[8];
+            for (int i = 0; i < 8; i++) v[i] = tile[r][c + i];
+            store_split(v, x, split_at(p.ld, (uint32_t)(m0 + r), (uint32_t)(n0 + c)));
+        }
+    } else {
+        const uint32_t r = threadIdx.x / 8, c = threadIdx.x % 8 * 8;
+        if (m0 + r < m && n0 + c < p.ld) {
+            float v[8];
+            load_split(v, x, split_at(p.ld, (uint32_t)(m0 + r), (uint32_t)(n0 + c)));
+            for (int i = 0; i < 8; i++) tile[r][c + i] = v[i] * (1.0f / ORTH_SCALE);
+        }
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < 2048; i += 256) {
+            const uint32_t rr = p.flip ? i % 32 : i / 64, cc = p.flip ? i / 32 : i % 64;
+            const uint64_t mm = m0 + rr, nn = n0 + cc;
+            if (mm < m && nn < n) ((typename D::raw *)p.out)[base + (p.flip ? nn * p.cols + mm : mm * p.cols + nn)] = D::put(tile[rr][cc]);
+        }
+    }
+}
+
+/* ------------------------------------------------------------------------ */
+/* matrices of up to 64 rows (of X): a launch a step                         */
+/* ------------------------------------------------------------------------ */
+
+/* A workgroup has a slab of X's columns in LDS.  A step takes the slabs' sums of
+ * products together to P, makes B = b P + c P P by itself, X = a X + B X of its
+ * slab, and the slab's part of the next P.  Bound by latency: a launch, the parts
+ * through memory, and four products one after another. */
+constexpr uint32_t SLAB_ROWS = 64, SLAB_COLS = 256, SLABS = 32;       /* at most */
+constexpr uint32_t SLAB_THREADS = 512;
+
+struct SlabP {
+    const void *in;
+    void *out;
+    const double *norm;
+    char *x;                     /* slabs as they lie in LDS, kept from step to step */
+    const float *part;           /* [count][slabs][ROWS][ROWS] of the step before */
+    float *next;
+    uint64_t size, sm, sn;       /* of in and out: elements of a matrix, between rows and columns of X */
+    double eps;
+    uint32_t m, n, slabs, wide;  /* wide: columns of a slab, a multiple of 32 */
+    uint32_t first, last;
+    float a, b, c;
+};
+
+/* ROWS (32 or 64) rows by 32 columns of a split matrix in LDS: rows of 128 bytes,
+ * high parts and low ones, in pieces of 16 that are exchanged by the row; further
+ * columns follow. */
+template <uint32_t ROWS> struct Slab {
+    static constexpr uint32_t BYTES = ROWS * 128;    /* of 32 columns */
+    typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+    typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
+
+    /* where the parts of columns c, c + 1, ... of a row begin */
+    static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t c, uint32_t low)
+    {
+        return c / 32 * BYTES + row * 128 + ((c % 32 / 8 + low * 4) ^ (row >> 1 & 7)) * 16 + c % 8 * 2;
+    }
+    /* four columns */
+    static __device__ __forceinline__ void put(char *lds, uint32_t row, uint32_t c, const float *v)
+    {
+        u16x4 h, l;
+        for (int i = 0; i < 4; i++) {
+            uint16_t a, b;
+            split_of(v[i], a, b);
+            h[i] = a;
+            l[i] = b;
+        }
+        *(u16x4 *)(lds + at(row, c, 0)) = h;
+        *(u16x4 *)(lds + at(row, c, 1)) = l;
+    }
+    static __device__ __forceinline__ void get(const char *lds, uint32_t row, uint32_t c, float *v)
+    {
+        const u16x4 h = *(const u16x4 *)(lds + at(row, c, 0)), l = *(const u16x4 *)(lds + at(row, c, 1));
+        for (int i = 0; i < 4; i++) v[i] = F16::get(h[i]) + F16::get(l[i]);
+    }
+    /* fragments: 32 rows from `row` on, 16 columns from c on */
+    static __device__ __forceinline__ f16x8 rows(const char *lds, uint32_t row, uint32_t c, uint32_t low)
+    {
+        const uint32_t lane = threadIdx.x & 63;
+        return *(const f16x8 *)(lds + at(row + (lane & 31), c + (lane >> 5) * 8, low));
+    }
+    /* 16 rows from `row` on, 32 columns from c on, transposed */
+    static __device__ __forceinline__ f16x8 columns(const char *lds, uint32_t row, uint32_t c, uint32_t low)
+    {
+        const uint32_t lane = threadIdx.x & 63, r = row + (lane >> 5) * 8 + (lane >> 2 & 3), k = c + (lane >> 4 & 1) * 16 + (lane & 3) * 4;
+        typedef __attribute__((address_space(3))) i16x4 *ptr;
+        const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(lds + at(r, k, low)));
+        const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(lds + at(r + 4, k, low)));
+        return __builtin_bit_cast(f16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mma_split(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, f32x16 c)
+{
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bh, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(al, bh, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bl, c, 0, 0, 0);
+}
+
+/* rows i .. times rows j .. over columns k0 .. k1 - 1: lane l has row i + l % 32 and columns j + 8 g + 4 (l / 32) + 0 .. 3 */
+template <uint32_t ROWS> __device__ __forceinline__ f32x16 slab_square(const char *lds, uint32_t i, uint32_t j, uint32_t k0, uint32_t k1)
+{
+    typedef Slab<ROWS> S;
+    f32x16 c = 0.0f;
+    for (uint32_t k = k0; k < k1; k += 16) c = mma_split(S::rows(lds, j, k, 0), S::rows(lds, j, k, 1), S::rows(lds, i, k, 0), S::rows(lds, i, k, 1), c);
+    return c;
+}
+
+template <typename D, uint32_t ROWS> __global__ void __launch_bounds__(SLAB_THREADS) msim_orth_slab(SlabP p)
+{
+    typedef typename D::raw raw;
+    typedef Slab<ROWS> S;
+    constexpr uint32_t BLOCKS = ROWS / 32 * (ROWS / 32), WAVES = SLAB_THREADS / 64, RUNS = WAVES / BLOCKS;
+    constexpr uint32_t SQUARE = ROWS * ROWS, PER = SQUARE / SLAB_THREADS;          /* elements of P, and of them a thread's */
+    __shared__ __attribute__((aligned(256))) char xs[SLAB_COLS / 32 * S::BYTES], ps[ROWS / 32 * S::BYTES], bs[ROWS / 32 * S::BYTES];
+    __shared__ f32x4 sums[(WAVES - BLOCKS) * 4 * 64];
+    __shared__ double factor;
+    const uint32_t batch = blockIdx.x / p.slabs, slab = blockIdx.x - batch * p.slabs, n0 = slab * p.wide, tid = threadIdx.x;
+    const uint32_t lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane & 31, half = lane >> 5;
+    const uint32_t block = wave % BLOCKS, i = block % (ROWS / 32) * 32, j = block / (ROWS / 32) * 32;    /* of a ROWS x ROWS product */
+    char *const kept = p.x + (uint64_t)blockIdx.x * (p.wide / 32 * S::BYTES);
+    const uint32_t units = ROWS * p.wide / 4, pieces = p.wide / 32 * (S::BYTES / 16);
+    /* four columns of a row; neighbouring lanes take neighbouring elements of the caller's matrix */
+    const auto unit = [&](uint32_t e, uint32_t &row, uint32_t &c) {
+        if (p.sn == 1) row = e / (p.wide / 4), c = e % (p.wide / 4) * 4;
+        else row = e % ROWS, c = e / ROWS * 4;
+    };
+    if (p.first) {
+        if (tid < 64) {
+            const double f = scale_of(p.norm + batch * NORM_PARTS, p.eps);
+            if (tid == 0) factor = f;
+        }
+        __syncthreads();
+        const double f = factor;
+        const raw *in = (const raw *)p.in + batch * p.size;
+        _Pragma("unroll 2") for (uint32_t e = tid; e < units; e += SLAB_THREADS) {
+            uint32_t row, c;
+            unit(e, row, c);
+            float v[4];
+            for (uint32_t k = 0; k < 4; k++)
+                v[k] = row < p.m && n0 + c + k < p.n ? (float)(f * (double)D::get(in[row * p.sm + (n0 + c + k) * p.sn])) : 0.0f;
+            S::put(xs, row, c, v);
+        }
+    } else {
+        typedef float part __attribute__((ext_vector_type(PER < 4 ? PER : 4)));
+        constexpr uint32_t N = PER < 4 ? PER : 4, V = PER / N;
+        part sum[V] = {};
+        const part *q = (const part *)(p.part + (uint64_t)batch * p.slabs * SQUARE) + tid;
+        _Pragma("unroll 8") for (uint32_t s = 0; s < p.slabs; s++, q += SQUARE / N)
+            for (uint32_t k = 0; k < V; k++) sum[k] += q[k * SLAB_THREADS];
+        for (uint32_t e = tid; e < pieces; e += SLAB_THREADS) ((u32x4 *)xs)[e] = ((const u32x4 *)kept)[e];
+        for (uint32_t k = 0; k < V; k++) {
+            const uint32_t e = (k * SLAB_THREADS + tid) * N, row = e / ROWS, c = e % ROWS;
+            for (uint32_t t = 0; t < N; t++) {
+                uint16_t h, lo;
+                split_of(sum[k][t] * (1.0f / ORTH_SCALE), h, lo);
+                *(uint16_t *)(ps + S::at(row, c + t, 0)) = h;
+                *(uint16_t *)(ps + S::at(row, c + t, 1)) = lo;
+            }
+        }
+        __syncthreads();
+        if (wave < BLOCKS) {
+            const f32x16 sq = slab_square<ROWS>(ps, i, j, 0, ROWS);
+            for (uint32_t g = 0; g < 4; g++) {
+                float v[4];
+                S::get(ps, i + l, j + g * 8 + half * 4, v);
+                for (int t = 0; t < 4; t++) v[t] = p.b * v[t] + p.c * (1.0f / ORTH_SCALE) * sq[g * 4 + t];
+                S::put(bs, i + l, j + g * 8 + half * 4, v);
+            }
+        }
+        __syncthreads();
+        for (uint32_t c = wave * 32; c < p.wide; c += WAVES * 32) {
+            f32x16 y[ROWS / 32];
+            for (uint32_t r = 0; r < ROWS / 32; r++) y[r] = 0.0f;
+            for (uint32_t k = 0; k < ROWS; k += 16) {
+                const f16x8 xh = S::columns(xs, k, c, 0), xl = S::columns(xs, k, c, 1);
+                for (uint32_t r = 0; r < ROWS / 32; r++) y[r] = mma_split(xh, xl, S::rows(bs, r * 32, k, 0), S::rows(bs, r * 32, k, 1), y[r]);
+            }
+            wave_sync();                   /* the columns are this wavefront's alone, and read */
+            for (uint32_t r = 0; r < ROWS / 32; r++)
+                for (uint32_t g = 0; g < 4; g++) {
+                    float v[4];
+                    S::get(xs, r * 32 + l, c + g * 8 + half * 4, v);
+                    for (int t = 0; t < 4; t++) v[t] = p.a * v[t] + (1.0f / ORTH_SCALE) * y[r][g * 4 + t];
+                    S::put(xs, r * 32 + l, c + g * 8 + half * 4, v);
+                }
+        }
+    }
+    __syncthreads();
+    if (p.last) {
+        raw *out = (raw *)p.out + batch * p.size;
+        for (uint32_t e = tid; e < units; e += SLAB_THREADS) {
+            uint32_t row, c;
+            unit(e, row, c);
+            float v[4];
+            S::get(xs, row, c, v);
+            for (uint32_t k = 0; k < 4; k++)
+                if (row < p.m && n0 + c + k < p.n) out[row * p.sm + (n0 + c + k) * p.sn] = D::put(v[k] * (1.0f / ORTH_SCALE));
+        }
+        return;
+    }
+    for (uint32_t e = tid; e < pieces; e += SLAB_THREADS) ((u32x4 *)kept)[e] = ((const u32x4 *)xs)[e];
+    /* each block of the slab's part of P by RUNS wavefronts, a run of columns each */
+    const uint32_t run = wave / BLOCKS, per = (p.wide / 16 + RUNS - 1) / RUNS * 16;
+    const f32x16 sq = slab_square<ROWS>(xs, i, j, run * per, min(p.wide, (run + 1) * per));
+    f32x4 part[4];
+    for (int g = 0; g < 4; g++) part[g] = f32x4{sq[g * 4], sq[g * 4 + 1], sq[g * 4 + 2], sq[g * 4 + 3]};
+    if (run)
+        for (int g = 0; g < 4; g++) sums[((wave - BLOCKS) * 4 + g) * 64 + lane] = part[g];
+    __syncthreads();
+    if (run) return;
+    float *to = p.next + (uint64_t)blockIdx.x * SQUARE + (i + l) * ROWS + j + half * 4;
+    for (uint32_t g = 0; g < 4; g++) {
+        for (uint32_t r = 1; r < RUNS; r++) part[g] += sums[(((r - 1) * BLOCKS + block) * 4 + g) * 64 + lane];
+        *(f32x4 *)(to + g * 8) = part[g];
+    }
+}
+
+struct Orth {
+    uint64_t m, n, lx, lp;       /* of X: rows, columns, columns as held; of P: as held */
+    uint64_t slabs, wide;        /* msim_orth_slab, or 0 */
+    uint64_t norm_bytes, x_bytes, p_bytes, bytes;
+    Plan square, poly, update;
+};
+
+Orth orth_of(const msim_orthogonalize_spec *s)
+{
+    Orth o = {};
+    o.m = std::min(s->rows, s->cols);
+    o.n = std::max(s->rows, s->cols);
+    o.lx = up(o.n, 32);
+    o.lp = up(o.m, 32);
+    o.norm_bytes = up((uint64_t)s->count * NORM_PARTS * 8, 256);
+    if (o.m <= SLAB_ROWS && o.n <= SLABS * SLAB_COLS) {
+        /* slabs enough to fill the card, of 64 columns at least */
+        const uint64_t want = std::min<uint64_t>(SLABS, std::max<uint64_t>(1, 512 / s->count));
+        const uint64_t most = std::max((o.n + SLAB_COLS - 1) / SLAB_COLS, std::min((o.n + 63) / 64, want));
+        o.wide = up((o.n + most - 1) / most, 32);
+        o.slabs = (o.n + o.wide - 1) / o.wide;
+        const uint64_t rows = up(o.m, 32);
+        o.x_bytes = s->count * o.slabs * o.wide * rows * 4;
+        o.p_bytes = s->count * o.slabs * rows * rows * 4;
+        o.bytes = o.norm_bytes + o.x_bytes + 2 * o.p_bytes;
+        return o;
+    }
+    o.x_bytes = up(s->count * o.m * o.lx * 4, 256);
+    o.p_bytes = up(s->count * o.m * o.lp * 4, 256);
+    o.square = plan_of(M_SPLIT, {o.m, o.lp, o.lx, s->count});
+    o.poly = plan_of(M_SPLIT, {o.m, o.lp, o.lp, s->count});
+    o.update = plan_of(M_SPLIT, {o.m, o.lx, o.lp, s->count});
+    o.bytes = o.norm_bytes + 2 * o.x_bytes + 2 * o.p_bytes +
+              std::max(o.square.part_bytes, std::max(o.poly.part_bytes, o.update.part_bytes));
+    return o;
+}
+
+/* The largest singular value and |B| that the steps can meet, from any in 0 .. 1:
+ * both have to fit f16 times ORTH_SCALE. */
+const char *check_steps(const msim_orthogonalize_spec *s)
+{
+    const double a = s->a, b = s->b, c = s->c;
+    double top = 1.0;
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return "orthogonalize: coefficients out of range";
+    for (uint32_t k = 0; k < s->steps; k++) {
+        double x = 0, poly = 0;
+        for (int i = 0; i <= 4096; i++) {
+            const double v = top * i / 4096, q = v * v;
+            x = std::max(x, std::fabs(v * (a + q * (b + c * q))));
+            poly = std::max(poly, std::fabs(q * (b + c * q)));
+        }
+        if (!(poly <= 24.0 && top * top <= 24.0)) return "orthogonalize: steps with these coefficients leave the range of the products";
+        top = x * 1.001;
+        if (!(top <= 24.0)) return "orthogonalize: steps with these coefficients leave the range of the products";
+    }
+    return nullptr;
+}
+
+const char *check_orth(const msim_orthogonalize_spec *s, int *code)
+{
+    *code = MSIM_E_ARG;
+    if (!s) return "orthogonalize: null spec";
+    if (s->version != MSIM_ABI_VERSION) return "orthogonalize: spec version mismatch";
+    if (s->dtype > MSIM_BF16) return "orthogonalize: unknown dtype";
+    if (!s->rows || !s->cols) return "orthogonalize: rows and cols must be at least 1";
+    if (s->reserved) return "orthogonalize: reserved must be 0";
+    if (!(s->eps >= 0) || !std::isfinite(s->eps)) return "orthogonalize: eps must be finite and not negative";
+    *code = MSIM_E_LIMIT;
+    if (s->rows > MSIM_MAX_LINEAR || s->cols > MSIM_MAX_LINEAR) return "orthogonalize: rows or cols above MSIM_MAX_LINEAR";
+    if (s->count > 65536 || (uint64_t)s->count * s->rows * s->cols >> 36) return "orthogonalize: more than 65,536 matrices or 2^36 elements";
+    if (s->steps > 64) return "orthogonalize: more than 64 steps";
+    *code = MSIM_E_ARG;
+    return check_steps(s);
+}
+
+template <typename D>
+hipError_t run_slabs(const msim_orthogonalize_spec *s, const Orth &o, const void *in, void *out, char *ws, hipStream_t st)
+{
+    char *x = ws + o.norm_bytes, *part = x + o.x_bytes, *next = part + o.p_bytes;
+    const bool flip = s->rows > s->cols;
+    SlabP p = {in, out, (const double *)ws, x, (const float *)part, (float *)next, s->rows * s->cols, flip ? 1 : s->cols, flip ? s->cols : 1,
+               s->eps, (uint32_t)o.m, (uint32_t)o.n, (uint32_t)o.slabs, (uint32_t)o.wide, 1, s->steps == 0, s->a, s->b, s->c};
+    hipError_t e = launch(msim_orth_norm<D>, s->count * NORM_PARTS, 256, 0, st, in, s->rows * s->cols, (double *)ws);
+    for (uint32_t k = 0; k <= s->steps && e == hipSuccess; k++) {
+        p.first = k == 0;
+        p.last = k == s->steps;
+        e = launch(o.m <= 32 ? msim_orth_slab<D, 32> : msim_orth_slab<D, 64>, s->count * p.slabs, SLAB_THREADS, 0, st, p);
+        const float *was = p.part;
+        p.part = p.next;
+        p.next = (float *)was;
+    }
+    return e;
+}
+
+template <typename D>
+hipError_t run_orth(const msim_orthogonalize_spec *s, const Orth &o, const void *in, void *out, char *ws, hipStream_t st)
+{
+    if (o.slabs) return run_slabs<D>(s, o, in, out, ws, st);
+    char *norms = ws, *x = norms + o.norm_bytes, *y = x + o.x_bytes, *sq = y + o.x_bytes, *poly = sq + o.p_bytes, *part = poly + o.p_bytes;
+    OrthP q = {in, out, x, (const double *)norms, s->rows, s->cols, o.lx, o.m * o.lx * 4, s->eps, s->count, s->rows > s->cols};
+    const uint32_t moves = (uint32_t)((o.lx + 63) / 64 * ((o.m + 31) / 32) * s->count);
+    hipError_t e = launch(msim_orth_norm<D>, s->count * NORM_PARTS, 256, 0, st, in, s->rows * s->cols, (double *)norms);
+    if (e == hipSuccess) e = launch(msim_orth_move<D, true>, moves, 256, 0, st, q);
+    for (uint32_t k = 0; k < s->steps && e == hipSuccess; k++) {
+        const Operand ox = {x, o.m * o.lx * 4, o.lx * 4, o.m * o.lx * 4};
+        const Operand osq = {sq, o.m * o.lp * 4, o.lp * 4, o.m * o.lp * 4}, opoly = {poly, o.m * o.lp * 4, o.lp * 4, o.m * o.lp * 4};
+        GemmP p = {};
+        p.batch = s->count;
+        p.part = (float *)part;
+        p.M = p.N = p.e.M = p.e.N = (uint32_t)o.m;
+        p.mirror = 1;
+        p.a = p.b = ox;
+        p.K = (uint32_t)o.lx;
+        p.e.out = sq;
+        p.e.out_ld = o.lp;
+        p.e.out_batch = o.m * o.lp * 4;
+        p.e.beta = 1.0f / ORTH_SCALE;
+        e = launch_gemm<M_SPLIT, false>(p, o.square, st);
+        if (e != hipSuccess) break;
+        p.a = p.b = osq;
+        p.K = (uint32_t)o.lp;
+        p.e.out = poly;
+        p.e.src = sq;
+        p.e.alpha = s->b;
+        p.e.beta = s->c / ORTH_SCALE;
+        e = launch_gemm<M_SPLIT, false>(p, o.poly, st);
+        if (e != hipSuccess) break;
+        p.mirror = 0;
+        p.a = opoly;
+        p.b = ox;
+        p.N = p.e.N = (uint32_t)o.n;
+        p.e.out = y;
+        p.e.out_ld = o.lx;
+        p.e.out_batch = o.m * o.lx * 4;
+        p.e.src = x;
+        p.e.alpha = s->a;
+        p.e.beta = 1.0f / ORTH_SCALE;
+        e = launch_gemm<M_SPLIT, true>(p, o.update, st);
+        std::swap(x, y);
+    }
+    q.x = x;
+    if (e == hipSuccess) e = launch(msim_orth_move<D, false>, moves, 256, 0, st, q);
+    return e;
+}
+
+}   // namespace
+
+extern "C" int msim_orthogonalize_workspace(const msim_orthogonalize_spec *s, uint64_t *bytes)
+{
+    int code;
+    if (const char *why = check_orth(s, &code)) return fail(code, why);
+    if (!bytes) return fail(MSIM_E_ARG, "orthogonalize: null bytes");
+    *bytes = s->count ? orth_of(s).bytes : 0;
+    return MSIM_OK;
+}
+
+extern "C" int msim_orthogonalize(const msim_orthogonalize_spec *s, const void *update, void *out, void *workspace,
+                                  uint64_t workspace_bytes, void *hip_stream)
+{
+    int code;
+    if (const char *why = check_orth(s, &code)) return fail(code, why);
+    if (s->count == 0) return MSIM_OK;
+    if (!update || !out) return fail(MSIM_E_ARG, "orthogonalize: null update or out");
+    const Orth o = orth_of(s);
+    if (int rc = check_workspace(workspace, workspace_bytes, o.bytes, "orthogonalize: workspace missing, too small or not on 256 bytes")) return rc;
+    hipStream_t st = (hipStream_t)hip_stream;
+    const hipError_t e = s->dtype == MSIM_F32 ? run_orth<F32>(s, o, update, out, (char *)workspace, st)
+        : s->dtype == MSIM_F16 ? run_orth<F16>(s, o, update, out, (char *)workspace, st)
+                               : run_orth<BF16>(s, o, update, out, (char *)workspace, st);
+    return launched(e, "orthogonalize launch");
+}

@@ -388,7 +388,8 @@ def orth64(T, u, steps, abc, eps=1e-7):
 
 
 ABC = (3.4445, -4.7750, 2.0315)
-MATRICES = [(1, 1), (1, 7), (8, 8), (33, 31), (64, 64), (65, 200), (200, 65), (130, 257), (256, 1000), (300, 300), (520, 264)]
+MATRICES = [(1, 1), (1, 7), (8, 8), (33, 31), (64, 64), (65, 200), (200, 65), (130, 257), (256, 1000), (300, 300), (520, 264), (3, 8192), (64, 5000),
+            (7000, 40), (50, 8193)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
