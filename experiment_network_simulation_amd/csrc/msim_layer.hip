@@ -14,7 +14,6 @@
 
 namespace {
 
-constexpr int WAVES = 4;                   /* wavefronts of a workgroup: k is shared among them */
 constexpr uint32_t MAX_ROWS = MSIM_MAX_LAYER_ROWS;
 
 struct LayerP {
@@ -70,16 +69,16 @@ template <typename D, int TT> __global__ void __launch_bounds__(256) msim_layer_
  * order.  Where there are fewer assignments than experts a slot is an assignment,
  * and the first that names an expert has it; otherwise a slot is an expert.  The
  * number of assignments, 0 where another slot has the expert. */
-__device__ __forceinline__ uint32_t tokens_of(const LayerP &p, uint32_t slot, uint32_t *list, uint32_t *counts, int32_t &expert)
+template <int WAVES> __device__ __forceinline__ uint32_t tokens_of(const LayerP &p, const int32_t *ids, uint32_t slot, uint32_t *list, uint32_t *counts, int32_t &expert)
 {
     const uint32_t n = p.rows * p.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const bool by_choice = p.slots == n;
-    expert = by_choice ? p.ids[slot] : (int32_t)slot;
+    expert = by_choice ? ids[slot] : (int32_t)slot;
     if (expert < 0) return 0;
     uint32_t have = 0;
     for (uint32_t j0 = 0; j0 < n; j0 += 64 * WAVES) {
         const uint32_t j = j0 + threadIdx.x;
-        const bool mine = j < n && p.ids[j] == expert;
+        const bool mine = j < n && ids[j] == expert;
         const uint64_t all = __ballot(mine);
         if (lane == 0) counts[wave] = __popcll(all);
         __syncthreads();
@@ -110,7 +109,7 @@ template <typename D> __device__ __forceinline__ void hidden_of(const LayerP &p,
 
 /* h = act(gate rows x) (up rows x), or act(rows x): 16 hidden units (32 without a
  * gate) of one expert for up to 16 MT of its tokens */
-template <typename D, int MT>
+template <typename D, int MT, int WAVES>
 __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, f32x4 *lds)
 {
     typedef typename D::raw raw;
@@ -132,7 +131,7 @@ __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint3
 }
 
 /* 32 columns of what one expert answers to up to 16 MT of its tokens, in 32 bits */
-template <typename D, int MT>
+template <typename D, int MT, int WAVES>
 __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, f32x4 *lds)
 {
     typedef typename D::raw raw;
@@ -156,22 +155,20 @@ __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uin
     }
 }
 
-/* One or a few tokens (rows <= FEW_ROWS): three launches.  Every choice of every
- * token is a product of its own, and an expert that two tokens chose is read twice.
- *
- * The first product routes, too: every workgroup all rows, by route_row, which
- * takes 1 to 2 us where msim_route would be a launch or two more. */
-constexpr uint32_t FEW_ROWS = 4;
+/* The first product of up to FEW_ROWS tokens, which routes, too: every workgroup all
+ * rows, a wavefront each, by route_row, which takes 1 to 2 us where msim_route
+ * would be a launch or two more. */
+constexpr uint32_t FEW_ROWS = 16;
 constexpr int FEW_WAVES = 16;
 
 template <typename D, int VPL> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_layer_up_few(LayerP p, RouteP r, int32_t *ids, float *weights, int32_t *load)
 {
-    typedef typename D::raw raw;
     extern __shared__ double keys[];
     __shared__ int32_t chosen[FEW_ROWS * MSIM_MAX_TOP_K];
     __shared__ float shares[FEW_ROWS * MSIM_MAX_TOP_K];
+    __shared__ uint32_t list[MAX_ROWS], counts[FEW_WAVES];
     __shared__ f32x4 sums[FEW_WAVES * 2 * 64];
-    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15, n = p.rows * p.K;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = p.rows * p.K;
     r.ids = chosen;
     r.w = shares;
     if (wave < p.rows) route_row<F32, VPL>(r, wave, keys + wave * p.E, nullptr);
@@ -188,20 +185,14 @@ template <typename D, int VPL> __global__ void __launch_bounds__(64 * FEW_WAVES)
                 load[e] = c;
             }
     }
-    const uint32_t tile = blockIdx.x % p.tiles, j = blockIdx.x / p.tiles, f0 = tile * (p.gated ? 16 : 32);
-    const int32_t expert = chosen[j];
-    if (expert < 0) return;
-    const raw *base = (const raw *)p.w_in + (uint64_t)expert * (p.gated ? 2 : 1) * p.F * p.C;
-    const raw *w[2] = {base + (uint64_t)min(f0 + l, p.F - 1) * p.C,
-                       base + (uint64_t)(p.gated ? p.F + min(f0 + l, p.F - 1) : min(f0 + 16 + l, p.F - 1)) * p.C};
-    const raw *x[1] = {(const raw *)p.x + j / p.K * p.x_ld};
-    f32x4 acc[1][2] = {};
-    stream<D, 1, 2>(w, x, p.C, wave, FEW_WAVES, acc);
-    join<1, 2, FEW_WAVES>(sums, wave, acc);
-    if (wave == 0 && l == 0) hidden_of<D>(p, acc[0], f0 + (lane >> 4) * 4, (raw *)p.h + (uint64_t)j * p.h_ld);
+    int32_t expert;
+    const uint32_t have = tokens_of<FEW_WAVES>(p, chosen, blockIdx.x / p.tiles, list, counts, expert);
+    if (have) up_tokens<D, 1, FEW_WAVES>(p, expert, blockIdx.x % p.tiles, list, have, sums);
 }
 
-/* 32 columns of a token's result a workgroup, whose wavefronts share all runs of k of all its choices */
+/* The second product and the sum of few tokens: 32 columns of one token's result a
+ * workgroup, whose wavefronts share all runs of k of all its choices.  An expert
+ * that two tokens chose is read twice. */
 template <typename D> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_layer_down_few(LayerP p)
 {
     typedef typename D::raw raw;
@@ -241,18 +232,23 @@ template <typename D> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_lay
     }
 }
 
-/* MT: tokens of a run, in 16; runs of at most 16 take the leaner code */
-template <typename D, int MT, bool DOWN> __global__ void __launch_bounds__(64 * WAVES) msim_layer_product(LayerP p)
+/* MT: tokens of a run, in 16; runs of at most 16 take the leaner code.  WAVES: k is shared among them. */
+template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bounds__(64 * WAVES) msim_layer_product(LayerP p)
 {
     __shared__ uint32_t list[MAX_ROWS], counts[WAVES];
     __shared__ f32x4 sums[WAVES * MT * 2 * 64];
     const uint32_t tile = blockIdx.x % p.tiles, rest = blockIdx.x / p.tiles, chunk = rest % p.chunks, slot = rest / p.chunks;
     int32_t expert;
-    const uint32_t all = tokens_of(p, slot, list, counts, expert), first = chunk * 16 * MT;
+    const uint32_t all = tokens_of<WAVES>(p, p.ids, slot, list, counts, expert), first = chunk * 16 * MT;
     if (first >= all) return;
     const uint32_t n = min(all - first, 16u * MT);
-    if (n <= 16) DOWN ? down_tokens<D, 1>(p, expert, tile, list + first, n, sums) : up_tokens<D, 1>(p, expert, tile, list + first, n, sums);
-    else DOWN ? down_tokens<D, MT>(p, expert, tile, list + first, n, sums) : up_tokens<D, MT>(p, expert, tile, list + first, n, sums);
+    if constexpr (DOWN) {
+        if (n <= 16) down_tokens<D, 1, WAVES>(p, expert, tile, list + first, n, sums);
+        else down_tokens<D, MT, WAVES>(p, expert, tile, list + first, n, sums);
+    } else {
+        if (n <= 16) up_tokens<D, 1, WAVES>(p, expert, tile, list + first, n, sums);
+        else up_tokens<D, MT, WAVES>(p, expert, tile, list + first, n, sums);
+    }
 }
 
 /* The weighted sum over a token's choices, in their order, and the residual.  A
@@ -319,11 +315,21 @@ const char *check_layer(const msim_layer_spec *s, int *code)
     return nullptr;
 }
 
-template <typename D, int MT, bool DOWN> hipError_t launch_product(LayerP p, uint64_t tiles, hipStream_t st)
+template <typename D, bool DOWN> hipError_t launch_product(LayerP p, uint64_t tiles, hipStream_t st)
 {
+    const uint32_t mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
     p.tiles = (uint32_t)tiles;
-    p.chunks = (p.rows + 16 * MT - 1) / (16 * MT);
-    return launch(msim_layer_product<D, MT, DOWN>, p.slots * p.chunks * p.tiles, 64 * WAVES, 0, st, p);
+    p.chunks = (p.rows + 16 * mt - 1) / (16 * mt);
+    const uint32_t grid = p.slots * p.chunks * p.tiles;
+    /* few workgroups: more wavefronts in each */
+    if (grid < 1024) {
+        if (mt == 1) return launch(msim_layer_product<D, 1, 16, DOWN>, grid, 1024, 0, st, p);
+        if (mt == 2) return launch(msim_layer_product<D, 2, 8, DOWN>, grid, 512, 0, st, p);
+        return launch(msim_layer_product<D, 4, 8, DOWN>, grid, 512, 0, st, p);
+    }
+    if (mt == 1) return launch(msim_layer_product<D, 1, 4, DOWN>, grid, 256, 0, st, p);
+    if (mt == 2) return launch(msim_layer_product<D, 2, 4, DOWN>, grid, 256, 0, st, p);
+    return launch(msim_layer_product<D, 4, 4, DOWN>, grid, 256, 0, st, p);
 }
 
 template <typename D> int run_layer(const msim_layer_spec *s, LayerP p, const float *bias, int32_t *ids, float *weights, int32_t *load, hipStream_t st)
@@ -332,25 +338,29 @@ template <typename D> int run_layer(const msim_layer_spec *s, LayerP p, const fl
                                : launch(msim_layer_gate<D, 4>, p.E * ((p.rows + 3) / 4), 256, 0, st, p);
     if (e != hipSuccess) return launched(e, "layer launch");
     const uint64_t in = (p.F + (p.gated ? 15 : 31)) / (p.gated ? 16 : 32), out = (p.C + 31) / 32;
-    if (p.rows <= FEW_ROWS) {
+    p.slots = std::min(p.rows * p.K, p.E);
+    const size_t keys = s->route.groups > 1 ? p.rows * p.E * sizeof(double) : 0;
+    /* every workgroup routes: one round of them, two a compute unit */
+    if (p.rows <= FEW_ROWS && p.slots * in <= 512 && keys <= 32768) {
         const msim_route_spec &r = s->route;
         RouteP q = {p.logits, bias, nullptr, nullptr, nullptr, r.rows, r.experts, r.experts, r.top_k, r.groups, r.top_groups,
                     r.group_top, r.renorm, r.score == MSIM_SCORE_SIGMOID, r.scale, 0, 0, 0, 0};
         if (q.TG == q.G) q.G = q.TG = q.gtop = 1;       /* every group stays */
-        const size_t lds = q.G > 1 ? p.rows * p.E * sizeof(double) : 0;
         p.tiles = (uint32_t)in;
-        e = launch(p.E <= 256 ? msim_layer_up_few<D, 4> : msim_layer_up_few<D, 16>, p.rows * p.K * p.tiles, 64 * FEW_WAVES, lds, st, p, q, ids, weights, load);
-        p.tiles = (uint32_t)out;
-        if (e == hipSuccess) e = launch(msim_layer_down_few<D>, p.rows * p.tiles, 64 * FEW_WAVES, 0, st, p);
-        return launched(e, "layer launch");
+        e = launch(p.E <= 256 ? msim_layer_up_few<D, 4> : msim_layer_up_few<D, 16>, p.slots * p.tiles, 64 * FEW_WAVES, keys, st, p, q, ids, weights, load);
+        if (e != hipSuccess) return launched(e, "layer launch");
+    } else {
+        if (int rc = msim_route(&s->route, p.logits, bias, ids, weights, load, st)) return rc;
+        e = launch_product<D, false>(p, in, st);
+        if (e != hipSuccess) return launched(e, "layer launch");
     }
-    if (int rc = msim_route(&s->route, p.logits, bias, ids, weights, load, st)) return rc;
-    p.slots = std::min(p.rows * p.K, p.E);
-    e = p.rows <= 16 ? launch_product<D, 1, false>(p, in, st)
-        : p.rows <= 32 ? launch_product<D, 2, false>(p, in, st) : launch_product<D, 4, false>(p, in, st);
-    if (e == hipSuccess)
-        e = p.rows <= 16 ? launch_product<D, 1, true>(p, out, st)
-            : p.rows <= 32 ? launch_product<D, 2, true>(p, out, st) : launch_product<D, 4, true>(p, out, st);
+    /* one token, or experts that are read again from a cache, and few runs of k, in less time than a launch takes */
+    const uint64_t runs = (p.F + RUN<D> - 1) / RUN<D> * p.K;
+    if (p.rows == 1 || (p.rows <= FEW_ROWS && (uint64_t)p.rows * p.K * p.C * p.F * sizeof(typename D::raw) <= 64u << 20 && runs <= 4 * FEW_WAVES)) {
+        p.tiles = (uint32_t)out;
+        return launched(launch(msim_layer_down_few<D>, p.rows * p.tiles, 64 * FEW_WAVES, 0, st, p), "layer launch");
+    }
+    e = launch_product<D, true>(p, out, st);
     if (e == hipSuccess) e = launch(msim_layer_sum<D>, (uint32_t)(((uint64_t)p.rows * ((p.C + 3) / 4) + 255) / 256), 256, 0, st, p);
     return launched(e, "layer launch");
 }

@@ -238,11 +238,12 @@ const char *check_linear(const msim_linear_spec *s, int *code)
 
 /* Few rows are streamed while that is faster than tiles: 16 x 4,096 -> 4,096 bf16 10.0
  * us (12.2 in tiles), -> 16,384 31 (21); 24 x 1,000 -> 1,000 5.2 (6.7), 64 rows of
- * them 6.5 (6.8), 40 x 4,096 -> 4,096 16.4 (11.7). */
+ * them 6.5 (6.8), 40 x 4,096 -> 4,096 16.4 (11.7).  A workgroup's 16 wavefronts take
+ * 4 KiB of k at a time, so long rows want several workgroups: tiles of parts of k. */
 bool few_rows(const msim_linear_spec *s)
 {
-    if (s->rows <= MSIM_LINEAR_FEW) return s->outs <= MSIM_LINEAR_FEW_OUTS;
-    return s->rows <= 64 && s->cols <= 1024 && s->outs <= 1024;
+    if (s->rows <= MSIM_LINEAR_FEW && s->outs <= MSIM_LINEAR_FEW_OUTS) return s->cols * (uint64_t)size_of(s->dtype) <= 16384;
+    return s->rows <= 64 && s->cols <= 4096 && (uint64_t)s->cols * s->outs <= 1u << 20;
 }
 
 struct Forward {
@@ -296,7 +297,7 @@ struct Backward {
     bool own;                    /* d is made: an activation, another type, or a grad that does not lie as it is read */
     uint64_t wide;               /* columns of d */
     uint64_t d_bytes, sum_bytes;
-    uint32_t blocks, part;       /* of rows, for the sums: one of up to 256, or about 1,024 of at least 8 */
+    uint32_t blocks, part;       /* of rows, for the sums, and rows of one */
     Plan px, pw;
     uint64_t bytes;
 };
@@ -310,7 +311,10 @@ Backward backward_of(const msim_linear_spec *s, const void *x, const void *weigh
     const bool need = dx || dw;
     b.own = need && (s->act || s->out_dtype != s->dtype || !ready(grad, s->rows, s->outs, s->out_stride, size));
     b.wide = b.own ? up(s->outs, 16 / size * (size == 4 ? 2 : 1)) : s->outs;
-    b.part = s->rows <= 256 ? 256 : (uint32_t)std::max<uint64_t>(8, (s->rows + 1023) / 1024);
+    /* a thread has 8 columns and a row of `part` at a time: two rows at least, about 1,024 blocks at most */
+    uint32_t lanes = 1;
+    while (lanes < 32 && 8 * lanes < s->outs) lanes *= 2;
+    b.part = s->rows <= 256 ? 256 : (uint32_t)std::max<uint64_t>(512 / lanes, (s->rows + 1023) / 1024);
     b.blocks = (uint32_t)((s->rows + b.part - 1) / b.part);
     b.d_bytes = b.own ? up(s->rows * b.wide * size, 256) : 0;
     b.sum_bytes = db ? up((uint64_t)b.blocks * s->outs * 4, 256) : 0;

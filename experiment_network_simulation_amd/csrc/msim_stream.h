@@ -61,40 +61,52 @@ template <typename D> __device__ __forceinline__ u32x4 piece(const typename D::r
 /* elements of k that a wavefront takes at a time */
 template <typename D> constexpr uint32_t RUN = 256 / sizeof(typename D::raw);
 
-/* acc[i][j] += over a run of k: weight rows w[j], vectors x[i], both those of lane % 16 */
+/* acc[i][j] += over N runs of k, at k, k + step, ..., all within K: weight rows
+ * w[j], vectors x[i], both those of lane % 16.  All loads are asked for before the first is used. */
+template <typename D, int MT, int NT, int N>
+__device__ __forceinline__ void stream_whole(const typename D::raw *const *w, const typename D::raw *const *x, uint32_t k, uint32_t step,
+                                             f32x4 (&acc)[MT][NT])
+{
+    constexpr uint32_t PER = 16 / sizeof(typename D::raw), U = 4;
+    const uint32_t q = (threadIdx.x & 63) >> 4;
+    u32x4 a[N * U][NT], b[N * U][MT];
+    _Pragma("unroll") for (uint32_t u = 0; u < N * U; u++) {
+        const uint32_t at = k + u / U * step + (u % U * 4 + q) * PER;
+        _Pragma("unroll") for (int j = 0; j < NT; j++) a[u][j] = piece<D>(w[j] + at);
+        _Pragma("unroll") for (int i = 0; i < MT; i++) b[u][i] = piece<D>(x[i] + at);
+    }
+    _Pragma("unroll") for (uint32_t u = 0; u < N * U; u++)
+        _Pragma("unroll") for (int i = 0; i < MT; i++)
+            _Pragma("unroll") for (int j = 0; j < NT; j++) acc[i][j] = mma16<D>(a[u][j], b[u][i], acc[i][j]);
+}
+
+/* one run, or what there is of it */
 template <typename D, int MT, int NT>
 __device__ __forceinline__ void stream_run(const typename D::raw *const *w, const typename D::raw *const *x, uint32_t k, uint32_t K,
                                            f32x4 (&acc)[MT][NT])
 {
-    constexpr uint32_t PER = 16 / sizeof(typename D::raw), U = 4;
+    constexpr uint32_t PER = 16 / sizeof(typename D::raw);
     const uint32_t q = (threadIdx.x & 63) >> 4;
-    if (k + RUN<D> <= K) {
-        u32x4 a[U][NT], b[U][MT];
-        _Pragma("unroll") for (uint32_t u = 0; u < U; u++) {
-            const uint32_t at = k + (u * 4 + q) * PER;
-            _Pragma("unroll") for (int j = 0; j < NT; j++) a[u][j] = piece<D>(w[j] + at);
-            _Pragma("unroll") for (int i = 0; i < MT; i++) b[u][i] = piece<D>(x[i] + at);
-        }
-        _Pragma("unroll") for (uint32_t u = 0; u < U; u++)
-            _Pragma("unroll") for (int i = 0; i < MT; i++)
-                _Pragma("unroll") for (int j = 0; j < NT; j++) acc[i][j] = mma16<D>(a[u][j], b[u][i], acc[i][j]);
-    } else {
-        for (; k < K; k += 4 * PER) {
-            u32x4 a[NT], b[MT];
-            _Pragma("unroll") for (int j = 0; j < NT; j++) a[j] = piece<D>(w[j], k + q * PER, K);
-            _Pragma("unroll") for (int i = 0; i < MT; i++) b[i] = piece<D>(x[i], k + q * PER, K);
-            _Pragma("unroll") for (int i = 0; i < MT; i++)
-                _Pragma("unroll") for (int j = 0; j < NT; j++) acc[i][j] = mma16<D>(a[j], b[i], acc[i][j]);
-        }
+    if (k + RUN<D> <= K) return stream_whole<D, MT, NT, 1>(w, x, k, 0, acc);
+    for (; k < K; k += 4 * PER) {
+        u32x4 a[NT], b[MT];
+        _Pragma("unroll") for (int j = 0; j < NT; j++) a[j] = piece<D>(w[j], k + q * PER, K);
+        _Pragma("unroll") for (int i = 0; i < MT; i++) b[i] = piece<D>(x[i], k + q * PER, K);
+        _Pragma("unroll") for (int i = 0; i < MT; i++)
+            _Pragma("unroll") for (int j = 0; j < NT; j++) acc[i][j] = mma16<D>(a[j], b[i], acc[i][j]);
     }
 }
 
-/* the wavefront's share of k: every waves-th run */
+/* the wavefront's share of k, every waves-th run: of few vectors two at a time, whose loads fit its registers */
 template <typename D, int MT, int NT>
 __device__ __forceinline__ void stream(const typename D::raw *const *w, const typename D::raw *const *x, uint32_t K,
                                        uint32_t wave, uint32_t waves, f32x4 (&acc)[MT][NT])
 {
-    for (uint32_t k = wave * RUN<D>; k < K; k += waves * RUN<D>) stream_run<D, MT, NT>(w, x, k, K, acc);
+    uint32_t k = wave * RUN<D>;
+    const uint32_t step = waves * RUN<D>;
+    if constexpr (MT + NT <= 3)
+        for (; k + step + RUN<D> <= K; k += 2 * step) stream_whole<D, MT, NT, 2>(w, x, k, step, acc);
+    for (; k < K; k += step) stream_run<D, MT, NT>(w, x, k, K, acc);
 }
 
 /* The wavefronts' sums together, in order.  lds: waves x MT x NT x 64 pieces.

@@ -29,8 +29,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .sim import (ABI_VERSION, LINEAR_FEW, LINEAR_FEW_OUTS, MAX_TRAFFIC_HOSTS, LayerSpec, LinearSpec, MsimError,
-                  OrthogonalizeSpec, RouteSpec, TrafficSpec, load_library)
+from .sim import (ABI_VERSION, LINEAR_FEW, LINEAR_FEW_COLS, LINEAR_FEW_OUTS, MAX_TRAFFIC_HOSTS, LayerSpec, LinearSpec,
+                  MsimError, OrthogonalizeSpec, RouteSpec, TrafficSpec, load_library)
 
 __all__ = ["Routing", "route", "route_backward", "dropout", "dropout_backward", "traffic", "LinearGrads", "linear",
            "linear_backward", "Layer", "layer", "orthogonalize"]
@@ -376,7 +376,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     def call(on):
         lib = load_library()
         y = x.new_empty(shape, dtype=to) if out is None else out
-        mem, size = (None, 0) if rows <= LINEAR_FEW and outs <= LINEAR_FEW_OUTS else \
+        none = rows <= LINEAR_FEW and outs <= LINEAR_FEW_OUTS and cols <= LINEAR_FEW_COLS
+        mem, size = (None, 0) if none else \
             _workspace(x, lib.msim_linear_workspace, C.byref(spec), x.data_ptr(), weight.data_ptr())
         _call(lib.msim_linear(C.byref(spec), x.data_ptr(), weight.data_ptr(), _p(bias), _p(residual), y.data_ptr(), _p(pre),
                               _p(mem), size, on))

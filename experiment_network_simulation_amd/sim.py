@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(HERE, "libmsim.so")
 
 ABI_VERSION = 5
 MAX_TRAFFIC_HOSTS = 16384                # MSIM_MAX_TRAFFIC_HOSTS
-LINEAR_FEW, LINEAR_FEW_OUTS = 16, 16383  # MSIM_LINEAR_FEW, MSIM_LINEAR_FEW_OUTS
+LINEAR_FEW, LINEAR_FEW_OUTS, LINEAR_FEW_COLS = 16, 16383, 4096    # MSIM_LINEAR_FEW, _OUTS, _COLS
 OK, S_INCOMPLETE, S_DEADLOCK = 0, 1, 2
 E_INVALID_SPEC, E_UNROUTABLE, E_WORKSPACE, E_HIP, E_ARG, E_STATE, E_LIMIT = -1, -2, -3, -4, -5, -6, -7
 EXP_DONE, EXP_INCOMPLETE, EXP_DEADLOCK = 0, 1, 2

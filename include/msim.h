@@ -555,9 +555,10 @@ int msim_traffic(const msim_traffic_spec *spec, const int32_t *ids, const int64_
  * elements.
  */
 #define MSIM_MAX_LINEAR (1u << 20)
-/* rows and outs up to which msim_linear needs no workspace */
+/* rows, outs and cols up to which msim_linear needs no workspace */
 #define MSIM_LINEAR_FEW 16
 #define MSIM_LINEAR_FEW_OUTS 16383
+#define MSIM_LINEAR_FEW_COLS 4096
 
 /*
  * z = x weight^T + bias, out = act(z) + residual.  x: rows x cols, weight: outs x

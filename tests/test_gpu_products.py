@@ -340,6 +340,15 @@ def test_layer_masks(T, M, rows):
     assert bool(r.y[rows - 1].isnan().all()) and T.equal(r.y[:rows - 1], clean[:rows - 1])
 
 
+@pytest.mark.parametrize("rows", [3, 16, 17, 40])
+@pytest.mark.parametrize("experts,groups,top_groups", [(256, 8, 4), (512, 16, 3), (1024, 1, 1), (1024, 64, 40)])
+def test_layer_of_many_experts(T, M, rows, experts, groups, top_groups):
+    args = layer_of(T, rows, T.float16, rows, 32, 8, experts)
+    for how in (dict(score="sigmoid", bias=0.05 * T.randn(experts, device=DEV, generator=args[4]), group_top=2),
+                dict(score="softmax", renorm=False)):
+        check_layer(T, M, "f16", args, 8, dict(how, groups=groups, top_groups=top_groups), "silu", True, None, args[0])
+
+
 def test_layer_reads_no_expert_that_is_not_chosen(T, M):
     for rows in (1, 3, 40):
         args = layer_of(T, 5, T.float16, rows, 64, 48, 16)
