@@ -34,10 +34,10 @@ struct Epilogue {
     void *pre;                   /* of the operands' type */
     uint64_t pre_ld;
     uint32_t act, out32;
-    /* orthogonal update: out = alpha src + beta sum, split matrices of out_ld columns (a multiple of 32) */
+    /* orthogonal update: out = alpha src + beta sum + diag I, split matrices of out_ld columns (a multiple of 32) */
     const void *src;
     uint64_t out_batch;          /* bytes between matrices of out and src */
-    float alpha, beta;
+    float alpha, beta, diag;
 };
 
 struct GemmP {

@@ -191,6 +191,7 @@ __device__ __forceinline__ void after(const Epilogue &e, uint32_t batch, uint32_
         } else {
             for (int i = 0; i < 8; i++) v[i] *= e.beta;
         }
+        for (int i = 0; i < 8; i++) v[i] += m == n + i ? e.diag : 0.0f;
         store_split(v, (char *)e.out + batch * e.out_batch, split_at(e.out_ld, m, n));
     } else {
         typedef typename Type<MODE>::D D;

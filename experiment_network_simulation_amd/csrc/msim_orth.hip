@@ -18,6 +18,8 @@ namespace {
  * inside f16 and low parts above its subnormal numbers where they matter. */
 constexpr float ORTH_SCALE = 2048.0f;
 constexpr uint32_t NORM_PARTS = 256;
+/* a product of several steps' factors, which reaches a^3, is held times this less */
+constexpr float PASS_DOWN = 16.0f;
 
 /* sums of squares in 64 bits: NORM_PARTS workgroups a matrix */
 template <typename D> __global__ void __launch_bounds__(256) msim_orth_norm(const void *from, uint64_t size, double *part)
@@ -55,56 +57,66 @@ struct OrthP {
     void *out;
     char *x;                     /* split, m rows of ld columns */
     const double *part;
-    uint64_t rows, cols, ld, batch;        /* rows <= cols unless `flip`; batch: bytes between matrices of x */
+    uint64_t rows, cols, ld, batch;        /* batch: bytes between matrices of x */
     double eps;
-    uint32_t count, flip;
 };
 
-/* Tiles of 32 x 64 between the caller's matrices and X (flip: its transpose).
- * BEGIN: X = scale in / (norm + eps); otherwise out = X / scale. */
-template <typename D, bool BEGIN> __global__ void __launch_bounds__(256) msim_orth_move(OrthP p)
+/* Tiles of 32 x 64 between the caller's matrices and X (flip: its transpose, through
+ * LDS).  BEGIN: X = scale in / (norm + eps); otherwise out = X / scale.  A launch
+ * each; what bounds them is the way from the norm's parts to the result, so the
+ * elements are asked for before those. */
+template <typename D, bool BEGIN, bool FLIP> __global__ void __launch_bounds__(256) msim_orth_move(OrthP p)
 {
+    typedef typename D::raw raw;
     __shared__ float tile[32][65];
     __shared__ double factor;
-    const uint64_t m = p.flip ? p.cols : p.rows, n = p.flip ? p.rows : p.cols;
+    const uint64_t m = FLIP ? p.cols : p.rows, n = FLIP ? p.rows : p.cols;
     const uint64_t tn = (p.ld + 63) / 64, tm = (m + 31) / 32;
     const uint32_t batch = (uint32_t)(blockIdx.x / (tm * tn)), at = (uint32_t)(blockIdx.x - batch * tm * tn);
     const uint64_t m0 = at / tn * 32, n0 = at % tn * 64;
     char *x = p.x + batch * p.batch;
     const uint64_t base = batch * p.rows * p.cols;
+    /* eight columns of a row of X; there are `there` of them in the caller's */
+    const uint32_t r = threadIdx.x / 8, c = threadIdx.x % 8 * 8;
+    const uint64_t row = m0 + r, col = n0 + c;
+    const bool mine = row < m && col < p.ld;
+    const uint32_t there = mine && col < n ? (uint32_t)min((uint64_t)8, n - col) : 0;
+    float v[8];
     if constexpr (BEGIN) {
+        raw u[8];
+        if constexpr (FLIP) {
+            for (uint32_t i = 0; i < 8; i++) {
+                const uint64_t mm = m0 + threadIdx.x % 32, nn = n0 + i * 8 + threadIdx.x / 32;
+                u[i] = mm < m && nn < n ? ((const raw *)p.in)[base + nn * p.cols + mm] : raw(0);
+            }
+        } else {
+            load8<D>(v, p.in, base + row * p.cols + col, there);
+        }
         if (threadIdx.x < 64) {
             const double f = scale_of(p.part + batch * NORM_PARTS, p.eps);
             if (threadIdx.x == 0) factor = f;
         }
+        if constexpr (FLIP)
+            for (uint32_t i = 0; i < 8; i++) tile[threadIdx.x % 32][i * 8 + threadIdx.x / 32] = D::get(u[i]);
         __syncthreads();
-        const double f = factor;
-        for (uint32_t i = threadIdx.x; i < 2048; i += 256) {
-            const uint32_t r = p.flip ? i % 32 : i / 64, c = p.flip ? i / 32 : i % 64;
-            const uint64_t mm = m0 + r, nn = n0 + c;
-            float v = 0;
-            if (mm < m && nn < n) v = (float)(f * (double)D::get(((const typename D::raw *)p.in)[base + (p.flip ? nn * p.cols + mm : mm * p.cols + nn)]));
-            tile[r][c] = v;
-        }
-        __syncthreads();
-        const uint32_t r = threadIdx.x / 8, c = threadIdx.x % 8 * 8;
-        if (m0 + r < m && n0 + c < p.ld) {
-            float v[8];
-            for (int i = 0; i < 8; i++) v[i] = tile[r][c + i];
-            store_split(v, x, split_at(p.ld, (uint32_t)(m0 + r), (uint32_t)(n0 + c)));
-        }
+        if (!mine) return;
+        for (int i = 0; i < 8; i++) v[i] = (float)(factor * (double)(FLIP ? tile[r][c + i] : v[i]));
+        store_split(v, x, split_at(p.ld, (uint32_t)row, (uint32_t)col));
     } else {
-        const uint32_t r = threadIdx.x / 8, c = threadIdx.x % 8 * 8;
-        if (m0 + r < m && n0 + c < p.ld) {
-            float v[8];
-            load_split(v, x, split_at(p.ld, (uint32_t)(m0 + r), (uint32_t)(n0 + c)));
-            for (int i = 0; i < 8; i++) tile[r][c + i] = v[i] * (1.0f / ORTH_SCALE);
+        if (mine) {
+            load_split(v, x, split_at(p.ld, (uint32_t)row, (uint32_t)col));
+            for (int i = 0; i < 8; i++) v[i] *= 1.0f / ORTH_SCALE;
         }
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < 2048; i += 256) {
-            const uint32_t rr = p.flip ? i % 32 : i / 64, cc = p.flip ? i / 32 : i % 64;
-            const uint64_t mm = m0 + rr, nn = n0 + cc;
-            if (mm < m && nn < n) ((typename D::raw *)p.out)[base + (p.flip ? nn * p.cols + mm : mm * p.cols + nn)] = D::put(tile[rr][cc]);
+        if constexpr (!FLIP) {
+            store8<D>(v, p.out, base + row * p.cols + col, there);
+        } else {
+            if (mine)
+                for (int i = 0; i < 8; i++) tile[r][c + i] = v[i];
+            __syncthreads();
+            for (uint32_t i = 0; i < 8; i++) {
+                const uint64_t mm = m0 + threadIdx.x % 32, nn = n0 + i * 8 + threadIdx.x / 32;
+                if (mm < m && nn < n) ((raw *)p.out)[base + nn * p.cols + mm] = D::put(tile[threadIdx.x % 32][i * 8 + threadIdx.x / 32]);
+            }
         }
     }
 }
@@ -312,7 +324,9 @@ template <typename D, uint32_t ROWS> __global__ void __launch_bounds__(SLAB_THRE
 
 struct Orth {
     uint64_t m, n, lx, lp;       /* of X: rows, columns, columns as held; of P: as held */
-    uint64_t slabs, wide;        /* msim_orth_slab, or 0 */
+    uint64_t slabs, slab;        /* msim_orth_slab: slabs, or 0, and their columns */
+    bool wide;                   /* several steps a pass over X */
+    uint32_t squares;            /* of P's size beside P */
     uint64_t norm_bytes, x_bytes, p_bytes, bytes;
     Plan square, poly, update;
 };
@@ -329,10 +343,10 @@ Orth orth_of(const msim_orthogonalize_spec *s)
         /* slabs enough to fill the card, of 64 columns at least */
         const uint64_t want = std::min<uint64_t>(SLABS, std::max<uint64_t>(1, 512 / s->count));
         const uint64_t most = std::max((o.n + SLAB_COLS - 1) / SLAB_COLS, std::min((o.n + 63) / 64, want));
-        o.wide = up((o.n + most - 1) / most, 32);
-        o.slabs = (o.n + o.wide - 1) / o.wide;
+        o.slab = up((o.n + most - 1) / most, 32);
+        o.slabs = (o.n + o.slab - 1) / o.slab;
         const uint64_t rows = up(o.m, 32);
-        o.x_bytes = s->count * o.slabs * o.wide * rows * 4;
+        o.x_bytes = s->count * o.slabs * o.slab * rows * 4;
         o.p_bytes = s->count * o.slabs * rows * rows * 4;
         o.bytes = o.norm_bytes + o.x_bytes + 2 * o.p_bytes;
         return o;
@@ -342,30 +356,70 @@ Orth orth_of(const msim_orthogonalize_spec *s)
     o.square = plan_of(M_SPLIT, {o.m, o.lp, o.lx, s->count});
     o.poly = plan_of(M_SPLIT, {o.m, o.lp, o.lp, s->count});
     o.update = plan_of(M_SPLIT, {o.m, o.lx, o.lp, s->count});
-    o.bytes = o.norm_bytes + 2 * o.x_bytes + 2 * o.p_bytes +
+    /* What a pass over X costs more than products of m rows has to be worth four launches of those, which are
+     * slower by themselves: 1,024 x 4,096 404 -> 330 us, 8 x 512 x 2,048 378 -> 304, 64 x 20,000 148 -> 125; below, 512 x
+     * 1,024 164 -> 178, 1,536 x 2,304 689 -> 773. */
+    o.wide = s->steps > 1 && (o.n >= 64 * o.m || (2 * o.n > 3 * o.m && (double)s->count * o.m * o.m * (o.n - 1.5 * o.m) >= 4e8));
+    o.squares = o.wide ? 5 : 1;
+    o.bytes = o.norm_bytes + 2 * o.x_bytes + (1 + o.squares) * o.p_bytes +
               std::max(o.square.part_bytes, std::max(o.poly.part_bytes, o.update.part_bytes));
     return o;
 }
 
-/* The largest singular value and |B| that the steps can meet, from any in 0 .. 1:
- * both have to fit f16 times ORTH_SCALE. */
+/* What a step can meet, from singular values of 0 .. top: the largest it leaves, and the largest |B| and |a + B|. */
+struct Range { double left, poly, factor; };
+
+Range range_of(const msim_orthogonalize_spec *s, double top)
+{
+    const double a = s->a, b = s->b, c = s->c, d = 9 * b * b - 20 * a * c, r = d > 0 ? std::sqrt(d) : 0;
+    /* of q, a singular value's square: the ends, and where a derivative is 0 */
+    const double at[] = {0, top * top, -b / (2 * c), -a / (3 * b), (-3 * b + r) / (10 * c), (-3 * b - r) / (10 * c)};
+    Range x = {0, 0, 0};
+    for (double q : at) {
+        if (!(q >= 0 && q <= top * top)) continue;
+        const double poly = q * (b + c * q);
+        x.left = std::max(x.left, std::sqrt(q) * std::fabs(a + poly));
+        x.poly = std::max(x.poly, std::fabs(poly));
+        x.factor = std::max(x.factor, std::fabs(a + poly));
+    }
+    return x;
+}
+
+/* Singular values and |B| of all steps, from any update's, 0 .. 1: both have to fit f16 times ORTH_SCALE. */
 const char *check_steps(const msim_orthogonalize_spec *s)
 {
-    const double a = s->a, b = s->b, c = s->c;
+    static const char *const why = "orthogonalize: steps with these coefficients leave the range of the products";
     double top = 1.0;
-    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return "orthogonalize: coefficients out of range";
+    if (!std::isfinite(s->a) || !std::isfinite(s->b) || !std::isfinite(s->c)) return "orthogonalize: coefficients out of range";
     for (uint32_t k = 0; k < s->steps; k++) {
-        double x = 0, poly = 0;
-        for (int i = 0; i <= 4096; i++) {
-            const double v = top * i / 4096, q = v * v;
-            x = std::max(x, std::fabs(v * (a + q * (b + c * q))));
-            poly = std::max(poly, std::fabs(q * (b + c * q)));
-        }
-        if (!(poly <= 24.0 && top * top <= 24.0)) return "orthogonalize: steps with these coefficients leave the range of the products";
-        top = x * 1.001;
-        if (!(top <= 24.0)) return "orthogonalize: steps with these coefficients leave the range of the products";
+        const Range x = range_of(s, top);
+        if (!(x.poly <= 24.0 && top * top <= 24.0)) return why;
+        top = x.left * 1.001;
+        if (!(top <= 24.0)) return why;
     }
     return nullptr;
+}
+
+/* How many steps, from step k on, are taken in one pass over X: without it, P of the
+ * next step is (a + B) P (a + B), and X gets the product Q of all a + B.  That is 3
+ * m^2 n a pass and 4 m^3 a step more (symmetric ones counted by their half),
+ * instead of 3 m^2 n + m^3 a step.  Errors of 22 bits grow with P's small values
+ * until P is made of X again: up to three steps from the start, where no value is
+ * far above the others' reach yet, and two later leave five steps' result as near
+ * as single ones do (2e-5 to 3e-4 of its mean magnitude, by the update's values). */
+uint32_t pass_of(const msim_orthogonalize_spec *s, bool wide, uint32_t k)
+{
+    const uint32_t most = std::min(s->steps - k, !wide ? 1u : k == 0 ? 3u : 2u);
+    double top = 1.0, q = 1.0;
+    for (uint32_t i = 0; i < k; i++) top = range_of(s, top).left * 1.001;
+    uint32_t n = 0;
+    for (; n < most; n++) {
+        const Range x = range_of(s, top);
+        q *= x.factor;
+        if (!(x.factor <= 24.0 && q <= 24.0 * PASS_DOWN)) break;      /* as check_steps */
+        top = x.left * 1.001;
+    }
+    return std::max(n, 1u);
 }
 
 const char *check_orth(const msim_orthogonalize_spec *s, int *code)
@@ -391,7 +445,7 @@ hipError_t run_slabs(const msim_orthogonalize_spec *s, const Orth &o, const void
     char *x = ws + o.norm_bytes, *part = x + o.x_bytes, *next = part + o.p_bytes;
     const bool flip = s->rows > s->cols;
     SlabP p = {in, out, (const double *)ws, x, (const float *)part, (float *)next, s->rows * s->cols, flip ? 1 : s->cols, flip ? s->cols : 1,
-               s->eps, (uint32_t)o.m, (uint32_t)o.n, (uint32_t)o.slabs, (uint32_t)o.wide, 1, s->steps == 0, s->a, s->b, s->c};
+               s->eps, (uint32_t)o.m, (uint32_t)o.n, (uint32_t)o.slabs, (uint32_t)o.slab, 1, s->steps == 0, s->a, s->b, s->c};
     hipError_t e = launch(msim_orth_norm<D>, s->count * NORM_PARTS, 256, 0, st, in, s->rows * s->cols, (double *)ws);
     for (uint32_t k = 0; k <= s->steps && e == hipSuccess; k++) {
         p.first = k == 0;
@@ -408,50 +462,72 @@ template <typename D>
 hipError_t run_orth(const msim_orthogonalize_spec *s, const Orth &o, const void *in, void *out, char *ws, hipStream_t st)
 {
     if (o.slabs) return run_slabs<D>(s, o, in, out, ws, st);
-    char *norms = ws, *x = norms + o.norm_bytes, *y = x + o.x_bytes, *sq = y + o.x_bytes, *poly = sq + o.p_bytes, *part = poly + o.p_bytes;
-    OrthP q = {in, out, x, (const double *)norms, s->rows, s->cols, o.lx, o.m * o.lx * 4, s->eps, s->count, s->rows > s->cols};
+    char *norms = ws, *x = norms + o.norm_bytes, *y = x + o.x_bytes, *sq = y + o.x_bytes, *m2[5], *part = sq + o.p_bytes;
+    for (uint32_t i = 0; i < o.squares; i++, part += o.p_bytes) m2[i] = part;
+    OrthP q = {in, out, x, (const double *)norms, s->rows, s->cols, o.lx, o.m * o.lx * 4, s->eps};
+    const bool flip = s->rows > s->cols;
     const uint32_t moves = (uint32_t)((o.lx + 63) / 64 * ((o.m + 31) / 32) * s->count);
     hipError_t e = launch(msim_orth_norm<D>, s->count * NORM_PARTS, 256, 0, st, in, s->rows * s->cols, (double *)norms);
-    if (e == hipSuccess) e = launch(msim_orth_move<D, true>, moves, 256, 0, st, q);
-    for (uint32_t k = 0; k < s->steps && e == hipSuccess; k++) {
-        const Operand ox = {x, o.m * o.lx * 4, o.lx * 4, o.m * o.lx * 4};
-        const Operand osq = {sq, o.m * o.lp * 4, o.lp * 4, o.m * o.lp * 4}, opoly = {poly, o.m * o.lp * 4, o.lp * 4, o.m * o.lp * 4};
+    if (e == hipSuccess) e = launch(flip ? msim_orth_move<D, true, true> : msim_orth_move<D, true, false>, moves, 256, 0, st, q);
+    /* to = alpha src + beta a b + diag I, symmetric; b of X or of a matrix of m columns */
+    const auto square = [&](char *to, const char *fa, const char *fb, uint64_t ld, const Plan &plan, const char *src, float alpha, float beta, float diag) {
         GemmP p = {};
         p.batch = s->count;
         p.part = (float *)part;
         p.M = p.N = p.e.M = p.e.N = (uint32_t)o.m;
         p.mirror = 1;
-        p.a = p.b = ox;
-        p.K = (uint32_t)o.lx;
-        p.e.out = sq;
+        p.a = {fa, o.m * ld * 4, ld * 4, o.m * ld * 4};
+        p.b = {fb, o.m * ld * 4, ld * 4, o.m * ld * 4};
+        p.K = (uint32_t)ld;
+        p.e.out = to;
         p.e.out_ld = o.lp;
         p.e.out_batch = o.m * o.lp * 4;
-        p.e.beta = 1.0f / ORTH_SCALE;
-        e = launch_gemm<M_SPLIT, false>(p, o.square, st);
+        p.e.src = src;
+        p.e.alpha = alpha;
+        p.e.beta = beta;
+        p.e.diag = diag;
+        if (e == hipSuccess) e = launch_gemm<M_SPLIT, false>(p, plan, st);
+    };
+    constexpr float ONE = 1.0f / ORTH_SCALE;
+    for (uint32_t k = 0; k < s->steps && e == hipSuccess;) {
+        const uint32_t n = pass_of(s, o.wide, k);
+        k += n;
+        square(sq, x, x, o.lx, o.square, nullptr, 0, ONE, 0);
+        char *w = m2[0], *factor = w;
+        for (uint32_t i = 0; i < n; i++) {
+            /* B, or a + B where there are several steps */
+            square(w, sq, sq, o.lp, o.poly, sq, s->b, s->c * ONE, n > 1 ? s->a * ORTH_SCALE : 0);
+            if (i) {
+                char *to = m2[2 + (i & 1)];
+                square(to, w, factor, o.lp, o.poly, nullptr, 0, i == 1 ? ONE / PASS_DOWN : ONE, 0);
+                factor = to;
+            }
+            if (i + 1 < n) {
+                square(m2[4], w, sq, o.lp, o.poly, nullptr, 0, ONE, 0);
+                square(sq, m2[4], w, o.lp, o.poly, nullptr, 0, ONE, 0);
+                w = i ? m2[0] : m2[1];
+            }
+        }
         if (e != hipSuccess) break;
-        p.a = p.b = osq;
-        p.K = (uint32_t)o.lp;
-        p.e.out = poly;
-        p.e.src = sq;
-        p.e.alpha = s->b;
-        p.e.beta = s->c / ORTH_SCALE;
-        e = launch_gemm<M_SPLIT, false>(p, o.poly, st);
-        if (e != hipSuccess) break;
-        p.mirror = 0;
-        p.a = opoly;
-        p.b = ox;
+        GemmP p = {};
+        p.batch = s->count;
+        p.part = (float *)part;
+        p.M = p.e.M = (uint32_t)o.m;
         p.N = p.e.N = (uint32_t)o.n;
+        p.a = {factor, o.m * o.lp * 4, o.lp * 4, o.m * o.lp * 4};
+        p.b = {x, o.m * o.lx * 4, o.lx * 4, o.m * o.lx * 4};
+        p.K = (uint32_t)o.lp;
         p.e.out = y;
         p.e.out_ld = o.lx;
         p.e.out_batch = o.m * o.lx * 4;
-        p.e.src = x;
+        p.e.src = n == 1 ? x : nullptr;
         p.e.alpha = s->a;
-        p.e.beta = 1.0f / ORTH_SCALE;
+        p.e.beta = n == 1 ? ONE : ONE * PASS_DOWN;
         e = launch_gemm<M_SPLIT, true>(p, o.update, st);
         std::swap(x, y);
     }
     q.x = x;
-    if (e == hipSuccess) e = launch(msim_orth_move<D, false>, moves, 256, 0, st, q);
+    if (e == hipSuccess) e = launch(flip ? msim_orth_move<D, false, true> : msim_orth_move<D, false, false>, moves, 256, 0, st, q);
     return e;
 }
 

@@ -447,6 +447,26 @@ def test_orthogonalize_against_64_bits(T, M, types, dt):
             assert bool((err <= tol).all())
 
 
+@pytest.mark.parametrize("shape", [(70, 4481), (300, 8003), (8003, 300), (9, 200, 2000), (1024, 2600), (50, 8193)])
+def test_orthogonalize_steps_without_the_update(T, M, types, shape):
+    """Wide updates, of which several steps are taken at a time, with singular values over three orders.  Of P, a + B, (a + B) P,
+    (a + B) P (a + B) and Q up to nine are rounded for three steps, each by at most 2^-23 of its norm; an error of P comes
+    into a + B at most |b| + 2 |c| = 8.8 times, and what a + B are off by meets the other two factors, 3.5^2 at most:
+    9 * 8.8 * 12 * 2^-23 = 1.2e-4 a group of steps, of which there are up to three."""
+    *count, rows, cols = shape
+    g = gen(T, rows)
+    u = T.randn(*count, rows, cols, device=DEV, generator=g)
+    u = (u * T.logspace(0, -3, rows, device=DEV)[:, None] if rows <= cols else u * T.logspace(0, -3, cols, device=DEV))
+    for dt, steps in (("f32", 2), ("bf16", 3), ("f16", 4), ("f32", 5), ("f16", 5), ("f32", 6)):
+        v = u.to(types[dt])
+        y = M.orthogonalize(v, steps=steps).double()
+        want = orth64(T, v, steps, ABC)
+        err = float(((y - want).flatten(-2).norm(dim=-1) / want.flatten(-2).norm(dim=-1)).max())
+        print(shape, dt, steps, err, flush=True)
+        assert err <= U[dt] + 3 * 1.2e-4
+        assert T.equal(y, M.orthogonalize(v, steps=steps).double())
+
+
 def test_orthogonalize_moves_singular_values_to_one(T, M):
     """Five steps take singular values from 0.01 of the norm on to 0.65 .. 1.25 (the polynomial's own range, 0.68 .. 1.13
     there, and the errors above)."""
