@@ -244,9 +244,11 @@ template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bou
     const uint32_t n = min(all - first, 16u * MT);
     if constexpr (DOWN) {
         if (n <= 16) down_tokens<D, 1, WAVES>(p, expert, tile, list + first, n, sums);
+        else if (MT > 2 && n <= 32) down_tokens<D, 2, WAVES>(p, expert, tile, list + first, n, sums);
         else down_tokens<D, MT, WAVES>(p, expert, tile, list + first, n, sums);
     } else {
         if (n <= 16) up_tokens<D, 1, WAVES>(p, expert, tile, list + first, n, sums);
+        else if (MT > 2 && n <= 32) up_tokens<D, 2, WAVES>(p, expert, tile, list + first, n, sums);
         else up_tokens<D, MT, WAVES>(p, expert, tile, list + first, n, sums);
     }
 }
