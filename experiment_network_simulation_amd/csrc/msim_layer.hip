@@ -8,6 +8,7 @@
  */
 
 #include <algorithm>
+#include <type_traits>
 
 #include "msim_route.h"
 #include "msim_stream.h"
@@ -23,6 +24,7 @@ struct LayerP {
     float *logits;
     const int32_t *ids;
     const float *weights;
+    const int32_t *load;         /* tokens of each expert, or null: counted where it is asked for */
     void *h;                     /* [rows * top_k][h_ld], of the layer's type */
     float *part;                 /* [rows * top_k][part_ld] */
     uint64_t x_ld, out_ld, res_ld, h_ld, part_ld;
@@ -68,28 +70,33 @@ template <typename D, int TT> __global__ void __launch_bounds__(256) msim_layer_
 /* The expert of a slot and the list of its assignments (row * K + choice), in
  * order.  Where there are fewer assignments than experts a slot is an assignment,
  * and the first that names an expert has it; otherwise a slot is an expert.  The
- * number of assignments, 0 where another slot has the expert. */
+ * number of assignments, 0 where another slot has the expert.  Each thread looks
+ * at as many ids next to each other as it takes. */
 template <int WAVES> __device__ __forceinline__ uint32_t tokens_of(const LayerP &p, const int32_t *ids, uint32_t slot, uint32_t *list, uint32_t *counts, int32_t &expert)
 {
     const uint32_t n = p.rows * p.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const bool by_choice = p.slots == n;
     expert = by_choice ? ids[slot] : (int32_t)slot;
     if (expert < 0) return 0;
-    uint32_t have = 0;
-    for (uint32_t j0 = 0; j0 < n; j0 += 64 * WAVES) {
-        const uint32_t j = j0 + threadIdx.x;
-        const bool mine = j < n && ids[j] == expert;
-        const uint64_t all = __ballot(mine);
-        if (lane == 0) counts[wave] = __popcll(all);
-        __syncthreads();
-        uint32_t at = have + __popcll(all & ((1ull << lane) - 1));
-        for (uint32_t w = 0; w < WAVES; w++) {
-            if (w < wave) at += counts[w];
-            have += counts[w];
-        }
-        if (mine && at < MAX_ROWS) list[at] = j;
-        __syncthreads();
+    const uint32_t per = (n + 64 * WAVES - 1) / (64 * WAVES), first = threadIdx.x * per, last = min(n, first + per);
+    uint32_t mine = 0;
+    for (uint32_t j = first; j < last; j++) mine += ids[j] == expert;
+    uint32_t upto = mine;
+    for (uint32_t d = 1; d < 64; d *= 2) {
+        const uint32_t before = __shfl_up(upto, d);
+        if (lane >= d) upto += before;
     }
+    if (lane == 63) counts[wave] = upto;
+    __syncthreads();
+    uint32_t at = upto - mine, have = 0;
+    for (uint32_t w = 0; w < WAVES; w++) {
+        if (w < wave) at += counts[w];
+        have += counts[w];
+    }
+    if (mine)
+        for (uint32_t j = first; j < last; j++)
+            if (ids[j] == expert && at < MAX_ROWS) list[at++] = j;
+    __syncthreads();
     return by_choice && list[0] != slot ? 0 : min(have, MAX_ROWS);
 }
 
@@ -109,7 +116,7 @@ template <typename D> __device__ __forceinline__ void hidden_of(const LayerP &p,
 
 /* h = act(gate rows x) (up rows x), or act(rows x): 16 hidden units (32 without a
  * gate) of one expert for up to 16 MT of its tokens */
-template <typename D, int MT, int WAVES>
+template <typename D, int MT, int WAVES, bool ALL = true>
 __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, f32x4 *lds)
 {
     typedef typename D::raw raw;
@@ -122,7 +129,7 @@ __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint3
     for (int i = 0; i < MT; i++) x[i] = (const raw *)p.x + list[min(i * 16 + l, n - 1)] / p.K * p.x_ld;
     f32x4 acc[MT][2];
     for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
-    stream<D, MT, 2>(w, x, p.C, wave, WAVES, acc);
+    stream<D, MT, 2, ALL>(w, x, p.C, wave, WAVES, acc);
     join<MT, 2, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
@@ -131,7 +138,7 @@ __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint3
 }
 
 /* 32 columns of what one expert answers to up to 16 MT of its tokens, in 32 bits */
-template <typename D, int MT, int WAVES>
+template <typename D, int MT, int WAVES, bool ALL = true>
 __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, f32x4 *lds)
 {
     typedef typename D::raw raw;
@@ -143,7 +150,7 @@ __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uin
     for (int i = 0; i < MT; i++) x[i] = (const raw *)p.h + (uint64_t)list[min(i * 16 + l, n - 1)] * p.h_ld;
     f32x4 acc[MT][2];
     for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
-    stream<D, MT, 2>(w, x, p.F, wave, WAVES, acc);
+    stream<D, MT, 2, ALL>(w, x, p.F, wave, WAVES, acc);
     join<MT, 2, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
@@ -238,19 +245,19 @@ template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bou
     __shared__ uint32_t list[MAX_ROWS], counts[WAVES];
     __shared__ f32x4 sums[WAVES * MT * 2 * 64];
     const uint32_t tile = blockIdx.x % p.tiles, rest = blockIdx.x / p.tiles, chunk = rest % p.chunks, slot = rest / p.chunks;
+    constexpr bool ALL = MT <= 2;
+    if (p.load && p.slots == p.E && chunk * 16 * MT >= (uint32_t)p.load[slot]) return;
     int32_t expert;
     const uint32_t all = tokens_of<WAVES>(p, p.ids, slot, list, counts, expert), first = chunk * 16 * MT;
     if (first >= all) return;
     const uint32_t n = min(all - first, 16u * MT);
-    if constexpr (DOWN) {
-        if (n <= 16) down_tokens<D, 1, WAVES>(p, expert, tile, list + first, n, sums);
-        else if (MT > 2 && n <= 32) down_tokens<D, 2, WAVES>(p, expert, tile, list + first, n, sums);
-        else down_tokens<D, MT, WAVES>(p, expert, tile, list + first, n, sums);
-    } else {
-        if (n <= 16) up_tokens<D, 1, WAVES>(p, expert, tile, list + first, n, sums);
-        else if (MT > 2 && n <= 32) up_tokens<D, 2, WAVES>(p, expert, tile, list + first, n, sums);
-        else up_tokens<D, MT, WAVES>(p, expert, tile, list + first, n, sums);
-    }
+    const auto part = [&](auto mt) {
+        if constexpr (DOWN) down_tokens<D, mt.value, WAVES, ALL>(p, expert, tile, list + first, n, sums);
+        else up_tokens<D, mt.value, WAVES, ALL>(p, expert, tile, list + first, n, sums);
+    };
+    if (n <= 16) part(std::integral_constant<int, 1>());
+    else if (MT > 2 && n <= 32) part(std::integral_constant<int, 2>());
+    else part(std::integral_constant<int, MT>());
 }
 
 /* The weighted sum over a token's choices, in their order, and the residual.  A
@@ -391,7 +398,7 @@ extern "C" int msim_layer(const msim_layer_spec *s, const void *x, const void *g
     if (!workspace || workspace_bytes < l.bytes || (uintptr_t)workspace % 256)
         return fail(MSIM_E_WORKSPACE, "layer: workspace missing, too small or not on 256 bytes");
     char *ws = (char *)workspace;
-    const LayerP p = {x, gate, w_in, w_out, residual, mask, out, (float *)ws, ids, weights, ws + l.logits,
+    const LayerP p = {x, gate, w_in, w_out, residual, mask, out, (float *)ws, ids, weights, load, ws + l.logits,
                       (float *)(ws + l.logits + l.h), s->x_stride, s->out_stride, s->residual_stride, l.h_ld, l.part_ld,
                       (uint32_t)s->route.rows, s->route.experts, s->route.top_k, s->cols, s->hidden, s->act, s->gated, 0, 0, 0};
     hipStream_t st = (hipStream_t)hip_stream;

@@ -62,8 +62,11 @@ template <typename D> __device__ __forceinline__ u32x4 piece(const typename D::r
 template <typename D> constexpr uint32_t RUN = 256 / sizeof(typename D::raw);
 
 /* acc[i][j] += over N runs of k, at k, k + step, ..., all within K: weight rows
- * w[j], vectors x[i], both those of lane % 16.  All loads are asked for before the first is used. */
-template <typename D, int MT, int NT, int N>
+ * w[j], vectors x[i], both those of lane % 16.  ALL: all loads are asked for before the
+ * first is used, which the compiler would not do by itself (32 tokens of 7,168
+ * columns, 8 of 128 experts 1,430 -> 1,286 us); where there are so many of them that
+ * their registers cost wavefronts, it is left to it. */
+template <typename D, int MT, int NT, int N, bool ALL>
 __device__ __forceinline__ void stream_whole(const typename D::raw *const *w, const typename D::raw *const *x, uint32_t k, uint32_t step,
                                              f32x4 (&acc)[MT][NT])
 {
@@ -75,19 +78,20 @@ __device__ __forceinline__ void stream_whole(const typename D::raw *const *w, co
         _Pragma("unroll") for (int j = 0; j < NT; j++) a[u][j] = piece<D>(w[j] + at);
         _Pragma("unroll") for (int i = 0; i < MT; i++) b[u][i] = piece<D>(x[i] + at);
     }
+    if constexpr (ALL) __builtin_amdgcn_sched_barrier(0);
     _Pragma("unroll") for (uint32_t u = 0; u < N * U; u++)
         _Pragma("unroll") for (int i = 0; i < MT; i++)
             _Pragma("unroll") for (int j = 0; j < NT; j++) acc[i][j] = mma16<D>(a[u][j], b[u][i], acc[i][j]);
 }
 
 /* one run, or what there is of it */
-template <typename D, int MT, int NT>
+template <typename D, int MT, int NT, bool ALL = true>
 __device__ __forceinline__ void stream_run(const typename D::raw *const *w, const typename D::raw *const *x, uint32_t k, uint32_t K,
                                            f32x4 (&acc)[MT][NT])
 {
     constexpr uint32_t PER = 16 / sizeof(typename D::raw);
     const uint32_t q = (threadIdx.x & 63) >> 4;
-    if (k + RUN<D> <= K) return stream_whole<D, MT, NT, 1>(w, x, k, 0, acc);
+    if (k + RUN<D> <= K) return stream_whole<D, MT, NT, 1, ALL>(w, x, k, 0, acc);
     for (; k < K; k += 4 * PER) {
         u32x4 a[NT], b[MT];
         _Pragma("unroll") for (int j = 0; j < NT; j++) a[j] = piece<D>(w[j], k + q * PER, K);
@@ -98,15 +102,15 @@ __device__ __forceinline__ void stream_run(const typename D::raw *const *w, cons
 }
 
 /* the wavefront's share of k, every waves-th run: of few vectors two at a time, whose loads fit its registers */
-template <typename D, int MT, int NT>
+template <typename D, int MT, int NT, bool ALL = true>
 __device__ __forceinline__ void stream(const typename D::raw *const *w, const typename D::raw *const *x, uint32_t K,
                                        uint32_t wave, uint32_t waves, f32x4 (&acc)[MT][NT])
 {
     uint32_t k = wave * RUN<D>;
     const uint32_t step = waves * RUN<D>;
     if constexpr (MT + NT <= 3)
-        for (; k + step + RUN<D> <= K; k += 2 * step) stream_whole<D, MT, NT, 2>(w, x, k, step, acc);
-    for (; k < K; k += step) stream_run<D, MT, NT>(w, x, k, K, acc);
+        for (; k + step + RUN<D> <= K; k += 2 * step) stream_whole<D, MT, NT, 2, ALL>(w, x, k, step, acc);
+    for (; k < K; k += step) stream_run<D, MT, NT, ALL>(w, x, k, K, acc);
 }
 
 /* The wavefronts' sums together, in order.  lds: waves x MT x NT x 64 pieces.
