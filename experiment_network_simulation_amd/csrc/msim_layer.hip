@@ -24,12 +24,14 @@ struct LayerP {
     float *logits;
     const int32_t *ids;
     const float *weights;
-    const int32_t *load;         /* tokens of each expert, or null: counted where it is asked for */
+    int32_t *load;               /* tokens of each expert */
     void *h;                     /* [rows * top_k][h_ld], of the layer's type */
     float *part;                 /* [rows * top_k][part_ld] */
     uint64_t x_ld, out_ld, res_ld, h_ld, part_ld;
     uint32_t rows, E, K, C, F, act, gated;
-    uint32_t slots, tiles, chunks;         /* of a product: experts, tiles of weight rows, runs of tokens */
+    /* Of a product.  slots: assignments, of which the first that names an expert has it, if they are fewer than
+     * experts; otherwise experts.  tiles of weight rows. */
+    uint32_t slots, tiles;
 };
 
 /* Logits in 64 bits, rounded to 32: of 16-bit inputs every product is exact, and
@@ -67,17 +69,11 @@ template <typename D, int TT> __global__ void __launch_bounds__(256) msim_layer_
     }
 }
 
-/* The expert of a slot and the list of its assignments (row * K + choice), in
- * order.  Where there are fewer assignments than experts a slot is an assignment,
- * and the first that names an expert has it; otherwise a slot is an expert.  The
- * number of assignments, 0 where another slot has the expert.  Each thread looks
- * at as many ids next to each other as it takes. */
-template <int WAVES> __device__ __forceinline__ uint32_t tokens_of(const LayerP &p, const int32_t *ids, uint32_t slot, uint32_t *list, uint32_t *counts, int32_t &expert)
+/* The list of an expert's assignments (row * K + choice), in order, and their number.
+ * Each thread looks at as many ids next to each other as it takes. */
+template <int WAVES> __device__ __forceinline__ uint32_t tokens_of(const LayerP &p, const int32_t *ids, int32_t expert, uint32_t *list, uint32_t *counts)
 {
     const uint32_t n = p.rows * p.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const bool by_choice = p.slots == n;
-    expert = by_choice ? ids[slot] : (int32_t)slot;
-    if (expert < 0) return 0;
     const uint32_t per = (n + 64 * WAVES - 1) / (64 * WAVES), first = threadIdx.x * per, last = min(n, first + per);
     uint32_t mine = 0;
     for (uint32_t j = first; j < last; j++) mine += ids[j] == expert;
@@ -97,7 +93,7 @@ template <int WAVES> __device__ __forceinline__ uint32_t tokens_of(const LayerP 
         for (uint32_t j = first; j < last; j++)
             if (ids[j] == expert && at < MAX_ROWS) list[at++] = j;
     __syncthreads();
-    return by_choice && list[0] != slot ? 0 : min(have, MAX_ROWS);
+    return min(have, MAX_ROWS);
 }
 
 /* Four hidden units from f on (16 more of them 16 further, without a gate) of what
@@ -168,7 +164,7 @@ __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uin
 constexpr uint32_t FEW_ROWS = 16;
 constexpr int FEW_WAVES = 16;
 
-template <typename D, int VPL> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_layer_up_few(LayerP p, RouteP r, int32_t *ids, float *weights, int32_t *load)
+template <typename D, int VPL> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_layer_up_few(LayerP p, RouteP r, int32_t *ids, float *weights)
 {
     extern __shared__ double keys[];
     __shared__ int32_t chosen[FEW_ROWS * MSIM_MAX_TOP_K];
@@ -185,16 +181,17 @@ template <typename D, int VPL> __global__ void __launch_bounds__(64 * FEW_WAVES)
             ids[j] = chosen[j];
             weights[j] = shares[j];
         }
-        if (load)
-            for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
-                int32_t c = 0;
-                for (uint32_t j = 0; j < n; j++) c += chosen[j] == (int32_t)e;
-                load[e] = c;
-            }
+        for (uint32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
+            int32_t c = 0;
+            for (uint32_t j = 0; j < n; j++) c += chosen[j] == (int32_t)e;
+            p.load[e] = c;
+        }
     }
-    int32_t expert;
-    const uint32_t have = tokens_of<FEW_WAVES>(p, chosen, blockIdx.x / p.tiles, list, counts, expert);
-    if (have) up_tokens<D, 1, FEW_WAVES>(p, expert, blockIdx.x % p.tiles, list, have, sums);
+    const uint32_t slot = blockIdx.x / p.tiles;
+    const int32_t expert = p.slots < p.E ? chosen[slot] : (int32_t)slot;
+    if (expert < 0) return;
+    const uint32_t have = tokens_of<FEW_WAVES>(p, chosen, expert, list, counts);
+    if (have && (p.slots == p.E || list[0] == slot)) up_tokens<D, 1, FEW_WAVES>(p, expert, blockIdx.x % p.tiles, list, have, sums);
 }
 
 /* The second product and the sum of few tokens: 32 columns of one token's result a
@@ -239,17 +236,43 @@ template <typename D> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_lay
     }
 }
 
-/* MT: tokens of a run, in 16; runs of at most 16 take the leaner code.  WAVES: k is shared among them. */
+/* Which expert has run `run`, and which of its own that is: an expert has a run for every
+ * `tokens` that chose it, or part of them.  -1 behind the last.  Each wavefront by itself. */
+__device__ __forceinline__ int32_t expert_of(const LayerP &p, uint32_t run, uint32_t tokens, uint32_t &own)
+{
+    const uint32_t lane = threadIdx.x & 63, per = (p.E + 63) / 64, first = lane * per, last = min(p.E, first + per);
+    uint32_t mine = 0;
+    for (uint32_t e = first; e < last; e++) mine += (p.load[e] + tokens - 1) / tokens;
+    uint32_t upto = mine;
+    for (uint32_t d = 1; d < 64; d *= 2) {
+        const uint32_t before = __shfl_up(upto, d);
+        if (lane >= d) upto += before;
+    }
+    const uint64_t behind = __ballot(upto > run);
+    if (!behind) return -1;
+    const uint32_t at = __builtin_ctzll(behind);
+    own = run - __builtin_amdgcn_readlane(upto - mine, at);
+    for (uint32_t e = at * per; e < p.E; e++) {
+        const uint32_t n = (p.load[e] + tokens - 1) / tokens;
+        if (own < n) return e;
+        own -= n;
+    }
+    return -1;
+}
+
+/* MT: tokens of a run, in 16; fewer take leaner code.  WAVES: k is shared among them.  Runs of four 16 are so
+ * many loads that all of them ahead cost more wavefronts than they hide (512 x 2,048, 6 of 64 experts 549 -> 880 us). */
 template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bounds__(64 * WAVES) msim_layer_product(LayerP p)
 {
     __shared__ uint32_t list[MAX_ROWS], counts[WAVES];
     __shared__ f32x4 sums[WAVES * MT * 2 * 64];
-    const uint32_t tile = blockIdx.x % p.tiles, rest = blockIdx.x / p.tiles, chunk = rest % p.chunks, slot = rest / p.chunks;
     constexpr bool ALL = MT <= 2;
-    if (p.load && p.slots == p.E && chunk * 16 * MT >= (uint32_t)p.load[slot]) return;
-    int32_t expert;
-    const uint32_t all = tokens_of<WAVES>(p, p.ids, slot, list, counts, expert), first = chunk * 16 * MT;
-    if (first >= all) return;
+    const uint32_t run = blockIdx.x / p.tiles, tile = blockIdx.x - run * p.tiles;
+    uint32_t own = 0;
+    const int32_t expert = p.rows > 16 * MT ? expert_of(p, run, 16 * MT, own) : p.slots < p.E ? p.ids[run] : p.load[run] ? (int32_t)run : -1;
+    if (expert < 0) return;
+    const uint32_t all = tokens_of<WAVES>(p, p.ids, expert, list, counts), first = own * 16 * MT;
+    if (first >= all || (p.rows <= 16 * MT && p.slots < p.E && list[0] != run)) return;
     const uint32_t n = min(all - first, 16u * MT);
     const auto part = [&](auto mt) {
         if constexpr (DOWN) down_tokens<D, mt.value, WAVES, ALL>(p, expert, tile, list + first, n, sums);
@@ -288,7 +311,7 @@ template <typename D> __global__ void __launch_bounds__(256) msim_layer_sum(Laye
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
-struct Layout { uint64_t logits, h, part, bytes, h_ld, part_ld; };
+struct Layout { uint64_t logits, h, part, load, bytes, h_ld, part_ld; };
 
 Layout layout_of(const msim_layer_spec *s)
 {
@@ -299,7 +322,8 @@ Layout layout_of(const msim_layer_spec *s)
     l.logits = up(s->route.rows * s->route.experts * 4, 256);
     l.h = up(n * l.h_ld * (s->dtype == MSIM_F32 ? 4 : 2), 256);
     l.part = up(n * l.part_ld * 4, 256);
-    l.bytes = l.logits + l.h + l.part;
+    l.load = up(s->route.experts * 4ull, 256);
+    l.bytes = l.logits + l.h + l.part + l.load;
     return l;
 }
 
@@ -328,8 +352,8 @@ template <typename D, bool DOWN> hipError_t launch_product(LayerP p, uint64_t ti
 {
     const uint32_t mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
     p.tiles = (uint32_t)tiles;
-    p.chunks = (p.rows + 16 * mt - 1) / (16 * mt);
-    const uint32_t grid = p.slots * p.chunks * p.tiles;
+    /* a run for each expert that may be chosen, and one more for every 16 mt assignments */
+    const uint32_t grid = (p.slots + (p.rows <= 16 * mt ? 0 : p.rows * p.K / (16 * mt))) * p.tiles;
     /* few workgroups: more wavefronts in each */
     if (grid < 1024) {
         if (mt == 1) return launch(msim_layer_product<D, 1, 16, DOWN>, grid, 1024, 0, st, p);
@@ -341,7 +365,7 @@ template <typename D, bool DOWN> hipError_t launch_product(LayerP p, uint64_t ti
     return launch(msim_layer_product<D, 4, 4, DOWN>, grid, 256, 0, st, p);
 }
 
-template <typename D> int run_layer(const msim_layer_spec *s, LayerP p, const float *bias, int32_t *ids, float *weights, int32_t *load, hipStream_t st)
+template <typename D> int run_layer(const msim_layer_spec *s, LayerP p, const float *bias, int32_t *ids, float *weights, hipStream_t st)
 {
     hipError_t e = p.rows == 1 ? launch(msim_layer_gate<D, 1>, p.E, 256, 0, st, p)
                                : launch(msim_layer_gate<D, 4>, p.E * ((p.rows + 3) / 4), 256, 0, st, p);
@@ -356,10 +380,10 @@ template <typename D> int run_layer(const msim_layer_spec *s, LayerP p, const fl
                     r.group_top, r.renorm, r.score == MSIM_SCORE_SIGMOID, r.scale, 0, 0, 0, 0};
         if (q.TG == q.G) q.G = q.TG = q.gtop = 1;       /* every group stays */
         p.tiles = (uint32_t)in;
-        e = launch(p.E <= 256 ? msim_layer_up_few<D, 4> : msim_layer_up_few<D, 16>, p.slots * p.tiles, 64 * FEW_WAVES, keys, st, p, q, ids, weights, load);
+        e = launch(p.E <= 256 ? msim_layer_up_few<D, 4> : msim_layer_up_few<D, 16>, p.slots * p.tiles, 64 * FEW_WAVES, keys, st, p, q, ids, weights);
         if (e != hipSuccess) return launched(e, "layer launch");
     } else {
-        if (int rc = msim_route(&s->route, p.logits, bias, ids, weights, load, st)) return rc;
+        if (int rc = msim_route(&s->route, p.logits, bias, ids, weights, p.load, st)) return rc;
         e = launch_product<D, false>(p, in, st);
         if (e != hipSuccess) return launched(e, "layer launch");
     }
@@ -398,11 +422,11 @@ extern "C" int msim_layer(const msim_layer_spec *s, const void *x, const void *g
     if (!workspace || workspace_bytes < l.bytes || (uintptr_t)workspace % 256)
         return fail(MSIM_E_WORKSPACE, "layer: workspace missing, too small or not on 256 bytes");
     char *ws = (char *)workspace;
-    const LayerP p = {x, gate, w_in, w_out, residual, mask, out, (float *)ws, ids, weights, load, ws + l.logits,
+    const LayerP p = {x, gate, w_in, w_out, residual, mask, out, (float *)ws, ids, weights, load ? load : (int32_t *)(ws + l.logits + l.h + l.part), ws + l.logits,
                       (float *)(ws + l.logits + l.h), s->x_stride, s->out_stride, s->residual_stride, l.h_ld, l.part_ld,
-                      (uint32_t)s->route.rows, s->route.experts, s->route.top_k, s->cols, s->hidden, s->act, s->gated, 0, 0, 0};
+                      (uint32_t)s->route.rows, s->route.experts, s->route.top_k, s->cols, s->hidden, s->act, s->gated, 0, 0};
     hipStream_t st = (hipStream_t)hip_stream;
-    return s->dtype == MSIM_F32 ? run_layer<F32>(s, p, bias, ids, weights, load, st)
-        : s->dtype == MSIM_F16 ? run_layer<F16>(s, p, bias, ids, weights, load, st)
-                               : run_layer<BF16>(s, p, bias, ids, weights, load, st);
+    return s->dtype == MSIM_F32 ? run_layer<F32>(s, p, bias, ids, weights, st)
+        : s->dtype == MSIM_F16 ? run_layer<F16>(s, p, bias, ids, weights, st)
+                               : run_layer<BF16>(s, p, bias, ids, weights, st);
 }
