@@ -113,19 +113,19 @@ template <typename D> __device__ __forceinline__ void hidden_of(const LayerP &p,
 /* h = act(gate rows x) (up rows x), or act(rows x): 16 hidden units (32 without a
  * gate) of one expert for up to 16 MT of its tokens */
 template <typename D, int MT, int WAVES, bool ALL = true>
-__device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, f32x4 *lds)
+__device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, char *lds)
 {
     typedef typename D::raw raw;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
     const uint32_t f0 = tile * (p.gated ? 16 : 32);
-    const raw *w[2], *x[MT];
+    Rows<D> w[2], x[MT];
     const raw *base = (const raw *)p.w_in + (uint64_t)expert * (p.gated ? 2 : 1) * p.F * p.C;
-    w[0] = base + (uint64_t)min(f0 + l, p.F - 1) * p.C;
-    w[1] = base + (uint64_t)(p.gated ? p.F + min(f0 + l, p.F - 1) : min(f0 + 16 + l, p.F - 1)) * p.C;
-    for (int i = 0; i < MT; i++) x[i] = (const raw *)p.x + list[min(i * 16 + l, n - 1)] / p.K * p.x_ld;
+    w[0].set([&](uint32_t r) { return base + (uint64_t)min(f0 + r, p.F - 1) * p.C; });
+    w[1].set([&](uint32_t r) { return base + (uint64_t)(p.gated ? p.F + min(f0 + r, p.F - 1) : min(f0 + 16 + r, p.F - 1)) * p.C; });
+    for (int i = 0; i < MT; i++) x[i].set([&](uint32_t r) { return (const raw *)p.x + list[min(i * 16 + r, n - 1)] / p.K * p.x_ld; });
     f32x4 acc[MT][2];
     for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
-    stream<D, MT, 2, ALL>(w, x, p.C, wave, WAVES, acc);
+    stream<D, MT, 2, ALL>(w, x, p.C, wave, WAVES, lds + wave * STREAM_LDS<MT, 2>, acc);
     join<MT, 2, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
@@ -135,18 +135,18 @@ __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint3
 
 /* 32 columns of what one expert answers to up to 16 MT of its tokens, in 32 bits */
 template <typename D, int MT, int WAVES, bool ALL = true>
-__device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, f32x4 *lds)
+__device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, char *lds)
 {
     typedef typename D::raw raw;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
     const uint32_t c0 = tile * 32;
-    const raw *w[2], *x[MT];
+    Rows<D> w[2], x[MT];
     const raw *base = (const raw *)p.w_out + (uint64_t)expert * p.C * p.F;
-    for (int j = 0; j < 2; j++) w[j] = base + (uint64_t)min(c0 + j * 16 + l, p.C - 1) * p.F;
-    for (int i = 0; i < MT; i++) x[i] = (const raw *)p.h + (uint64_t)list[min(i * 16 + l, n - 1)] * p.h_ld;
+    for (int j = 0; j < 2; j++) w[j].set([&](uint32_t r) { return base + (uint64_t)min(c0 + j * 16 + r, p.C - 1) * p.F; });
+    for (int i = 0; i < MT; i++) x[i].set([&](uint32_t r) { return (const raw *)p.h + (uint64_t)list[min(i * 16 + r, n - 1)] * p.h_ld; });
     f32x4 acc[MT][2];
     for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
-    stream<D, MT, 2, ALL>(w, x, p.F, wave, WAVES, acc);
+    stream<D, MT, 2, ALL>(w, x, p.F, wave, WAVES, lds + wave * STREAM_LDS<MT, 2>, acc);
     join<MT, 2, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
@@ -170,7 +170,7 @@ template <typename D, int VPL> __global__ void __launch_bounds__(64 * FEW_WAVES)
     __shared__ int32_t chosen[FEW_ROWS * MSIM_MAX_TOP_K];
     __shared__ float shares[FEW_ROWS * MSIM_MAX_TOP_K];
     __shared__ uint32_t list[MAX_ROWS], counts[FEW_WAVES];
-    __shared__ f32x4 sums[FEW_WAVES * 2 * 64];
+    __shared__ __attribute__((aligned(16))) char sums[FEW_WAVES * STREAM_LDS<1, 2>];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = p.rows * p.K;
     r.ids = chosen;
     r.w = shares;
@@ -200,7 +200,7 @@ template <typename D, int VPL> __global__ void __launch_bounds__(64 * FEW_WAVES)
 template <typename D> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_layer_down_few(LayerP p)
 {
     typedef typename D::raw raw;
-    __shared__ f32x4 sums[FEW_WAVES * 2 * 64];
+    __shared__ __attribute__((aligned(16))) char sums[FEW_WAVES * STREAM_LDS<1, 2>];
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15;
     const uint32_t t = blockIdx.x / p.tiles, c0 = blockIdx.x % p.tiles * 32, runs = (p.F + RUN<D> - 1) / RUN<D>;
     /* lane k has choice k; the residual is asked for now */
@@ -219,10 +219,11 @@ template <typename D> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_lay
         const int32_t expert = __builtin_amdgcn_readlane(id, k);
         if (expert < 0) continue;
         const raw *base = (const raw *)p.w_out + (uint64_t)expert * p.C * p.F;
-        const raw *w[2] = {base + (uint64_t)min(c0 + l, p.C - 1) * p.F, base + (uint64_t)min(c0 + 16 + l, p.C - 1) * p.F};
-        const raw *x[1] = {(const raw *)p.h + (uint64_t)(t * p.K + k) * p.h_ld};
+        Rows<D> w[2], x[1];
+        for (int j = 0; j < 2; j++) w[j].set([&](uint32_t r) { return base + (uint64_t)min(c0 + j * 16 + r, p.C - 1) * p.F; });
+        x[0].set([&](uint32_t) { return (const raw *)p.h + (uint64_t)(t * p.K + k) * p.h_ld; });
         f32x4 acc[1][2] = {};
-        stream_run<D, 1, 2>(w, x, i % runs * RUN<D>, p.F, acc);
+        stream_run<D, 1, 2>(w, x, i % runs * RUN<D>, p.F, sums + wave * STREAM_LDS<1, 2>, acc);
         const float s = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, share), k));
         for (int m = 0; m < 2; m++) y[0][m] += s * acc[0][m];
     }
@@ -265,7 +266,7 @@ __device__ __forceinline__ int32_t expert_of(const LayerP &p, uint32_t run, uint
 template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bounds__(64 * WAVES) msim_layer_product(LayerP p)
 {
     __shared__ uint32_t list[MAX_ROWS], counts[WAVES];
-    __shared__ f32x4 sums[WAVES * MT * 2 * 64];
+    __shared__ __attribute__((aligned(16))) char sums[WAVES * STREAM_LDS<MT, 2>];
     constexpr bool ALL = MT <= 2;
     const uint32_t run = blockIdx.x / p.tiles, tile = blockIdx.x - run * p.tiles;
     uint32_t own = 0;
@@ -354,8 +355,9 @@ template <typename D, bool DOWN> hipError_t launch_product(LayerP p, uint64_t ti
     p.tiles = (uint32_t)tiles;
     /* a run for each expert that may be chosen, and one more for every 16 mt assignments */
     const uint32_t grid = (p.slots + (p.rows <= 16 * mt ? 0 : p.rows * p.K / (16 * mt))) * p.tiles;
-    /* few workgroups: more wavefronts in each */
-    if (grid < 1024) {
+    /* few workgroups and long rows: more wavefronts in each (32 x 2,048, 768 hidden units, 2 of 16 experts bf16 52.8 ->
+     * 47.2 us; rows of up to 8 runs 24 x 1,000, 520, 3 of 24 f16 34.7, with more 39.5) */
+    if (grid < 1024 && ((DOWN ? p.F : p.C) + RUN<D> - 1) / RUN<D> > 8) {
         if (mt == 1) return launch(msim_layer_product<D, 1, 16, DOWN>, grid, 1024, 0, st, p);
         if (mt == 2) return launch(msim_layer_product<D, 2, 8, DOWN>, grid, 512, 0, st, p);
         return launch(msim_layer_product<D, 4, 8, DOWN>, grid, 512, 0, st, p);

@@ -27,15 +27,16 @@ template <int MODE, int MT, int WAVES> __global__ void __launch_bounds__(64 * WA
 {
     typedef typename Type<MODE>::D D;
     typedef typename D::raw raw;
-    __shared__ f32x4 sums[WAVES * MT * 64];
+    __shared__ __attribute__((aligned(16))) char lds[WAVES * STREAM_LDS<MT, 1>];
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = lane & 15;
     const uint32_t n0 = blockIdx.x * 16;
-    const raw *w[1] = {(const raw *)p.w + min(n0 + l, p.e.N - 1) * p.w_ld}, *x[MT];
-    for (int i = 0; i < MT; i++) x[i] = (const raw *)p.x + min(i * 16 + l, p.e.M - 1) * p.x_ld;
+    Rows<D> w[1], x[MT];
+    w[0].set([&](uint32_t r) { return (const raw *)p.w + min(n0 + r, p.e.N - 1) * p.w_ld; });
+    for (int i = 0; i < MT; i++) x[i].set([&](uint32_t r) { return (const raw *)p.x + min(i * 16 + r, p.e.M - 1) * p.x_ld; });
     f32x4 acc[MT][1];
     for (int i = 0; i < MT; i++) acc[i][0] = f32x4{0, 0, 0, 0};
-    stream<D, MT, 1>(w, x, p.K, wave, WAVES, acc);
-    join<MT, 1, WAVES>(sums, wave, acc);
+    stream<D, MT, 1>(w, x, p.K, wave, WAVES, lds + wave * STREAM_LDS<MT, 1>, acc);
+    join<MT, 1, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         const uint32_t m = i * 16 + l, n = n0 + (lane >> 4) * 4, have = n < p.e.N ? min(4u, p.e.N - n) : 0;
         if (i % WAVES != (int)wave || m >= p.e.M) continue;

@@ -1,11 +1,13 @@
 /* Products of a weight matrix with a few vectors: the weights are read once, from
- * memory to registers, and nothing of them passes through LDS.
+ * memory to registers.
  *
- * A wavefront has 16 rows of weights (NT times) and 16 vectors (MT times).  Lane l
- * reads 16 bytes of row (or vector) l % 16 at every fourth 16 bytes of k, which is
- * a matrix instruction's operand as it lies; the order of k is the same for both.
- * Wavefronts of a workgroup take runs of 256 bytes of k in turn, so that every
- * cache line is read by one of them, and join their sums in LDS.
+ * A wavefront has 16 rows of weights (NT times) and 16 vectors (MT times), and takes
+ * 256 bytes of k at a time.  A matrix instruction wants 16 bytes of row l % 16 in
+ * lane l, but loads of neighbouring lanes in different rows are a cache access for
+ * each lane (53 counted for a load of 64 lanes, which bounded these products); so 16
+ * lanes read a row's 256 bytes, and four such loads are exchanged among the lanes
+ * through LDS.  The order of k is the same for weights and vectors.  Wavefronts of
+ * a workgroup take runs of k in turn and join their sums in LDS.
  */
 #ifndef MSIM_STREAM_H
 #define MSIM_STREAM_H
@@ -61,71 +63,117 @@ template <typename D> __device__ __forceinline__ u32x4 piece(const typename D::r
 /* elements of k that a wavefront takes at a time */
 template <typename D> constexpr uint32_t RUN = 256 / sizeof(typename D::raw);
 
-/* acc[i][j] += over N runs of k, at k, k + step, ..., all within K: weight rows
- * w[j], vectors x[i], both those of lane % 16.  ALL: all loads are asked for before the
- * first is used, which the compiler would not do by itself (32 tokens of 7,168
- * columns, 8 of 128 experts 1,430 -> 1,286 us); where there are so many of them that
- * their registers cost wavefronts, it is left to it. */
-template <typename D, int MT, int NT, int N, bool ALL>
-__device__ __forceinline__ void stream_whole(const typename D::raw *const *w, const typename D::raw *const *x, uint32_t k, uint32_t step,
-                                             f32x4 (&acc)[MT][NT])
-{
-    constexpr uint32_t PER = 16 / sizeof(typename D::raw), U = 4;
-    const uint32_t q = (threadIdx.x & 63) >> 4;
-    u32x4 a[N * U][NT], b[N * U][MT];
-    _Pragma("unroll") for (uint32_t u = 0; u < N * U; u++) {
-        const uint32_t at = k + u / U * step + (u % U * 4 + q) * PER;
-        _Pragma("unroll") for (int j = 0; j < NT; j++) a[u][j] = piece<D>(w[j] + at);
-        _Pragma("unroll") for (int i = 0; i < MT; i++) b[u][i] = piece<D>(x[i] + at);
+/* Of a block of 16 rows, those that a lane reads: row 4 u + lane / 16. */
+template <typename D> struct Rows {
+    const typename D::raw *at[4];
+    /* row(r): where row r of the block begins */
+    template <typename F> __device__ __forceinline__ void set(F row)
+    {
+        for (uint32_t u = 0; u < 4; u++) at[u] = row(4 * u + ((threadIdx.x & 63) >> 4));
     }
-    if constexpr (ALL) __builtin_amdgcn_sched_barrier(0);
-    _Pragma("unroll") for (uint32_t u = 0; u < N * U; u++)
-        _Pragma("unroll") for (int i = 0; i < MT; i++)
-            _Pragma("unroll") for (int j = 0; j < NT; j++) acc[i][j] = mma16<D>(a[u][j], b[u][i], acc[i][j]);
+};
+
+/* LDS of a wavefront: what its lanes exchange, and then its sums for join() */
+template <int MT, int NT> constexpr uint32_t STREAM_LDS = (MT * NT < 4 ? 4 : MT * NT) * 1024;
+
+/* v[u] is piece lane % 16 of row 4 u + lane / 16; then piece 4 u + lane / 16 of row
+ * lane % 16.  In LDS the pieces of a row are exchanged by the row, so that 16 lanes
+ * cover all banks both ways. */
+__device__ __forceinline__ void exchange(char *lds, u32x4 (&v)[4])
+{
+    const uint32_t lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+    for (uint32_t u = 0; u < 4; u++) *(u32x4 *)(lds + u * 1024 + g * 256 + ((l ^ g) ^ u * 4) * 16) = v[u];
+    wave_sync();
+    for (uint32_t u = 0; u < 4; u++) v[u] = *(const u32x4 *)(lds + l * 256 + ((l ^ g) ^ u * 4) * 16);
+    wave_sync();
+}
+
+/* What 16 bytes that were read `early` elements too early have from their place on, and zeros. */
+template <typename D> __device__ __forceinline__ u32x4 behind(u32x4 v, uint32_t early)
+{
+    const unsigned __int128 q = __builtin_bit_cast(unsigned __int128, v);
+    const uint32_t bits = early * sizeof(typename D::raw) * 8;
+    return __builtin_bit_cast(u32x4, bits < 128 ? q >> bits : 0);
+}
+
+/* acc[i][j] += over N runs of k, at k, k + step, ...: weights w[j], vectors x[i].
+ * WHOLE: all within K; otherwise N is 1, and 16 bytes that would pass the end of a
+ * row are read before it (rows shorter than that, element by element).  ALL: all
+ * loads are asked for before the first is used, which the compiler would not do by
+ * itself; where there are so many of them that their registers cost wavefronts,
+ * it is left to it. */
+template <typename D, int MT, int NT, int N, bool ALL, bool WHOLE>
+__device__ __forceinline__ void stream_runs(const Rows<D> *w, const Rows<D> *x, uint32_t k, uint32_t step, uint32_t K, char *lds, f32x4 (&acc)[MT][NT])
+{
+    constexpr uint32_t PER = 16 / sizeof(typename D::raw);
+    const uint32_t c = k + (threadIdx.x & 15) * PER, last = K >= PER ? K - PER : 0, at = WHOLE ? c : min(c, last), early = c - at;
+    u32x4 a[N][NT][4], b[N][MT][4];
+    if (WHOLE || K >= PER) {
+        _Pragma("unroll") for (int n = 0; n < N; n++) {
+            _Pragma("unroll") for (int j = 0; j < NT; j++)
+                _Pragma("unroll") for (int u = 0; u < 4; u++) a[n][j][u] = piece<D>(w[j].at[u] + at + n * step);
+            _Pragma("unroll") for (int i = 0; i < MT; i++)
+                _Pragma("unroll") for (int u = 0; u < 4; u++) b[n][i][u] = piece<D>(x[i].at[u] + at + n * step);
+        }
+        if constexpr (ALL) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!WHOLE) {
+            const bool cut = K % PER;          /* a piece has both elements and none */
+            const auto there = [&](u32x4 &v) { v = cut ? behind<D>(v, early) : early ? u32x4{0, 0, 0, 0} : v; };
+            _Pragma("unroll") for (int j = 0; j < NT; j++)
+                _Pragma("unroll") for (int u = 0; u < 4; u++) there(a[0][j][u]);
+            _Pragma("unroll") for (int i = 0; i < MT; i++)
+                _Pragma("unroll") for (int u = 0; u < 4; u++) there(b[0][i][u]);
+        }
+    } else {
+        for (int j = 0; j < NT; j++)
+            for (int u = 0; u < 4; u++) a[0][j][u] = piece<D>(w[j].at[u], c, K);
+        for (int i = 0; i < MT; i++)
+            for (int u = 0; u < 4; u++) b[0][i][u] = piece<D>(x[i].at[u], c, K);
+    }
+    _Pragma("unroll") for (int n = 0; n < N; n++) {
+        _Pragma("unroll") for (int j = 0; j < NT; j++) exchange(lds, a[n][j]);
+        _Pragma("unroll") for (int i = 0; i < MT; i++) {
+            exchange(lds, b[n][i]);
+            _Pragma("unroll") for (int j = 0; j < NT; j++)
+                _Pragma("unroll") for (int u = 0; u < 4; u++) acc[i][j] = mma16<D>(a[n][j][u], b[n][i][u], acc[i][j]);
+        }
+    }
 }
 
 /* one run, or what there is of it */
 template <typename D, int MT, int NT, bool ALL = true>
-__device__ __forceinline__ void stream_run(const typename D::raw *const *w, const typename D::raw *const *x, uint32_t k, uint32_t K,
-                                           f32x4 (&acc)[MT][NT])
+__device__ __forceinline__ void stream_run(const Rows<D> *w, const Rows<D> *x, uint32_t k, uint32_t K, char *lds, f32x4 (&acc)[MT][NT])
 {
-    constexpr uint32_t PER = 16 / sizeof(typename D::raw);
-    const uint32_t q = (threadIdx.x & 63) >> 4;
-    if (k + RUN<D> <= K) return stream_whole<D, MT, NT, 1, ALL>(w, x, k, 0, acc);
-    for (; k < K; k += 4 * PER) {
-        u32x4 a[NT], b[MT];
-        _Pragma("unroll") for (int j = 0; j < NT; j++) a[j] = piece<D>(w[j], k + q * PER, K);
-        _Pragma("unroll") for (int i = 0; i < MT; i++) b[i] = piece<D>(x[i], k + q * PER, K);
-        _Pragma("unroll") for (int i = 0; i < MT; i++)
-            _Pragma("unroll") for (int j = 0; j < NT; j++) acc[i][j] = mma16<D>(a[j], b[i], acc[i][j]);
-    }
+    if (k + RUN<D> <= K) stream_runs<D, MT, NT, 1, ALL, true>(w, x, k, 0, K, lds, acc);
+    else stream_runs<D, MT, NT, 1, ALL, false>(w, x, k, 0, K, lds, acc);
 }
 
 /* the wavefront's share of k, every waves-th run: of few vectors two at a time, whose loads fit its registers */
 template <typename D, int MT, int NT, bool ALL = true>
-__device__ __forceinline__ void stream(const typename D::raw *const *w, const typename D::raw *const *x, uint32_t K,
-                                       uint32_t wave, uint32_t waves, f32x4 (&acc)[MT][NT])
+__device__ __forceinline__ void stream(const Rows<D> *w, const Rows<D> *x, uint32_t K, uint32_t wave, uint32_t waves, char *lds, f32x4 (&acc)[MT][NT])
 {
     uint32_t k = wave * RUN<D>;
     const uint32_t step = waves * RUN<D>;
     if constexpr (MT + NT <= 3)
-        for (; k + step + RUN<D> <= K; k += 2 * step) stream_whole<D, MT, NT, 2, ALL>(w, x, k, step, acc);
-    for (; k < K; k += step) stream_run<D, MT, NT, ALL>(w, x, k, K, acc);
+        for (; k + step + RUN<D> <= K; k += 2 * step) stream_runs<D, MT, NT, 2, ALL, true>(w, x, k, step, K, lds, acc);
+    for (; k < K; k += step) stream_run<D, MT, NT, ALL>(w, x, k, K, lds, acc);
 }
 
-/* The wavefronts' sums together, in order.  lds: waves x MT x NT x 64 pieces.
- * Afterwards wavefront i has acc[i][...] whole, i < MT (in turns of waves). */
-template <int MT, int NT, int WAVES> __device__ __forceinline__ void join(f32x4 *lds, uint32_t wave, f32x4 (&acc)[MT][NT])
+/* The wavefronts' sums together, in order.  lds: STREAM_LDS<MT, NT> each, of which
+ * a wavefront writes its own alone.  Afterwards wavefront i has acc[i][...] whole,
+ * i < MT (in turns of waves). */
+template <int MT, int NT, int WAVES> __device__ __forceinline__ void join(char *lds, uint32_t wave, f32x4 (&acc)[MT][NT])
 {
     const uint32_t lane = threadIdx.x & 63;
+    const auto at = [&](uint32_t v, int i, int j) { return (f32x4 *)(lds + v * STREAM_LDS<MT, NT>) + (i * NT + j) * 64 + lane; };
     _Pragma("unroll") for (int i = 0; i < MT; i++)
-        _Pragma("unroll") for (int j = 0; j < NT; j++) lds[((wave * MT + i) * NT + j) * 64 + lane] = acc[i][j];
+        _Pragma("unroll") for (int j = 0; j < NT; j++) *at(wave, i, j) = acc[i][j];
     __syncthreads();
     _Pragma("unroll") for (int i = 0; i < MT; i++)
         if (i % WAVES == (int)wave)
             _Pragma("unroll") for (int j = 0; j < NT; j++) {
-                f32x4 s = lds[(i * NT + j) * 64 + lane];
-                for (int v = 1; v < WAVES; v++) s += lds[((v * MT + i) * NT + j) * 64 + lane];
+                f32x4 s = *at(0, i, j);
+                for (int v = 1; v < WAVES; v++) s += *at(v, i, j);
                 acc[i][j] = s;
             }
 }
