@@ -15,7 +15,8 @@ namespace {
 /* ------------------------------------------------------------------------ */
 
 /* A linear layer of up to 16 MT rows: 16 outs a workgroup, whose wavefronts
- * share k.  The weights are read once, from where they lie on any element. */
+ * share k.  The weights are read once, from where they lie on any element.  A small
+ * one is as long as a launch; 16 x 4,096 -> 4,096 bf16 takes 9.5 us, 3.5 TB/s. */
 struct FewP {
     const void *x, *w;
     uint64_t x_ld, w_ld;
@@ -237,14 +238,17 @@ const char *check_linear(const msim_linear_spec *s, int *code)
     return nullptr;
 }
 
-/* Few rows are streamed while that is faster than tiles: 16 x 4,096 -> 4,096 bf16 10.0
- * us (12.2 in tiles), -> 16,384 31 (21); 24 x 1,000 -> 1,000 5.2 (6.7), 64 rows of
- * them 6.5 (6.8), 40 x 4,096 -> 4,096 16.4 (11.7).  A workgroup's 16 wavefronts take
- * 4 KiB of k at a time, so long rows want several workgroups: tiles of parts of k. */
+/* Few rows are streamed while that is faster than tiles, in the stream of calls: up to
+ * 16 of them 16 x 4,096 -> 4,096 bf16 9.5 us (14.0 in tiles, which is two launches),
+ * -> 16,384 33.7 (22.0), 16 x 20,000 -> 256 16.4 (14.1); up to 64 64 x 2,048 -> 4,096 10.5
+ * (11.0), 64 x 2,001 -> 2,001 f16 10.3 (17.8), 32 x 4,096 -> 4,096 19.1 (14.0), 64 x 2,048
+ * -> 512 f32 15.9 (14.5).  A workgroup's 16 wavefronts take 4 KiB of k at a time, so long
+ * rows want several workgroups: tiles of parts of k. */
 bool few_rows(const msim_linear_spec *s)
 {
-    if (s->rows <= MSIM_LINEAR_FEW && s->outs <= MSIM_LINEAR_FEW_OUTS) return s->cols * (uint64_t)size_of(s->dtype) <= 16384;
-    return s->rows <= 64 && s->cols <= 4096 && (uint64_t)s->cols * s->outs <= 1u << 20;
+    const uint64_t size = size_of(s->dtype);
+    if (s->rows <= MSIM_LINEAR_FEW && s->outs <= MSIM_LINEAR_FEW_OUTS) return s->cols * size <= 16384;
+    return s->rows <= 64 && s->cols <= (size == 4 ? 1024 : 4096) && s->cols * size * s->outs <= 1u << 24;
 }
 
 struct Forward {
