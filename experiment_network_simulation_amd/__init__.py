@@ -3,8 +3,9 @@
 Thousands of independent experiments -- collective-communication traffic over
 switched topologies -- simulated tick by tick in one HIP megakernel behind the
 C ABI of include/msim.h.  `inputs` builds seeded synthetic batches; `sim.Sim`
-is the thin binding over libmsim.so; `moe` routes tokens to experts on the GPU
-and counts the all-to-all traffic they cause.
+is the thin binding over libmsim.so; `moe` routes tokens to experts on the GPU,
+counts the all-to-all traffic they cause, and has the products of the gate and the
+experts around it.
 """
 
 from . import inputs  # noqa: F401

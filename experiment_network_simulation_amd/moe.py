@@ -1,6 +1,9 @@
-"""Expert-parallel routing on the GPU: from gate logits to all-to-all traffic.
+"""Expert-parallel routing on the GPU: from gate logits to all-to-all traffic, and
+the products around the router: the gate's, its gradient and update, and a whole
+layer for a few tokens.
 
-Thin binding of msim_route, msim_route_backward, msim_dropout and msim_traffic
+Thin binding of msim_route, msim_route_backward, msim_dropout, msim_traffic,
+msim_linear, msim_linear_backward, msim_layer and msim_orthogonalize
 (include/msim.h has the definitions): argument checks and marshalling only,
 every value is computed by the HIP library.
 
@@ -9,6 +12,13 @@ every value is computed by the HIP library.
     pkts = traffic(r.ids, token_off, home, place, hosts, token_bytes=14336, pkt_bytes=4096,
                    drop=0.1, seed=seed)                # the same assignments, drawn again
     work = inputs.traffic_flows(pkts.cpu().numpy())    # explicit flows of an experiment
+
+    logits = linear(x, gate, out_dtype=torch.float32)  # a training step of the gate
+    r = route(logits, 8, score="sigmoid")
+    d = route_backward(logits, r.ids, grad_weights, score="sigmoid")
+    step = orthogonalize(linear_backward(x, gate, d).weight)
+
+    y = layer(x, gate, w_in, w_out, 8, residual=x).y   # gate, router and experts of a decoding batch
 
 All tensors are on one GPU, whichever is current.  A call enqueues on `stream`
 (a torch stream or a raw handle; default: the current stream of the tensors'

@@ -396,7 +396,9 @@ int msim_get_info(const msim_ctx *ctx, msim_info *info);
 
 /* Message of the last error on this context (or, for ctx == NULL, of the last
  * failed call without a context on the calling thread: msim_create,
- * msim_route, msim_route_backward, msim_dropout, msim_traffic). */
+ * msim_route, msim_route_backward, msim_dropout, msim_traffic, msim_linear,
+ * msim_linear_backward, msim_layer, msim_orthogonalize and the calls that ask for
+ * their workspaces). */
 const char *msim_last_error(const msim_ctx *ctx);
 
 /* Frees host-side state; the workspace stays the caller's. */
