@@ -112,7 +112,7 @@ template <typename D> __device__ __forceinline__ void hidden_of(const LayerP &p,
 
 /* h = act(gate rows x) (up rows x), or act(rows x): 16 hidden units (32 without a
  * gate) of one expert for up to 16 MT of its tokens */
-template <typename D, int MT, int WAVES, bool ALL = true>
+template <typename D, int MT, int WAVES>
 __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, char *lds)
 {
     typedef typename D::raw raw;
@@ -125,7 +125,7 @@ __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint3
     for (int i = 0; i < MT; i++) x[i].set([&](uint32_t r) { return (const raw *)p.x + list[min(i * 16 + r, n - 1)] / p.K * p.x_ld; });
     f32x4 acc[MT][2];
     for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
-    stream<D, MT, 2, ALL>(w, x, p.C, wave, WAVES, lds + wave * STREAM_LDS<MT, 2>, acc);
+    stream<D, MT, 2, WAVES>(w, x, p.C, wave, lds + wave * STREAM_LDS<MT, 2>, acc);
     join<MT, 2, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
@@ -134,7 +134,7 @@ __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint3
 }
 
 /* 32 columns of what one expert answers to up to 16 MT of its tokens, in 32 bits */
-template <typename D, int MT, int WAVES, bool ALL = true>
+template <typename D, int MT, int WAVES>
 __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, char *lds)
 {
     typedef typename D::raw raw;
@@ -146,7 +146,7 @@ __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uin
     for (int i = 0; i < MT; i++) x[i].set([&](uint32_t r) { return (const raw *)p.h + (uint64_t)list[min(i * 16 + r, n - 1)] * p.h_ld; });
     f32x4 acc[MT][2];
     for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
-    stream<D, MT, 2, ALL>(w, x, p.F, wave, WAVES, lds + wave * STREAM_LDS<MT, 2>, acc);
+    stream<D, MT, 2, WAVES>(w, x, p.F, wave, lds + wave * STREAM_LDS<MT, 2>, acc);
     join<MT, 2, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
@@ -261,13 +261,12 @@ __device__ __forceinline__ int32_t expert_of(const LayerP &p, uint32_t run, uint
     return -1;
 }
 
-/* MT: tokens of a run, in 16; fewer take leaner code.  WAVES: k is shared among them.  Runs of four 16 are so
- * many loads that all of them ahead cost more wavefronts than they hide (512 x 2,048, 6 of 64 experts 549 -> 880 us). */
-template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bounds__(64 * WAVES) msim_layer_product(LayerP p)
+/* MT: tokens of a run, in 16; fewer take leaner code.  WAVES: k is shared among them.  Bound by reading the
+ * weights: 32 x 7,168, 8 of 128 experts bf16 takes 7.7 GB in 790 + 396 us, 6.4 TB/s. */
+template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bounds__(64 * WAVES, MT <= 2 ? 3 : 2) msim_layer_product(LayerP p)
 {
     __shared__ uint32_t list[MAX_ROWS], counts[WAVES];
     __shared__ __attribute__((aligned(16))) char sums[WAVES * STREAM_LDS<MT, 2>];
-    constexpr bool ALL = MT <= 2;
     const uint32_t run = blockIdx.x / p.tiles, tile = blockIdx.x - run * p.tiles;
     uint32_t own = 0;
     const int32_t expert = p.rows > 16 * MT ? expert_of(p, run, 16 * MT, own) : p.slots < p.E ? p.ids[run] : p.load[run] ? (int32_t)run : -1;
@@ -276,8 +275,8 @@ template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bou
     if (first >= all || (p.rows <= 16 * MT && p.slots < p.E && list[0] != run)) return;
     const uint32_t n = min(all - first, 16u * MT);
     const auto part = [&](auto mt) {
-        if constexpr (DOWN) down_tokens<D, mt.value, WAVES, ALL>(p, expert, tile, list + first, n, sums);
-        else up_tokens<D, mt.value, WAVES, ALL>(p, expert, tile, list + first, n, sums);
+        if constexpr (DOWN) down_tokens<D, mt.value, WAVES>(p, expert, tile, list + first, n, sums);
+        else up_tokens<D, mt.value, WAVES>(p, expert, tile, list + first, n, sums);
     };
     if (n <= 16) part(std::integral_constant<int, 1>());
     else if (MT > 2 && n <= 32) part(std::integral_constant<int, 2>());
@@ -351,7 +350,10 @@ const char *check_layer(const msim_layer_spec *s, int *code)
 
 template <typename D, bool DOWN> hipError_t launch_product(LayerP p, uint64_t tiles, hipStream_t st)
 {
-    const uint32_t mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+    /* runs of up to 64 tokens read an expert's weights once more seldom, those of 32 leave room for half as many wavefronts
+     * again: 200 x 2,048, 6 of 64 experts bf16 (19 tokens each) 289 us in runs of 64, 271 of 32, with 512 rows (48) 424 and
+     * 442; 400 x 7,168, 8 of 128 (25) 2,490 and 2,580 */
+    const uint32_t mt = p.rows <= 16 ? 1 : p.rows <= 32 || p.rows * p.K <= 24 * p.E ? 2 : 4;
     p.tiles = (uint32_t)tiles;
     /* a run for each expert that may be chosen, and one more for every 16 mt assignments */
     const uint32_t grid = (p.slots + (p.rows <= 16 * mt ? 0 : p.rows * p.K / (16 * mt))) * p.tiles;

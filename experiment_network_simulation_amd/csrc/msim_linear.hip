@@ -36,7 +36,7 @@ template <int MODE, int MT, int WAVES> __global__ void __launch_bounds__(64 * WA
     for (int i = 0; i < MT; i++) x[i].set([&](uint32_t r) { return (const raw *)p.x + min(i * 16 + r, p.e.M - 1) * p.x_ld; });
     f32x4 acc[MT][1];
     for (int i = 0; i < MT; i++) acc[i][0] = f32x4{0, 0, 0, 0};
-    stream<D, MT, 1>(w, x, p.K, wave, WAVES, lds + wave * STREAM_LDS<MT, 1>, acc);
+    stream<D, MT, 1, WAVES>(w, x, p.K, wave, lds + wave * STREAM_LDS<MT, 1>, acc);
     join<MT, 1, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
         const uint32_t m = i * 16 + l, n = n0 + (lane >> 4) * 4, have = n < p.e.N ? min(4u, p.e.N - n) : 0;

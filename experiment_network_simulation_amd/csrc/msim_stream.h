@@ -4,9 +4,9 @@
  * A wavefront has 16 rows of weights (NT times) and 16 vectors (MT times), and takes
  * 256 bytes of k at a time.  A matrix instruction wants 16 bytes of row l % 16 in
  * lane l, but loads of neighbouring lanes in different rows are a cache access for
- * each lane (53 counted for a load of 64 lanes, which bounded these products); so 16
- * lanes read a row's 256 bytes, and four such loads are exchanged among the lanes
- * through LDS.  The order of k is the same for weights and vectors.  Wavefronts of
+ * each lane (53 counted for a load of 64 lanes, which bounded these products: 512 x
+ * 2,048, 6 of 64 experts bf16 525 us, and 424 like this); so 16 lanes read a row's 256
+ * bytes, and four such loads are exchanged among the lanes through LDS.  The order of k is the same for weights and vectors.  Wavefronts of
  * a workgroup take runs of k in turn and join their sums in LDS.
  */
 #ifndef MSIM_STREAM_H
@@ -96,67 +96,70 @@ template <typename D> __device__ __forceinline__ u32x4 behind(u32x4 v, uint32_t 
     return __builtin_bit_cast(u32x4, bits < 128 ? q >> bits : 0);
 }
 
+enum { WHOLE, END, SHORT };
 /* acc[i][j] += over N runs of k, at k, k + step, ...: weights w[j], vectors x[i].
- * WHOLE: all within K; otherwise N is 1, and 16 bytes that would pass the end of a
- * row are read before it (rows shorter than that, element by element).  ALL: all
- * loads are asked for before the first is used, which the compiler would not do by
- * itself; where there are so many of them that their registers cost wavefronts,
- * it is left to it. */
-template <typename D, int MT, int NT, int N, bool ALL, bool WHOLE>
+ * WHOLE: all within K.  END: one that is not; 16 bytes that would pass the end of a
+ * row are read before it.  SHORT: of rows of less than 16 bytes, by elements.
+ *
+ * The loads of weights and of the first two blocks of vectors are all asked for before
+ * the first is used, which the compiler would not do by itself (32 tokens of 7,168
+ * columns, 8 of 128 experts 1,430 -> 1,286 us); those of further vectors when a block before
+ * them has been used, in its registers. */
+template <typename D, int MT, int NT, int N, int WHERE>
 __device__ __forceinline__ void stream_runs(const Rows<D> *w, const Rows<D> *x, uint32_t k, uint32_t step, uint32_t K, char *lds, f32x4 (&acc)[MT][NT])
 {
     constexpr uint32_t PER = 16 / sizeof(typename D::raw);
-    const uint32_t c = k + (threadIdx.x & 15) * PER, last = K >= PER ? K - PER : 0, at = WHOLE ? c : min(c, last), early = c - at;
-    u32x4 a[N][NT][4], b[N][MT][4];
-    if (WHOLE || K >= PER) {
-        _Pragma("unroll") for (int n = 0; n < N; n++) {
-            _Pragma("unroll") for (int j = 0; j < NT; j++)
-                _Pragma("unroll") for (int u = 0; u < 4; u++) a[n][j][u] = piece<D>(w[j].at[u] + at + n * step);
-            _Pragma("unroll") for (int i = 0; i < MT; i++)
-                _Pragma("unroll") for (int u = 0; u < 4; u++) b[n][i][u] = piece<D>(x[i].at[u] + at + n * step);
+    constexpr int AHEAD = MT < 2 ? MT : 2;
+    const uint32_t c = k + (threadIdx.x & 15) * PER, at = WHERE == END ? min(c, K - PER) : c, early = c - at;
+    const bool cut = K % PER;                  /* a piece has both elements and none */
+    u32x4 a[N][NT][4], b[N][AHEAD][4];
+    const auto load = [&](const Rows<D> &r, int n, u32x4 (&v)[4]) {
+        _Pragma("unroll") for (int u = 0; u < 4; u++) {
+            if constexpr (WHERE == SHORT) v[u] = piece<D>(r.at[u], c, K);
+            else v[u] = piece<D>(r.at[u] + at + n * step);
         }
-        if constexpr (ALL) __builtin_amdgcn_sched_barrier(0);
-        if constexpr (!WHOLE) {
-            const bool cut = K % PER;          /* a piece has both elements and none */
-            const auto there = [&](u32x4 &v) { v = cut ? behind<D>(v, early) : early ? u32x4{0, 0, 0, 0} : v; };
-            _Pragma("unroll") for (int j = 0; j < NT; j++)
-                _Pragma("unroll") for (int u = 0; u < 4; u++) there(a[0][j][u]);
-            _Pragma("unroll") for (int i = 0; i < MT; i++)
-                _Pragma("unroll") for (int u = 0; u < 4; u++) there(b[0][i][u]);
-        }
-    } else {
-        for (int j = 0; j < NT; j++)
-            for (int u = 0; u < 4; u++) a[0][j][u] = piece<D>(w[j].at[u], c, K);
-        for (int i = 0; i < MT; i++)
-            for (int u = 0; u < 4; u++) b[0][i][u] = piece<D>(x[i].at[u], c, K);
-    }
+    };
+    const auto give = [&](u32x4 (&v)[4]) {
+        if constexpr (WHERE == END)
+            _Pragma("unroll") for (int u = 0; u < 4; u++) v[u] = cut ? behind<D>(v[u], early) : early ? u32x4{0, 0, 0, 0} : v[u];
+        exchange(lds, v);
+    };
     _Pragma("unroll") for (int n = 0; n < N; n++) {
-        _Pragma("unroll") for (int j = 0; j < NT; j++) exchange(lds, a[n][j]);
+        _Pragma("unroll") for (int j = 0; j < NT; j++) load(w[j], n, a[n][j]);
+        _Pragma("unroll") for (int i = 0; i < AHEAD; i++) load(x[i], n, b[n][i]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    _Pragma("unroll") for (int n = 0; n < N; n++) {
+        _Pragma("unroll") for (int j = 0; j < NT; j++) give(a[n][j]);
         _Pragma("unroll") for (int i = 0; i < MT; i++) {
-            exchange(lds, b[n][i]);
+            auto &v = b[n][i % AHEAD];
+            give(v);
             _Pragma("unroll") for (int j = 0; j < NT; j++)
-                _Pragma("unroll") for (int u = 0; u < 4; u++) acc[i][j] = mma16<D>(a[n][j][u], b[n][i][u], acc[i][j]);
+                _Pragma("unroll") for (int u = 0; u < 4; u++) acc[i][j] = mma16<D>(a[n][j][u], v[u], acc[i][j]);
+            if (i + AHEAD < MT) load(x[i + AHEAD], n, v);
+            if (MT > AHEAD) __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
 
 /* one run, or what there is of it */
-template <typename D, int MT, int NT, bool ALL = true>
+template <typename D, int MT, int NT>
 __device__ __forceinline__ void stream_run(const Rows<D> *w, const Rows<D> *x, uint32_t k, uint32_t K, char *lds, f32x4 (&acc)[MT][NT])
 {
-    if (k + RUN<D> <= K) stream_runs<D, MT, NT, 1, ALL, true>(w, x, k, 0, K, lds, acc);
-    else stream_runs<D, MT, NT, 1, ALL, false>(w, x, k, 0, K, lds, acc);
+    if (k + RUN<D> <= K) stream_runs<D, MT, NT, 1, WHOLE>(w, x, k, 0, K, lds, acc);
+    else if (K * sizeof(typename D::raw) >= 16) stream_runs<D, MT, NT, 1, END>(w, x, k, 0, K, lds, acc);
+    else stream_runs<D, MT, NT, 1, SHORT>(w, x, k, 0, K, lds, acc);
 }
 
-/* the wavefront's share of k, every waves-th run: of few vectors two at a time, whose loads fit its registers */
-template <typename D, int MT, int NT, bool ALL = true>
-__device__ __forceinline__ void stream(const Rows<D> *w, const Rows<D> *x, uint32_t K, uint32_t wave, uint32_t waves, char *lds, f32x4 (&acc)[MT][NT])
+/* the wavefront's share of k, every WAVES-th run: of few vectors two at a time, where their loads fit its registers */
+template <typename D, int MT, int NT, int WAVES>
+__device__ __forceinline__ void stream(const Rows<D> *w, const Rows<D> *x, uint32_t K, uint32_t wave, char *lds, f32x4 (&acc)[MT][NT])
 {
     uint32_t k = wave * RUN<D>;
-    const uint32_t step = waves * RUN<D>;
-    if constexpr (MT + NT <= 3)
-        for (; k + step + RUN<D> <= K; k += 2 * step) stream_runs<D, MT, NT, 2, ALL, true>(w, x, k, step, K, lds, acc);
-    for (; k < K; k += step) stream_run<D, MT, NT, ALL>(w, x, k, K, lds, acc);
+    const uint32_t step = WAVES * RUN<D>;
+    if constexpr (MT + NT <= 3 && WAVES < 16)
+        for (; k + step + RUN<D> <= K; k += 2 * step) stream_runs<D, MT, NT, 2, WHOLE>(w, x, k, step, K, lds, acc);
+    for (; k < K; k += step) stream_run<D, MT, NT>(w, x, k, K, lds, acc);
 }
 
 /* The wavefronts' sums together, in order.  lds: STREAM_LDS<MT, NT> each, of which
