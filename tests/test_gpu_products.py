@@ -349,6 +349,34 @@ def test_layer_of_many_experts(T, M, rows, experts, groups, top_groups):
         check_layer(T, M, "f16", args, 8, dict(how, groups=groups, top_groups=top_groups), "silu", True, None, args[0])
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [65, 193, 512])
+def test_layer_of_crowded_experts(T, M, types, rows, dt):
+    """A bias sends every token to one expert and most to another, so that experts have many runs of tokens, others none; with
+    padding in between; the counts in the caller's array or in none."""
+    args = layer_of(T, rows, types[dt], rows, 72, 40, 12)
+    g = args[4]
+    mask = T.rand(rows, device=DEV, generator=g) < 0.9
+    args[0][~mask] = math.nan
+    bias = T.zeros(12, device=DEV)
+    bias[7], bias[2], bias[:2] = 9.0, 0.6, -math.inf
+    how = dict(score="sigmoid", bias=bias)
+    r = check_layer(T, M, dt, args, 3, how, "silu", True, mask, None)
+    assert int(r.routing.load[7]) == int(mask.sum()) and int(r.routing.load[:2].sum()) == 0
+    y = T.empty_like(r.y)
+    M.layer(*args[:4], 3, mask=mask, out=M.Layer(y, r.routing._replace(load=None)), **how)
+    assert T.equal(y, r.y)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_layer_rows_of_any_length(T, M, types, dt):
+    """Weights whose rows end anywhere in 16 and in 256 bytes, and are shorter than that, the last in memory at its end."""
+    for rows, n in ((3, 1), (3, 3), (3, 7), (20, 4), (20, 8), (5, 9), (40, 33), (3, 63), (20, 64), (40, 65), (3, 127), (5, 129), (20, 200), (40, 257)):
+        for cols, hidden in ((n, 24), (24, n)):
+            check_layer(T, M, dt, layer_of(T, n, types[dt], rows, cols, hidden, 6), 2, {}, "silu", True, None, None)
+            check_layer(T, M, dt, layer_of(T, n, types[dt], rows, cols, hidden, 6, False), 2, {}, "relu", False, None, None)
+
+
 def test_layer_reads_no_expert_that_is_not_chosen(T, M):
     for rows in (1, 3, 40):
         args = layer_of(T, 5, T.float16, rows, 64, 48, 16)
