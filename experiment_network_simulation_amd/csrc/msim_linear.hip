@@ -114,40 +114,76 @@ struct GradP {
     uint32_t act, grad32, lglanes, part, blocks;
 };
 
+/* eight elements as they lie, the first n of them there, others zero */
+template <typename D> __device__ __forceinline__ auto raw8(const void *at, uint64_t i, uint32_t n)
+{
+    typedef typename D::raw raw;
+    typedef raw vec __attribute__((ext_vector_type(8)));
+    typedef raw loose __attribute__((ext_vector_type(8), aligned(sizeof(raw))));
+    const raw *q = (const raw *)at + i;
+    if (n == 8) return (vec)*(const loose *)q;
+    vec v = 0;
+    for (uint32_t k = 0; k < 8; k++)
+        if (k < n) v[k] = q[k];
+    return v;
+}
+
+/* The sums of a thread's eight columns (k of them there) over its rows, m and every `step`-th up to end, four of
+ * which are read before the first is used; G: the type of grad. */
+template <typename D, typename G> __device__ __forceinline__ void grad_columns(const GradP &p, uint32_t m, uint32_t step, uint32_t end, uint32_t n, uint32_t k, float *sum)
+{
+    constexpr uint32_t U = 4;
+    for (; m < end; m += U * step) {
+        decltype(raw8<G>(nullptr, 0, 0)) g[U];
+        decltype(raw8<D>(nullptr, 0, 0)) z[U];
+        _Pragma("unroll") for (uint32_t u = 0; u < U; u++) {
+            const uint32_t row = m + u * step, there = row < end ? k : 0;
+            g[u] = raw8<G>(p.grad, row * p.grad_ld + n, there);
+            if (p.act) z[u] = raw8<D>(p.pre, row * p.pre_ld + n, there);
+        }
+        _Pragma("unroll") for (uint32_t u = 0; u < U; u++) {
+            const uint32_t row = m + u * step;
+            if (row >= end) break;
+            float v[8], slope[8];
+            for (uint32_t i = 0; i < 8; i++) v[i] = G::get(g[u][i]);
+            if (p.act) {
+                for (uint32_t i = 0; i < 8; i++) slope[i] = D::get(z[u][i]);
+                slope_of<8>(slope, p.act);
+                for (uint32_t i = 0; i < 8; i++) v[i] = i < k ? v[i] * slope[i] : 0.0f;
+            }
+            for (int i = 0; i < 8; i++) sum[i] += v[i];
+            if (p.d) store8<D>(v, p.d, (uint64_t)row * p.wide + n, 8);
+        }
+    }
+}
+
 template <typename D> __device__ __forceinline__ void grad_rows(const GradP &p, uint32_t block, float *part)
 {
     const uint32_t lanes = 1u << p.lglanes, cols = 8 * lanes;
     const uint32_t across = (p.wide + cols - 1) / cols, by = block / across, bx = block - by * across;
     const uint32_t n = bx * cols + (threadIdx.x & (lanes - 1)) * 8, k = n < p.outs ? min(8u, p.outs - n) : 0;
-    const uint32_t end = min(p.rows, (by + 1) * p.part);
+    const uint32_t first = by * p.part + (threadIdx.x >> p.lglanes), step = 256u >> p.lglanes, end = min(p.rows, (by + 1) * p.part);
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (n < p.wide)
-        for (uint32_t m = by * p.part + (threadIdx.x >> p.lglanes); m < end; m += 256u >> p.lglanes) {
-            float g[8], z[8];
-            if (p.grad32) load8<F32>(g, p.grad, m * p.grad_ld + n, k);
-            else load8<D>(g, p.grad, m * p.grad_ld + n, k);
-            if (p.act) {
-                load8<D>(z, p.pre, m * p.pre_ld + n, k);
-                slope_of<8>(z, p.act);
-                for (uint32_t i = 0; i < 8; i++) g[i] = i < k ? g[i] * z[i] : 0.0f;
-            }
-            for (int i = 0; i < 8; i++) sum[i] += g[i];
-            if (p.d) store8<D>(g, p.d, (uint64_t)m * p.wide + n, 8);
-        }
-    if (!p.sums) return;
-    for (int i = 0; i < 8; i++) part[i * 256 + threadIdx.x] = sum[i];
-    __syncthreads();
-    for (uint32_t c = threadIdx.x; c < cols; c += 256) {
-        float s = 0;
-        for (uint32_t t = c / 8; t < 256; t += lanes) s += part[(c & 7) * 256 + t];
-        if (bx * cols + c < p.outs) p.sums[(uint64_t)by * p.outs + bx * cols + c] = s;
+    if (n < p.wide) {
+        if (p.grad32) grad_columns<D, F32>(p, first, step, end, n, k, sum);
+        else grad_columns<D, D>(p, first, step, end, n, k, sum);
     }
+    if (!p.sums) return;
+    /* lanes of the same columns together, then the four wavefronts */
+    for (int i = 0; i < 8; i++)
+        for (uint32_t d = lanes; d < 64; d *= 2) sum[i] += __shfl_xor(sum[i], d);
+    if ((threadIdx.x & 63) < lanes)
+        for (int i = 0; i < 8; i++) part[(threadIdx.x >> 6) * cols + (threadIdx.x & 63) * 8 + i] = sum[i];
+    __syncthreads();
+    const uint32_t c = threadIdx.x;
+    if (c < cols && bx * cols + c < p.outs)
+        p.sums[(uint64_t)by * p.outs + bx * cols + c] = part[c] + part[cols + c] + part[2 * cols + c] + part[3 * cols + c];
 }
 
 /* What the products of a call need first: x and weight packed, and the gradient. */
 template <typename D> __global__ void __launch_bounds__(256) msim_linear_prepare(PackP x, PackP w, GradP g)
 {
-    __shared__ float part[256 * 8];
+    __shared__ float part[4 * 256];
     if (blockIdx.x < x.blocks) pack_rows<D>(x, blockIdx.x);
     else if (blockIdx.x < x.blocks + w.blocks) pack_rows<D>(w, blockIdx.x - x.blocks);
     else grad_rows<D>(g, blockIdx.x - x.blocks - w.blocks, part);
@@ -247,7 +283,8 @@ const char *check_linear(const msim_linear_spec *s, int *code)
 bool few_rows(const msim_linear_spec *s)
 {
     const uint64_t size = size_of(s->dtype);
-    if (s->rows <= MSIM_LINEAR_FEW && s->outs <= MSIM_LINEAR_FEW_OUTS) return s->cols * size <= 16384;
+    if (s->outs > MSIM_LINEAR_FEW_OUTS) return false;
+    if (s->rows <= MSIM_LINEAR_FEW) return s->cols * size <= 16384;
     return s->rows <= 64 && s->cols <= (size == 4 ? 1024 : 4096) && s->cols * size * s->outs <= 1u << 24;
 }
 
@@ -316,7 +353,8 @@ Backward backward_of(const msim_linear_spec *s, const void *x, const void *weigh
     const bool need = dx || dw;
     b.own = need && (s->act || s->out_dtype != s->dtype || !ready(grad, s->rows, s->outs, s->out_stride, size));
     b.wide = b.own ? up(s->outs, 16 / size * (size == 4 ? 2 : 1)) : s->outs;
-    /* a thread has 8 columns and a row of `part` at a time: two rows at least, about 1,024 blocks at most */
+    /* a thread has 8 columns: two rows of them at least where there are several workgroups of rows, of which there are about
+     * 1,024 at most */
     uint32_t lanes = 1;
     while (lanes < 32 && 8 * lanes < s->outs) lanes *= 2;
     b.part = s->rows <= 256 ? 256 : (uint32_t)std::max<uint64_t>(512 / lanes, (s->rows + 1023) / 1024);
@@ -342,7 +380,8 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
     if ((b.own || dbias) && s->rows) {
         g = {grad, pre, s->out_stride, s->pre_stride, b.own ? wd : nullptr, !dbias ? nullptr : b.blocks == 1 ? dbias : (float *)wsum,
              (uint32_t)s->rows, s->outs, b.own ? (uint32_t)b.wide : (uint32_t)up(s->outs, 8), s->act, s->out_dtype == MSIM_F32, 0, b.part, 0};
-        while (g.lglanes < 5 && (8u << g.lglanes) < g.wide) g.lglanes++;
+        /* of rows for one workgroup 64 at a time, four a thread (69 x 142 f16 with gelu 22 -> 9 us) */
+        while (g.lglanes < (b.blocks == 1 ? 2 : 5) && (8u << g.lglanes) < g.wide) g.lglanes++;
         g.blocks = b.blocks * ((g.wide + (8u << g.lglanes) - 1) / (8u << g.lglanes));
     }
     hipError_t r = prepare<D>(dweight ? pack_of(b.x, wx) : PackP{}, dx ? pack_of(b.w, ww) : PackP{}, g, st);
