@@ -51,6 +51,9 @@ struct GemmP {
     Epilogue e;
 };
 
+/* Sums of columns to be joined beside the parts of a backward pass's products: [blocks][outs] */
+struct Columns { const float *sums; uint32_t blocks, outs; float *out; };
+
 /* A kernel: tiles of bt x bt, stages in LDS, threads. */
 struct Kind { uint32_t bt, depth, threads; };
 constexpr Kind KINDS[] = {{256, 2, 512}, {128, 2, 256}, {64, 4, 256}};
@@ -67,9 +70,9 @@ __attribute__((visibility("hidden"))) void plan_pair(uint32_t mode, const Produc
 /* Enqueues a product of A contiguous along k and B along k (BMC: along n); p.part
  * has room for the plan's parts.  launch_pair: of a backward pass, x of A along k
  * and B along n, w of both along m and n, in one launch and with plans of one
- * kind; either may be left out (batch 0). */
+ * kind; either may be left out (batch 0).  The columns, if any, are joined behind them. */
 template <int MODE, bool BMC> __attribute__((visibility("hidden"))) hipError_t launch_gemm(GemmP p, const Plan &c, hipStream_t st);
-template <int MODE> __attribute__((visibility("hidden"))) hipError_t launch_pair(GemmP x, const Plan &cx, GemmP w, const Plan &cw, hipStream_t st);
+template <int MODE> __attribute__((visibility("hidden"))) hipError_t launch_pair(GemmP x, const Plan &cx, GemmP w, const Plan &cw, const Columns &c, hipStream_t st);
 
 inline uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 

@@ -486,9 +486,27 @@ template <int MODE> __device__ __forceinline__ void join_parts(const GemmP &p, u
     after<MODE>(p.e, batch, m, c, v, early);
 }
 
-template <int MODE> __global__ void __launch_bounds__(256) msim_gemm_join(GemmP a, uint64_t na, GemmP b, uint64_t nb)
+/* eight columns of a workgroup's, 32 runs of blocks, in 64 bits */
+__device__ __forceinline__ void join_columns(const Columns &p, uint32_t block, double *part)
 {
-    for (uint64_t id = blockIdx.x * 256ull + threadIdx.x; id < na + nb; id += gridDim.x * 256ull) {
+    const uint32_t c = block * 8 + (threadIdx.x & 7);
+    double s = 0;
+    if (c < p.outs)
+        _Pragma("unroll 8") for (uint32_t b = threadIdx.x >> 3; b < p.blocks; b += 32) s += p.sums[(uint64_t)b * p.outs + c];
+    part[threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.x >= 8 || c >= p.outs) return;
+    for (int i = 1; i < 32; i++) s += part[i * 8 + threadIdx.x];
+    p.out[c] = (float)s;
+}
+
+/* the first workgroups have the columns */
+template <int MODE> __global__ void __launch_bounds__(256) msim_gemm_join(GemmP a, uint64_t na, GemmP b, uint64_t nb, Columns c)
+{
+    __shared__ double part[256];
+    const uint32_t first = (c.outs + 7) / 8;
+    if (blockIdx.x < first) return join_columns(c, blockIdx.x, part);
+    for (uint64_t id = (blockIdx.x - first) * 256ull + threadIdx.x; id < na + nb; id += (gridDim.x - first) * 256ull) {
         if (id < na) join_parts<MODE>(a, id);
         else join_parts<MODE>(b, id - na);
     }
@@ -515,11 +533,11 @@ template <int MODE> uint64_t ready(GemmP &p, const Plan &c)
     return (uint64_t)p.tm * p.tn * p.parts * p.batch;
 }
 
-template <int MODE> hipError_t launch_join(const GemmP &a, const GemmP &b, hipStream_t st)
+template <int MODE> hipError_t launch_join(const GemmP &a, const GemmP &b, const Columns &c, hipStream_t st)
 {
     const uint64_t na = a.parts > 1 ? (uint64_t)a.batch * a.M * (a.part_ld / 8) : 0, nb = b.parts > 1 ? (uint64_t)b.batch * b.M * (b.part_ld / 8) : 0;
-    if (na + nb == 0) return hipSuccess;
-    return launch(msim_gemm_join<MODE>, (uint32_t)std::min<uint64_t>((na + nb + 255) / 256, 1u << 16), 256, 0, st, a, na, b, nb);
+    if (na + nb + c.outs == 0) return hipSuccess;
+    return launch(msim_gemm_join<MODE>, (c.outs + 7) / 8 + (uint32_t)std::min<uint64_t>((na + nb + 255) / 256, 1u << 16), 256, 0, st, a, na, b, nb, c);
 }
 
 template <int MODE, bool BMC, uint32_t I = 0> hipError_t launch_kind(uint32_t kind, uint32_t grid, const GemmP &p, hipStream_t st)
@@ -538,7 +556,7 @@ template <int MODE, bool BMC> hipError_t launch_gemm(GemmP p, const Plan &c, hip
     const uint64_t grid = ready<MODE>(p, c);
     if (!grid) return hipSuccess;
     const hipError_t r = launch_kind<MODE, BMC>(c.kind, (uint32_t)grid, p, st);
-    return r == hipSuccess ? launch_join<MODE>(p, GemmP{}, st) : r;
+    return r == hipSuccess ? launch_join<MODE>(p, GemmP{}, Columns{}, st) : r;
 }
 
 template <int MODE, uint32_t I = 0> hipError_t launch_pair_kind(uint32_t kind, uint32_t nx, uint32_t nw, const GemmP &x, const GemmP &w, hipStream_t st)
@@ -552,12 +570,11 @@ template <int MODE, uint32_t I = 0> hipError_t launch_pair_kind(uint32_t kind, u
     return hipErrorInvalidValue;
 }
 
-template <int MODE> hipError_t launch_pair(GemmP x, const Plan &cx, GemmP w, const Plan &cw, hipStream_t st)
+template <int MODE> hipError_t launch_pair(GemmP x, const Plan &cx, GemmP w, const Plan &cw, const Columns &c, hipStream_t st)
 {
     const uint64_t nx = x.batch ? ready<MODE>(x, cx) : 0, nw = w.batch ? ready<MODE>(w, cw) : 0;
-    if (nx + nw == 0) return hipSuccess;
-    const hipError_t r = launch_pair_kind<MODE>(x.batch ? cx.kind : cw.kind, (uint32_t)nx, (uint32_t)nw, x, w, st);
-    return r == hipSuccess ? launch_join<MODE>(x, w, st) : r;
+    const hipError_t r = nx + nw == 0 ? hipSuccess : launch_pair_kind<MODE>(x.batch ? cx.kind : cw.kind, (uint32_t)nx, (uint32_t)nw, x, w, st);
+    return r == hipSuccess ? launch_join<MODE>(x, w, c, st) : r;
 }
 
 } // namespace msim

@@ -191,22 +191,6 @@ template <typename D> __global__ void __launch_bounds__(256) msim_linear_prepare
     else grad_rows<D>(g, blockIdx.x - x.blocks - w.blocks, part);
 }
 
-/* column sums of the workgroups together: 32 columns and 32 runs of rows a workgroup */
-__global__ void __launch_bounds__(1024) msim_linear_bias_grad(const float *sums, uint32_t blocks, uint32_t outs, float *out)
-{
-    __shared__ double part[1024];
-    const uint32_t c = blockIdx.x * 32 + (threadIdx.x & 31);
-    double s = 0;
-    if (c < outs)
-        _Pragma("unroll 4") for (uint32_t b = threadIdx.x >> 5; b < blocks; b += 32) s += sums[(uint64_t)b * outs + c];
-    part[threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.x < 32 && c < outs) {
-        for (int i = 1; i < 32; i++) s += part[i * 32 + threadIdx.x];
-        out[c] = (float)s;
-    }
-}
-
 /* ------------------------------------------------------------------------ */
 /* host: products                                                            */
 /* ------------------------------------------------------------------------ */
@@ -387,8 +371,7 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
         g.blocks = b.blocks * ((g.wide + (8u << g.lglanes) - 1) / (8u << g.lglanes));
     }
     hipError_t r = prepare<D>(dweight ? pack_of(b.x, wx) : PackP{}, dx ? pack_of(b.w, ww) : PackP{}, g, st);
-    if (r == hipSuccess && dbias && b.blocks != 1)
-        r = launch(msim_linear_bias_grad, (s->outs + 31) / 32, 1024, 0, st, (const float *)wsum, b.blocks, s->outs, dbias);
+    const Columns c = dbias && b.blocks != 1 ? Columns{(const float *)wsum, b.blocks, s->outs, dbias} : Columns{};
     const Operand d = b.own ? Operand{wd, s->rows * b.wide * size, b.wide * size, 0}
                             : Matrix{grad, s->rows, s->outs, s->out_stride, size, false}.operand(nullptr);
     GemmP px = {}, pw = {};
@@ -414,7 +397,7 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
         pw.e.out = dweight;
         pw.e.out_ld = s->dweight_stride;
     }
-    if (r == hipSuccess) r = launch_pair<MODE>(px, b.px, pw, b.pw, st);
+    if (r == hipSuccess) r = launch_pair<MODE>(px, b.px, pw, b.pw, c, st);
     return launched(r, "linear backward launch");
 }
 
