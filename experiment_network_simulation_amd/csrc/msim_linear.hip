@@ -130,11 +130,11 @@ template <typename D> __device__ __forceinline__ auto raw8(const void *at, uint6
     return v;
 }
 
-/* The sums of a thread's eight columns (k of them there) over its rows, m and every `step`-th up to end, four of
+/* The sums of a thread's eight columns (k of them there) over its rows, m and every `step`-th up to end, two of
  * which are read before the first is used; G: the type of grad. */
 template <typename D, typename G> __device__ __forceinline__ void grad_columns(const GradP &p, uint32_t m, uint32_t step, uint32_t end, uint32_t n, uint32_t k, float *sum)
 {
-    constexpr uint32_t U = 4;
+    constexpr uint32_t U = 2;
     for (; m < end; m += U * step) {
         decltype(raw8<G>(nullptr, 0, 0)) g[U];
         decltype(raw8<D>(nullptr, 0, 0)) z[U];
