@@ -96,6 +96,21 @@ template <typename D> __device__ __forceinline__ u32x4 behind(u32x4 v, uint32_t 
     return __builtin_bit_cast(u32x4, bits < 128 ? q >> bits : 0);
 }
 
+template <uint32_t BITS> struct Bits { typedef uint32_t T; };
+template <> struct Bits<16> { typedef uint16_t T; };
+/* a row of K elements, less than 16 bytes, and zeros; a loop, for the code of others beside it */
+template <typename D> __device__ __forceinline__ u32x4 short_row(const typename D::raw *row, uint32_t K)
+{
+    constexpr uint32_t BITS = sizeof(typename D::raw) * 8;
+    uint64_t half[2] = {0, 0};
+    _Pragma("unroll 1") for (uint32_t i = 0; i < K; i++) {
+        const uint64_t v = (uint64_t)__builtin_bit_cast(typename Bits<BITS>::T, row[i]) << i * BITS % 64;
+        if (i * BITS < 64) half[0] |= v;
+        else half[1] |= v;
+    }
+    return u32x4{(uint32_t)half[0], (uint32_t)(half[0] >> 32), (uint32_t)half[1], (uint32_t)(half[1] >> 32)};
+}
+
 enum { WHOLE, END, SHORT };
 /* acc[i][j] += over N runs of k, at k, k + step, ...: weights w[j], vectors x[i].
  * WHOLE: all within K.  END: one that is not; 16 bytes that would pass the end of a
@@ -115,7 +130,7 @@ __device__ __forceinline__ void stream_runs(const Rows<D> *w, const Rows<D> *x, 
     u32x4 a[N][NT][4], b[N][AHEAD][4];
     const auto load = [&](const Rows<D> &r, int n, u32x4 (&v)[4]) {
         _Pragma("unroll") for (int u = 0; u < 4; u++) {
-            if constexpr (WHERE == SHORT) v[u] = piece<D>(r.at[u], c, K);
+            if constexpr (WHERE == SHORT) v[u] = short_row<D>(r.at[u], c ? 0 : K);
             else v[u] = piece<D>(r.at[u] + at + n * step);
         }
     };
