@@ -564,6 +564,38 @@ def test_a_gates_training_step(T, M):
     assert float((update.double() - want).norm() / want.norm()) < 2.0 ** -8 + 1e-3
 
 
+def test_graph_of_many_runs_and_wide_updates(T, M):
+    """A captured layer of experts with several runs of tokens, a gradient with a bias's and an update of several steps a pass:
+    as the eager results at every replay, with new inputs and eager work between."""
+    def inputs(seed):
+        a = layer_of(T, seed, T.float16, 300, 72, 40, 5)
+        w = real(T, a[4], T.float16)
+        return [a[0], a[1], a[2], a[3], w(300, 5), w(70, 4490)]
+
+    def run(x, gate, w_in, w_out, grad, wide):
+        y, r = M.layer(x, gate, w_in, w_out, 2, residual=x)
+        d = M.linear_backward(x, gate, grad, need_x=False)
+        return [y, r.ids, r.weights, r.load, d.weight, d.bias, M.orthogonalize(wide)]
+
+    args = inputs(0)
+    run(*args)
+    T.cuda.synchronize()
+    g = T.cuda.CUDAGraph()
+    with T.cuda.graph(g):
+        out = run(*args)
+    for k in range(4):
+        fresh = inputs(1 + k)
+        for a, b in zip(args, fresh):
+            a.copy_(b)
+        want = run(*fresh)
+        if k % 2:
+            T.cuda.synchronize()
+        g.replay()
+        again = run(*fresh)
+        T.cuda.synchronize()
+        assert all(T.equal(a, b) for a, b in zip(out, want)) and all(T.equal(a, b) for a, b in zip(again, want))
+
+
 def test_graphs_streams_and_workspaces(T, M):
     """Two graphs of all the operators, replayed in turn on new inputs with eager work and synchronisations between, and
     the same on a stream that is given: as the eager results, every time."""
