@@ -240,12 +240,12 @@ def _plain_layer(st):
     w = torch.where(live, w / w.sum(1, keepdim=True), torch.zeros_like(w)).float()
     x = x.float()
     if T * K < E:                          # the experts that are named, one after another
-        h = torch.matmul(st["w_in"][ids.reshape(-1)].float(), x.repeat_interleave(K, dim=0)[:, :, None])[:, :, 0]
+        h = torch.matmul(st["w_in"][ids.view(-1)].float(), x.repeat_interleave(K, dim=0)[:, :, None])[:, :, 0]
     else:                                  # every expert for every token
         h = torch.matmul(x, st["w_in"].float().mT.contiguous())
     h = _act(h[..., :F], st["act"]) * h[..., F:] if st["gated"] else _act(h, st["act"])
     if T * K < E:
-        o = torch.matmul(st["w_out"][ids.reshape(-1)].float(), h[:, :, None])[:, :, 0].view(T, K, -1)
+        o = torch.matmul(st["w_out"][ids.view(-1)].float(), h[:, :, None])[:, :, 0].view(T, K, -1)
         y = (o * w[:, :, None]).sum(1)
     else:
         share = torch.zeros(T, E, device=x.device).scatter_(1, ids, w)
