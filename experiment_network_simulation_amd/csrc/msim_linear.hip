@@ -334,6 +334,7 @@ Backward backward_of(const msim_linear_spec *s, const void *x, const void *weigh
 {
     Backward b = {};
     const uint32_t size = size_of(s->dtype);
+    dx &= s->rows != 0;
     if (dw) b.x = matrix_of(x, s->rows, s->cols, s->x_stride, size);
     if (dx) b.w = matrix_of(weight, s->outs, s->cols, s->weight_stride, size);
     const bool need = dx || dw;
@@ -463,6 +464,7 @@ extern "C" int msim_linear_backward(const msim_linear_spec *s, const void *x, co
     if (s->rows && (!grad || (dx && !weight) || (dweight && !x))) return fail(MSIM_E_ARG, "linear: null grad, weight or x");
     if (s->act && s->rows && !pre) return fail(MSIM_E_ARG, "linear: the gradient of an activation needs pre");
     if (s->act && s->rows > 1 && s->pre_stride < s->outs) return fail(MSIM_E_ARG, "linear: pre_stride below outs");
+    if (!s->rows) dx = nullptr;            /* nothing of it: weight, which may be NULL then, is not read */
     if (dx && s->rows > 1 && s->dx_stride < s->cols) return fail(MSIM_E_ARG, "linear: dx_stride below cols");
     if (dweight && s->outs > 1 && s->dweight_stride < s->cols) return fail(MSIM_E_ARG, "linear: dweight_stride below cols");
     const Backward b = backward_of(s, x, weight, grad, dx, dweight, dbias);
