@@ -80,21 +80,29 @@ template <typename D> __device__ __forceinline__ void pack_rows(const PackP &p, 
     }
 }
 
-/* v[i] = the activation's slope at v[i] */
+/* What is further than MAX from 0 taken as that far, infinities too; a NaN stays one. */
+template <int MAX> __device__ __forceinline__ float within(float z) { return z < -MAX ? -MAX : z > MAX ? MAX : z; }
+
+/* v[i] = the activation's slope at v[i].  Far from 0 it is 0 or 1 in 32 bits, but a product of 0 and what overflows is
+ * NaN (gelu_tanh from -1.2e13 on, all at infinities): taken where both factors are still finite and the one that is 0
+ * or 1 is so, e^-142 and e^-200 being 0 and their reciprocals infinite. */
 template <int N> __device__ __forceinline__ void slope_of(float *v, uint32_t act)
 {
     switch (act) {
     case MSIM_ACT_RELU: return each<N>(v, [](float z) { return z > 0 ? 1.0f : z != z ? z : 0.0f; });
     case MSIM_ACT_SILU:
-        return each<N>(v, [](float z) {
-            const float s = logistic(z);
+        return each<N>(v, [](float y) {
+            const float z = within<200>(y), s = logistic(z);
             return s * (1.0f + z * (1.0f - s));
         });
     case MSIM_ACT_GELU:
-        return each<N>(v, [](float z) { return normal_below(z) + z * 0.39894228f * expf(-0.5f * z * z); });
+        return each<N>(v, [](float y) {
+            const float z = within<20>(y);
+            return normal_below(z) + z * 0.39894228f * expf(-0.5f * z * z);
+        });
     case MSIM_ACT_GELU_TANH:
-        return each<N>(v, [](float z) {
-            const float s = logistic(z * (TANH_A + TANH_B * z * z));
+        return each<N>(v, [](float y) {
+            const float z = within<12>(y), s = logistic(z * (TANH_A + TANH_B * z * z));
             return s * (1.0f + (1.0f - s) * z * (TANH_A + 3.0f * TANH_B * z * z));
         });
     }

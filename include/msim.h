@@ -591,8 +591,9 @@ int msim_linear(const msim_linear_spec *spec, const void *x, const void *weight,
  * (not read without an activation).  dx (at dx_stride) and dweight (at
  * dweight_stride) are of type dtype.  Any of dx, dweight and dbias may be NULL; x
  * may be without dweight, weight without dx.  d is rounded to dtype where it is
- * not there already (an activation, or a grad of 32 bits).  rows = 0: dweight and
- * dbias are zeros.
+ * not there already (an activation, or a grad of 32 bits).  The slope of an
+ * infinite pre is its limit, 0 or 1; a NaN stays one.  rows = 0: dweight and dbias
+ * are zeros.
  */
 int msim_linear_backward_workspace(const msim_linear_spec *spec, const void *x, const void *weight, const void *grad,
                                    uint32_t dx, uint32_t dweight, uint32_t dbias, uint64_t *bytes);
