@@ -54,6 +54,18 @@ hipError_t launch(void (*kernel)(P...), uint32_t grid, uint32_t block, size_t ld
     }(args...);
 }
 
+/* Enqueues `blocks` workgroups by f(first, how many), in as many launches as the runtime needs, which takes less than
+ * 2^32 work-items in one; `first` is a multiple of 8. */
+template <typename F> hipError_t in_turns(uint64_t blocks, uint32_t threads, F f)
+{
+    if (blocks >> 32) return hipErrorInvalidConfiguration;
+    const uint64_t most = 0xFFFFFFFFu / threads & ~7u;
+    hipError_t e = hipSuccess;
+    for (uint64_t first = 0; first < blocks && e == hipSuccess; first += most)
+        e = f((uint32_t)first, (uint32_t)(blocks - first < most ? blocks - first : most));
+    return e;
+}
+
 [[maybe_unused]] inline int launched(hipError_t e, const char *what)
 {
     if (e == hipSuccess) return MSIM_OK;

@@ -443,21 +443,21 @@ template <int BT, int DEPTH> struct Room {
     typedef Room<BT, DEPTH> R_;                                                                     \
     __shared__ __attribute__((aligned(256))) char lds0[R_::STAGE], lds1[R_::STAGE], lds2[R_::SPARE], lds3[R_::SPARE]
 
-template <int MODE, bool BMC, int BT, int DEPTH, int THREADS> __global__ void __launch_bounds__(THREADS, 2) msim_gemm(GemmP p)
+template <int MODE, bool BMC, int BT, int DEPTH, int THREADS> __global__ void __launch_bounds__(THREADS, 2) msim_gemm(GemmP p, uint32_t total, uint32_t first)
 {
     MSIM_ROOM(BT, DEPTH);
-    product<MODE, false, BMC, BT, DEPTH, THREADS>(p, gridDim.x, blockIdx.x, lds0, lds1, lds2, lds3);
+    product<MODE, false, BMC, BT, DEPTH, THREADS>(p, total, first + blockIdx.x, lds0, lds1, lds2, lds3);
 }
 
 /* The two products of a backward pass in one launch: n of the first, and from the
  * next multiple of 8 on, so that dies are numbered alike, those of the second. */
 template <int MODE, int BT, int DEPTH, int THREADS>
-__global__ void __launch_bounds__(THREADS, 2) msim_gemm_pair(GemmP x, GemmP w, uint32_t n)
+__global__ void __launch_bounds__(THREADS, 2) msim_gemm_pair(GemmP x, GemmP w, uint32_t n, uint32_t nw, uint32_t first)
 {
     MSIM_ROOM(BT, DEPTH);
-    const uint32_t n8 = (n + 7) & ~7u;
-    if (blockIdx.x < n) product<MODE, false, true, BT, DEPTH, THREADS>(x, n, blockIdx.x, lds0, lds1, lds2, lds3);
-    else if (blockIdx.x >= n8) product<MODE, true, true, BT, DEPTH, THREADS>(w, gridDim.x - n8, blockIdx.x - n8, lds0, lds1, lds2, lds3);
+    const uint32_t n8 = (n + 7) & ~7u, block = first + blockIdx.x;
+    if (block < n) product<MODE, false, true, BT, DEPTH, THREADS>(x, n, block, lds0, lds1, lds2, lds3);
+    else if (block >= n8) product<MODE, true, true, BT, DEPTH, THREADS>(w, nw, block - n8, lds0, lds1, lds2, lds3);
 }
 
 /* The parts' sums together, in order, and what becomes of them: of one product, or of two.  Eight columns a thread;
@@ -540,32 +540,36 @@ template <int MODE> hipError_t launch_join(const GemmP &a, const GemmP &b, const
     return launch(msim_gemm_join<MODE>, (c.outs + 7) / 8 + (uint32_t)std::min<uint64_t>((na + nb + 255) / 256, 1u << 16), 256, 0, st, a, na, b, nb, c);
 }
 
-template <int MODE, bool BMC, uint32_t I = 0> hipError_t launch_kind(uint32_t kind, uint32_t grid, const GemmP &p, hipStream_t st)
+template <int MODE, bool BMC, uint32_t I = 0> hipError_t launch_kind(uint32_t kind, uint64_t total, const GemmP &p, hipStream_t st)
 {
     if constexpr (I < N_KINDS) {
         constexpr Kind k = KINDS[I];
-        if (kind != I) return launch_kind<MODE, BMC, I + 1>(kind, grid, p, st);
+        if (kind != I) return launch_kind<MODE, BMC, I + 1>(kind, total, p, st);
         if constexpr (!(MODE == M_F32 && k.bt == 256))
-            return launch(msim_gemm<MODE, BMC, k.bt, k.depth, k.threads>, grid, k.threads, 0, st, p);
+            return in_turns(total, k.threads, [&](uint32_t first, uint32_t grid) {
+                return launch(msim_gemm<MODE, BMC, k.bt, k.depth, k.threads>, grid, k.threads, 0, st, p, (uint32_t)total, first);
+            });
     }
     return hipErrorInvalidValue;
 }
 
 template <int MODE, bool BMC> hipError_t launch_gemm(GemmP p, const Plan &c, hipStream_t st)
 {
-    const uint64_t grid = ready<MODE>(p, c);
-    if (!grid) return hipSuccess;
-    const hipError_t r = launch_kind<MODE, BMC>(c.kind, (uint32_t)grid, p, st);
+    const uint64_t total = ready<MODE>(p, c);
+    if (!total) return hipSuccess;
+    const hipError_t r = launch_kind<MODE, BMC>(c.kind, total, p, st);
     return r == hipSuccess ? launch_join<MODE>(p, GemmP{}, Columns{}, st) : r;
 }
 
-template <int MODE, uint32_t I = 0> hipError_t launch_pair_kind(uint32_t kind, uint32_t nx, uint32_t nw, const GemmP &x, const GemmP &w, hipStream_t st)
+template <int MODE, uint32_t I = 0> hipError_t launch_pair_kind(uint32_t kind, uint64_t nx, uint64_t nw, const GemmP &x, const GemmP &w, hipStream_t st)
 {
     if constexpr (I < N_KINDS) {
         constexpr Kind k = KINDS[I];
         if (kind != I) return launch_pair_kind<MODE, I + 1>(kind, nx, nw, x, w, st);
         if constexpr (!(MODE == M_F32 && k.bt == 256))
-            return launch(msim_gemm_pair<MODE, k.bt, k.depth, k.threads>, (nx + 7) / 8 * 8 + nw, k.threads, 0, st, x, w, nx);
+            return in_turns(up(nx, 8) + nw, k.threads, [&](uint32_t first, uint32_t grid) {
+                return launch(msim_gemm_pair<MODE, k.bt, k.depth, k.threads>, grid, k.threads, 0, st, x, w, (uint32_t)nx, (uint32_t)nw, first);
+            });
     }
     return hipErrorInvalidValue;
 }
@@ -573,7 +577,7 @@ template <int MODE, uint32_t I = 0> hipError_t launch_pair_kind(uint32_t kind, u
 template <int MODE> hipError_t launch_pair(GemmP x, const Plan &cx, GemmP w, const Plan &cw, const Columns &c, hipStream_t st)
 {
     const uint64_t nx = x.batch ? ready<MODE>(x, cx) : 0, nw = w.batch ? ready<MODE>(w, cw) : 0;
-    const hipError_t r = nx + nw == 0 ? hipSuccess : launch_pair_kind<MODE>(x.batch ? cx.kind : cw.kind, (uint32_t)nx, (uint32_t)nw, x, w, st);
+    const hipError_t r = nx + nw == 0 ? hipSuccess : launch_pair_kind<MODE>(x.batch ? cx.kind : cw.kind, nx, nw, x, w, st);
     return r == hipSuccess ? launch_join<MODE>(x, w, c, st) : r;
 }
 

@@ -21,16 +21,22 @@ constexpr uint32_t NORM_PARTS = 256;
 /* a product of several steps' factors, which reaches a^3, is held times this less */
 constexpr float PASS_DOWN = 16.0f;
 
-/* sums of squares in 64 bits: NORM_PARTS workgroups a matrix (4 of 2,048 x 7,168 bf16 27 us, 4.3 TB/s) */
-template <typename D> __global__ void __launch_bounds__(256) msim_orth_norm(const void *from, uint64_t size, double *part)
+/* Sums of squares in 64 bits: NORM_PARTS workgroups a matrix, or as many as have an element (4 of 2,048 x 7,168 bf16
+ * 27 us, 4.3 TB/s).  part: [matrix][workgroups]. */
+template <typename D> uint32_t norm_parts(uint64_t size)
+{
+    constexpr uint64_t EACH = 256 * 16 / sizeof(typename D::raw);
+    return (uint32_t)std::min<uint64_t>(NORM_PARTS, (size + EACH - 1) / EACH);
+}
+template <typename D> __global__ void __launch_bounds__(256) msim_orth_norm(const void *from, uint64_t size, double *part, uint32_t parts, uint32_t first)
 {
     constexpr uint32_t PER = 16 / sizeof(typename D::raw);
     typedef typename D::raw vec __attribute__((ext_vector_type(PER)));
     __shared__ double sums[4];
-    const uint32_t batch = blockIdx.x / NORM_PARTS, k = blockIdx.x % NORM_PARTS;
+    const uint32_t block = first + blockIdx.x, batch = block / parts, k = block - batch * parts;
     const typename D::raw *x = (const typename D::raw *)from + batch * size;
     double s = 0;
-    _Pragma("unroll 2") for (uint64_t i = (k * 256 + threadIdx.x) * PER; i < size; i += NORM_PARTS * 256 * PER) {
+    _Pragma("unroll 2") for (uint64_t i = (k * 256 + threadIdx.x) * PER; i < size; i += (uint64_t)parts * 256 * PER) {
         const vec v = __builtin_bit_cast(vec, i + PER <= size ? piece<D>(x + i) : piece<D>(x + i, 0, (uint32_t)(size - i)));
         for (uint32_t j = 0; j < PER; j++) {
             const double d = D::get(v[j]);
@@ -40,14 +46,16 @@ template <typename D> __global__ void __launch_bounds__(256) msim_orth_norm(cons
     for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
     __syncthreads();
-    if (threadIdx.x == 0) part[blockIdx.x] = sums[0] + sums[1] + sums[2] + sums[3];
+    if (threadIdx.x == 0) part[block] = sums[0] + sums[1] + sums[2] + sums[3];
 }
 
 /* what X is the update times: one wavefront asks, all its lanes know.  A norm that is not finite makes it NaN. */
-__device__ __forceinline__ double scale_of(const double *part, double eps)
+__device__ __forceinline__ double scale_of(const double *part, uint32_t batch, uint32_t parts, double eps)
 {
     const uint32_t lane = threadIdx.x & 63;
-    double s = part[lane] + part[lane + 64] + part[lane + 128] + part[lane + 192];
+    part += (uint64_t)batch * parts;
+    double s = 0;
+    for (uint32_t k = 0; k < NORM_PARTS; k += 64) s += lane + k < parts ? part[lane + k] : 0.0;
     for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
     return s < INFINITY ? ORTH_SCALE / (sqrt(s) + eps) : NAN;
 }
@@ -59,6 +67,7 @@ struct OrthP {
     const double *part;
     uint64_t rows, cols, ld, batch;        /* batch: bytes between matrices of x */
     double eps;
+    uint32_t parts, first;
 };
 
 /* Tiles of 32 x 64 between the caller's matrices and X (flip: its transpose, through
@@ -72,7 +81,8 @@ template <typename D, bool BEGIN, bool FLIP> __global__ void __launch_bounds__(2
     __shared__ double factor;
     const uint64_t m = FLIP ? p.cols : p.rows, n = FLIP ? p.rows : p.cols;
     const uint64_t tn = (p.ld + 63) / 64, tm = (m + 31) / 32;
-    const uint32_t batch = (uint32_t)(blockIdx.x / (tm * tn)), at = (uint32_t)(blockIdx.x - batch * tm * tn);
+    const uint64_t block = p.first + blockIdx.x;
+    const uint32_t batch = (uint32_t)(block / (tm * tn)), at = (uint32_t)(block - batch * tm * tn);
     const uint64_t m0 = at / tn * 32, n0 = at % tn * 64;
     char *x = p.x + batch * p.batch;
     const uint64_t base = batch * p.rows * p.cols;
@@ -93,7 +103,7 @@ template <typename D, bool BEGIN, bool FLIP> __global__ void __launch_bounds__(2
             load8<D>(v, p.in, base + row * p.cols + col, there);
         }
         if (threadIdx.x < 64) {
-            const double f = scale_of(p.part + batch * NORM_PARTS, p.eps);
+            const double f = scale_of(p.part, batch, p.parts, p.eps);
             if (threadIdx.x == 0) factor = f;
         }
         if constexpr (FLIP)
@@ -143,7 +153,7 @@ struct SlabP {
     uint64_t size, sm, sn;       /* of in and out: elements of a matrix, between rows and columns of X */
     double eps;
     uint32_t m, n, slabs, wide;  /* wide: columns of a slab, a multiple of 32 */
-    uint32_t first, last;
+    uint32_t first, last, parts;           /* parts: of the norm */
     float a, b, c;
 };
 
@@ -236,7 +246,7 @@ template <typename D, uint32_t ROWS> __global__ void __launch_bounds__(SLAB_THRE
     };
     if (p.first) {
         if (tid < 64) {
-            const double f = scale_of(p.norm + batch * NORM_PARTS, p.eps);
+            const double f = scale_of(p.norm, batch, p.parts, p.eps);
             if (tid == 0) factor = f;
         }
         __syncthreads();
@@ -442,14 +452,31 @@ const char *check_orth(const msim_orthogonalize_spec *s, int *code)
     return check_steps(s);
 }
 
+template <typename D> hipError_t launch_norm(const msim_orthogonalize_spec *s, const void *in, void *to, hipStream_t st)
+{
+    const uint64_t size = s->rows * s->cols;
+    const uint32_t parts = norm_parts<D>(size);
+    return in_turns((uint64_t)s->count * parts, 256, [&](uint32_t first, uint32_t grid) {
+        return launch(msim_orth_norm<D>, grid, 256, 0, st, in, size, (double *)to, parts, first);
+    });
+}
+
+template <typename D, bool BEGIN> hipError_t launch_move(const msim_orthogonalize_spec *s, const Orth &o, OrthP q, hipStream_t st)
+{
+    return in_turns((o.lx + 63) / 64 * ((o.m + 31) / 32) * s->count, 256, [&](uint32_t first, uint32_t grid) {
+        q.first = first;
+        return launch(s->rows > s->cols ? msim_orth_move<D, BEGIN, true> : msim_orth_move<D, BEGIN, false>, grid, 256, 0, st, q);
+    });
+}
+
 template <typename D>
 hipError_t run_slabs(const msim_orthogonalize_spec *s, const Orth &o, const void *in, void *out, char *ws, hipStream_t st)
 {
     char *x = ws + o.norm_bytes, *part = x + o.x_bytes, *next = part + o.p_bytes;
     const bool flip = s->rows > s->cols;
     SlabP p = {in, out, (const double *)ws, x, (const float *)part, (float *)next, s->rows * s->cols, flip ? 1 : s->cols, flip ? s->cols : 1,
-               s->eps, (uint32_t)o.m, (uint32_t)o.n, (uint32_t)o.slabs, (uint32_t)o.slab, 1, s->steps == 0, s->a, s->b, s->c};
-    hipError_t e = launch(msim_orth_norm<D>, s->count * NORM_PARTS, 256, 0, st, in, s->rows * s->cols, (double *)ws);
+               s->eps, (uint32_t)o.m, (uint32_t)o.n, (uint32_t)o.slabs, (uint32_t)o.slab, 1, s->steps == 0, norm_parts<D>(s->rows * s->cols), s->a, s->b, s->c};
+    hipError_t e = launch_norm<D>(s, in, ws, st);
     for (uint32_t k = 0; k <= s->steps && e == hipSuccess; k++) {
         p.first = k == 0;
         p.last = k == s->steps;
@@ -467,11 +494,9 @@ hipError_t run_orth(const msim_orthogonalize_spec *s, const Orth &o, const void 
     if (o.slabs) return run_slabs<D>(s, o, in, out, ws, st);
     char *norms = ws, *x = norms + o.norm_bytes, *y = x + o.x_bytes, *sq = y + o.x_bytes, *m2[5], *part = sq + o.p_bytes;
     for (uint32_t i = 0; i < o.squares; i++, part += o.p_bytes) m2[i] = part;
-    OrthP q = {in, out, x, (const double *)norms, s->rows, s->cols, o.lx, o.m * o.lx * 4, s->eps};
-    const bool flip = s->rows > s->cols;
-    const uint32_t moves = (uint32_t)((o.lx + 63) / 64 * ((o.m + 31) / 32) * s->count);
-    hipError_t e = launch(msim_orth_norm<D>, s->count * NORM_PARTS, 256, 0, st, in, s->rows * s->cols, (double *)norms);
-    if (e == hipSuccess) e = launch(flip ? msim_orth_move<D, true, true> : msim_orth_move<D, true, false>, moves, 256, 0, st, q);
+    OrthP q = {in, out, x, (const double *)norms, s->rows, s->cols, o.lx, o.m * o.lx * 4, s->eps, norm_parts<D>(s->rows * s->cols), 0};
+    hipError_t e = launch_norm<D>(s, in, norms, st);
+    if (e == hipSuccess) e = launch_move<D, true>(s, o, q, st);
     /* to = alpha src + beta a b + diag I, symmetric; b of X or of a matrix of m columns */
     const auto square = [&](char *to, const char *fa, const char *fb, uint64_t ld, const Plan &plan, const char *src, float alpha, float beta, float diag) {
         GemmP p = {};
@@ -530,8 +555,7 @@ hipError_t run_orth(const msim_orthogonalize_spec *s, const Orth &o, const void 
         std::swap(x, y);
     }
     q.x = x;
-    if (e == hipSuccess) e = launch(flip ? msim_orth_move<D, false, true> : msim_orth_move<D, false, false>, moves, 256, 0, st, q);
-    return e;
+    return e == hipSuccess ? launch_move<D, false>(s, o, q, st) : e;
 }
 
 }   // namespace

@@ -44,3 +44,38 @@ def test_slopes_far_from_zero(T, M, types, dt, act, copies):  # noqa: F811
         assert bool(got.x[5].isnan().all()) and bool(got.weight[3].isnan().all()) and bool(got.bias[3].isnan())
         got.x[5], got.weight[3], got.bias[3] = 0, 0, 0
         assert all(bool(v.isfinite().all()) for v in got)
+
+
+def test_linear_of_two_launches(T, M):  # noqa: F811
+    """2^30 rows: the products are 2^32 work-items and more, in several launches.  Rows at both ends and around the places where the
+    launches part are those of a call of their own, all others are zeros."""
+    rows, n = (1 << 30) + 70, 8
+    g = gen(T, 12)
+    x, w = T.zeros(rows, n, device=DEV, dtype=T.float16), whole(T, g, T.float16)(n, n)
+    some = T.cat([T.arange(k, k + 300, device=DEV) for k in (0, rows // 4, (1 << 29) - 600, (1 << 30) - 600, rows - 300)])
+    x[some] = whole(T, g, T.float16)(some.numel(), n)
+    want = x[some].double() @ w.double().T
+    y = M.linear(x, w)
+    assert T.equal(y[some], want.to(T.float16))
+    assert int(y.count_nonzero()) == int(want.count_nonzero())
+    y.zero_()
+    y[some] = whole(T, g, T.float16)(some.numel(), n)
+    dx, dw, db = M.linear_backward(x, w, y)
+    want = y[some].double() @ w.double()
+    assert T.equal(dx[some], want.to(T.float16)) and int(dx.count_nonzero()) == int(want.count_nonzero())
+    assert T.equal(dw, (y[some].double().T @ x[some].double()).to(T.float16)) and T.equal(db, y[some].double().sum(0).float())
+
+
+@pytest.mark.parametrize("rows,cols", [(8, 8), (1, 16384)])
+def test_orthogonalize_as_many_as_there_may_be(T, M, rows, cols):  # noqa: F811
+    """65,536 updates, of which few are not zero: each by itself, the last ones too."""
+    g = gen(T, rows)
+    u = T.zeros(65536, rows, cols, device=DEV, dtype=T.bfloat16)
+    at = T.tensor([0, 1, 32767, 32768, 65000, 65535], device=DEV)
+    u[at] = real(T, g, T.bfloat16)(6, rows, cols)
+    y = M.orthogonalize(u, steps=1)
+    for k in at.tolist():
+        assert T.equal(y[k], M.orthogonalize(u[k].contiguous(), steps=1)) if cols > 8192 else \
+            T.allclose(y[k].float(), M.orthogonalize(u[k].contiguous(), steps=1).float(), atol=2.0 ** -7)
+    y[at] = 0
+    assert not bool(y.any())

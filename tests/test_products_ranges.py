@@ -94,3 +94,35 @@ def test_a_gradient_of_no_rows_reads_no_array(S, launched):  # noqa: F811
         n, lib = C.c_uint64(9), S.load_library()
         s = linear_spec(S, rows=0, cols=cols, outs=4000, x_stride=cols, weight_stride=cols, out_stride=4000, dx_stride=cols, dweight_stride=cols)
         assert lib.msim_linear_backward_workspace(C.byref(s), None, None, None, 1, 0, 0, C.byref(n)) == 0 and n.value == 0, cols
+
+
+MOST = (1 << 31) - 1
+WIDE = ["linear(1 << 30, 8, 8)", "linear(1 << 30, 8, 8, dtype=0)", f"linear({MOST}, 8, 256)", f"linear({MOST}, 8, 1, dtype=1)",
+        f"linear({MOST}, 1, 1, dtype=0)", f"linear({MOST}, 9, 300, act=2)", "linear(1 << 20, 8, 1 << 19)",
+        f"backward({MOST}, 8, 8)", f"backward({MOST}, 300, 9, dtype=0, act=1)", f"backward({MOST}, 8, 8, out_dtype=0, dtype=1)",
+        "backward(1 << 30, 8, 8, db=None, dw=None)", "backward(100, 1 << 20, 1 << 20)",
+        "orth(65536, 8, 8)", "orth(65536, 1, 1)", "orth(65536, 1023, 1024, dtype=0)", "orth(65536, 1, 16384)", "orth(65536, 16384, 1)",
+        "orth(65536, 64, 8192, steps=2)", "orth(65536, 65, 66)", "orth(1, 1 << 17, 1 << 18)"]
+
+
+def test_no_launch_is_larger_than_the_runtime_takes(launched):
+    """The largest counts and rows that the calls accept, where what is launched has 2^32 work-items and more in all: every part of
+    it is below that, and the parts follow each other in steps of 8 workgroups."""
+    large = 0
+    large = 0
+    for name, (rc, launches, why) in zip(WIDE, launched(WIDE)):
+        assert rc == 0, (name, why)
+        assert launches and all(0 < g * b < 1 << 32 for g, b in launches), (name, launches)
+        for (g, b), (_, after) in zip(launches, launches[1:]):
+            if g * b > (1 << 32) - 8 * b - 1:
+                large += 1
+                assert g % 8 == 0 and after == b, (name, launches)
+    assert large >= 8
+
+
+def test_norms_have_workgroups_for_elements_alone(launched):
+    """Of 2,048 elements of 16 bits (1,024 of 32) each, up to 256 a matrix."""
+    sizes = [(64, 8, 8, 2, 64), (64, 8, 8, 0, 64), (3, 64, 32, 2, 3), (3, 64, 33, 2, 6), (3, 64, 32, 0, 6), (2, 2048, 7168, 2, 512),
+             (1, 100, 8191, 0, 256)]
+    for (count, rows, cols, dtype, norm), (rc, launches, why) in zip(sizes, launched([f"orth({c}, {r}, {k}, dtype={d})" for c, r, k, d, _ in sizes])):
+        assert rc == 0 and launches[0] == [norm, 256], (count, rows, cols, launches[0])
