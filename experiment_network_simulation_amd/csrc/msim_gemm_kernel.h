@@ -175,7 +175,8 @@ template <int MODE> __device__ __forceinline__ void before(const Epilogue &e, ui
     if (m >= e.M || n >= e.N) return;
     const uint32_t k = min(8u, e.N - n);
     if (e.pre) store8<D>(v, e.pre, m * e.pre_ld + n, k);
-    act_of<8>(v, e.act);
+    if (MODE == M_F32 || e.out32) act_of<8, true>(v, e.act);
+    else act_of<8, false>(v, e.act);
 }
 
 /* and residual and result, or the next split matrix */

@@ -107,7 +107,7 @@ template <typename D> __device__ __forceinline__ void hidden_of(const LayerP &p,
         if (f >= p.F) continue;
         float v[4];
         for (int k = 0; k < 4; k++) v[k] = j ? sums[1][k] : sums[0][k];
-        act_of<4>(v, p.act);
+        act_of<4, std::is_same<D, F32>::value>(v, p.act);
         for (int k = 0; k < 4; k++) h[f + k] = D::put(p.gated ? v[k] * sums[1][k] : v[k]);
     }
 }

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "msim_gemm.h"
 
@@ -46,7 +47,8 @@ template <int MODE, int MT, int WAVES> __global__ void __launch_bounds__(64 * WA
             v[k] = acc[i][0][k] + (p.e.bias && k < have ? p.e.bias[n + k] : 0.0f);
             if (p.e.pre && k < have) ((raw *)p.e.pre)[m * p.e.pre_ld + n + k] = D::put(v[k]);
         }
-        act_of<4>(v, p.e.act);
+        if (MODE == M_F32 || p.e.out32) act_of<4, true>(v, p.e.act);
+        else act_of<4, false>(v, p.e.act);
         for (uint32_t k = 0; k < have; k++) {
             const uint64_t at = m * p.e.res_ld + n + k;
             if (p.e.res) v[k] += p.e.out32 ? ((const float *)p.e.res)[at] : D::get(((const raw *)p.e.res)[at]);
@@ -86,23 +88,23 @@ template <int MAX> __device__ __forceinline__ float within(float z) { return z <
 /* v[i] = the activation's slope at v[i].  Far from 0 it is 0 or 1 in 32 bits, but a product of 0 and what overflows is
  * NaN (gelu_tanh from -1.2e13 on, all at infinities): taken where both factors are still finite and the one that is 0
  * or 1 is so, e^-142 and e^-200 being 0 and their reciprocals infinite. */
-template <int N> __device__ __forceinline__ void slope_of(float *v, uint32_t act)
+template <int N, bool FULL> __device__ __forceinline__ void slope_of(float *v, uint32_t act)
 {
     switch (act) {
     case MSIM_ACT_RELU: return each<N>(v, [](float z) { return z > 0 ? 1.0f : z != z ? z : 0.0f; });
     case MSIM_ACT_SILU:
         return each<N>(v, [](float y) {
-            const float z = within<200>(y), s = logistic(z);
+            const float z = within<200>(y), s = logistic<FULL>(z);
             return s * (1.0f + z * (1.0f - s));
         });
     case MSIM_ACT_GELU:
         return each<N>(v, [](float y) {
             const float z = within<20>(y);
-            return normal_below(z) + z * 0.39894228f * expf(-0.5f * z * z);
+            return normal_below<FULL>(z) + z * 0.39894228f * expf(-0.5f * z * z);
         });
     case MSIM_ACT_GELU_TANH:
         return each<N>(v, [](float y) {
-            const float z = within<12>(y), s = logistic(z * (TANH_A + TANH_B * z * z));
+            const float z = within<12>(y), s = logistic<FULL>(z * (TANH_A + TANH_B * z * z));
             return s * (1.0f + (1.0f - s) * z * (TANH_A + 3.0f * TANH_B * z * z));
         });
     }
@@ -158,7 +160,7 @@ template <typename D, typename G> __device__ __forceinline__ void grad_columns(c
             for (uint32_t i = 0; i < 8; i++) v[i] = G::get(g[u][i]);
             if (p.act) {
                 for (uint32_t i = 0; i < 8; i++) slope[i] = D::get(z[u][i]);
-                slope_of<8>(slope, p.act);
+                slope_of<8, std::is_same<D, F32>::value>(slope, p.act);
                 for (uint32_t i = 0; i < 8; i++) v[i] = i < k ? v[i] * slope[i] : 0.0f;
             }
             for (int i = 0; i < 8; i++) sum[i] += v[i];

@@ -201,31 +201,40 @@ template <int N, typename F> __device__ __forceinline__ void each(float *v, F f)
 {
     _Pragma("unroll") for (int i = 0; i < N; i++) v[i] = f(v[i]);
 }
-/* 1 / (1 + e^-z) */
-__device__ __forceinline__ float logistic(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+/* Activations and their slopes are FULL where what becomes of them has 32 bits; what is rounded to 16 bits takes shorter
+ * ways, off by a hundredth of its own rounding at most. */
 
-/* The share of a normal distribution below z: 1/2 of erfc of |z| / sqrt(2), by
- * formula 7.1.26 of Abramowitz and Stegun, off by at most 0.8e-7, from the side of
- * the sign.  A third of the library function's instructions: of 8,192 x 8,192 with
- * gelu it takes 40 us off 570. */
-__device__ __forceinline__ float normal_below(float z)
+/* 1 / (1 + e^-z) */
+template <bool FULL> __device__ __forceinline__ float logistic(float z)
 {
-    const float x = fabsf(z) * 0.70710678f, t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
-    const float q = 0.5f * t * expf(-x * x) *
-        (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    const float d = 1.0f + expf(-z);
+    return FULL ? 1.0f / d : __builtin_amdgcn_rcpf(d);
+}
+
+/* The share of a normal distribution below z: 1/2 of erfc(x), x = |z| / sqrt(2), from the side of the sign.  Otherwise
+ * t P(t) e^(-x^2), t = 1 / (1 + 0.51 x), which is smooth down to t = 0: P fits erfc(x) e^(x^2) / 2 t with the least largest
+ * relative error for x up to 9.5, 7.4e-7.  In 32 bits off by at most 5e-6 relative and 7e-7 in all, a hundredth of a
+ * rounding to 11 bits down to the smallest results (a fit of erfc to 1.5e-7 in all was 5e-4 off at z = -4).  2,048 x
+ * 4,096 results of 32 bits 34 us by the library function, 30 like this; 8,192 x 8,192 of 16 bits 501. */
+template <bool FULL> __device__ __forceinline__ float normal_below(float z)
+{
+    if constexpr (FULL) return 0.5f * erfcf(z * -0.70710678f);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.36062446f, fabsf(z), 1.0f));
+    const float p = 0.143964782f + t * (0.14199096f + t * (0.140001565f + t * (0.0262380857f + t * (0.181102261f + t * (-0.180954888f + t * 0.0476572923f)))));
+    const float q = t * expf(-0.5f * z * z) * p;
     return z < 0 ? q : 1.0f - q;
 }
 
 constexpr float TANH_A = 1.59576912f, TANH_B = 0.0713548162f;      /* 2 sqrt(2 / pi), times 0.044715 */
 
-template <int N> __device__ __forceinline__ void act_of(float *v, uint32_t act)
+template <int N, bool FULL> __device__ __forceinline__ void act_of(float *v, uint32_t act)
 {
     switch (act) {
     case MSIM_ACT_RELU: return each<N>(v, [](float z) { return z < 0 ? 0.0f : z; });      /* a NaN stays one */
-    case MSIM_ACT_SILU: return each<N>(v, [](float z) { return z * logistic(z); });
-    case MSIM_ACT_GELU: return each<N>(v, [](float z) { return z * normal_below(z); });
+    case MSIM_ACT_SILU: return each<N>(v, [](float z) { return z * logistic<FULL>(z); });
+    case MSIM_ACT_GELU: return each<N>(v, [](float z) { return z * normal_below<FULL>(z); });
     case MSIM_ACT_GELU_TANH:               /* (1 + tanh(u)) / 2 = 1 / (1 + e^-2u) */
-        return each<N>(v, [](float z) { return z * logistic(z * (TANH_A + TANH_B * z * z)); });
+        return each<N>(v, [](float z) { return z * logistic<FULL>(z * (TANH_A + TANH_B * z * z)); });
     }
 }
 

@@ -79,3 +79,54 @@ def test_orthogonalize_as_many_as_there_may_be(T, M, rows, cols):  # noqa: F811
             T.allclose(y[k].float(), M.orthogonalize(u[k].contiguous(), steps=1).float(), atol=2.0 ** -7)
     y[at] = 0
     assert not bool(y.any())
+
+
+def grid(T):  # noqa: F811
+    """-13 .. 13 in steps of 2^-13, and small numbers of both signs"""
+    z = T.arange(-13 * 8192, 13 * 8192 + 1, device=DEV, dtype=T.float64) / 8192
+    small = T.logspace(-30, -4, 500, device=DEV, dtype=T.float64)
+    return T.cat([z, small, -small])
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("long", [True, False])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_activations_on_a_grid(T, M, types, dt, long, act):  # noqa: F811
+    """A product of one column with 1 shows the activation, relative to its value, however small that is.  Of 32-bit results
+    an exponential is off by 2^-23 and its argument's roundings, a sum, a quotient and a product by 2^-24 each: 2^-24 (8 + 5 |u|)
+    where e^-u is taken; erfc by at most 16 units of 2^-23, its argument by 1.5 2^-24, which counts 2 x^2 = z^2 times.  16-bit
+    results are off by 2^-17 before they are rounded.  What is multiplied by z is 0 below 2^-126."""
+    t = types[dt]
+    z = grid(T).to(t)
+    to = T.float32 if long else t
+    want = 0.5 * z.double() * T.special.erfc(-z.double() / math.sqrt(2)) if act == "gelu" else \
+        z.double() * T.sigmoid(z.double()) if act == "silu" else \
+        z.double() * T.sigmoid(math.sqrt(8 / math.pi) * (z.double() + 0.044715 * z.double() ** 3))
+    u = z.double().abs() if act == "silu" else math.sqrt(8 / math.pi) * (z.double().abs() + 0.044715 * z.double().abs() ** 3)
+    near = 2.0 ** -24 * (34 + 4 * z.double() ** 2) if act == "gelu" else 2.0 ** -24 * (8 + 5 * u)
+    tol = want.abs() * (near if to == T.float32 else 2.0 ** -17 + U[dt]) + (2.0 ** -25 if to == T.float16 else 2.0 ** -126 * (1 + z.double().abs()))
+    w = T.ones(1, 1, device=DEV, dtype=t)
+    for x in (z[:, None].contiguous(), z[-1050:-1000, None].contiguous(), z[::5000][:16, None].contiguous()):
+        y = M.linear(x, w, act=act, out_dtype=to)[:, 0].double()
+        k = (z[None, :] == x[:50]).double().argmax(1) if x.shape[0] <= 64 else T.arange(z.numel(), device=DEV)
+        worst = float(((y - want[k]).abs() / tol[k]).nan_to_num(math.inf).max())
+        print(dt, long, act, x.shape[0], worst, flush=True)
+        assert worst <= 1
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", ACTS)
+def test_linear_has_no_other_result(T, M, types, dt, act):  # noqa: F811
+    """Real values in every size of tile, each within its bound, which no NaN is."""
+    for n, (rows, cols, outs, pad) in enumerate([(5, 300, 40, 0), (40, 333, 65, 3), (60, 96, 500, 0), (300, 520, 200, 0), (130, 777, 131, 5),
+                                                 (2100, 256, 1024, 0), (100, 8192, 40, 0)]):
+        g, t = gen(T, 300 + n), types[dt]
+        x, w = wide(T, rows, cols, pad, real(T, g, t)), wide(T, outs, cols, pad, real(T, g, t, 2 / math.sqrt(cols)))
+        b, r = real(T, g, T.float32, 0.5)(outs), wide(T, rows, outs, pad, real(T, g, t))
+        y = M.linear(x, w, b, act=act, residual=r)
+        z, S = x.double() @ w.double().T + b.double(), x.double().abs() @ w.double().abs().T + b.double().abs()
+        a = act64(T, z, act)
+        want = a + r.double()
+        tol = 1.13 * SUM(cols) * S + (2 ** -20) * (z.abs() + a.abs()) + 2 ** -23 * (a.abs() + r.double().abs()) + U[dt] * want.abs() \
+            + (2.0 ** -25 if dt == "f16" else 0)
+        assert bool(((y.double() - want).abs() <= tol).all()), (rows, cols, outs)
