@@ -369,10 +369,13 @@ Orth orth_of(const msim_orthogonalize_spec *s)
     o.square = plan_of(M_SPLIT, {o.m, o.lp, o.lx, s->count});
     o.poly = plan_of(M_SPLIT, {o.m, o.lp, o.lp, s->count});
     o.update = plan_of(M_SPLIT, {o.m, o.lx, o.lp, s->count});
-    /* What a pass over X costs more than products of m rows has to be worth four launches of those, which are
-     * slower by themselves: 1,024 x 4,096 404 -> 330 us, 8 x 512 x 2,048 378 -> 304, 64 x 20,000 148 -> 125; below, 512 x
-     * 1,024 164 -> 178, 1,536 x 2,304 689 -> 773. */
-    o.wide = s->steps > 1 && (o.n >= 64 * o.m || (2 * o.n > 3 * o.m && (double)s->count * o.m * o.m * (o.n - 1.5 * o.m) >= 4e8));
+    /* Of 32 bits every step is taken by itself (pass_of has the errors).  Otherwise what a pass over X costs more than
+     * products of m rows has to be worth four launches of those, which are slower by themselves: 1,024 x 4,096 (2.7e9)
+     * 405 -> 330 us, 8 x 256 x 2,048 (8.7e8) 202 -> 174, 256 x 5,120 (3.1e8) 162 -> 155, 512 x 2,048 (3.4e8) 181 -> 178;
+     * below, 256 x 4,096 (2.4e8) 138 -> 143, 384 x 2,304 (2.6e8) 155 -> 162, 512 x 1,024 (6.7e7) 159 -> 174, 1,536 x
+     * 2,304 681 -> 765; but 768 x 2,048 (5.3e8) 221 -> 226.  64 x 20,000 148 -> 125. */
+    o.wide = s->dtype != MSIM_F32 && s->steps > 1 &&
+             (o.n >= 64 * o.m || (2 * o.n > 3 * o.m && (double)s->count * o.m * o.m * (o.n - 1.5 * o.m) >= 3e8));
     o.squares = o.wide ? 5 : 1;
     o.bytes = o.norm_bytes + 2 * o.x_bytes + (1 + o.squares) * o.p_bytes +
               std::max(o.square.part_bytes, std::max(o.poly.part_bytes, o.update.part_bytes));
@@ -417,9 +420,12 @@ const char *check_steps(const msim_orthogonalize_spec *s)
  * next step is (a + B) P (a + B), and X gets the product Q of all a + B.  That is 3
  * m^2 n a pass and 4 m^3 a step more (symmetric ones counted by their half),
  * instead of 3 m^2 n + m^3 a step.  Errors of 22 bits grow with P's small values
- * until P is made of X again: up to three steps from the start, where no value is
- * far above the others' reach yet, and two later leave five steps' result as near
- * as single ones do (2e-5 to 3e-4 of its mean magnitude, by the update's values). */
+ * until P is made of X again, so these are up to three steps from the start and two
+ * later.  Measured against 64 bits, relative to the norm: after two steps 3e-7 to
+ * 6e-7, single ones 0.9e-7 to 4e-7 and products of 32 bits 0.6e-7 to 5e-7; after five
+ * 1.4e-6 to 6.3e-6, 1.2e-6 to 2.8e-6 and 1.4e-6 to 6e-6 (70 x 4,481 to 1,024 x 4,096, noise, a
+ * momentum, singular values over three orders).  A hundredth of what a result of 16 bits
+ * is rounded by, but not for one of 32 bits. */
 uint32_t pass_of(const msim_orthogonalize_spec *s, bool wide, uint32_t k)
 {
     const uint32_t most = std::min(s->steps - k, !wide ? 1u : k == 0 ? 3u : 2u);

@@ -637,9 +637,12 @@ int msim_layer(const msim_layer_spec *spec, const void *x, const void *gate, con
  * X <- a X + (b X X^T + c (X X^T)^2) X; of a tall matrix on its transpose, which is
  * the same.  count matrices of rows x cols (contiguous) in one call, each by
  * itself.  out may be update.  Products are made from numbers of 22 bits (the sum
- * of two f16) with sums in 32; steps whose numbers would leave their range are
- * refused (MSIM_E_ARG), as singular values beyond 24 are.  A matrix that is not
- * finite gives NaN.  Limits: rows and cols <= MSIM_MAX_LINEAR, count <= 65,536,
+ * of two f16) with sums in 32: of a 32-bit update each step by itself, of a wide one
+ * of 16 bits up to three at a time (five steps end within 1e-5 of the norm before the
+ * result is rounded).  Those numbers have a lowest place, 2^-35 of X, so an update
+ * whose norm is far below eps has fewer bits.  Steps whose numbers would leave their
+ * range are refused (MSIM_E_ARG), as singular values beyond 24 are.  A matrix that is
+ * not finite gives NaN.  Limits: rows and cols <= MSIM_MAX_LINEAR, count <= 65,536,
  * steps <= 64, 2^36 elements.
  */
 typedef struct msim_orthogonalize_spec {

@@ -130,3 +130,54 @@ def test_linear_has_no_other_result(T, M, types, dt, act):  # noqa: F811
         tol = 1.13 * SUM(cols) * S + (2 ** -20) * (z.abs() + a.abs()) + 2 ** -23 * (a.abs() + r.double().abs()) + U[dt] * want.abs() \
             + (2.0 ** -25 if dt == "f16" else 0)
         assert bool(((y.double() - want).abs() <= tol).all()), (rows, cols, outs)
+
+
+def plain_steps(T, u, steps, dt):  # noqa: F811
+    """The definition in products of type dt."""
+    x = u.to(dt) if u.shape[-2] <= u.shape[-1] else u.to(dt).mT.contiguous()
+    x = (x / (x.double().square().sum((-1, -2), keepdim=True).sqrt() + 1e-7)).to(dt)
+    for _ in range(steps):
+        p = x @ x.mT.contiguous()
+        x = ABC[0] * x + (ABC[1] * p + ABC[2] * (p @ p)) @ x
+    return (x if u.shape[-2] <= u.shape[-1] else x.mT).double()
+
+
+@pytest.mark.parametrize("rows,cols", [(1024, 4096), (512, 2048), (256, 7168), (8003, 300), (70, 4481), (777, 3001), (1024, 2600), (64, 5000)])
+def test_updates_of_32_bits_are_as_near_as_products_of_32_bits(T, M, rows, cols):  # noqa: F811
+    """Numbers of 22 bits are rounded by 2^-23 where those of 32 bits are by 2^-24, at the same places of a step, and sums are of
+    32 bits in both: twice the error of plain products at most, by the norm, against 64 bits."""
+    g = gen(T, rows)
+    m = min(rows, cols)
+    rank = max(1, m // 8)
+    noise = T.randn(rows, cols, device=DEV, generator=g)
+    fall = noise * (T.logspace(0, -3, rows, device=DEV)[:, None] if rows <= cols else T.logspace(0, -3, cols, device=DEV))
+    strong = T.randn(rows, rank, device=DEV, generator=g) * T.logspace(0, -1, rank, device=DEV)
+    momentum = strong @ T.randn(rank, cols, device=DEV, generator=g) / math.sqrt(rank) + 0.3 * noise
+    for name, u in (("noise", noise), ("three orders", fall), ("momentum", momentum)):
+        for steps in (2, 3, 5):
+            want = orth64(T, u, steps, ABC)
+            plain, own = (float((y - want).norm() / want.norm()) for y in (plain_steps(T, u, steps, T.float32), M.orthogonalize(u, steps=steps).double()))
+            print(rows, cols, name, steps, plain, own, flush=True)
+            assert own <= 2 * plain + 2.0 ** -24, (name, steps, own, plain)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(1024, 4096), (256, 7168), (8003, 300), (70, 4481), (300, 301), (40, 900), (64, 5000), (3, 8192)])
+def test_updates_of_16_bits_are_off_by_their_rounding(T, M, types, dt, rows, cols):  # noqa: F811
+    """Five steps end within 1e-5 of the norm before the result is rounded, which is at most U[dt] of each element and half the
+    smallest f16 (2^-25) where that is more.  An element is then its exact value's rounding, but where that lies nearer to a
+    border than the error: of borders every s = 2 U[dt] 2^floor(log2 |x|), for at most 2 e / s of those elements, e = 1e-5
+    of the mean magnitude (a product of single f16, off by 1e-3, would miss most)."""
+    g = gen(T, cols)
+    u = (T.randn(rows, cols, device=DEV, generator=g) * T.logspace(0, -2, cols, device=DEV)).to(types[dt])
+    for steps in (1, 2, 5):
+        want = orth64(T, u, steps, ABC)
+        y = M.orthogonalize(u, steps=steps).double()
+        err = float((y - want).norm() / want.norm())
+        print(dt, rows, cols, steps, err, flush=True)
+        assert err <= 1e-5 + U[dt] + (2.0 ** -25 * math.sqrt(rows * cols) / float(want.norm()) if dt == "f16" else 0)
+        e = 1e-5 * float(want.square().mean().sqrt())
+        space = 2 * U[dt] * 2.0 ** want.abs().clamp_min(2.0 ** (-14 if dt == "f16" else -126)).log2().floor()
+        other, most = int((y != want.to(types[dt]).double()).sum()), float((2 * e / space).clamp_max(1).sum())
+        print(other, most, rows * cols, flush=True)
+        assert other <= most + 3 * math.sqrt(most) + 1 and most < 0.5 * rows * cols       # and that says something
