@@ -16,8 +16,6 @@ namespace msim {
  * of two f16, of which 32 columns lie as 32 high parts and 32 low ones */
 enum { M_F32 = MSIM_F32, M_F16 = MSIM_F16, M_BF16 = MSIM_BF16, M_SPLIT = 3 };
 
-constexpr uint32_t OUTSIDE = 0x80000000u;  /* an offset past every buffer: the load gives zeros */
-
 struct Operand {
     const char *at;
     uint64_t extent;             /* bytes that may be read from `at` on */
