@@ -10,6 +10,9 @@ namespace {
 
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 
+/* numbers as sums of two */
+template <int MODE> constexpr bool HALVES = MODE == M_SPLIT || MODE == M_PAIR;
+
 constexpr uint32_t OUTSIDE = 0x80000000u;  /* an offset past every buffer: the load gives zeros */
 
 /* BT rows (m or n) by 128 bytes of k (64 columns of 16 bits, 32 of 32 bits or of
@@ -57,8 +60,8 @@ template <int MODE, bool MC, int BT, int THREADS> struct Tile {
         k_end = MC ? K : K * ES;
         _Pragma("unroll") for (int i = 0; i < LOADS; i++) {
             const uint32_t c = i * THREADS + threadIdx.x, r = c / (W / 16), b = exchange(r, c % (W / 16) * 16);
-            /* of a split matrix 32 columns lie together, high parts and low ones */
-            const uint32_t col = MODE == M_SPLIT ? b / 128 * 32 : b / ES;
+            /* of halves 32 columns lie together, high parts and low ones */
+            const uint32_t col = HALVES<MODE> ? b / 128 * 32 : b / ES;
             const bool in = MC ? row0 + col < rows : row0 + r < rows;
             off[i] = in ? (uint32_t)(r * o.ld) + b : OUTSIDE;
         }
@@ -107,7 +110,7 @@ template <int MODE, bool MC, int BT> struct Reader {
         }
     }
 
-    /* Block i of 32 rows, step s of k (32 bytes; of a split matrix 32 of high parts
+    /* Block i of 32 rows, step s of k (32 bytes; of halves 32 of high parts
      * and 32 of low ones).  The rows of k that a lane reads have the same exchange;
      * row0 is a multiple of the wavefront's rows, so blocks are other bits of x. */
     __device__ __forceinline__ u32x4 get(const char *lds, int i, int s, int low) const
@@ -119,7 +122,7 @@ template <int MODE, bool MC, int BT> struct Reader {
             for (int e = 0; e < 4; e++) v[e] = *(const uint32_t *)(lds + base + (s * 8 + e) * T::W + (x ^ (i * 128)));
             return v;
         } else {
-            const uint32_t b = base + s * 16 * T::W + (x ^ (MODE == M_SPLIT ? i * 128 + low * 64 : i * 64));
+            const uint32_t b = base + s * 16 * T::W + (x ^ (HALVES<MODE> ? i * 128 + low * 64 : i * 64));
             typedef __attribute__((address_space(3))) i16x4 *ptr;
             const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(lds + b));
             const i16x4 c = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(lds + b + 4 * T::W));
@@ -136,7 +139,7 @@ template <int MODE> __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x
         const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
         for (int e = 0; e < 4; e++) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], y[e], c, 0, 0, 0);
         return c;
-    } else if constexpr (MODE == M_BF16)
+    } else if constexpr (MODE == M_BF16 || MODE == M_PAIR)
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -236,7 +239,7 @@ __device__ __forceinline__ void product(const GemmP &p, uint32_t total, uint32_t
 {
     constexpr int WAVES = THREADS / WAVE, WM = 2, WN = WAVES / WM;      /* wavefronts along m and n */
     constexpr int RM = BT / WM, RN = BT / WN, IM = RM / 32, IN = RN / 32;
-    constexpr int STEPS = MODE == M_SPLIT ? 2 : 4;
+    constexpr int STEPS = HALVES<MODE> ? 2 : 4;
     typedef Tile<MODE, AMC, BT, THREADS> TA;
     typedef Tile<MODE, BMC, BT, THREADS> TB;
     constexpr int STAGE = TA::BYTES + TB::BYTES;
@@ -276,11 +279,11 @@ __device__ __forceinline__ void product(const GemmP &p, uint32_t total, uint32_t
     };
     /* Fragments of a step; those of the next one are read while the matrix
      * instructions of this one run, across stages too. */
-    struct Step { u32x4 a[IM], b[IN], al[MODE == M_SPLIT ? IM : 1], bl[MODE == M_SPLIT ? IN : 1]; };
+    struct Step { u32x4 a[IM], b[IN], al[HALVES<MODE> ? IM : 1], bl[HALVES<MODE> ? IN : 1]; };
     const auto read = [&](const char *from, int k, Step &f) {
         _Pragma("unroll") for (int j = 0; j < IN; j++) f.b[j] = rb.get(from + TA::BYTES, j, k, 0);
         _Pragma("unroll") for (int i = 0; i < IM; i++) f.a[i] = ra.get(from, i, k, 0);
-        if constexpr (MODE == M_SPLIT) {
+        if constexpr (HALVES<MODE>) {
             _Pragma("unroll") for (int j = 0; j < IN; j++) f.bl[j] = rb.get(from + TA::BYTES, j, k, 1);
             _Pragma("unroll") for (int i = 0; i < IM; i++) f.al[i] = ra.get(from, i, k, 1);
         }
@@ -288,7 +291,7 @@ __device__ __forceinline__ void product(const GemmP &p, uint32_t total, uint32_t
     const auto multiply = [&](const Step &f) {
         _Pragma("unroll") for (int i = 0; i < IM; i++)
             _Pragma("unroll") for (int j = 0; j < IN; j++) acc[i][j] = mma<MODE>(f.b[j], f.a[i], acc[i][j]);
-        if constexpr (MODE == M_SPLIT) {
+        if constexpr (HALVES<MODE>) {
             _Pragma("unroll") for (int i = 0; i < IM; i++)
                 _Pragma("unroll") for (int j = 0; j < IN; j++) acc[i][j] = mma<MODE>(f.bl[j], f.a[i], acc[i][j]);
             _Pragma("unroll") for (int i = 0; i < IM; i++)
@@ -334,7 +337,7 @@ __device__ __forceinline__ void product(const GemmP &p, uint32_t total, uint32_t
     __syncthreads();
     const uint32_t l = lane & 31, ni = n0 + wn * RN;
     const auto room = [&](uint32_t i) -> char * { return i == 0 ? lds0 : i == 1 ? lds1 : i == 2 ? lds2 : lds3; };
-    if constexpr (MODE == M_F16 || MODE == M_BF16)
+    if constexpr (MODE != M_F32 && MODE != M_SPLIT)
         if (p.plain == 2) {
             /* nothing but a rounding: all rows of the wavefront at once, 16 bits each */
             typedef typename Type<MODE>::D D;

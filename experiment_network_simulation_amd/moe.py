@@ -403,7 +403,10 @@ def linear_backward(x: torch.Tensor, weight: torch.Tensor, grad: torch.Tensor, *
                     need_bias: bool = True, out: Optional[LinearGrads] = None, stream=None) -> LinearGrads:
     """The gradients of linear()'s x, weight and bias, given that of its result
     (float32 or x's type [rows, outs]; the residual's gradient is grad itself) and
-    for an activation what the forward pass kept in pre.  With out, those of its
+    for an activation what the forward pass kept in pre.  Through an activation,
+    and from a float32 grad of bfloat16 arrays, the gradient in front of the
+    products is rounded to x's type (half a step; the bias's is not); from a float32
+    grad of float16 ones it has 16 bits and float32's range.  With out, those of its
     tensors that are not None are written, whatever the need flags say."""
     dev, rows, cols, outs, xs, ws = _weights(x, weight)
     if not isinstance(grad, torch.Tensor) or grad.dtype not in (x.dtype, torch.float32):

@@ -591,7 +591,10 @@ int msim_linear(const msim_linear_spec *spec, const void *x, const void *weight,
  * (not read without an activation).  dx (at dx_stride) and dweight (at
  * dweight_stride) are of type dtype.  Any of dx, dweight and dbias may be NULL; x
  * may be without dweight, weight without dx.  d is rounded to dtype where it is
- * not there already (an activation, or a grad of 32 bits).  The slope of an
+ * not there already (an activation, or a grad of 32 bits), half a step of that type;
+ * dbias is the sum of what is not rounded.  f16 and a grad of 32 bits: d may be outside
+ * of f16, so d, x and weight are taken as sums of two bf16, 16 bits in the range of 32;
+ * an infinity in one of them then answers NaN.  The slope of an
  * infinite pre is its limit, 0 or 1; a NaN stays one.  rows = 0: dweight and dbias
  * are zeros.
  */

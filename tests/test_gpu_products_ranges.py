@@ -181,3 +181,36 @@ def test_updates_of_16_bits_are_off_by_their_rounding(T, M, types, dt, rows, col
         other, most = int((y != want.to(types[dt]).double()).sum()), float((2 * e / space).clamp_max(1).sum())
         print(other, most, rows * cols, flush=True)
         assert other <= most + 3 * math.sqrt(most) + 1 and most < 0.5 * rows * cols       # and that says something
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("low,high,size", [(-9, -9, 1000.0), (6, 6, 1e-4), (-8, 1, 300.0), (-30, -29, 60000.0), (0, 0, 1.0)])
+def test_f16_takes_gradients_in_the_range_of_32_bits(T, M, act, low, high, size):  # noqa: F811
+    """Rows of a 32-bit grad of 10^low .. 10^high, far outside f16.  Its parts hold 2^-18 of an element, and the product of two
+    low parts, 2^-18 of a term, is left out; three products a term make sums of three times as many."""
+    for n, (rows, cols, outs, pad) in enumerate([(5, 300, 40, 0), (260, 333, 65, 3), (1300, 104, 200, 0), (2050, 256, 264, 0), (70, 31, 1, 1)]):
+        g = gen(T, 400 + n)
+        x, w = wide(T, rows, cols, pad, real(T, g, T.float16, size)), wide(T, outs, cols, pad, real(T, g, T.float16, size))
+        x, w = x.clamp(-60000, 60000), w.clamp(-60000, 60000)
+        scale = 10.0 ** (low + (high - low) * T.rand(rows, 1, device=DEV, generator=g))
+        gr = wide(T, rows, outs, pad, lambda *s: scale * T.randn(*s, device=DEV, generator=g))
+        pre = None if act == "none" else wide(T, rows, outs, pad, real(T, g, T.float16, 2.0))
+        dx, dw, db = M.linear_backward(x, w, gr, act=act, pre=pre)
+        one_x = M.linear_backward(x, w, gr, act=act, pre=pre, need_weight=False, need_bias=False).x
+        one_w = M.linear_backward(x, w, gr, act=act, pre=pre, need_x=False, need_bias=False).weight
+        slope = T.ones_like(gr, dtype=T.float64) if pre is None else slope64(T, pre.double(), act)
+        d = gr.double() * slope
+        ed = gr.double().abs() * 2 ** -20 * (2 + (pre.double().abs() if pre is not None else 0)) + d.abs() * 2.0 ** -17
+        for what, both, alone, want, tol in (
+                ("x", dx, one_x, d @ w.double(), ed @ w.double().abs() + SUM(3 * outs + 96) * (d.abs() @ w.double().abs())),
+                ("weight", dw, one_w, d.T @ x.double(), ed.T @ x.double().abs() + SUM(3 * rows + 96) * (d.abs().T @ x.double().abs())),
+                ("bias", db, db, d.sum(0), ed.sum(0) + rows * 2 ** -24 * d.abs().sum(0))):
+            tol = tol + (U["f16"] * want.abs() + 2.0 ** -25 if what != "bias" else 2.0 ** -24 * want.abs())
+            fits = (want.abs() + tol < 65504) | (what == "bias")         # an f16 result; 65,520 and more is an infinity
+            over = (want.abs() - tol >= 65520) & ~fits
+            assert float(fits.double().mean()) > 0.9
+            for got in (both, alone):
+                off = float(((got.double() - want).abs() / tol).nan_to_num(math.inf)[fits].max())
+                assert T.equal(got[over], (want.sign() * math.inf)[over].half())
+                print(act, low, rows, cols, outs, what, off, float(want.abs().max()), flush=True)
+                assert off <= 1
