@@ -427,6 +427,8 @@ extern "C" int msim_layer(const msim_layer_spec *s, const void *x, const void *g
     if (s->route.rows == 0) return msim_route(&s->route, nullptr, bias, ids, weights, load, hip_stream);
     if (!x || !gate || !w_in || !w_out || !out || !ids || !weights) return fail(MSIM_E_ARG, "layer: null array");
     if (residual && s->route.rows > 1 && s->residual_stride < s->cols) return fail(MSIM_E_ARG, "layer: residual_stride below cols");
+    if (residual == out && s->route.rows > 1 && s->residual_stride != s->out_stride)
+        return fail(MSIM_E_ARG, "layer: residual is out, with two strides");
     const Layout l = layout_of(s);
     if (!workspace || workspace_bytes < l.bytes || (uintptr_t)workspace % 256)
         return fail(MSIM_E_WORKSPACE, "layer: workspace missing, too small or not on 256 bytes");

@@ -10,7 +10,7 @@ import sys
 import pytest
 
 from test_moe_launch import ROOT
-from test_products import AT, S, linear_spec, orth_spec  # noqa: F401
+from test_products import AT, E_ARG, S, layer_spec, linear_spec  # noqa: F401
 
 # grids of 2^32 work-items or more are refused, as the runtime refuses them
 RUNTIME = r"""
@@ -126,3 +126,12 @@ def test_norms_have_workgroups_for_elements_alone(launched):
              (1, 100, 8191, 0, 256)]
     for (count, rows, cols, dtype, norm), (rc, launches, why) in zip(sizes, launched([f"orth({c}, {r}, {k}, dtype={d})" for c, r, k, d, _ in sizes])):
         assert rc == 0 and launches[0] == [norm, 256], (count, rows, cols, launches[0])
+
+
+def test_a_layer_refuses_a_residual_that_is_out_with_another_stride(S):  # noqa: F811
+    """As msim_linear: a row of one would be written before it is read as another of the other.  Of one row strides do not count."""
+    lib, ws = S.load_library(), 1 << 40
+    for rows, want in ((4, E_ARG), (2, E_ARG)):
+        s = layer_spec(S, dict(rows=rows), out_stride=64, residual_stride=72)
+        assert lib.msim_layer(C.byref(s), AT, AT, None, AT, AT, None, 2 * AT, 2 * AT, AT, AT, None, AT, ws, None) == want
+        assert b"two strides" in lib.msim_last_error(None)
