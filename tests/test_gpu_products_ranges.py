@@ -214,3 +214,65 @@ def test_f16_takes_gradients_in_the_range_of_32_bits(T, M, act, low, high, size)
                 assert T.equal(got[over], (want.sign() * math.inf)[over].half())
                 print(act, low, rows, cols, outs, what, off, float(want.abs().max()), flush=True)
                 assert off <= 1
+
+
+@pytest.mark.parametrize("rows,cols,outs", [(9, 40, 24), (300, 136, 150)])
+def test_f16_gradients_carry_what_is_not_finite(T, M, rows, cols, outs):  # noqa: F811
+    """From a grad of 32 bits: an infinity or NaN reaches its row of dx, its row (of grad) or column (of x) of the weight's and its
+    element of the bias's gradient, and nothing else; the largest numbers are no infinity before they are in f16."""
+    g = gen(T, rows)
+    x, w, gr = real(T, g, T.float16)(rows, cols), real(T, g, T.float16)(outs, cols), real(T, g, T.float32)(rows, outs)
+    clean = M.linear_backward(x, w, gr)
+    for bad in (math.inf, -math.inf, math.nan):
+        x2, gr2 = x.clone(), gr.clone()
+        gr2[3, 2], gr2[4, 7], x2[5, 1] = bad, math.nan, bad
+        dx, dw, db = M.linear_backward(x2, w, gr2)
+        hit = T.zeros(rows, cols, dtype=T.bool, device=DEV)
+        hit[3], hit[4] = True, True
+        assert T.equal(dx[~hit], clean.x[~hit]) and not bool(dx[hit].isfinite().any())
+        hit = T.zeros(outs, cols, dtype=T.bool, device=DEV)
+        hit[2], hit[7], hit[:, 1] = True, True, True
+        assert T.equal(dw[~hit], clean.weight[~hit]) and not bool(dw[hit].isfinite().any())
+        hit = T.zeros(outs, dtype=T.bool, device=DEV)
+        hit[2], hit[7] = True, True
+        assert T.equal(db[~hit], clean.bias[~hit]) and not bool(db[hit].isfinite().any())
+    big, one = T.zeros(rows, outs, device=DEV), T.ones(outs, cols, device=DEV, dtype=T.float16)
+    big[0, 0], big[1, 1] = T.finfo(T.float32).max, -T.finfo(T.float32).max
+    dx = M.linear_backward(x, one, big, need_weight=False, need_bias=False).x
+    assert bool((dx[0] == math.inf).all()) and bool((dx[1] == -math.inf).all()) and not bool(dx[2:].any())
+    dx = M.linear_backward(x, one * 2.0 ** -24, big * 2.0 ** -100, need_weight=False, need_bias=False).x
+    assert bool((dx[0] == 16.0).all()) and bool((dx[1] == -16.0).all())
+
+
+def test_graph_of_f16_gradients(T, M):  # noqa: F811
+    """Captured from grads of 32 bits, with and without an activation, replayed on new inputs with eager work between."""
+    def inputs(seed):
+        g = gen(T, seed)
+        h, s = real(T, g, T.float16), real(T, g, T.float32, 1e-9)
+        return [h(700, 96), h(200, 96), s(700, 200), h(700, 200), h(5000, 40), h(24, 40), s(5000, 24)]
+
+    def run(x, w, gr, pre, x2, w2, gr2):
+        return [*M.linear_backward(x, w, gr, act="gelu", pre=pre), *M.linear_backward(x2, w2, gr2), M.linear_backward(x, w, gr, need_x=False).weight]
+
+    args = inputs(0)
+    run(*args)
+    T.cuda.synchronize()
+    graph = T.cuda.CUDAGraph()
+    with T.cuda.graph(graph):
+        out = run(*args)
+    for k in range(4):
+        fresh = inputs(1 + k)
+        for a, b in zip(args, fresh):
+            a.copy_(b)
+        want = run(*fresh)
+        if k % 2:
+            T.cuda.synchronize()
+        graph.replay()
+        again = run(*fresh)
+        T.cuda.synchronize()
+        assert all(T.equal(a, b) for a, b in zip(out, want)) and all(T.equal(a, b) for a, b in zip(again, want))
+    s = T.cuda.Stream()
+    s.wait_stream(T.cuda.current_stream())
+    got = M.linear_backward(*fresh[:3], act="gelu", pre=fresh[3], stream=s)
+    T.cuda.synchronize()
+    assert all(T.equal(a, b) for a, b in zip(got, want[:3]))
