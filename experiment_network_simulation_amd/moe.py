@@ -459,7 +459,8 @@ def layer(x: torch.Tensor, gate: torch.Tensor, w_in: torch.Tensor, w_out: torch.
     gate [experts, cols]; an expert answers w_out[e] h with h = act(a) * b, a and
     b the two halves of w_in[e] x; without gated, h = act(w_in[e] x).  w_in
     [experts, 2 hidden (or hidden), cols], w_out [experts, cols, hidden]; all of
-    x's type.  act as in linear().  mask (bool [rows]): False for rows of padding,
+    x's type, to which h is rounded (float16: an h above 65,504 is an infinity).  act
+    as in linear().  mask (bool [rows]): False for rows of padding,
     which route nowhere and get the residual alone, whatever x holds there.
     out.y may be residual."""
     dev, rows, cols, xs = _need_rows(x, "x")
@@ -519,7 +520,9 @@ def orthogonalize(update: torch.Tensor, *, steps: int = 5, coefficients=(3.4445,
     (contiguous), each with its singular values moved towards 1: X = update /
     (norm + eps), then `steps` times X = a X + (b X X^T + c (X X^T)^2) X.  With
     the default coefficients singular values from about 0.01 of the norm on end
-    within 0.7 .. 1.2.  out may be update."""
+    within 0.7 .. 1.2.  Products are of 22 bits, errors of float32 updates those of
+    float32 products; an update whose norm is far below eps has fewer bits.  out may
+    be update."""
     if not isinstance(update, torch.Tensor):
         raise TypeError("update must be a tensor")
     if update.dtype not in _DTYPES:
