@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmsim.so")
 SOURCES = [os.path.join(CSRC, f) for f in
-           ("msim_gemm_split.hip", "msim_gemm_pair.hip", "msim_gemm_bf16.hip", "msim_gemm_f16.hip", "msim_gemm_f32.hip", "msim_kernel.hip",
+           ("msim_gemm_split.hip", "msim_gemm_two.hip", "msim_gemm_bf16.hip", "msim_gemm_f16.hip", "msim_gemm_f32.hip", "msim_kernel.hip",
             "msim_probe.hip", "msim_moe.hip", "msim_linear.hip", "msim_orth.hip", "msim_layer.hip",
             "msim_plan.cpp", "msim_host.cpp")]
 ARCH = os.environ.get("MSIM_OFFLOAD_ARCH", "gfx950")

@@ -13,8 +13,8 @@
 namespace msim {
 
 /* element types of a product: the three of the library, and a number as the sum
- * of two f16 (M_SPLIT) or two bf16 (M_PAIR, results in f16), of which 32 columns lie as 32 high parts and 32 low ones */
-enum { M_F32 = MSIM_F32, M_F16 = MSIM_F16, M_BF16 = MSIM_BF16, M_SPLIT = 3, M_PAIR = 4 };
+ * of two f16 (M_SPLIT) or two bf16 (M_TWO, results in f16), of which 32 columns lie as 32 high parts and 32 low ones */
+enum { M_F32 = MSIM_F32, M_F16 = MSIM_F16, M_BF16 = MSIM_BF16, M_SPLIT = 3, M_TWO = 4 };
 
 struct Operand {
     const char *at;
@@ -155,7 +155,7 @@ __device__ __forceinline__ void store_split(const float *v, void *p, uint64_t at
 
 /* A number as the sum of two bf16: 16 bits of it, in the range of 32 bits; the 11 of an f16 whole.  What is not finite is so in
  * both products with the other number's parts, which makes it NaN. */
-__device__ __forceinline__ void store_pair(const float *v, void *p, uint64_t at)
+__device__ __forceinline__ void store_two(const float *v, void *p, uint64_t at)
 {
     u16x8 h, l;
     for (int i = 0; i < 8; i++) {

@@ -11,7 +11,7 @@ namespace {
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 
 /* numbers as sums of two */
-template <int MODE> constexpr bool HALVES = MODE == M_SPLIT || MODE == M_PAIR;
+template <int MODE> constexpr bool HALVES = MODE == M_SPLIT || MODE == M_TWO;
 
 constexpr uint32_t OUTSIDE = 0x80000000u;  /* an offset past every buffer: the load gives zeros */
 
@@ -139,7 +139,7 @@ template <int MODE> __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x
         const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
         for (int e = 0; e < 4; e++) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], y[e], c, 0, 0, 0);
         return c;
-    } else if constexpr (MODE == M_BF16 || MODE == M_PAIR)
+    } else if constexpr (MODE == M_BF16 || MODE == M_TWO)
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);

@@ -3,6 +3,6 @@
 
 namespace msim {
 
-template hipError_t launch_pair<M_PAIR>(GemmP, const Plan &, GemmP, const Plan &, const Columns &, hipStream_t);
+template hipError_t launch_pair<M_TWO>(GemmP, const Plan &, GemmP, const Plan &, const Columns &, hipStream_t);
 
 } // namespace msim

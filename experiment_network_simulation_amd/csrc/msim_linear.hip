@@ -62,7 +62,7 @@ template <int MODE, int MT, int WAVES> __global__ void __launch_bounds__(64 * WA
 /* operands that do not lie as the product reads them                        */
 /* ------------------------------------------------------------------------ */
 
-/* rows x cols of a strided matrix to rows of `wide` columns, zeros behind the last; PAIR: as sums of two bf16 */
+/* rows x cols of a strided matrix to rows of `wide` columns, zeros behind the last; TWO: as sums of two bf16 */
 struct PackP {
     const void *from;
     uint64_t ld;
@@ -70,18 +70,18 @@ struct PackP {
     uint32_t rows, cols, wide, blocks;
 };
 
-template <typename D, bool PAIR> __device__ __forceinline__ void pack_rows(const PackP &p, uint32_t block)
+template <typename D, bool TWO> __device__ __forceinline__ void pack_rows(const PackP &p, uint32_t block)
 {
-    constexpr uint32_t PER = PAIR ? 8 : 16 / sizeof(typename D::raw);
+    constexpr uint32_t PER = TWO ? 8 : 16 / sizeof(typename D::raw);
     const uint32_t turns = p.wide / PER;
     const uint64_t n = (uint64_t)p.rows * turns;
     _Pragma("unroll 2") for (uint64_t id = block * 256ull + threadIdx.x; id < n; id += p.blocks * 256ull) {
         const uint64_t r = id / turns;
         const uint32_t c = (uint32_t)(id - r * turns) * PER;
-        if constexpr (PAIR) {
+        if constexpr (TWO) {
             float v[8];
             load8<D>(v, p.from, r * p.ld + c, c < p.cols ? min(8u, p.cols - c) : 0);
-            store_pair(v, p.to, split_at(p.wide, (uint32_t)r, c));
+            store_two(v, p.to, split_at(p.wide, (uint32_t)r, c));
         } else
             *(u32x4 *)((typename D::raw *)p.to + r * p.wide + c) = piece<D>((const typename D::raw *)p.from + r * p.ld, c, p.cols);
     }
@@ -121,7 +121,7 @@ template <int N, bool FULL> __device__ __forceinline__ void slope_of(float *v, u
  * read it, and the sums of its columns over each workgroup's rows.  A workgroup
  * has `part` rows and 8 * lanes columns.  d is rounded to the operands' type,
  * as a matrix instruction reads it, half a step of that type; the sums are of what is
- * not rounded.  PAIR: a grad of 32 bits beside f16, whose range it may leave on both sides
+ * not rounded.  TWO: a grad of 32 bits beside f16, whose range it may leave on both sides
  * (a mean's over 10^5 rows has elements below 6e-8): d, x and weight as sums of two
  * bf16, 16 bits in the range of 32, and three products (8,192 x 1,024 -> 4,096 400 us, and
  * 177 of single f16; 2,047 x 1,000 -> 513 35 and 31). */
@@ -151,7 +151,7 @@ template <typename D> __device__ __forceinline__ auto raw8(const void *at, uint6
 
 /* The sums of a thread's eight columns (k of them there) over its rows, m and every `step`-th up to end, two of
  * which are read before the first is used; G: the type of grad. */
-template <typename D, typename G, bool PAIR> __device__ __forceinline__ void grad_columns(const GradP &p, uint32_t m, uint32_t step, uint32_t end, uint32_t n, uint32_t k, float *sum)
+template <typename D, typename G, bool TWO> __device__ __forceinline__ void grad_columns(const GradP &p, uint32_t m, uint32_t step, uint32_t end, uint32_t n, uint32_t k, float *sum)
 {
     constexpr uint32_t U = 2;
     for (; m < end; m += U * step) {
@@ -174,14 +174,14 @@ template <typename D, typename G, bool PAIR> __device__ __forceinline__ void gra
             }
             for (int i = 0; i < 8; i++) sum[i] += v[i];
             if (p.d) {
-                if constexpr (PAIR) store_pair(v, p.d, split_at(p.wide, row, n));
+                if constexpr (TWO) store_two(v, p.d, split_at(p.wide, row, n));
                 else store8<D>(v, p.d, (uint64_t)row * p.wide + n, 8);
             }
         }
     }
 }
 
-template <typename D, bool PAIR> __device__ __forceinline__ void grad_rows(const GradP &p, uint32_t block, float *part)
+template <typename D, bool TWO> __device__ __forceinline__ void grad_rows(const GradP &p, uint32_t block, float *part)
 {
     const uint32_t lanes = 1u << p.lglanes, cols = 8 * lanes;
     const uint32_t across = (p.wide + cols - 1) / cols, by = block / across, bx = block - by * across;
@@ -189,7 +189,7 @@ template <typename D, bool PAIR> __device__ __forceinline__ void grad_rows(const
     const uint32_t first = by * p.part + (threadIdx.x >> p.lglanes), step = 256u >> p.lglanes, end = min(p.rows, (by + 1) * p.part);
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (n < p.wide) {
-        if (PAIR || p.grad32) grad_columns<D, F32, PAIR>(p, first, step, end, n, k, sum);
+        if (TWO || p.grad32) grad_columns<D, F32, TWO>(p, first, step, end, n, k, sum);
         else grad_columns<D, D, false>(p, first, step, end, n, k, sum);
     }
     if (!p.sums) return;
@@ -205,12 +205,12 @@ template <typename D, bool PAIR> __device__ __forceinline__ void grad_rows(const
 }
 
 /* What the products of a call need first: x and weight packed, and the gradient. */
-template <typename D, bool PAIR> __global__ void __launch_bounds__(256) msim_linear_prepare(PackP x, PackP w, GradP g)
+template <typename D, bool TWO> __global__ void __launch_bounds__(256) msim_linear_prepare(PackP x, PackP w, GradP g)
 {
     __shared__ float part[4 * 256];
-    if (blockIdx.x < x.blocks) pack_rows<D, PAIR>(x, blockIdx.x);
-    else if (blockIdx.x < x.blocks + w.blocks) pack_rows<D, PAIR>(w, blockIdx.x - x.blocks);
-    else grad_rows<D, PAIR>(g, blockIdx.x - x.blocks - w.blocks, part);
+    if (blockIdx.x < x.blocks) pack_rows<D, TWO>(x, blockIdx.x);
+    else if (blockIdx.x < x.blocks + w.blocks) pack_rows<D, TWO>(w, blockIdx.x - x.blocks);
+    else grad_rows<D, TWO>(g, blockIdx.x - x.blocks - w.blocks, part);
 }
 
 /* ------------------------------------------------------------------------ */
@@ -227,14 +227,14 @@ bool ready(const void *at, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t s
     return (uintptr_t)at % 4 == 0 && cols * size % 16 == 0 && (rows <= 1 || (ld * size % 4 == 0 && ld * size <= MAX_LD));
 }
 
-/* A rows x cols matrix as an operand: as it lies, or packed at ws, as sums of two bf16 if it is a pair. */
+/* A rows x cols matrix as an operand: as it lies, or packed at ws, as sums of two bf16 (two). */
 struct Matrix {
     const void *at;
     uint64_t rows, cols, ld;
     uint32_t size;
-    bool packed, pair;
-    uint64_t wide() const { return pair ? up(cols, 32) : packed ? up(cols, 16 / size) : cols; }
-    uint64_t row() const { return wide() * (pair ? 4 : size); }
+    bool packed, two;
+    uint64_t wide() const { return two ? up(cols, 32) : packed ? up(cols, 16 / size) : cols; }
+    uint64_t row() const { return wide() * (two ? 4 : size); }
     uint64_t bytes() const { return packed ? up(rows * row(), 256) : 0; }
     Operand operand(const char *ws) const
     {
@@ -243,22 +243,22 @@ struct Matrix {
     }
 };
 
-Matrix matrix_of(const void *at, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t size, bool pair = false)
+Matrix matrix_of(const void *at, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t size, bool two = false)
 {
-    return {at, rows, cols, ld, size, pair || !ready(at, rows, cols, ld, size), pair};
+    return {at, rows, cols, ld, size, two || !ready(at, rows, cols, ld, size), two};
 }
 
 PackP pack_of(const Matrix &m, char *ws)
 {
     if (!m.packed || !m.rows) return {};
-    const uint64_t n = m.rows * m.wide() / (m.pair ? 8 : 16 / m.size);
+    const uint64_t n = m.rows * m.wide() / (m.two ? 8 : 16 / m.size);
     return {m.at, m.ld, ws, (uint32_t)m.rows, (uint32_t)m.cols, (uint32_t)m.wide(), (uint32_t)std::min<uint64_t>((n + 511) / 512, 1u << 14)};
 }
 
-template <typename D, bool PAIR = false> hipError_t prepare(const PackP &x, const PackP &w, const GradP &g, hipStream_t st)
+template <typename D, bool TWO = false> hipError_t prepare(const PackP &x, const PackP &w, const GradP &g, hipStream_t st)
 {
     const uint32_t grid = x.blocks + w.blocks + g.blocks;
-    return grid ? launch(msim_linear_prepare<D, PAIR>, grid, 256, 0, st, x, w, g) : hipSuccess;
+    return grid ? launch(msim_linear_prepare<D, TWO>, grid, 256, 0, st, x, w, g) : hipSuccess;
 }
 
 const char *check_linear(const msim_linear_spec *s, int *code)
@@ -346,7 +346,7 @@ int run_forward(const msim_linear_spec *s, const Forward &f, const Epilogue &e, 
 struct Backward {
     Matrix x, w;
     bool own;                    /* d is made: an activation, another type, or a grad that does not lie as it is read */
-    bool pair;                   /* operands as sums of two bf16: f16 and a grad of 32 bits */
+    bool two;                    /* operands as sums of two bf16: f16 and a grad of 32 bits */
     uint64_t wide, row;          /* columns of d, bytes of a row */
     uint64_t d_bytes, sum_bytes;
     uint32_t blocks, part;       /* of rows, for the sums, and rows of one */
@@ -360,12 +360,12 @@ Backward backward_of(const msim_linear_spec *s, const void *x, const void *weigh
     const uint32_t size = size_of(s->dtype);
     dx &= s->rows != 0;
     const bool need = dx || dw;
-    b.pair = need && s->dtype == MSIM_F16 && s->out_dtype == MSIM_F32;
-    if (dw) b.x = matrix_of(x, s->rows, s->cols, s->x_stride, size, b.pair);
-    if (dx) b.w = matrix_of(weight, s->outs, s->cols, s->weight_stride, size, b.pair);
+    b.two = need && s->dtype == MSIM_F16 && s->out_dtype == MSIM_F32;
+    if (dw) b.x = matrix_of(x, s->rows, s->cols, s->x_stride, size, b.two);
+    if (dx) b.w = matrix_of(weight, s->outs, s->cols, s->weight_stride, size, b.two);
     b.own = need && (s->act || s->out_dtype != s->dtype || !ready(grad, s->rows, s->outs, s->out_stride, size));
-    b.wide = b.own ? up(s->outs, b.pair ? 32 : 8) : s->outs;
-    b.row = b.wide * (b.pair ? 4 : size);
+    b.wide = b.own ? up(s->outs, b.two ? 32 : 8) : s->outs;
+    b.row = b.wide * (b.two ? 4 : size);
     /* a thread has 8 columns: two rows of them at least where there are several workgroups of rows, of which there are about
      * 1,024 at most */
     uint32_t lanes = 1;
@@ -375,7 +375,7 @@ Backward backward_of(const msim_linear_spec *s, const void *x, const void *weigh
     b.d_bytes = b.own ? up(s->rows * b.row, 256) : 0;
     b.sum_bytes = db ? up((uint64_t)b.blocks * s->outs * 4, 256) : 0;
     const Product x1 = {s->rows, s->cols, b.wide, 1}, w1 = {s->outs, s->cols, s->rows, 1};
-    const uint32_t mode = b.pair ? (uint32_t)M_PAIR : s->dtype;
+    const uint32_t mode = b.two ? (uint32_t)M_TWO : s->dtype;
     if (dx && dw) plan_pair(mode, x1, w1, &b.px, &b.pw);
     else if (dx) b.px = plan_of(mode, x1);
     else if (dw) b.pw = plan_of(mode, w1);
@@ -398,7 +398,7 @@ int run_backward(const msim_linear_spec *s, const Backward &b, const void *grad,
         while (g.lglanes < (b.blocks == 1 ? 2 : 5) && (8u << g.lglanes) < g.wide) g.lglanes++;
         g.blocks = b.blocks * ((g.wide + (8u << g.lglanes) - 1) / (8u << g.lglanes));
     }
-    hipError_t r = prepare<D, MODE == M_PAIR>(dweight ? pack_of(b.x, wx) : PackP{}, dx ? pack_of(b.w, ww) : PackP{}, g, st);
+    hipError_t r = prepare<D, MODE == M_TWO>(dweight ? pack_of(b.x, wx) : PackP{}, dx ? pack_of(b.w, ww) : PackP{}, g, st);
     const Columns c = dbias && b.blocks != 1 ? Columns{(const float *)wsum, b.blocks, s->outs, dbias} : Columns{};
     const Operand d = b.own ? Operand{wd, s->rows * b.row, b.row, 0}
                             : Matrix{grad, s->rows, s->outs, s->out_stride, size, false, false}.operand(nullptr);
@@ -499,7 +499,7 @@ extern "C" int msim_linear_backward(const msim_linear_spec *s, const void *x, co
     char *ws = (char *)workspace;
     hipStream_t st = (hipStream_t)hip_stream;
     return s->dtype == MSIM_F32 ? run_backward<M_F32>(s, b, grad, pre, dx, dweight, dbias, ws, st)
-        : b.pair ? run_backward<M_PAIR>(s, b, grad, pre, dx, dweight, dbias, ws, st)
+        : b.two ? run_backward<M_TWO>(s, b, grad, pre, dx, dweight, dbias, ws, st)
         : s->dtype == MSIM_F16 ? run_backward<M_F16>(s, b, grad, pre, dx, dweight, dbias, ws, st)
                                : run_backward<M_BF16>(s, b, grad, pre, dx, dweight, dbias, ws, st);
 }

@@ -594,9 +594,9 @@ int msim_linear(const msim_linear_spec *spec, const void *x, const void *weight,
  * not there already (an activation, or a grad of 32 bits), half a step of that type;
  * dbias is the sum of what is not rounded.  f16 and a grad of 32 bits: d may be outside
  * of f16, so d, x and weight are taken as sums of two bf16, 16 bits in the range of 32;
- * an infinity in one of them then answers NaN.  The slope of an
- * infinite pre is its limit, 0 or 1; a NaN stays one.  rows = 0: dweight and dbias
- * are zeros.
+ * an infinity in one of them then answers NaN.  The slope of an infinite pre is its
+ * limit, 0 or 1; a NaN stays one.  rows = 0: dweight and dbias are zeros, and no array
+ * is read.
  */
 int msim_linear_backward_workspace(const msim_linear_spec *spec, const void *x, const void *weight, const void *grad,
                                    uint32_t dx, uint32_t dweight, uint32_t dbias, uint64_t *bytes);
@@ -612,10 +612,11 @@ int msim_linear_backward(const msim_linear_spec *spec, const void *x, const void
  * half of it); out = y + residual.  x, out, residual: rows x cols of type dtype;
  * gate: experts x cols, w_in: experts x (hidden, gated: 2 hidden) x cols, w_out:
  * experts x cols x hidden, all of type dtype and contiguous.  h is rounded to
- * dtype (of f16, above 65,504 to an infinity), the sums are not.  mask (may be NULL): one byte a row; a row with 0 is padding, whatever x
- * holds there: ids -1, weights 0, y 0.  A row that the router voids (a NaN logit)
- * has y NaN.  bias is msim_route's.  route.dtype is MSIM_F32 and route.row_stride
- * is route.experts.  Only chosen experts' weights are read.  residual may be out.
+ * dtype (of f16, above 65,504 to an infinity), the sums are not.  mask (may be
+ * NULL): one byte a row; a row with 0 is padding, whatever x holds there: ids -1,
+ * weights 0, y 0.  A row that the router voids (a NaN logit) has y NaN.  bias is
+ * msim_route's.  route.dtype is MSIM_F32 and route.row_stride is route.experts.  Only
+ * chosen experts' weights are read.  residual may be out, at the same stride.
  * Limits: msim_route's, rows <= MSIM_MAX_LAYER_ROWS, cols and hidden <=
  * MSIM_MAX_LINEAR, experts times either below 2^24.
  */
