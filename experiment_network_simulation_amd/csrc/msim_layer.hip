@@ -25,9 +25,9 @@ struct LayerP {
     const int32_t *ids;
     const float *weights;
     int32_t *load;               /* tokens of each expert */
-    void *h;                     /* [rows * top_k][h_ld], of the layer's type */
+    void *h;                     /* [rows * top_k][h_ld], of the layer's type; of f16 low parts follow, h_low elements on */
     float *part;                 /* [rows * top_k][part_ld] */
-    uint64_t x_ld, out_ld, res_ld, h_ld, part_ld;
+    uint64_t x_ld, out_ld, res_ld, h_ld, h_low, part_ld;
     uint32_t rows, E, K, C, F, act, gated;
     /* Of a product.  slots: assignments, of which the first that names an expert has it, if they are fewer than
      * experts; otherwise experts.  tiles of weight rows. */
@@ -98,9 +98,26 @@ template <int WAVES> __device__ __forceinline__ uint32_t tokens_of(const LayerP 
     return min(have, MAX_ROWS);
 }
 
+/* Hidden units are rounded to the layer's type, as matrix instructions read them, half a step of it.  In f16 a product of two
+ * halves is soon above 65,504, so there they are held in two parts, HIGH times the first and the second: 22 bits, and
+ * up to 2.7e8.  16 vectors of a matrix instruction of the second product are both parts of 8 tokens: no more time
+ * up to 8 tokens an expert, and then (100 x 1,000, 3 of 24 experts 33.5 -> 38.6 us, 512 x 2,048, 6 of 64 315 -> 396)
+ * what bf16 is spared, whose range is that of 32 bits. */
+template <typename D> constexpr bool PARTS = std::is_same<D, F16>::value;
+constexpr float HIGH = 4096.0f;
+template <typename D> constexpr uint32_t TOKENS = PARTS<D> ? 8 : 16;      /* of 16 vectors */
+
+/* 16 vectors of the second product: row(t) is where token t's first part begins, t < TOKENS */
+template <typename D> struct Hidden : std::conditional<PARTS<D>, RowsOfTwo<D>, Rows<D>>::type {
+    template <typename F> __device__ __forceinline__ void of(const LayerP &p, F row)
+    {
+        if constexpr (PARTS<D>) this->set(p.h_low, row);
+        else this->set(row);
+    }
+};
+
 /* Four hidden units from f on (16 more of them 16 further, without a gate) of what
- * goes into a token's row h of the second product, rounded to the layer's type, as
- * its matrix instructions read it.  h has room to a multiple of 8. */
+ * goes into a token's row h of the second product.  h has room to a multiple of 8. */
 template <typename D> __device__ __forceinline__ void hidden_of(const LayerP &p, const f32x4 *sums, uint32_t f, typename D::raw *h)
 {
     for (uint32_t j = 0; j < (p.gated ? 1 : 2); j++, f += 16) {
@@ -108,7 +125,15 @@ template <typename D> __device__ __forceinline__ void hidden_of(const LayerP &p,
         float v[4];
         for (int k = 0; k < 4; k++) v[k] = j ? sums[1][k] : sums[0][k];
         act_of<4, std::is_same<D, F32>::value>(v, p.act);
-        for (int k = 0; k < 4; k++) h[f + k] = D::put(p.gated ? v[k] * sums[1][k] : v[k]);
+        for (int k = 0; k < 4; k++) {
+            const float x = p.gated ? v[k] * sums[1][k] : v[k];
+            const typename D::raw high = D::put(PARTS<D> ? x * (1.0f / HIGH) : x);
+            h[f + k] = high;
+            if constexpr (PARTS<D>) {
+                const float y = D::get(high) * HIGH;
+                h[p.h_low + f + k] = fabsf(y) < INFINITY ? D::put(x - y) : typename D::raw(0);
+            }
+        }
     }
 }
 
@@ -135,27 +160,39 @@ __device__ __forceinline__ void up_tokens(const LayerP &p, int32_t expert, uint3
     }
 }
 
-/* 32 columns of what one expert answers to up to 16 MT of its tokens, in 32 bits */
+/* what both parts of a hidden row gave, in the lanes of the first: lane ^ 8 has the second */
+template <typename D> __device__ __forceinline__ f32x4 whole(f32x4 v)
+{
+    if constexpr (PARTS<D>)
+        for (int k = 0; k < 4; k++) v[k] = HIGH * v[k] + __shfl_xor(v[k], 8);
+    return v;
+}
+
+/* 32 columns of what one expert answers to up to TOKENS MT of its tokens, in 32 bits */
 template <typename D, int MT, int WAVES>
 __device__ __forceinline__ void down_tokens(const LayerP &p, int32_t expert, uint32_t tile, const uint32_t *list, uint32_t n, char *lds)
 {
     typedef typename D::raw raw;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
     const uint32_t c0 = tile * 32;
-    Rows<D> w[2], x[MT];
+    Rows<D> w[2];
+    Hidden<D> x[MT];
     const raw *base = (const raw *)p.w_out + (uint64_t)expert * p.C * p.F;
     for (int j = 0; j < 2; j++) w[j].set([&](uint32_t r) { return base + (uint64_t)min(c0 + j * 16 + r, p.C - 1) * p.F; });
-    for (int i = 0; i < MT; i++) x[i].set([&](uint32_t r) { return (const raw *)p.h + (uint64_t)list[min(i * 16 + r, n - 1)] * p.h_ld; });
+    constexpr uint32_t T = TOKENS<D>;
+    for (int i = 0; i < MT; i++) x[i].of(p, [&](uint32_t t) { return (const raw *)p.h + (uint64_t)list[min(i * T + t, n - 1)] * p.h_ld; });
     f32x4 acc[MT][2];
     for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
     stream<D, MT, 2, WAVES>(w, x, p.F, wave, lds + wave * STREAM_LDS<MT, 2>, acc);
     join<MT, 2, WAVES>(lds, wave, acc);
     _Pragma("unroll") for (int i = 0; i < MT; i++) {
-        if (i % WAVES != (int)wave || i * 16 + l >= n) continue;
-        float *to = p.part + (uint64_t)list[i * 16 + l] * p.part_ld;
+        if (i % WAVES != (int)wave) continue;
+        const f32x4 y[2] = {whole<D>(acc[i][0]), whole<D>(acc[i][1])};
+        if (l >= T || i * T + l >= n) continue;
+        float *to = p.part + (uint64_t)list[i * T + l] * p.part_ld;
         for (int j = 0; j < 2; j++) {
             const uint32_t c = c0 + j * 16 + (lane >> 4) * 4;
-            if (c < p.C) *(f32x4 *)(to + c) = acc[i][j];       /* rows of part have room to a multiple of 4 */
+            if (c < p.C) *(f32x4 *)(to + c) = y[j];            /* rows of part have room to a multiple of 4 */
         }
     }
 }
@@ -223,15 +260,17 @@ template <typename D> __global__ void __launch_bounds__(64 * FEW_WAVES) msim_lay
         const int32_t expert = __builtin_amdgcn_readlane(id, k);
         if (expert < 0) continue;
         const raw *base = (const raw *)p.w_out + (uint64_t)expert * p.C * p.F;
-        Rows<D> w[2], x[1];
+        Rows<D> w[2];
+        Hidden<D> x[1];
         for (int j = 0; j < 2; j++) w[j].set([&](uint32_t r) { return base + (uint64_t)min(c0 + j * 16 + r, p.C - 1) * p.F; });
-        x[0].set([&](uint32_t) { return (const raw *)p.h + (uint64_t)(t * p.K + k) * p.h_ld; });
+        x[0].of(p, [&](uint32_t) { return (const raw *)p.h + (uint64_t)(t * p.K + k) * p.h_ld; });
         f32x4 acc[1][2] = {};
         stream_run<D, 1, 2>(w, x, i % runs * RUN<D>, p.F, sums + wave * STREAM_LDS<1, 2>, acc);
         const float s = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, share), k));
         for (int m = 0; m < 2; m++) y[0][m] += s * acc[0][m];
     }
     join<1, 2, FEW_WAVES>(sums, wave, y);
+    for (int m = 0; m < 2; m++) y[0][m] = whole<D>(y[0][m]);
     const bool is_void = __any(share != share);        /* by the router */
     if (wave != 0 || l != 0) return;
     for (uint32_t i = 0; i < 8; i++) {
@@ -267,10 +306,11 @@ __device__ __forceinline__ int32_t expert_of(const LayerP &p, uint32_t run, uint
 
 /* MT: tokens of a run, in 16; fewer take leaner code.  WAVES: k is shared among them.  Bound by reading the
  * weights: 32 x 7,168, 8 of 128 experts bf16 takes 7.7 GB in 790 + 396 us, 6.4 TB/s. */
-template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bounds__(64 * WAVES, MT <= 2 ? 3 : 2) msim_layer_product(LayerP p)
+template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bounds__(64 * WAVES, MT * (DOWN && PARTS<D> ? 2 : 1) <= 2 ? 3 : 2) msim_layer_product(LayerP p)
 {
+    constexpr int MORE = DOWN && PARTS<D> ? 2 : 1;       /* vectors a token */
     __shared__ uint32_t list[MAX_ROWS], counts[WAVES];
-    __shared__ __attribute__((aligned(16))) char sums[WAVES * STREAM_LDS<MT, 2>];
+    __shared__ __attribute__((aligned(16))) char sums[WAVES * STREAM_LDS<MORE * MT, 2>];
     const uint32_t run = blockIdx.x / p.tiles, tile = blockIdx.x - run * p.tiles;
     uint32_t own = 0;
     const int32_t expert = p.rows > 16 * MT ? expert_of(p, run, 16 * MT, own) : p.slots < p.E ? p.ids[run] : p.load[run] ? (int32_t)run : -1;
@@ -282,9 +322,10 @@ template <typename D, int MT, int WAVES, bool DOWN> __global__ void __launch_bou
         if constexpr (DOWN) down_tokens<D, mt.value, WAVES>(p, expert, tile, list + first, n, sums);
         else up_tokens<D, mt.value, WAVES>(p, expert, tile, list + first, n, sums);
     };
-    if (n <= 16) part(std::integral_constant<int, 1>());
-    else if (MT > 2 && n <= 32) part(std::integral_constant<int, 2>());
-    else part(std::integral_constant<int, MT>());
+    if (MORE == 2 && n <= 8) part(std::integral_constant<int, 1>());
+    else if (n <= 16) part(std::integral_constant<int, MORE>());
+    else if (MT > 2 && n <= 32) part(std::integral_constant<int, MORE * 2>());
+    else part(std::integral_constant<int, MORE * MT>());
 }
 
 /* The weighted sum over a token's choices, in their order, and the residual.  A
@@ -325,7 +366,7 @@ Layout layout_of(const msim_layer_spec *s)
     l.h_ld = up(s->hidden, 8);
     l.part_ld = up(s->cols, 4);
     l.logits = up(s->route.rows * s->route.experts * 4, 256);
-    l.h = up(n * l.h_ld * (s->dtype == MSIM_F32 ? 4 : 2), 256);
+    l.h = up(n * l.h_ld * (s->dtype == MSIM_BF16 ? 2 : 4), 256);         /* of f16 two parts */
     l.part = up(n * l.part_ld * 4, 256);
     l.load = up(s->route.experts * 4ull, 256);
     l.bytes = l.logits + l.h + l.part + l.load;
@@ -358,7 +399,11 @@ template <typename D, bool DOWN> hipError_t launch_product(LayerP p, uint64_t ti
     /* runs of up to 64 tokens read an expert's weights once more seldom, those of 32 leave room for half as many wavefronts
      * again: 200 x 2,048, 6 of 64 experts bf16 (19 tokens each) 289 us in runs of 64, 271 of 32, with 512 rows (48) 424 and
      * 442; 400 x 7,168, 8 of 128 (25) 2,490 and 2,580 */
-    const uint32_t mt = p.rows <= 16 ? 1 : p.rows <= 32 || p.rows * p.K <= 24 * p.E ? 2 : 4;
+    constexpr bool MORE = DOWN && PARTS<D>;
+    uint32_t mt = p.rows <= 16 ? 1 : p.rows <= 32 || p.rows * p.K <= 24 * p.E ? 2 : 4;
+    /* two vectors a token: as many tokens a run as without, half of them (100 x 1,000, 3 of 24 experts f16 38.6 us in runs
+     * of 16, 40.7 of 32; 200 x 7,168, 8 of 128 (13) 2,155 and 2,220, 250 (16) 2,455 and 2,442; 8 blocks of vectors spill) */
+    if (MORE && mt > 1) mt = p.rows * p.K <= 16 * p.E ? 1 : 2;
     p.tiles = (uint32_t)tiles;
     /* a run for each expert that may be chosen, and one more for every 16 mt assignments */
     const uint32_t grid = (p.slots + (p.rows <= 16 * mt ? 0 : p.rows * p.K / (16 * mt))) * p.tiles;
@@ -367,11 +412,12 @@ template <typename D, bool DOWN> hipError_t launch_product(LayerP p, uint64_t ti
     if (grid < 1024 && ((DOWN ? p.F : p.C) + RUN<D> - 1) / RUN<D> > 8) {
         if (mt == 1) return launch(msim_layer_product<D, 1, 16, DOWN>, grid, 1024, 0, st, p);
         if (mt == 2) return launch(msim_layer_product<D, 2, 8, DOWN>, grid, 512, 0, st, p);
-        return launch(msim_layer_product<D, 4, 8, DOWN>, grid, 512, 0, st, p);
+        if constexpr (!MORE) return launch(msim_layer_product<D, 4, 8, DOWN>, grid, 512, 0, st, p);
     }
     if (mt == 1) return launch(msim_layer_product<D, 1, 4, DOWN>, grid, 256, 0, st, p);
     if (mt == 2) return launch(msim_layer_product<D, 2, 4, DOWN>, grid, 256, 0, st, p);
-    return launch(msim_layer_product<D, 4, 4, DOWN>, grid, 256, 0, st, p);
+    if constexpr (!MORE) return launch(msim_layer_product<D, 4, 4, DOWN>, grid, 256, 0, st, p);
+    return hipErrorInvalidValue;
 }
 
 template <typename D> int run_layer(const msim_layer_spec *s, LayerP p, const float *bias, int32_t *ids, float *weights, hipStream_t st)
@@ -434,7 +480,7 @@ extern "C" int msim_layer(const msim_layer_spec *s, const void *x, const void *g
         return fail(MSIM_E_WORKSPACE, "layer: workspace missing, too small or not on 256 bytes");
     char *ws = (char *)workspace;
     const LayerP p = {x, gate, w_in, w_out, residual, mask, out, (float *)ws, ids, weights, load ? load : (int32_t *)(ws + l.logits + l.h + l.part), ws + l.logits,
-                      (float *)(ws + l.logits + l.h), s->x_stride, s->out_stride, s->residual_stride, l.h_ld, l.part_ld,
+                      (float *)(ws + l.logits + l.h), s->x_stride, s->out_stride, s->residual_stride, l.h_ld, s->route.rows * s->route.top_k * l.h_ld, l.part_ld,
                       (uint32_t)s->route.rows, s->route.experts, s->route.top_k, s->cols, s->hidden, s->act, s->gated, 0, 0};
     hipStream_t st = (hipStream_t)hip_stream;
     return s->dtype == MSIM_F32 ? run_layer<F32>(s, p, bias, ids, weights, st)

@@ -71,6 +71,19 @@ template <typename D> struct Rows {
     {
         for (uint32_t u = 0; u < 4; u++) at[u] = row(4 * u + ((threadIdx.x & 63) >> 4));
     }
+    __device__ __forceinline__ const typename D::raw *operator[](uint32_t u) const { return at[u]; }
+};
+
+/* Rows 8 to 15 of the block lie `low` elements behind rows 0 to 7: half as many addresses. */
+template <typename D> struct RowsOfTwo {
+    const typename D::raw *at[2];
+    uint64_t low;
+    template <typename F> __device__ __forceinline__ void set(uint64_t behind, F row)
+    {
+        low = behind;
+        for (uint32_t u = 0; u < 2; u++) at[u] = row(4 * u + ((threadIdx.x & 63) >> 4));
+    }
+    __device__ __forceinline__ const typename D::raw *operator[](uint32_t u) const { return at[u & 1] + (u & 2 ? low : 0); }
 };
 
 /* LDS of a wavefront: what its lanes exchange, and then its sums for join() */
@@ -120,18 +133,18 @@ enum { WHOLE, END, SHORT };
  * the first is used, which the compiler would not do by itself (32 tokens of 7,168
  * columns, 8 of 128 experts 1,430 -> 1,286 us); those of further vectors when a block before
  * them has been used, in its registers. */
-template <typename D, int MT, int NT, int N, int WHERE>
-__device__ __forceinline__ void stream_runs(const Rows<D> *w, const Rows<D> *x, uint32_t k, uint32_t step, uint32_t K, char *lds, f32x4 (&acc)[MT][NT])
+template <typename D, int MT, int NT, int N, int WHERE, typename X>
+__device__ __forceinline__ void stream_runs(const Rows<D> *w, const X *x, uint32_t k, uint32_t step, uint32_t K, char *lds, f32x4 (&acc)[MT][NT])
 {
     constexpr uint32_t PER = 16 / sizeof(typename D::raw);
     constexpr int AHEAD = MT < 2 ? MT : 2;
     const uint32_t c = k + (threadIdx.x & 15) * PER, at = WHERE == END ? min(c, K - PER) : c, early = c - at;
     const bool cut = K % PER;                  /* a piece has both elements and none */
     u32x4 a[N][NT][4], b[N][AHEAD][4];
-    const auto load = [&](const Rows<D> &r, int n, u32x4 (&v)[4]) {
+    const auto load = [&](const auto &r, int n, u32x4 (&v)[4]) {
         _Pragma("unroll") for (int u = 0; u < 4; u++) {
-            if constexpr (WHERE == SHORT) v[u] = short_row<D>(r.at[u], c ? 0 : K);
-            else v[u] = piece<D>(r.at[u] + at + n * step);
+            if constexpr (WHERE == SHORT) v[u] = short_row<D>(r[u], c ? 0 : K);
+            else v[u] = piece<D>(r[u] + at + n * step);
         }
     };
     const auto give = [&](u32x4 (&v)[4]) {
@@ -158,8 +171,8 @@ __device__ __forceinline__ void stream_runs(const Rows<D> *w, const Rows<D> *x, 
 }
 
 /* one run, or what there is of it */
-template <typename D, int MT, int NT>
-__device__ __forceinline__ void stream_run(const Rows<D> *w, const Rows<D> *x, uint32_t k, uint32_t K, char *lds, f32x4 (&acc)[MT][NT])
+template <typename D, int MT, int NT, typename X>
+__device__ __forceinline__ void stream_run(const Rows<D> *w, const X *x, uint32_t k, uint32_t K, char *lds, f32x4 (&acc)[MT][NT])
 {
     if (k + RUN<D> <= K) stream_runs<D, MT, NT, 1, WHOLE>(w, x, k, 0, K, lds, acc);
     else if (K * sizeof(typename D::raw) >= 16) stream_runs<D, MT, NT, 1, END>(w, x, k, 0, K, lds, acc);
@@ -167,8 +180,8 @@ __device__ __forceinline__ void stream_run(const Rows<D> *w, const Rows<D> *x, u
 }
 
 /* the wavefront's share of k, every WAVES-th run: of few vectors two at a time, where their loads fit its registers */
-template <typename D, int MT, int NT, int WAVES>
-__device__ __forceinline__ void stream(const Rows<D> *w, const Rows<D> *x, uint32_t K, uint32_t wave, char *lds, f32x4 (&acc)[MT][NT])
+template <typename D, int MT, int NT, int WAVES, typename X>
+__device__ __forceinline__ void stream(const Rows<D> *w, const X *x, uint32_t K, uint32_t wave, char *lds, f32x4 (&acc)[MT][NT])
 {
     uint32_t k = wave * RUN<D>;
     const uint32_t step = WAVES * RUN<D>;

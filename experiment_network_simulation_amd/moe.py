@@ -459,8 +459,8 @@ def layer(x: torch.Tensor, gate: torch.Tensor, w_in: torch.Tensor, w_out: torch.
     gate [experts, cols]; an expert answers w_out[e] h with h = act(a) * b, a and
     b the two halves of w_in[e] x; without gated, h = act(w_in[e] x).  w_in
     [experts, 2 hidden (or hidden), cols], w_out [experts, cols, hidden]; all of
-    x's type, to which h is rounded (float16: an h above 65,504 is an infinity).  act
-    as in linear().  mask (bool [rows]): False for rows of padding,
+    x's type, to which h is rounded (float16: to 22 bits, and above 2.7e8 to an
+    infinity).  act as in linear().  mask (bool [rows]): False for rows of padding,
     which route nowhere and get the residual alone, whatever x holds there.
     out.y may be residual."""
     dev, rows, cols, xs = _need_rows(x, "x")

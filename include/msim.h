@@ -612,8 +612,8 @@ int msim_linear_backward(const msim_linear_spec *spec, const void *x, const void
  * half of it); out = y + residual.  x, out, residual: rows x cols of type dtype;
  * gate: experts x cols, w_in: experts x (hidden, gated: 2 hidden) x cols, w_out:
  * experts x cols x hidden, all of type dtype and contiguous.  h is rounded to
- * dtype (of f16, above 65,504 to an infinity), the sums are not.  mask (may be
- * NULL): one byte a row; a row with 0 is padding, whatever x holds there: ids -1,
+ * dtype, of f16 to 22 bits (above 2.7e8 to an infinity); the sums are not.  mask (may
+ * be NULL): one byte a row; a row with 0 is padding, whatever x holds there: ids -1,
  * weights 0, y 0.  A row that the router voids (a NaN logit) has y NaN.  bias is
  * msim_route's.  route.dtype is MSIM_F32 and route.row_stride is route.experts.  Only
  * chosen experts' weights are read.  residual may be out, at the same stride.

@@ -276,3 +276,38 @@ def test_graph_of_f16_gradients(T, M):  # noqa: F811
     got = M.linear_backward(*fresh[:3], act="gelu", pre=fresh[3], stream=s)
     T.cuda.synchronize()
     assert all(T.equal(a, b) for a, b in zip(got, want[:3]))
+
+
+@pytest.mark.parametrize("gated,act", [(True, "silu"), (False, "relu"), (True, "gelu")])
+@pytest.mark.parametrize("size", [1.0, 600.0, 6000.0])
+def test_f16_layers_hold_hidden_units_beyond_f16(T, M, gated, act, size):  # noqa: F811
+    """Halves of `size`, whose products are far above 65,504, and an answer that f16 holds.  A hidden unit is in two parts: off by
+    2^-22 relative, or 2^-25 where that is more (the second part's lowest place); what else is off as in a layer of small ones."""
+    for n, (rows, cols, hidden, experts, top_k) in enumerate([(1, 64, 32, 8, 2), (1, 300, 1000, 4, 4), (3, 72, 257, 6, 2), (12, 64, 48, 40, 6),
+                                                              (16, 320, 100, 16, 4), (40, 129, 33, 9, 1), (60, 256, 520, 3, 2), (100, 264, 136, 24, 3),
+                                                              (200, 128, 64, 1, 1), (512, 64, 40, 12, 2), (150, 64, 1300, 2, 1)]):
+        g = gen(T, 500 + n)
+        top = size if gated else size * size / 10
+        x, gate = real(T, g, T.float16)(rows, cols), real(T, g, T.float16, 1.5 / math.sqrt(cols))(experts, cols)
+        w_in = real(T, g, T.float16, min(top, 60000.0) / math.sqrt(cols) / 8)(experts, 2 * hidden if gated else hidden, cols)
+        w_out = real(T, g, T.float16, 8 / (top * top if gated else top) / math.sqrt(hidden))(experts, cols, hidden)
+        r = M.layer(x, gate, w_in, w_out, top_k, act=act, gated=gated)
+        y, tol, big = T.zeros(rows, cols, device=DEV, dtype=T.float64), T.zeros(rows, cols, device=DEV, dtype=T.float64), 0.0
+        for e in r.routing.ids.unique().tolist():
+            t, k = (r.routing.ids == e).nonzero(as_tuple=True)
+            xe, wi, wo = x[t].double(), w_in[e].double(), w_out[e].double()
+            a, S = xe @ wi.T, SUM(cols) * (xe.abs() @ wi.abs().T)
+            p = act64(T, a[:, :hidden], act)
+            ep = 1.13 * S[:, :hidden] + 2 ** -17 * (a[:, :hidden].abs() + p.abs())
+            h, eh = (p * a[:, hidden:], ep * a[:, hidden:].abs() + (p.abs() + ep) * S[:, hidden:]) if gated else (p, ep)
+            eh = eh + 2.0 ** -22 * h.abs() + 2.0 ** -25
+            big = max(big, float(h.abs().max()))
+            s = r.routing.weights[t, k].double()[:, None]
+            y[t] += s * (h @ wo.T)
+            tol[t] += s * (eh @ wo.abs().T + (SUM(2 * hidden + 32) + 2.0 ** -16) * ((h.abs() + eh) @ wo.abs().T))
+        tol += top_k * 2 ** -23 * (y.abs() + tol) + U["f16"] * y.abs() + 2.0 ** -25
+        off = float(((r.y.double() - y).abs() / tol).nan_to_num(math.inf).max())
+        print(gated, act, size, rows, cols, hidden, experts, top_k, off, big, flush=True)
+        assert off <= 1 and big < 2.6e8 and float(y.abs().max()) < 65000
+        again = M.layer(x, gate, w_in, w_out, top_k, act=act, gated=gated)
+        assert T.equal(r.y, again.y)
